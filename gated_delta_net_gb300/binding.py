@@ -1,4 +1,5 @@
-"""Thin Python binding of ``include/gdn_tree.h``: argument marshalling only.
+"""Thin Python binding of ``include/gdn_tree.h`` and ``include/gdn_layer.h``:
+argument marshalling only.
 
 Every function has the name of the C entry point it calls.  Tensors are torch
 tensors on the CUDA device (torch provides memory and streams; every step of
@@ -20,10 +21,13 @@ GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED = 0, 1, 2
 GDN_ERR_INVALID_TREE, GDN_ERR_INVALID_PATH, GDN_ERR_CUDA, GDN_ERR_DEVICE = 3, 4, 5, 6
 GDN_F32, GDN_BF16 = 0, 1
 DEV_BITS = {1: "BAD_TREE", 2: "BAD_PATH", 4: "TOO_MANY", 8: "TOO_DEEP", 16: "TIMEOUT", 64: "INTERNAL",
-            32: "BAD_DESC"}
+            32: "BAD_DESC", 128: "BAD_SLOT"}
+GDN_ACTS = {"silu": 0, "sigmoid": 1}
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
+_F = ctypes.c_float
 
 
 class VerifyArgs(ctypes.Structure):
@@ -49,6 +53,41 @@ class StatesArgs(ctypes.Structure):
                 ("node_offsets", _P), ("k", _P), ("v", _P), ("g", _P), ("beta", _P), ("S0", _P),
                 ("parent", _P), ("anc_mask", _P), ("mask_words", _I), ("n_sel", _I),
                 ("sel_request", _P), ("sel_node", _P), ("S_sel", _P), ("dev_status", _P)]
+
+
+class PrefillArgs(ctypes.Structure):
+    _fields_ = [("batch", _I), ("n_k_heads", _I), ("n_v_heads", _I), ("d_k", _I), ("d_v", _I),
+                ("total_tokens", _I), ("max_tokens", _I), ("n_states", _I), ("scale", _F), ("qkv_dtype", _I),
+                ("out_dtype", _I), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L), ("token_offsets", _P),
+                ("q", _P), ("k", _P), ("v", _P), ("g", _P), ("beta", _P), ("S0", _P), ("slots", _P),
+                ("fresh", _P), ("o", _P), ("S_new", _P), ("workspace", _P), ("workspace_bytes", _L),
+                ("dev_status", _P)]
+
+
+class DecodeArgs(ctypes.Structure):
+    _fields_ = [("batch", _I), ("n_k_heads", _I), ("n_v_heads", _I), ("d_k", _I), ("d_v", _I), ("n_states", _I),
+                ("scale", _F), ("qkv_dtype", _I), ("out_dtype", _I), ("q_stride", _L), ("k_stride", _L),
+                ("v_stride", _L), ("q", _P), ("k", _P), ("v", _P), ("g", _P), ("beta", _P), ("S", _P),
+                ("slots", _P), ("o", _P), ("dev_status", _P)]
+
+
+class QkGatesArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _I), ("n_k_heads", _I), ("n_v_heads", _I), ("d_k", _I), ("eps", _F),
+                ("dtype", _I), ("q_stride", _L), ("k_stride", _L), ("a_stride", _L), ("b_stride", _L), ("q", _P),
+                ("k", _P), ("a", _P), ("b", _P), ("A_log", _P), ("dt_bias", _P), ("q_out", _P), ("k_out", _P),
+                ("g", _P), ("beta", _P)]
+
+
+class NormGateArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _I), ("n_v_heads", _I), ("d_v", _I), ("eps", _F), ("act", _I), ("dtype", _I),
+                ("weight_dtype", _I), ("o_stride", _L), ("z_stride", _L), ("o", _P), ("z", _P), ("weight", _P),
+                ("y", _P)]
+
+
+class ResidualNormArgs(ctypes.Structure):
+    _fields_ = [("total_tokens", _I), ("width", _I), ("scale", _F), ("eps", _F), ("dtype", _I),
+                ("weight_dtype", _I), ("x_stride", _L), ("y_stride", _L), ("x", _P), ("y", _P), ("weight", _P),
+                ("post_weight", _P), ("h", _P), ("n", _P)]
 
 
 class GdnError(RuntimeError):
@@ -96,6 +135,12 @@ def lib():
         L.gdn_tree_relabel.restype = ctypes.c_int
         L.gdn_gather_rows.argtypes = [_P, _P, _P, _P, _I, _I, ctypes.c_int64, _P, _P]
         L.gdn_gather_rows.restype = ctypes.c_int
+        for fn, args in ((L.gdn_prefill, PrefillArgs), (L.gdn_decode, DecodeArgs), (L.gdn_qk_gates, QkGatesArgs),
+                         (L.gdn_norm_gate, NormGateArgs), (L.gdn_residual_norm, ResidualNormArgs)):
+            fn.argtypes = [ctypes.POINTER(args), _P]
+            fn.restype = ctypes.c_int
+        L.gdn_prefill_workspace.argtypes = [ctypes.POINTER(PrefillArgs)]
+        L.gdn_prefill_workspace.restype = _L
         L.gdn_last_error.restype = ctypes.c_char_p
         L.gdn_tree_version.restype = ctypes.c_int
         L.gdn_test_set_wait_probe.argtypes = [_I]
@@ -367,6 +412,189 @@ def gdn_tree_commit_verify(prev: dict, S0, max_nodes_prev: int, max_path: int,
                           max_depth, scale, out, out_dtype, dev_status)
     _check(lib().gdn_tree_commit_verify(ctypes.byref(c), ctypes.byref(a), _stream(stream)))
     return out, S_new
+
+
+# ----------------------------------------------------------------------------
+# the layer around the tree (gdn_layer.h)
+# ----------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """The distance between the tokens of ``t`` in elements (its other dimensions contiguous),
+    after a check of its type and shape."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return 0
+    if not t[0].is_contiguous():
+        raise ValueError(f"{name} must be contiguous inside a token")
+    stride = t.stride(0)
+    if shape[0] > 1 and stride < t[0].numel():
+        raise ValueError(f"the tokens of {name} overlap")
+    return stride if shape[0] > 1 else 0
+
+
+def _flat(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
+    """``t`` after a check of its type and shape; contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    return t
+
+
+def _keep(t: torch.Tensor, stream) -> None:
+    """Tell torch's allocator of a call's own temporary that it is used on ``stream``."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
+                                               device=t.device)
+        t.record_stream(stream)
+
+
+def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots=None, fresh=None,
+                scale: float = 1.0, S_new=None, out=None, out_dtype=None, workspace=None, dev_status=None,
+                stream=None):
+    """Prompts, packed: (o [T, Hv, d_v], S_new).  Prompt b is rows token_offsets[b] to
+    token_offsets[b + 1] of q, k [T, Hk, d_k], v [T, Hv, d_v] (tokens may be strided) and of
+    g, beta [T, Hv]; max_tokens bounds its length.  Its state is row slots[b] (or b) of the pools
+    S0 (None: zero; a prompt with fresh[b] != 0 starts from zero too) and S_new (may be S0)."""
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    dt = q.dtype
+    od = out_dtype or dt
+    qs, ks, vs = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk)), _rows(v, "v", dt, (T, Hv, dv))
+    _flat(g, "g", torch.float32, (T, Hv))
+    _flat(beta, "beta", torch.float32, (T, Hv))
+    _dev(token_offsets, "token_offsets", torch.int32)
+    B = token_offsets.numel() - 1
+    for name, t in (("slots", slots), ("fresh", fresh)):
+        if t is not None:
+            _flat(t, name, torch.int32, (B,))
+    if S_new is None:
+        if slots is not None:
+            raise ValueError("slots need S_new: the pool that they point into")
+        S_new = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device)
+    n_states = S_new.shape[0]
+    _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk))
+    if S0 is not None:
+        _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
+    if slots is None and n_states < B:
+        raise ValueError("the pool has fewer states than there are prompts")
+    if out is None:
+        out = torch.empty((T, Hv, dv), dtype=od, device=q.device)
+    _flat(out, "out", od, (T, Hv, dv))
+    a = PrefillArgs(B, Hk, Hv, dk, dv, T, int(max_tokens), n_states, float(scale), _code(dt), _code(od), qs, ks, vs,
+                    _ptr(token_offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(slots),
+                    _ptr(fresh), _ptr(out), _ptr(S_new), None, 0, _ptr(dev_status))
+    if workspace is None:
+        need = lib().gdn_prefill_workspace(ctypes.byref(a))
+        if need < 0:
+            _check(GDN_ERR_INVALID_ARG)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            _keep(workspace, stream)
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    _check(lib().gdn_prefill(ctypes.byref(a), _stream(stream)))
+    return out, S_new
+
+
+def gdn_prefill_workspace(batch: int, n_k_heads: int, n_v_heads: int, d_k: int, d_v: int, total_tokens: int,
+                          max_tokens: int, dtype=torch.bfloat16, out_dtype=None) -> int:
+    """Bytes of ``workspace`` with which gdn_prefill takes these sizes (it allocates its own otherwise)."""
+    a = PrefillArgs(batch, n_k_heads, n_v_heads, d_k, d_v, total_tokens, max_tokens, batch, 1.0, _code(dtype),
+                    _code(out_dtype or dtype))
+    need = lib().gdn_prefill_workspace(ctypes.byref(a))
+    if need < 0:
+        _check(GDN_ERR_INVALID_ARG)
+    return need
+
+
+def gdn_decode(q, k, v, g, beta, S, slots=None, scale: float = 1.0, out=None, out_dtype=None, dev_status=None,
+               stream=None) -> torch.Tensor:
+    """One token a request: o [B, Hv, d_v]; state slots[b] (or b) of the pool S is updated in place.
+    A row whose slot is -1 is not in use: its outputs are zero."""
+    B, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    dt = q.dtype
+    od = out_dtype or dt
+    qs, ks, vs = _rows(q, "q", dt, (B, Hk, dk)), _rows(k, "k", dt, (B, Hk, dk)), _rows(v, "v", dt, (B, Hv, dv))
+    _flat(g, "g", torch.float32, (B, Hv))
+    _flat(beta, "beta", torch.float32, (B, Hv))
+    n_states = S.shape[0]
+    _flat(S, "S", torch.float32, (n_states, Hv, dv, dk))
+    if slots is not None:
+        _flat(slots, "slots", torch.int32, (B,))
+    elif n_states < B:
+        raise ValueError("the pool has fewer states than there are requests")
+    if out is None:
+        out = torch.empty((B, Hv, dv), dtype=od, device=q.device)
+    else:
+        _flat(out, "out", od, (B, Hv, dv))
+    a = DecodeArgs(B, Hk, Hv, dk, dv, n_states, scale, _code(dt), _code(od), qs, ks, vs, _ptr(q), _ptr(k), _ptr(v),
+                   _ptr(g), _ptr(beta), _ptr(S), _ptr(slots), _ptr(out), _ptr(dev_status))
+    _check(lib().gdn_decode(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def gdn_qk_gates(q, k, a, b, A_log, dt_bias, eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Before the rule: (q, k of unit length per head, g [T, Hv], beta [T, Hv]) from a layer's
+    projections q, k [T, Hk, d_k] and a, b [T, Hv] (tokens may be strided) and its A_log, dt_bias [Hv]."""
+    T, Hk, dk = q.shape
+    Hv = a.shape[1]
+    dt = q.dtype
+    qs, ks = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk))
+    as_, bs = _rows(a, "a", dt, (T, Hv)), _rows(b, "b", dt, (T, Hv))
+    _flat(A_log, "A_log", torch.float32, (Hv,))
+    _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
+    q_out = torch.empty((T, Hk, dk), dtype=dt, device=q.device) if q_out is None else _flat(q_out, "q_out", dt, (T, Hk, dk))
+    k_out = torch.empty((T, Hk, dk), dtype=dt, device=q.device) if k_out is None else _flat(k_out, "k_out", dt, (T, Hk, dk))
+    g = torch.empty((T, Hv), dtype=torch.float32, device=q.device)
+    beta = torch.empty((T, Hv), dtype=torch.float32, device=q.device)
+    args = QkGatesArgs(T, Hk, Hv, dk, eps, _code(dt), qs, ks, as_, bs, _ptr(q), _ptr(k), _ptr(a), _ptr(b),
+                       _ptr(A_log), _ptr(dt_bias), _ptr(q_out), _ptr(k_out), _ptr(g), _ptr(beta))
+    _check(lib().gdn_qk_gates(ctypes.byref(args), _stream(stream)))
+    return q_out, k_out, g, beta
+
+
+def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, stream=None) -> torch.Tensor:
+    """After the rule: o [T, Hv, d_v] normed per head, times weight [d_v] and act(z) (silu or sigmoid)."""
+    T, Hv, dv = o.shape
+    dt = o.dtype
+    os_, zs = _rows(o, "o", dt, (T, Hv, dv)), _rows(z, "z", dt, (T, Hv, dv))
+    if act not in GDN_ACTS:
+        raise ValueError(f"act must be one of {sorted(GDN_ACTS)}, got {act!r}")
+    _flat(weight, "weight", weight.dtype, (dv,))
+    out = torch.empty((T, Hv, dv), dtype=dt, device=o.device) if out is None else _flat(out, "out", dt, (T, Hv, dv))
+    a = NormGateArgs(T, Hv, dv, eps, GDN_ACTS[act], _code(dt), _code(weight.dtype), os_, zs, _ptr(o), _ptr(z),
+                     _ptr(weight), _ptr(out))
+    _check(lib().gdn_norm_gate(ctypes.byref(a), _stream(stream)))
+    return out
+
+
+def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: float = 1e-6, h=None, out=None,
+                      stream=None):
+    """Between two blocks: (h, n) with h = x + scale * y (y normed first where post_weight is given)
+    and n = h normed, times weight; x, y [T, width] (tokens may be strided)."""
+    T, D = x.shape
+    dt = x.dtype
+    xs, ys = _rows(x, "x", dt, (T, D)), _rows(y, "y", dt, (T, D))
+    _flat(weight, "weight", weight.dtype, (D,))
+    if post_weight is not None:
+        _flat(post_weight, "post_weight", weight.dtype, (D,))
+    h = torch.empty((T, D), dtype=dt, device=x.device) if h is None else _flat(h, "h", dt, (T, D))
+    out = torch.empty((T, D), dtype=dt, device=x.device) if out is None else _flat(out, "out", dt, (T, D))
+    a = ResidualNormArgs(T, D, scale, eps, _code(dt), _code(weight.dtype), xs, ys, _ptr(x), _ptr(y), _ptr(weight),
+                         _ptr(post_weight), _ptr(h), _ptr(out))
+    _check(lib().gdn_residual_norm(ctypes.byref(a), _stream(stream)))
+    return h, out
 
 
 # ----------------------------------------------------------------------------

@@ -6,9 +6,13 @@
 
 #include "internal.cuh"
 
-namespace {
+namespace gdn {
 
+namespace {
 thread_local char g_err[512] = "";
+}
+
+void clear_error() { g_err[0] = 0; }
 
 int fail(int code, const char *fmt, ...) {
     va_list ap;
@@ -17,6 +21,12 @@ int fail(int code, const char *fmt, ...) {
     va_end(ap);
     return code;
 }
+
+}  // namespace gdn
+
+namespace {
+
+using gdn::fail;
 
 int cuda_fail(cudaError_t e, const char *what) {
     return fail(GDN_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
@@ -122,7 +132,7 @@ int wait_probe_polls() { return g_probe.load(std::memory_order_relaxed); }
 
 extern "C" {
 
-const char *gdn_last_error(void) { return g_err; }
+const char *gdn_last_error(void) { return gdn::g_err; }
 
 int gdn_tree_version(void) { return 200; }
 
@@ -131,7 +141,7 @@ void gdn_test_set_wait_probe(int32_t polls) { gdn::g_probe.store(polls > 0 ? pol
 int gdn_tree_build_desc(const int32_t *parent, const int32_t *node_offsets, int32_t batch,
                         int32_t max_nodes, uint32_t *anc_mask, int32_t mask_words,
                         int32_t *depth, int32_t *dev_status, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     if (batch < 0) return fail(GDN_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (max_nodes < 1) return fail(GDN_ERR_INVALID_ARG, "max_nodes %d < 1", max_nodes);
     if (max_nodes > gdn::kMaxNodes)
@@ -150,7 +160,7 @@ int gdn_tree_build_desc(const int32_t *parent, const int32_t *node_offsets, int3
 int gdn_tree_grow(const int32_t *node_offsets, int32_t batch, int32_t total_nodes, int32_t width, int32_t max_depth,
                   int32_t max_children, const int32_t *n_children, const float *draws, int32_t *parent, float *score,
                   int32_t *n_nodes, int32_t *dev_status, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     if (batch < 0) return fail(GDN_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (total_nodes < 0) return fail(GDN_ERR_INVALID_ARG, "total_nodes %d < 0", total_nodes);
     if (width < 1) return fail(GDN_ERR_INVALID_ARG, "width %d < 1", width);
@@ -168,7 +178,7 @@ int gdn_tree_grow(const int32_t *node_offsets, int32_t batch, int32_t total_node
 int gdn_tree_relabel(const int32_t *parent_in, const int32_t *node_offsets, int32_t batch, int32_t total_nodes,
                      int32_t max_nodes, int32_t *order, int32_t *rank, int32_t *parent_out, int32_t *dev_status,
                      void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     if (batch < 0) return fail(GDN_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (total_nodes < 0) return fail(GDN_ERR_INVALID_ARG, "total_nodes %d < 0", total_nodes);
     if (max_nodes < 1) return fail(GDN_ERR_INVALID_ARG, "max_nodes %d < 1", max_nodes);
@@ -184,7 +194,7 @@ int gdn_tree_relabel(const int32_t *parent_in, const int32_t *node_offsets, int3
 
 int gdn_gather_rows(const void *src, void *dst, const int32_t *index, const int32_t *node_offsets, int32_t batch,
                     int32_t total_nodes, int64_t row_bytes, int32_t *dev_status, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     if (batch < 0) return fail(GDN_ERR_INVALID_ARG, "batch %d < 0", batch);
     if (total_nodes < 0) return fail(GDN_ERR_INVALID_ARG, "total_nodes %d < 0", total_nodes);
     if (batch > 65535) return fail(GDN_ERR_UNSUPPORTED, "batch %d > 65535", batch);
@@ -203,7 +213,7 @@ int gdn_gather_rows(const void *src, void *dst, const int32_t *index, const int3
 }
 
 int gdn_tree_verify(const gdn_verify_args *a, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     int st = check_verify(a);
     if (st || a->batch == 0) return st;
     cudaError_t e = launch_verify_any(*a, (cudaStream_t)stream, false);
@@ -211,7 +221,7 @@ int gdn_tree_verify(const gdn_verify_args *a, void *stream) {
 }
 
 int gdn_tree_verify_branches(const gdn_verify_args *a, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     int st = check_verify(a);
     if (st || a->batch == 0) return st;
     cudaError_t e = gdn::launch_verify_branches(*a, (cudaStream_t)stream);
@@ -219,7 +229,7 @@ int gdn_tree_verify_branches(const gdn_verify_args *a, void *stream) {
 }
 
 int gdn_tree_commit(const gdn_commit_args *a, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     int st = check_commit(a);
     if (st || a->batch == 0) return st;
     cudaError_t e = launch_commit_any(*a, (cudaStream_t)stream);
@@ -227,7 +237,7 @@ int gdn_tree_commit(const gdn_commit_args *a, void *stream) {
 }
 
 int gdn_tree_commit_verify(const gdn_commit_args *c, const gdn_verify_args *v, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     int st = check_commit(c);
     if (st) return st;
     if (!v) return fail(GDN_ERR_INVALID_ARG, "verify args are NULL");
@@ -246,7 +256,7 @@ int gdn_tree_commit_verify(const gdn_commit_args *c, const gdn_verify_args *v, v
 }
 
 int gdn_tree_states(const gdn_states_args *a, void *stream) {
-    g_err[0] = 0;
+    gdn::clear_error();
     if (!a) return fail(GDN_ERR_INVALID_ARG, "args is NULL");
     int st = check_common(a->batch, a->n_k_heads, a->n_v_heads, a->d_k, a->d_v, a->max_nodes);
     if (st) return st;

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "gdn_layer.h"
 #include "gdn_tree.h"
 
 namespace gdn {
@@ -31,6 +32,10 @@ __device__ __forceinline__ float warp_sum(float x) {
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
+
+// the message behind gdn_last_error(): cleared at an entry, set with the code returned
+void clear_error();
+int fail(int code, const char *fmt, ...);
 
 // ---------------------------------------------------------------------------
 // launchers (one per translation unit); each returns a cudaError_t
@@ -62,6 +67,13 @@ cudaError_t launch_commit_tc(const gdn_commit_args &a, cudaStream_t stream);
 // the same kernel writing the states at selected nodes
 bool states_tc_supported(const gdn_states_args &a);
 cudaError_t launch_states_tc(const gdn_states_args &a, cudaStream_t stream);
+
+// the layer around the tree (gdn_layer.h)
+cudaError_t launch_prefill_simt(const gdn_prefill_args &a, cudaStream_t stream);
+cudaError_t launch_decode(const gdn_decode_args &a, cudaStream_t stream);
+cudaError_t launch_qk_gates(const gdn_qk_gates_args &a, cudaStream_t stream);
+cudaError_t launch_norm_gate(const gdn_norm_gate_args &a, cudaStream_t stream);
+cudaError_t launch_residual_norm(const gdn_residual_norm_args &a, cudaStream_t stream);
 
 // driver entry point for TMA descriptors (nullptr when the driver lacks it)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
