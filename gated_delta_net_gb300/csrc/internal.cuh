@@ -70,6 +70,9 @@ cudaError_t launch_states_tc(const gdn_states_args &a, cudaStream_t stream);
 
 // the layer around the tree (gdn_layer.h)
 cudaError_t launch_prefill_simt(const gdn_prefill_args &a, cudaStream_t stream);
+// chunked tensor-core prompts for bf16, d_k = d_v = 128
+bool prefill_tc_supported(const gdn_prefill_args &a);
+cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream);
 cudaError_t launch_decode(const gdn_decode_args &a, cudaStream_t stream);
 cudaError_t launch_qk_gates(const gdn_qk_gates_args &a, cudaStream_t stream);
 cudaError_t launch_norm_gate(const gdn_norm_gate_args &a, cudaStream_t stream);

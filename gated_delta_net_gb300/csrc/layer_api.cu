@@ -74,6 +74,8 @@ int gdn_prefill(const gdn_prefill_args *a, void *stream) {
     if (!a->token_offsets || !a->S_new) return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a->total_tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->o))
         return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (a->max_tokens >= 16 && gdn::prefill_tc_supported(*a))
+        return done(gdn::launch_prefill_tc(*a, (cudaStream_t)stream), "prefill launch");
     return done(gdn::launch_prefill_simt(*a, (cudaStream_t)stream), "prefill launch");
 }
 
