@@ -17,13 +17,15 @@
 // out (2^-18).  The state comes out about 5e-6 (norm-wise) from exact.  The output's own
 // products take S, U and Y rounded once to bf16, like the output itself.
 //
-// One block an SM (all 512 tensor-memory columns), 20 warps:
-//     warp 0        loads by TMA: K and Q of three chunks, V of two
-//     warp 1        issues the Gram and W products, whichever is ready
-//     warp 2        issues U, O and dS: the chain
-//     warps 4-7     gates, A, T = (I + A)^-1 by blocks of 16, 32, 64 in fp32, T', T'', Y
-//     warps 8-11    W to shared memory, the outputs to global memory
-//     warps 12-19   the state in registers (a row of 64 entries each), its hi + lo operand in
+// One block an SM (all 512 tensor-memory columns), 24 warps:
+//     warp 0        loads K and Q of three chunks by TMA
+//     warp 1        issues [K;Q] K^T
+//     warp 2        issues U, O and dS: the chain; loads V
+//     warp 3        the chunk's gates: gamma by a scan, and its exponentials
+//     warps 4-7     A and Y; T = (I + A)^-1 in blocks of 16, the diagonal ones
+//     warps 8-11    T's other blocks, T', T'', issue W
+//     warps 12-15   W to shared memory, the outputs to global memory
+//     warps 16-23   the state in registers (a row of 64 entries each), its hi + lo operand in
 //                   tensor memory, and U's
 // The chain for a chunk is: S split -> S W^T -> U split -> dS -> S.
 #include <algorithm>
@@ -43,26 +45,33 @@ using tiles::named_sync;
 using tiles::pack_bf16;
 
 constexpr int kC = 64;         // tokens a chunk
-constexpr int kThreads = 640;  // 20 warps
-constexpr int kKQ = 3, kV = 2, kRing = 3, kDecays = 8;
+constexpr int kThreads = 768;  // 24 warps
+constexpr int kKQ = 3;         // chunks of K and Q, of Y and of gates held at a time
+constexpr int kDecays = 8;
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: half of a token tile
 constexpr int OFF_KQ = 0;                    // [kKQ][2 halves of d][K, Q] tiles
-constexpr int OFF_V = OFF_KQ + kKQ * 4 * kTile;  // [kV][2 halves] tiles
-constexpr int OFF_T = OFF_V + kV * 2 * kTile;    // T' hi, lo, T'' hi, lo (negated): rows i, columns j
+constexpr int OFF_V = OFF_KQ + kKQ * 4 * kTile;  // [2 halves] tiles
+constexpr int OFF_T = OFF_V + 2 * kTile;     // T' hi, lo, T'' hi, lo (negated): rows i, columns j
 constexpr int OFF_W = OFF_T + 4 * kTile;     // W^T hi, lo: 128 rows of d_k, columns i
-constexpr int OFF_Y = OFF_W + 4 * kTile;     // [2] Y: rows i, columns j
-constexpr int OFF_A = OFF_Y + 2 * kTile;     // fp32 [64][64] A, then T
-constexpr int OFF_SC = OFF_A + kC * kC * 4;  // fp32 gamma hi, lo, beta, beta e^gamma (of the chunk in work)
-constexpr int OFF_RING = OFF_SC + 4 * kC * 4;    // [kRing] scale e^gamma, e^(gamma_63 - gamma)
-constexpr int OFF_EL = OFF_RING + kRing * 2 * kC * 4;  // [kDecays] e^gamma_63
+constexpr int OFF_Y = OFF_W + 4 * kTile;     // [kKQ] Y: rows i, columns j
+constexpr int OFF_A = OFF_Y + kKQ * kTile;   // [2] ten 16 x 16 blocks, bf16 hi and lo: A below the diagonal (6), T on
+                                             // it (4; before T is known, A's diagonal blocks in fp32)
+constexpr int kBlocks = 10 * 1024;
+constexpr int OFF_SC = OFF_A + 2 * kBlocks;  // [kKQ] gates of a chunk, floats:
+constexpr int SC_HI = 0, SC_LO = 64, SC_BETA = 128, SC_BG = 192;  // -gamma log2 e hi, lo; beta; beta e^gamma
+constexpr int SC_ROW = 256, SC_COL = 320;    // e^(gamma_i - gamma_r), r the first token of i's block of 16; e^(gamma_r - gamma_j)
+                                             // for the blocks' r = 16, 32, 48 and j < r
+constexpr int SC_EG = 416, SC_FD = 480;      // scale e^gamma, e^(gamma_63 - gamma)
+constexpr int kGates = 544 * 4;
+constexpr int OFF_EL = OFF_SC + kKQ * kGates;  // [kDecays] e^gamma_63
 constexpr int OFF_SLOT = OFF_EL + kDecays * 4;
 constexpr int OFF_BAR = OFF_SLOT + 16;
 enum Bar {
-    B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_VFULL = B_EMPTY + kKQ, B_VEMPTY = B_VFULL + kV,
-    B_G = B_VEMPTY + kV, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_UBF, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE,
-    B_PROBE, B_COUNT
+    B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
+    B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_VFULL = B_BLKFREE + 2,
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_UBF, B_SQ, B_UPD, B_O, B_OFREE, B_PROBE, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -107,30 +116,196 @@ __device__ __forceinline__ Item item_of(const Params &p, int idx) {
     return x;
 }
 
-// Bounded wait; after a first one that ran out the others only look once, so that a block
-// whose pipeline broke still ends soon.
+// Bounded wait: about a second; after a first one that ran out the others only look once, so that a
+// block whose pipeline broke still ends soon.  A phase is waited for before the one after it can
+// complete, or the parity would alias: what runs two chunks ahead or behind has two barriers.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
-    if (!mbar_wait(bar, parity, ok ? (1u << 20) : 1u)) ok = false;
+    if (mbar_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+#pragma unroll 1
+    for (uint32_t i = 0; ok && i < (1u << 24); ++i) {
+        if (mbar_try_wait(bar, parity)) return;
+        if (clock64() - t0 > (1ll << 31)) break;
+    }
+    ok = false;
+}
+
+// the same by a whole warp
+__device__ __forceinline__ void wwait(uint64_t *bar, uint32_t parity, bool &ok) {
+    wait(bar, parity, ok);
+    __syncwarp();
 }
 
 __device__ __forceinline__ uint32_t sw(int row, int chunk16) {  // byte offset in a tile of 128-byte rows
     return (uint32_t)(row * 128 + ((chunk16 ^ (row & 7)) << 4));
 }
 
+// MMA issue by a whole converged warp, one elected lane of which (lead) issues: descriptors stay in uniform
+// registers, and an MMA takes 25 cycles to issue (52 in a branch of lane 0, as long as a 128 x 64 x 16 one runs).
+// A descriptor is given by its low word (start address; the rest is the same for all 128-byte-swizzled tiles up
+// to the distance between the 64-element halves of an MN-major operand).
+__device__ __forceinline__ uint32_t desc_lo(const void *tile, int lbo_bytes) {
+    return ((smem_u32(tile) >> 4) & 0x3FFFu) | ((uint32_t)(lbo_bytes >> 4) << 16);
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+
+// two fp32 values in a register pair, for the packed fp32 instructions
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pair(uint32_t a, uint32_t b) { return pair(__uint_as_float(a), __uint_as_float(b)); }
+__device__ __forceinline__ float2 parts(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // hi + lo bf16 pairs of two values: packed hi, packed lo
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16(a, b);
-    lo = pack_bf16(a - bf16_lo(hi), b - bf16_hi(hi));
+__device__ __forceinline__ void split2(f2 x, uint32_t &hi, uint32_t &lo) {
+    const float2 v = parts(x);
+    hi = pack_bf16(v.x, v.y);
+    const float2 rest = parts(fma2(pair(bf16_lo(hi), bf16_hi(hi)), pair(-1.f, -1.f), x));
+    lo = pack_bf16(rest.x, rest.y);
 }
 
-// float index of (row, col) in the fp32 64 x 64 tile: 16-byte pieces permuted by the row, so that
-// a piece of eight consecutive rows covers all banks
-__device__ __forceinline__ int at(int row, int col) { return row * kC + ((((col >> 2) ^ (row & 7)) << 2) | (col & 3)); }
+// byte offset of 8 columns from 8 c8 of row r in a 16 x 16 bf16 block (rows of 32 bytes, halves exchanged in
+// every other group of four rows, so that eight rows cover all banks)
+__device__ __forceinline__ uint32_t blk(int r, int c8) { return (uint32_t)(r * 32 + ((c8 ^ ((r >> 2) & 1)) << 4)); }
 
-__device__ __forceinline__ float4 ld4(const float *a, int row, int col) {
-    return *reinterpret_cast<const float4 *>(a + at(row, col));
+// float index of columns 4 c4.. of row i of A's diagonal blocks
+__device__ __forceinline__ int diag_at(int i, int c4) { return i * 16 + ((c4 ^ ((i >> 1) & 3)) << 2); }
+
+// warp-wide 16 x 16 products of bf16 fragments in registers (the small triangular solve; fp32 sums)
+__device__ __forceinline__ void ldm(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void st4(float *a, int row, int col, float4 v) { *reinterpret_cast<float4 *>(a + at(row, col)) = v; }
+__device__ __forceinline__ void ldm_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// d += (hi + lo of a) (hi + lo of the block at `addr`, this lane's row address)
+__device__ __forceinline__ void mul_block(float (&d)[2][4], const uint32_t (&ahi)[4], const uint32_t (&alo)[4], uint32_t addr) {
+    uint32_t bh[4], bl[4];
+    ldm_t(addr, bh);
+    ldm_t(addr + 512, bl);
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        mma16(d[nt], ahi, bh[2 * nt], bh[2 * nt + 1]);
+        mma16(d[nt], alo, bh[2 * nt], bh[2 * nt + 1]);
+        mma16(d[nt], ahi, bl[2 * nt], bl[2 * nt + 1]);
+    }
+}
+struct Frag {  // a block as a left-hand operand
+    uint32_t hi[4], lo[4];
+};
+__device__ __forceinline__ void load_left(uint32_t addr, Frag &f) {
+    ldm(addr, f.hi);
+    ldm(addr + 512, f.lo);
+}
+
+// -(accumulators) as the left-hand operand of the next product
+__device__ __forceinline__ void to_left_neg(const float (&d)[2][4], Frag &f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split2(pair(-d[e >> 1][2 * (e & 1)], -d[e >> 1][2 * (e & 1) + 1]), f.hi[e], f.lo[e]);
+}
+
+// accumulators to a block in shared memory
+__device__ __forceinline__ void put_plain(uint8_t *at, const float (&d)[2][4], int lane) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t hi, lo;
+        split2(pair(d[e >> 1][2 * (e & 1)], d[e >> 1][2 * (e & 1) + 1]), hi, lo);
+        uint8_t *to = at + blk((lane >> 2) + 8 * (e & 1), e >> 1) + (lane & 3) * 4;
+        *reinterpret_cast<uint32_t *>(to) = hi;
+        *reinterpret_cast<uint32_t *>(to + 512) = lo;
+    }
+}
+
+// T's block (bi, bj) as T' and -T'', hi and lo, into the tiles the tensor cores read
+__device__ __forceinline__ void put_block(uint8_t *tt, const float *sc, int bi, int bj, int lane, const float (&v)[2][4]) {
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+        const int col = 16 * bj + 8 * nt + (lane & 3) * 2;
+        const f2 b = *reinterpret_cast<const f2 *>(sc + SC_BETA + col), bg = *reinterpret_cast<const f2 *>(sc + SC_BG + col);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int row = 16 * bi + (lane >> 2) + 8 * hh;
+            const f2 t = pair(v[nt][2 * hh], v[nt][2 * hh + 1]);
+            uint8_t *at = tt + sw(row, 2 * bj + nt) + (lane & 3) * 4;
+            uint32_t hi, lo;
+            split2(mul2(t, b), hi, lo);
+            *reinterpret_cast<uint32_t *>(at) = hi;
+            *reinterpret_cast<uint32_t *>(at + kTile) = lo;
+            split2(mul2(t, bg), hi, lo);
+            *reinterpret_cast<uint32_t *>(at + 2 * kTile) = hi ^ 0x80008000u;
+            *reinterpret_cast<uint32_t *>(at + 3 * kTile) = lo ^ 0x80008000u;
+        }
+    }
+}
+__device__ __forceinline__ void put_diag(uint8_t *tt, const float *sc, int bi, int lane, uint32_t addr) {
+    Frag f;
+    load_left(addr, f);
+    float v[2][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e >> 1][2 * (e & 1)] = bf16_lo(f.hi[e]) + bf16_lo(f.lo[e]);
+        v[e >> 1][2 * (e & 1) + 1] = bf16_hi(f.hi[e]) + bf16_hi(f.lo[e]);
+    }
+    put_block(tt, sc, bi, bi, lane, v);
+}
 
 // sum of two double-floats
 __device__ __forceinline__ void dd_add(float &ah, float &al, float bh, float bl) {
@@ -154,17 +329,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            const uint32_t n = i == B_GFREE || i == B_T || i == B_WRDY || i == B_SQRD || i == B_OFREE ? 4
-                               : i == B_S || i == B_UST || i == B_UBF                               ? 8
-                               : i == B_TFREE                                                       ? 2
-                                                                                                    : 1;
+            const bool four = i == B_GFREE || i == B_T || i == B_WRDY || i == B_OFREE ||
+                              (i >= B_SCFREE && i < B_GATES) || (i >= B_BLK && i < B_VFULL);
+            const uint32_t n = four ? 4 : i == B_S || i == B_UST || i == B_UBF ? 8 : i == B_TFREE ? 2 : 1;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
     }
-    // Y's tiles and A's upper blocks are zero above the diagonal blocks that are written
-    for (int i = tid; i < (2 * kTile + kC * kC * 4) / 16; i += kThreads)
-        *reinterpret_cast<uint4 *>(sm + OFF_Y + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    // T's and Y's tiles stay zero above the blocks that are written
+    for (int i = tid; i < (4 + kKQ) * kTile / 16; i += kThreads)
+        *reinterpret_cast<uint4 *>(sm + (i < 4 * kTile / 16 ? OFF_T : OFF_Y - 4 * kTile) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     if (warp == 2) {
         tmem_alloc(slot, 512);
@@ -178,109 +352,58 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 
     if (warp < 4) {
         reg_dealloc<40>();
+        const uint32_t lead = elect();
+        const uint32_t tm = uniform(tmem);
         if (warp == 0 && lane == 0) {
             // ---------------------------------------------------------------- loads
             if (p.probe > 0) ok = mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe);
             bool go = true;  // the pipeline's own waits
-            int cc = 0, kq = 0, n_kq = 0, n_v = 0;
+            int cc = 0, kq = 0;
             for (int idx = blockIdx.x; idx < p.items && go; idx += gridDim.x) {
                 const Item x = item_of(p, idx);
                 if (x.err) flag(p.status, x.err);
-                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
-                    const int row = x.lo + c * kC, v = cc & 1;
+                for (int c = 0; c < x.chunks && go; ++c) {
                     uint8_t *dst = sm + OFF_KQ + kq * 4 * kTile;
                     if (cc >= kKQ) wait(&bar[B_EMPTY + kq], (cc / kKQ - 1) & 1, go);
                     if (!go) break;  // nothing is loaded over a stage that may be in use
-                    ++n_kq;
                     mbar_arrive_expect_tx(&bar[B_FULL + kq], 4 * kTile);
                     for (int half = 0; half < 2; ++half) {
-                        tma_load_3d(dst + half * 2 * kTile, &tmK, &bar[B_FULL + kq], half * 64, x.hk, row);
-                        tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + kq], half * 64, x.hk, row);
+                        tma_load_3d(dst + half * 2 * kTile, &tmK, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
+                        tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
                     }
-                    if (cc >= kV) wait(&bar[B_VEMPTY + v], (cc / kV - 1) & 1, go);
-                    if (!go) break;
-                    ++n_v;
-                    mbar_arrive_expect_tx(&bar[B_VFULL + v], 2 * kTile);
-                    for (int half = 0; half < 2; ++half)
-                        tma_load_3d(sm + OFF_V + (v * 2 + half) * kTile, &tmV, &bar[B_VFULL + v], half * 64, x.h, row);
+                    ++cc;
+                    kq = kq + 1 == kKQ ? 0 : kq + 1;
                 }
             }
             // every load has landed before the block ends, whatever became of its reader
-            for (int i = 0; i < kKQ && i < n_kq; ++i) mbar_wait(&bar[B_FULL + i], ((n_kq - 1 - i) / kKQ) & 1, 1u << 16);
-            for (int i = 0; i < kV && i < n_v; ++i) mbar_wait(&bar[B_VFULL + i], ((n_v - 1 - i) / kV) & 1, 1u << 16);
+            for (int i = 0; i < kKQ && i < cc; ++i) mbar_wait(&bar[B_FULL + i], ((cc - 1 - i) / kKQ) & 1, 1u << 16);
             ok = ok && go;
         } else if (warp == 1) {
-            // ---------------------------------------------------------------- Gram and W products
-            const uint32_t id_g = idesc_bf16_f32(128, kC), id_w = idesc_bf16_f32(128, kC) | (1u << 15);
-            int idx = blockIdx.x, c = 0;  // the next Gram's item and chunk in it
-            Item x;
-            auto seek = [&]() {  // the first item from idx on that has chunks
-                for (; idx < p.items; idx += gridDim.x) {
-                    x = item_of(p, idx);
-                    if (x.chunks > 0) break;
-                }
-            };
-            seek();
-            int gcc = 0, wcc = 0, gkq = 0, wkq = 0;
-            for (uint32_t idle = 0; idx < p.items || wcc < gcc;) {
-                bool g = false, w = false;
-                if (lane == 0) {
-                    g = idx < p.items && mbar_test_wait(&bar[B_FULL + gkq], (gcc / kKQ) & 1) &&
-                        (gcc == 0 || mbar_test_wait(&bar[B_GFREE], (gcc - 1) & 1));
-                    w = wcc < gcc && mbar_test_wait(&bar[B_T], wcc & 1) &&
-                        (wcc == 0 || mbar_test_wait(&bar[B_WRDY], (wcc - 1) & 1));
-                }
-                g = __shfl_sync(0xffffffffu, g, 0);
-                w = __shfl_sync(0xffffffffu, w, 0);
-                if (w) {
-                    if (lane == 0) {
-                        tc_fence_after();
-                        const uint8_t *kt = sm + OFF_KQ + wkq * 4 * kTile;
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16(tmem + TM_W, smem_desc(smem_u32(kt + ks * 2048), 2 * kTile, 1024, 2),
-                                         smem_desc(smem_u32(sm + OFF_T + (2 + part) * kTile + ks * 32), 16, 1024, 2), id_w,
-                                         part > 0 || ks > 0);
-                        mma_commit(&bar[B_W]);
-                        mma_commit(&bar[B_TFREE]);
-                    }
-                    ++wcc;
-                    wkq = wkq + 1 == kKQ ? 0 : wkq + 1;
-                }
-                if (g) {
-                    wait(&bar[B_FULL + gkq], (gcc / kKQ) & 1, ok);  // complete: every lane sees the tile
-                    uint8_t *kt = sm + OFF_KQ + gkq * 4 * kTile;
+            // ---------------------------------------------------------------- [K;Q] K^T
+            const uint32_t id = idesc_bf16_f32(128, kC);
+            int cc = 0, kq = 0;
+            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+                const Item x = item_of(p, idx);
+                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                    uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
+                    wwait(&bar[B_FULL + kq], (cc / kKQ) & 1, ok);
+                    if (cc > 0) wwait(&bar[B_GFREE], (cc - 1) & 1, ok);
                     const int nv = x.n - c * kC;
                     if (nv < kC) {  // keys past the prompt's end: zero, whatever the next prompt holds
                         for (int half = 0; half < 2; ++half)
                             for (int i = nv * 8 + lane; i < kC * 8; i += 32)
                                 *reinterpret_cast<uint4 *>(kt + half * 2 * kTile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc_fence_after();
+                    tc_fence_after();
+                    const uint32_t d = uniform(desc_lo(kt, 0));
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks) {
-                            const uint64_t d = smem_desc(smem_u32(kt + (ks >> 2) * 2 * kTile + (ks & 3) * 32), 16, 1024, 2);
-                            mma_bf16(tmem + TM_G, d, d, id_g, ks > 0);
-                        }
-                        mma_commit(&bar[B_G]);
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t o = ((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4;
+                        mma_ss(lead, tm + TM_G, d + o, d + o, id, ks > 0);
                     }
-                    ++gcc;
-                    gkq = gkq + 1 == kKQ ? 0 : gkq + 1;
-                    if (++c == x.chunks) {
-                        c = 0;
-                        idx += gridDim.x;
-                        seek();
-                    }
-                }
-                idle = g || w ? 0 : idle + 1;
-                if (idle > (1u << 22)) {
-                    ok = false;
-                    break;
+                    commit(lead, &bar[B_G]);
                 }
             }
         } else if (warp == 2) {
@@ -289,13 +412,34 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t id_sw = idesc_bf16_f32(128, kC) | (1u << 16); // S (tensor memory) W^T, W MN-major
             const uint32_t id_k = idesc_bf16_f32(128, kC);               // K-major right-hand side
             const uint32_t id_ds = idesc_bf16_f32(128, kD) | (1u << 16); // U' K, K MN-major
-            int cc = 0, kq = 0;
-            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-                const Item x = item_of(p, idx);
+            uint8_t *vt = sm + OFF_V;
+            const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
+            int cc = 0, kq = 0, idx = blockIdx.x;
+            auto seek = [&](int i) {  // the first item from i on that has chunks
+                for (; i < p.items; i += gridDim.x)
+                    if (item_of(p, i).chunks > 0) break;
+                return i;
+            };
+            int loads = 0;
+            auto load_v = [&](const Item &x, int c) {
+                ++loads;
+                mbar_arrive_expect_tx(&bar[B_VFULL], 2 * kTile);
+                for (int half = 0; half < 2; ++half)
+                    tma_load_3d(vt + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
+            };
+            idx = seek(idx);
+            Item x = {}, nx = {};
+            if (idx < p.items) {
+                nx = item_of(p, idx);
+                if (lead) load_v(nx, 0);
+            }
+            while (idx < p.items) {
+                x = nx;
+                idx = seek(idx + gridDim.x);
+                if (idx < p.items) nx = item_of(p, idx);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
-                    const int v = cc & 1;
-                    uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile, *vt = sm + OFF_V + v * 2 * kTile;
-                    wait(&bar[B_VFULL + v], (cc / kV) & 1, ok);
+                    uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
+                    wwait(&bar[B_VFULL], cc & 1, ok);
                     const int nv = x.n - c * kC;
                     if (nv < kC) {
                         for (int half = 0; half < 2; ++half)
@@ -304,95 +448,85 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) {
-                        // U^T = V^T T'^T
-                        wait(&bar[B_T], cc & 1, ok);
-                        tc_fence_after();
+                    // U^T = V^T T'^T
+                    wwait(&bar[B_T], cc & 1, ok);
+                    tc_fence_after();
 #pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16(tmem + TM_U, smem_desc(smem_u32(vt + ks * 2048), kTile, 1024, 2),
-                                         smem_desc(smem_u32(sm + OFF_T + part * kTile + ks * 32), 16, 1024, 2), id_u,
-                                         part > 0 || ks > 0);
-                        mma_commit(&bar[B_TFREE]);
-                        mma_commit(&bar[B_VEMPTY + v]);
-                        // U^T += S (-W)^T: hi hi, lo hi, hi lo
-                        wait(&bar[B_WRDY], cc & 1, ok);
-                        wait(&bar[B_S], cc & 1, ok);
-                        tc_fence_after();
-#pragma unroll
-                        for (int part = 0; part < 3; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 8; ++ks)
-                                mma_bf16_ts(tmem + TM_U, tmem + (part == 1 ? TM_SLO : TM_SHI) + ks * 8,
-                                            smem_desc(smem_u32(sm + OFF_W + (part == 2 ? 2 * kTile : 0) + ks * 2048), kTile, 1024, 2),
-                                            id_sw, true);
-                        mma_commit(&bar[B_U]);
-                        // O^T = S Q^T
-                        if (cc > 0) wait(&bar[B_OFREE], (cc - 1) & 1, ok);
-                        tc_fence_after();
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_bf16_ts(tmem + TM_O, tmem + TM_SHI + ks * 8,
-                                        smem_desc(smem_u32(kt + kTile + (ks >> 2) * 2 * kTile + (ks & 3) * 32), 16, 1024, 2), id_k, ks > 0);
-                        mma_commit(&bar[B_SQ]);
-                        // dS = U'^T K
-                        wait(&bar[B_UST], cc & 1, ok);
-                        tc_fence_after();
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16_ts(tmem + TM_DS, tmem + (part ? TM_ULO : TM_UHI) + ks * 8,
-                                            smem_desc(smem_u32(kt + ks * 2048), 2 * kTile, 1024, 2), id_ds, part > 0 || ks > 0);
-                        mma_commit(&bar[B_UPD]);
-                        // O^T of the chunk's own tokens = U^T Y^T, once S Q^T has been read
-                        wait(&bar[B_UBF], cc & 1, ok);
-                        wait(&bar[B_SQRD], cc & 1, ok);
-                        tc_fence_after();
+                    for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_bf16_ts(tmem + TM_O, tmem + TM_UBF + ks * 8,
-                                        smem_desc(smem_u32(sm + OFF_Y + (cc & 1) * kTile + ks * 32), 16, 1024, 2), id_k, ks > 0);
-                        mma_commit(&bar[B_O]);
-                        mma_commit(&bar[B_EMPTY + kq]);
+                            mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + ((part * kTile + ks * 32) >> 4), id_u, part > 0 || ks > 0);
+                    commit(lead, &bar[B_TFREE]);
+                    // U^T += S (-W)^T: hi hi, lo hi, hi lo
+                    wwait(&bar[B_WRDY], cc & 1, ok);
+                    wwait(&bar[B_S], cc & 1, ok);
+                    tc_fence_after();
+#pragma unroll
+                    for (int part = 0; part < 3; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(lead, tm + TM_U, tm + (part == 1 ? TM_SLO : TM_SHI) + ks * 8,
+                                   d_w + (((part == 2 ? 2 * kTile : 0) + ks * 2048) >> 4), id_sw, true);
+                    commit(lead, &bar[B_U]);
+                    // O^T = S Q^T
+                    if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
+                    tc_fence_after();
+                    const uint32_t d_q = uniform(desc_lo(kt + kTile, 0)), d_k = uniform(desc_lo(kt, 2 * kTile));
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
+                    commit(lead, &bar[B_SQ]);
+                    // dS = U'^T K; U' is made of U^T's sum, so V has been read: the next chunk's may come
+                    wwait(&bar[B_UST], cc & 1, ok);
+                    tc_fence_after();
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(lead, tm + TM_DS, tm + (part ? TM_ULO : TM_UHI) + ks * 8, d_k + ks * 128, id_ds, part > 0 || ks > 0);
+                    commit(lead, &bar[B_UPD]);
+                    if (lead && ok) {
+                        if (c + 1 < x.chunks) load_v(x, c + 1);
+                        else if (idx < p.items) load_v(nx, 0);
                     }
                     __syncwarp();
+                    // O^T += U^T Y^T, once S Q^T has its factors
+                    wwait(&bar[B_UBF], cc & 1, ok);
+                    tc_fence_after();
+                    const uint32_t d_y = uniform(desc_lo(sm + OFF_Y + kq * kTile, 0));
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) mma_ts(lead, tm + TM_O, tm + TM_UBF + ks * 8, d_y + ((ks * 32) >> 4), id_k, true);
+                    commit(lead, &bar[B_O]);
+                    commit(lead, &bar[B_YFREE + kq]);
+                    commit(lead, &bar[B_EMPTY + kq]);
                 }
             }
-        }
-    } else if (warp < 8) {
-        // -------------------------------------------------------------------- gates, A, T, T', T'', Y
-        reg_dealloc<88>();
-        float *A = reinterpret_cast<float *>(sm + OFF_A);
-        float *ghi = reinterpret_cast<float *>(sm + OFF_SC), *glo = ghi + kC, *sbeta = ghi + 2 * kC, *sbg = ghi + 3 * kC;
-        float *el = reinterpret_cast<float *>(sm + OFF_EL);
-        const int t128 = tid - 128, row = quad * 32 + lane, i = row & 63;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        int cc = 0, ring = 0;
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const Item x = item_of(p, idx);
-            float pg[2] = {0.f, 0.f}, pb[2] = {0.f, 0.f};  // g and beta of tokens 2 lane, 2 lane + 1 of the next chunk
-            auto fetch = [&](int c) {
+            if (lead && loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
+        } else if (warp == 3) {
+            // ---------------------------------------------------------------- gates, ahead of everything
+            float *el = reinterpret_cast<float *>(sm + OFF_EL);
+            int cc = 0, kq = 0;
+            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+                const Item x = item_of(p, idx);
+                float g[2], b[2];  // of tokens 2 lane, 2 lane + 1 of the next chunk
+                auto fetch = [&](int c) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int t = c * kC + 2 * lane + e;
-                    pg[e] = pb[e] = 0.f;
-                    if (t < x.n) {
-                        pg[e] = __ldg(p.g + (int64_t)(x.lo + t) * p.hv_n + x.h);
-                        pb[e] = __ldg(p.beta + (int64_t)(x.lo + t) * p.hv_n + x.h);
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = c * kC + 2 * lane + e;
+                        g[e] = b[e] = 0.f;
+                        if (t < x.n) {
+                            g[e] = __ldg(p.g + (int64_t)(x.lo + t) * p.hv_n + x.h);
+                            b[e] = __ldg(p.beta + (int64_t)(x.lo + t) * p.hv_n + x.h);
+                        }
                     }
-                }
-            };
-            if (quad == 0 && x.chunks > 0) fetch(0);
-            for (int c = 0; c < x.chunks; ++c, ++cc, ring = ring + 1 == kRing ? 0 : ring + 1) {
-                wait(&bar[B_G], cc & 1, ok);
-                tc_fence_after();
-                if (quad == 0) {
+                };
+                if (x.chunks > 0) fetch(0);
+                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     // gamma: a scan in pairs of floats, so that a decay that forgets everything leaves the
                     // differences after it exact.  e^-200 is zero, whatever lies below it
-                    const float g0 = pg[0] < -200.f ? -200.f : pg[0], g1 = pg[1] < -200.f ? -200.f : pg[1];
+                    const float g0 = g[0] < -200.f ? -200.f : g[0], g1 = g[1] < -200.f ? -200.f : g[1];
+                    const float b0 = b[0], b1 = b[1];
+                    if (c + 1 < x.chunks) fetch(c + 1);
                     float h = g0, l = 0.f;
                     dd_add(h, l, g1, 0.f);
 #pragma unroll
@@ -407,253 +541,335 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     float h0 = h, l0 = l;  // without the lane's second token
                     dd_add(h0, l0, -g1, 0.f);
                     const float hl = __shfl_sync(0xffffffffu, h, 31), ll = __shfl_sync(0xffffffffu, l, 31);
-                    float *rg = reinterpret_cast<float *>(sm + OFF_RING) + ring * 2 * kC;
-                    const float hh[2] = {h0, h}, lw[2] = {l0, l};
+                    const float hh[2] = {h0, h}, lw[2] = {l0, l}, bb[2] = {b0, b1};
+                    float nh[2], nl[2], bg[2], eg[2], fd[2], rc[2][4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int t = 2 * lane + e;
-                        const float eg = expf(hh[e] + lw[e]);
-                        ghi[t] = hh[e];
-                        glo[t] = lw[e];
-                        sbeta[t] = pb[e];
-                        sbg[t] = pb[e] * eg;
-                        rg[t] = p.scale * eg;
-                        rg[kC + t] = expf((hl - hh[e]) + (ll - lw[e]));
+                        const float kLog2e = 1.4426950408889634f, kLog2eLo = 1.4426950408889634 - (double)1.4426950408889634f;
+                        nh[e] = -hh[e] * kLog2e;
+                        nl[e] = -(fmaf(hh[e], kLog2e, nh[e]) + fmaf(lw[e], kLog2e, hh[e] * kLog2eLo));
+                        const float x0 = __expf(hh[e] + lw[e]);
+                        bg[e] = bb[e] * x0;
+                        eg[e] = p.scale * x0;
+                        fd[e] = __expf((hl - hh[e]) + (ll - lw[e]));
                     }
-                    if (lane == 0) el[cc & (kDecays - 1)] = expf(hl + ll);
-                    if (c + 1 < x.chunks) fetch(c + 1);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {  // from the blocks' first tokens r = 16 q, held by lane 8 q
+                        const float rh = __shfl_sync(0xffffffffu, h0, 8 * q), rl = __shfl_sync(0xffffffffu, l0, 8 * q);
+                        const bool own = (lane >> 3) == q;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float d = (hh[e] - rh) + (lw[e] - rl);
+                            rc[e][q] = __expf(own ? d : -d);
+                        }
+                    }
+                    const float last = __expf(hl + ll);
+                    // the place was last read by T and the chain of three chunks before
+                    if (cc >= kKQ) {
+                        wwait(&bar[B_SCFREE + kq], (cc / kKQ - 1) & 1, ok);
+                        wwait(&bar[B_EMPTY + kq], (cc / kKQ - 1) & 1, ok);
+                    }
+                    float *sc = reinterpret_cast<float *>(sm + OFF_SC + kq * kGates);
+                    auto put = [&](int at, float v0, float v1) { *reinterpret_cast<float2 *>(sc + at + 2 * lane) = make_float2(v0, v1); };
+                    put(SC_HI, nh[0], nh[1]);
+                    put(SC_LO, nl[0], nl[1]);
+                    put(SC_BETA, b0, b1);
+                    put(SC_BG, bg[0], bg[1]);
+                    put(SC_EG, eg[0], eg[1]);
+                    put(SC_FD, fd[0], fd[1]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if ((lane >> 3) == q) put(SC_ROW, rc[0][q], rc[1][q]);
+                        else if (lane < 8 * q) put(SC_COL + 8 * q * (q - 1), rc[0][q], rc[1][q]);
+                    }
+                    if (lane == 0) el[cc & (kDecays - 1)] = last;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[B_GATES + kq]);
                 }
-                named_sync(1, 128);
-                const float gh = ghi[i], gl = glo[i], f = row < 64 ? sbeta[i] : p.scale;
-                const int cols = (quad & 1) ? 64 : 32;  // rows 0..31 have nothing right of column 31
-                uint32_t y[32];
+            }
+        }
+    } else if (warp < 8) {
+        // -------------------------------------------------------------------- A, Y, T's diagonal blocks
+        reg_dealloc<72>();
+        const int row = quad * 32 + lane, i = row & 63, own = i >> 4;  // own: the row's block of 16
+        const bool is_y = row >= 64;
+        const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
+        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        int cc = 0, kq = 0;
+        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            const Item x = item_of(p, idx);
+            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
+                uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
+                float *diag = reinterpret_cast<float *>(blocks + 6 * 1024);
+                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
+                const f2 gh = pair(-sc[SC_HI + i], -sc[SC_HI + i]), gl = pair(-sc[SC_LO + i], -sc[SC_LO + i]);
+                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * sc[SC_ROW + i];
+                if (cc >= 2) wwait(&bar[B_BLKFREE + (cc & 1)], (cc / 2 - 1) & 1, ok);
+                if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], (cc / kKQ - 1) & 1, ok);
+                wwait(&bar[B_G], cc & 1, ok);
+                tc_fence_after();
 #pragma unroll
-                for (int j0 = 0; j0 < 64; j0 += 16) {
-                    if (j0 < cols) {
-                        uint32_t r[16];
-                        tmem_ld16_nowait(tmem + lanes + TM_G + j0, r);
-                        tmem_wait_ld_into(r);
-                        float m[16];
+                for (int cb2 = 0; cb2 < 4; cb2 += 2) {
+                  if (cb2 == 0 || (quad & 1)) {  // rows 0..31 have nothing right of column 31
+                    uint32_t rr[32];
+                    tmem_ld32_nowait(tmem + lanes + TM_G + cb2 * 16, rr);
+                    tmem_wait_ld_into(rr);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int jj = j0 + j;
-                            const float d = f * __expf((gh - ghi[jj]) + (gl - glo[jj]));
-                            m[j] = jj < i + (row >> 6) ? d * __uint_as_float(r[j]) : 0.f;
+                    for (int cb = cb2; cb < cb2 + 2; ++cb) {
+                        const uint32_t *r = rr + (cb & 1) * 16;
+                        f2 m[8];
+                        if (cb < own) {  // left of the own block: e^(gamma_i - gamma_r) e^(gamma_r - gamma_j)
+                            const float *col = sc + SC_COL + 8 * own * (own - 1) + cb * 16;
+                            const f2 F = pair(fr, fr);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(col + j);
+                                m[j / 2] = mul2(mul2(F, e.x), pair(r[j], r[j + 1]));
+                                m[j / 2 + 1] = mul2(mul2(F, e.y), pair(r[j + 2], r[j + 3]));
+                            }
+                        } else if (cb == own) {
+                            const f2 F = pair(f, f);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const ulonglong2 h4 = *reinterpret_cast<const ulonglong2 *>(sc + SC_HI + cb * 16 + j);
+                                const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(sc + SC_LO + cb * 16 + j);
+                                const float2 d0 = parts(add2(add2(gh, h4.x), add2(gl, l4.x)));
+                                const float2 d1 = parts(add2(add2(gh, h4.y), add2(gl, l4.y)));
+                                const float2 m0 = parts(mul2(pair(exp2_approx(d0.x), exp2_approx(d0.y)), mul2(F, pair(r[j], r[j + 1]))));
+                                const float2 m1 = parts(mul2(pair(exp2_approx(d1.x), exp2_approx(d1.y)), mul2(F, pair(r[j + 2], r[j + 3]))));
+                                m[j / 2] = pair(j < last ? m0.x : 0.f, j + 1 < last ? m0.y : 0.f);
+                                m[j / 2 + 1] = pair(j + 2 < last ? m1.x : 0.f, j + 3 < last ? m1.y : 0.f);
+                            }
                         }
-                        if (row < 64) {
+                        if (cb <= own) {
+                            if (is_y) {
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) st4(A, i, j0 + j, make_float4(m[j], m[j + 1], m[j + 2], m[j + 3]));
-                        } else {
+                                for (int q = 0; q < 2; ++q) {
+                                    uint32_t y[4];
 #pragma unroll
-                            for (int j = 0; j < 16; j += 2) y[(j0 + j) >> 1] = pack_bf16(m[j], m[j + 1]);
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 v = parts(m[4 * q + e]);
+                                        y[e] = pack_bf16(v.x, v.y);
+                                    }
+                                    *reinterpret_cast<uint4 *>(yt + sw(i, 2 * cb + q)) = make_uint4(y[0], y[1], y[2], y[3]);
+                                }
+                            } else if (cb == own) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    *reinterpret_cast<ulonglong2 *>(diag + diag_at(i, q)) = make_ulonglong2(m[2 * q], m[2 * q + 1]);
+                            } else {
+                                uint8_t *at = blocks + (own * (own - 1) / 2 + cb) * 1024;
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    uint32_t hi[4], lo[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) split2(m[4 * q + e], hi[e], lo[e]);
+                                    *reinterpret_cast<uint4 *>(at + blk(i & 15, q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                    *reinterpret_cast<uint4 *>(at + 512 + blk(i & 15, q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                }
+                            }
                         }
+                        __syncwarp();
                     }
+                  }
                 }
                 tc_fence_before();
+                if (is_y) fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_GFREE]);
-                if (row >= 64) {
-                    if (cc >= 2) wait(&bar[B_O], (cc - 2) & 1, ok);
-                    uint8_t *yt = sm + OFF_Y + (cc & 1) * kTile;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (q * 8 < cols)
-                            *reinterpret_cast<uint4 *>(yt + sw(i, q)) = make_uint4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-                }
                 named_sync(1, 128);
-                // T, diagonal blocks of 16: warp w block w, lane r < 16 row r.  From T (I + A) = I,
-                // t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling j
+                // T, diagonal blocks of 16: warp w block w, lane r row r (the upper half-warp repeats it).  From
+                // T (I + A) = I, t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling k
                 {
-                    const int b0 = quad * 16, r = lane & 15;
-                    float t[16];
+                    const int r = lane & 15, b0 = quad * 16;
+                    f2 t[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 a = ld4(A, b0 + r, b0 + j);
-                        t[j] = -a.x; t[j + 1] = -a.y; t[j + 2] = -a.z; t[j + 3] = -a.w;
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 v = *reinterpret_cast<const float4 *>(diag + diag_at(b0 + r, q));
+                        t[2 * q] = pair(-v.x, -v.y);
+                        t[2 * q + 1] = pair(-v.z, -v.w);
                     }
 #pragma unroll
                     for (int k = 14; k >= 1; --k) {
-                        const float tk = k < r ? t[k] : 0.f;
+                        const float2 v = parts(t[k >> 1]);
+                        const float tk = k < r ? ((k & 1) ? -v.y : -v.x) : 0.f;
+                        const f2 n = pair(tk, tk);
 #pragma unroll
-                        for (int j = 0; j < k; j += 4) {
-                            const float4 a = ld4(A, b0 + k, b0 + j);
-                            t[j] = fmaf(-tk, a.x, t[j]);
-                            if (j + 1 < k) t[j + 1] = fmaf(-tk, a.y, t[j + 1]);
-                            if (j + 2 < k) t[j + 2] = fmaf(-tk, a.z, t[j + 2]);
-                            if (j + 3 < k) t[j + 3] = fmaf(-tk, a.w, t[j + 3]);
+                        for (int q = 0; 4 * q < k; ++q) {  // row k of A is zero from column k on
+                            const ulonglong2 v4 = *reinterpret_cast<const ulonglong2 *>(diag + diag_at(b0 + k, q));
+                            t[2 * q] = fma2(n, v4.x, t[2 * q]);
+                            if (4 * q + 2 < k) t[2 * q + 1] = fma2(n, v4.y, t[2 * q + 1]);
                         }
                     }
-                    __syncwarp();
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 v = parts(t[j]);
+                        split2(pair(2 * j < r ? v.x : 2 * j == r ? 1.f : 0.f, 2 * j + 1 < r ? v.y : 2 * j + 1 == r ? 1.f : 0.f), hi[j], lo[j]);
+                    }
+                    __syncwarp();  // the block has been read: T's takes its place
+                    uint8_t *at = blocks + (6 + quad) * 1024;
                     if (lane < 16) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) t[j] = j < r ? t[j] : j == r ? 1.f : 0.f;
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) st4(A, b0 + r, b0 + j, make_float4(t[j], t[j + 1], t[j + 2], t[j + 3]));
+                        for (int q = 0; q < 2; ++q) {
+                            *reinterpret_cast<uint4 *>(at + blk(r, q)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                            *reinterpret_cast<uint4 *>(at + 512 + blk(r, q)) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+                        }
                     }
                 }
-                named_sync(1, 128);
-                // blocks of 32: T21 = -T22 (A21 T11); the products A21 T11 lie in the free upper right quarter
-                {
-                    const int pr = t128 >> 6, r = (t128 & 63) >> 2, c4 = (t128 & 3) * 4, b0 = pr * 32;
-                    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const float4 a = ld4(A, b0 + 16 + r, b0 + k);
-                        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 t = ld4(A, b0 + k + e, b0 + c4);
-                            s.x = fmaf(av[e], t.x, s.x); s.y = fmaf(av[e], t.y, s.y);
-                            s.z = fmaf(av[e], t.z, s.z); s.w = fmaf(av[e], t.w, s.w);
-                        }
-                    }
-                    st4(A, pr * 16 + r, 32 + c4, s);
-                    named_sync(1, 128);
-                    s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < 16; k += 4) {
-                        const float4 a = ld4(A, b0 + 16 + r, b0 + 16 + k);
-                        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 t = ld4(A, pr * 16 + k + e, 32 + c4);
-                            s.x = fmaf(-av[e], t.x, s.x); s.y = fmaf(-av[e], t.y, s.y);
-                            s.z = fmaf(-av[e], t.z, s.z); s.w = fmaf(-av[e], t.w, s.w);
-                        }
-                    }
-                    st4(A, b0 + 16 + r, b0 + c4, s);
-                }
-                named_sync(1, 128);
-                // the block of 64, the same
-                {
-                    const int r = t128 >> 2, c8 = (t128 & 3) * 8;
-                    float s[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s[e] = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 a = ld4(A, 32 + r, k);
-                        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 t = ld4(A, k + e, c8), u = ld4(A, k + e, c8 + 4);
-                            s[0] = fmaf(av[e], t.x, s[0]); s[1] = fmaf(av[e], t.y, s[1]);
-                            s[2] = fmaf(av[e], t.z, s[2]); s[3] = fmaf(av[e], t.w, s[3]);
-                            s[4] = fmaf(av[e], u.x, s[4]); s[5] = fmaf(av[e], u.y, s[5]);
-                            s[6] = fmaf(av[e], u.z, s[6]); s[7] = fmaf(av[e], u.w, s[7]);
-                        }
-                    }
-                    st4(A, r, 32 + c8, make_float4(s[0], s[1], s[2], s[3]));
-                    st4(A, r, 36 + c8, make_float4(s[4], s[5], s[6], s[7]));
-                    named_sync(1, 128);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s[e] = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < 32; k += 4) {
-                        const float4 a = ld4(A, 32 + r, 32 + k);
-                        const float av[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 t = ld4(A, k + e, 32 + c8), u = ld4(A, k + e, 36 + c8);
-                            s[0] = fmaf(-av[e], t.x, s[0]); s[1] = fmaf(-av[e], t.y, s[1]);
-                            s[2] = fmaf(-av[e], t.z, s[2]); s[3] = fmaf(-av[e], t.w, s[3]);
-                            s[4] = fmaf(-av[e], u.x, s[4]); s[5] = fmaf(-av[e], u.y, s[5]);
-                            s[6] = fmaf(-av[e], u.z, s[6]); s[7] = fmaf(-av[e], u.w, s[7]);
-                        }
-                    }
-                    st4(A, 32 + r, c8, make_float4(s[0], s[1], s[2], s[3]));
-                    st4(A, 32 + r, c8 + 4, make_float4(s[4], s[5], s[6], s[7]));
-                }
-                named_sync(1, 128);
-                // T' and -T'' as hi + lo tiles: thread (row r, half of the columns)
-                if (cc > 0) wait(&bar[B_TFREE], (cc - 1) & 1, ok);
-                {
-                    const int r = t128 & 63, hf = t128 >> 6;
-                    const bool zero = hf == 1 && r < 32;
-                    uint8_t *tt = sm + OFF_T;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int j = hf * 32 + q * 8;
-                        uint32_t h1[4] = {}, l1[4] = {}, h2[4] = {}, l2[4] = {};
-                        if (!zero) {
-#pragma unroll
-                            for (int e = 0; e < 8; e += 4) {
-                                const float4 t = ld4(A, r, j + e);
-                                const float4 b = *reinterpret_cast<const float4 *>(sbeta + j + e);
-                                const float4 bg = *reinterpret_cast<const float4 *>(sbg + j + e);
-                                split2(t.x * b.x, t.y * b.y, h1[e / 2], l1[e / 2]);
-                                split2(t.z * b.z, t.w * b.w, h1[e / 2 + 1], l1[e / 2 + 1]);
-                                split2(-t.x * bg.x, -t.y * bg.y, h2[e / 2], l2[e / 2]);
-                                split2(-t.z * bg.z, -t.w * bg.w, h2[e / 2 + 1], l2[e / 2 + 1]);
-                            }
-                        }
-                        const uint32_t off = sw(r, hf * 4 + q);
-                        *reinterpret_cast<uint4 *>(tt + off) = make_uint4(h1[0], h1[1], h1[2], h1[3]);
-                        *reinterpret_cast<uint4 *>(tt + kTile + off) = make_uint4(l1[0], l1[1], l1[2], l1[3]);
-                        *reinterpret_cast<uint4 *>(tt + 2 * kTile + off) = make_uint4(h2[0], h2[1], h2[2], h2[3]);
-                        *reinterpret_cast<uint4 *>(tt + 3 * kTile + off) = make_uint4(l2[0], l2[1], l2[2], l2[3]);
-                    }
-                }
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_T]);
-                named_sync(1, 128);  // the gates and A are read: the next chunk may write them
+                if (lane == 0) mbar_arrive(&bar[B_BLK + (cc & 1)]);
             }
         }
     } else if (warp < 12) {
+        // -------------------------------------------------------------------- the rest of T, T', T''
+        reg_dealloc<72>();
+        uint8_t *tt = sm + OFF_T;
+        const uint32_t id_w = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
+        const uint32_t lane_at = blk((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
+        int cc = 0, kq = 0;
+        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
+            const Item x = item_of(p, idx);
+            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
+                uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
+                const uint32_t base = smem_u32(blocks) + lane_at;
+                // blocks: A10 0, A20 1, A21 2, A30 3, A31 4, A32 5, T00 6, T11 7, T22 8, T33 9.
+                // By blocks of 32, T21 = -T22 A21 T11: two warps take the two inner blocks T10 and T32 (into the
+                // places of A10 and A32) and the right half of T21, two its left half
+                wwait(&bar[B_BLK + (cc & 1)], (cc / 2) & 1, ok);
+                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
+                float t0[2][4] = {}, t1[2][4] = {};
+                if (quad == 0) {
+                    float a[2][4] = {};
+                    Frag f, n;
+                    load_left(base + 7 * 1024, f);
+                    mul_block(a, f.hi, f.lo, base);
+                    to_left_neg(a, n);
+                    mul_block(t0, n.hi, n.lo, base + 6 * 1024);  // T10 = -T11 A10 T00
+                    put_plain(blocks, t0, lane);
+                    named_sync(2, 128);
+                    float b[2][4] = {};
+                    load_left(base + 8 * 1024, f);
+                    mul_block(b, f.hi, f.lo, base + 2 * 1024);
+                    to_left_neg(b, n);
+                    mul_block(t1, n.hi, n.lo, base + 7 * 1024);  // T21 = -T22 A21 T11
+                } else if (quad == 1) {
+                    float a[2][4] = {}, b[2][4] = {};
+                    Frag f, n;
+                    load_left(base + 9 * 1024, f);
+                    mul_block(a, f.hi, f.lo, base + 5 * 1024);
+                    to_left_neg(a, n);
+                    mul_block(t0, n.hi, n.lo, base + 8 * 1024);  // T32 = -T33 A32 T22
+                    __syncwarp();
+                    put_plain(blocks + 5 * 1024, t0, lane);
+                    named_sync(2, 128);
+                    mul_block(b, f.hi, f.lo, base + 4 * 1024);
+                    load_left(base + 5 * 1024, f);
+                    mul_block(b, f.hi, f.lo, base + 2 * 1024);
+                    to_left_neg(b, n);
+                    mul_block(t1, n.hi, n.lo, base + 7 * 1024);  // T31 = -(T32 A21 + T33 A31) T11
+                } else {
+                    // quad 2: row 2, quad 3: row 3 of T21's left half, -(P0 T00 + P1 T10)
+                    float a[2][4] = {}, b[2][4] = {};
+                    Frag f;
+                    load_left(base + (quad == 2 ? 8 : 9) * 1024, f);
+                    mul_block(a, f.hi, f.lo, base + (quad == 2 ? 1 : 3) * 1024);
+                    mul_block(b, f.hi, f.lo, base + (quad == 2 ? 2 : 4) * 1024);
+                    named_sync(2, 128);
+                    if (quad == 3) {
+                        load_left(base + 5 * 1024, f);
+                        mul_block(a, f.hi, f.lo, base + 1 * 1024);
+                        mul_block(b, f.hi, f.lo, base + 2 * 1024);
+                    }
+                    to_left_neg(a, f);
+                    mul_block(t0, f.hi, f.lo, base + 6 * 1024);
+                    to_left_neg(b, f);
+                    mul_block(t0, f.hi, f.lo, base);
+                }
+                if (cc > 0) wwait(&bar[B_TFREE], (cc - 1) & 1, ok);
+                if (quad == 0) {
+                    put_block(tt, sc, 1, 0, lane, t0);
+                    put_block(tt, sc, 2, 1, lane, t1);
+                    put_diag(tt, sc, 0, lane, base + 6 * 1024);
+                } else if (quad == 1) {
+                    put_block(tt, sc, 3, 2, lane, t0);
+                    put_block(tt, sc, 3, 1, lane, t1);
+                } else if (quad == 2) {
+                    put_block(tt, sc, 2, 0, lane, t0);
+                    put_diag(tt, sc, 1, lane, base + 7 * 1024);
+                    put_diag(tt, sc, 2, lane, base + 8 * 1024);
+                } else {
+                    put_block(tt, sc, 3, 0, lane, t0);
+                    put_diag(tt, sc, 3, lane, base + 9 * 1024);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar[B_T]);
+                    mbar_arrive(&bar[B_SCFREE + kq]);
+                    mbar_arrive(&bar[B_BLKFREE + (cc & 1)]);
+                }
+                if (quad == 3) {  // W^T = K^T T''^T, once the W before it has been read
+                    wwait(&bar[B_T], cc & 1, ok);
+                    if (cc > 0) wwait(&bar[B_WRDY], (cc - 1) & 1, ok);
+                    tc_fence_after();
+                    const uint32_t d_k = uniform(desc_lo(sm + OFF_KQ + kq * 4 * kTile, 2 * kTile)), d_t = uniform(desc_lo(tt, 0));
+                    const uint32_t tm = uniform(tmem), lead = elect();
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ss(lead, tm + TM_W, d_k + ks * 128, d_t + (((2 + part) * kTile + ks * 32) >> 4), id_w, part > 0 || ks > 0);
+                    commit(lead, &bar[B_W]);
+                    commit(lead, &bar[B_TFREE]);
+                }
+            }
+        }
+    } else if (warp < 16) {
         // -------------------------------------------------------------------- W to shared memory, outputs
         const int row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        auto outputs = [&](int cc, int ring, int tok, int nv, int h) {
-            const float *rg = reinterpret_cast<const float *>(sm + OFF_RING) + ring * 2 * kC;
-            float acc[64];
-            wait(&bar[B_SQ], cc & 1, ok);
+        reg_dealloc<56>();
+        auto outputs = [&](int cc, int tok, int nv, int h) {
+            wwait(&bar[B_O], cc & 1, ok);
             tc_fence_after();
+            uint32_t w[32];
 #pragma unroll
             for (int j0 = 0; j0 < 64; j0 += 16) {
                 uint32_t r[16];
                 tmem_ld16_nowait(tmem + lanes + TM_O + j0, r);
                 tmem_wait_ld_into(r);
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    const float4 e = *reinterpret_cast<const float4 *>(rg + j0 + j);
-                    acc[j0 + j] = e.x * __uint_as_float(r[j]);
-                    acc[j0 + j + 1] = e.y * __uint_as_float(r[j + 1]);
-                    acc[j0 + j + 2] = e.z * __uint_as_float(r[j + 2]);
-                    acc[j0 + j + 3] = e.w * __uint_as_float(r[j + 3]);
-                }
+                for (int j = 0; j < 16; j += 2) w[(j0 + j) / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_SQRD]);
-            wait(&bar[B_O], cc & 1, ok);
-            tc_fence_after();
-            __nv_bfloat16 *dst = p.o + ((int64_t)tok * p.hv_n + h) * kD + row;
+            if (lane == 0) mbar_arrive(&bar[B_OFREE]);
+            uint16_t *dst = reinterpret_cast<uint16_t *>(p.o) + ((int64_t)tok * p.hv_n + h) * kD + row;
             const int64_t step = (int64_t)p.hv_n * kD;
+            if (nv >= kC) {
 #pragma unroll
-            for (int j0 = 0; j0 < 64; j0 += 16) {
-                uint32_t r[16];
-                tmem_ld16_nowait(tmem + lanes + TM_O + j0, r);
-                tmem_wait_ld_into(r);
-                if (j0 == 48) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[B_OFREE]);
+                for (int j = 0; j < 32; ++j) {
+                    dst[(2 * j) * step] = (uint16_t)w[j];
+                    dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
                 }
+            } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (j0 + j < nv) *dst = __float2bfloat16_rn(acc[j0 + j] + __uint_as_float(r[j]));
-                    dst += step;
+                for (int j = 0; j < 32; ++j) {
+                    if (2 * j < nv) dst[(2 * j) * step] = (uint16_t)w[j];
+                    if (2 * j + 1 < nv) dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
                 }
             }
         };
-        int cc = 0, ring = 0;
-        int p_tok = 0, p_nv = 0, p_h = 0, p_ring = 0;  // the chunk whose outputs are still to come
+        int cc = 0, kq = 0;
+        int p_tok = 0, p_nv = 0, p_h = 0;  // the chunk whose outputs are still to come
         for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const Item x = item_of(p, idx);
-            for (int c = 0; c < x.chunks; ++c, ++cc, ring = ring + 1 == kRing ? 0 : ring + 1) {
-                wait(&bar[B_W], cc & 1, ok);
-                if (cc > 0) wait(&bar[B_U], (cc - 1) & 1, ok);  // S W^T of the chunk before has read W
+            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                wwait(&bar[B_W], cc & 1, ok);
+                if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // S W^T of the chunk before has read W
                 tc_fence_after();
                 uint8_t *wt = sm + OFF_W;
 #pragma unroll
@@ -663,7 +879,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     tmem_wait_ld_into(r);
                     uint32_t hi[8], lw[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) split2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]), hi[j / 2], lw[j / 2]);
+                    for (int j = 0; j < 16; j += 2) split2(pair(r[j], r[j + 1]), hi[j / 2], lw[j / 2]);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const uint32_t off = sw(row, j0 / 8 + q);
@@ -675,54 +891,54 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_WRDY]);
-                if (cc > 0) outputs(cc - 1, p_ring, p_tok, p_nv, p_h);
+                if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
                 p_tok = x.lo + c * kC;
                 p_nv = x.n - c * kC;
                 p_h = x.h;
-                p_ring = ring;
             }
         }
-        if (cc > 0) outputs(cc - 1, p_ring, p_tok, p_nv, p_h);
+        if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
     } else {
         // -------------------------------------------------------------------- the state
-        reg_alloc<128>();
-        const int row = quad * 32 + lane, half = (warp - 12) >> 2;
+        reg_alloc<120>();
+        const int row = quad * 32 + lane, half = (warp - 16) >> 2;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const float *el = reinterpret_cast<const float *>(sm + OFF_EL);
-        int cc = 0, ring = 0;
+        int cc = 0, kq = 0;
         for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
             const Item x = item_of(p, idx);
             if (x.err) continue;
             const int64_t mine = x.state + row * kD + half * 64;
-            float s[64];
+            f2 s[32];
 #pragma unroll
-            for (int j = 0; j < 64; j += 4) {
-                const float4 v = x.zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(p.S0 + mine + j);
-                s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
+            for (int j = 0; j < 32; j += 2) {
+                const ulonglong2 v = x.zero ? make_ulonglong2(0, 0) : *reinterpret_cast<const ulonglong2 *>(p.S0 + mine + 2 * j);
+                s[j] = v.x;
+                s[j + 1] = v.y;
             }
             // s = e^gamma_63 s + dS of chunk number n
             auto advance = [&](int n) {
-                wait(&bar[B_UPD], n & 1, ok);
+                wwait(&bar[B_UPD], n & 1, ok);
                 tc_fence_after();
-                const float a = el[n & (kDecays - 1)];
+                const f2 a = pair(el[n & (kDecays - 1)], el[n & (kDecays - 1)]);
 #pragma unroll
                 for (int j0 = 0; j0 < 64; j0 += 16) {
                     uint32_t r[16];
                     tmem_ld16_nowait(tmem + lanes + TM_DS + half * 64 + j0, r);
                     tmem_wait_ld_into(r);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) s[j0 + j] = fmaf(a, s[j0 + j], __uint_as_float(r[j]));
+                    for (int j = 0; j < 16; j += 2) s[(j0 + j) / 2] = fma2(a, s[(j0 + j) / 2], pair(r[j], r[j + 1]));
                 }
             };
-            for (int c = 0; c < x.chunks; ++c, ++cc, ring = ring + 1 == kRing ? 0 : ring + 1) {
+            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 if (c > 0) advance(cc - 1);
-                if (cc > 0) wait(&bar[B_O], (cc - 1) & 1, ok);  // U of the chunk before lies over S hi
+                if (cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);  // U of the chunk before lies over S hi
                 tc_fence_after();
 #pragma unroll
                 for (int j0 = 0; j0 < 64; j0 += 16) {
                     uint32_t hi[8], lw[8];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) split2(s[j0 + j], s[j0 + j + 1], hi[j / 2], lw[j / 2]);
+                    for (int j = 0; j < 16; j += 2) split2(s[(j0 + j) / 2], hi[j / 2], lw[j / 2]);
                     tmem_st8(tmem + lanes + TM_SHI + half * 32 + j0 / 2, hi);
                     tmem_st8(tmem + lanes + TM_SLO + half * 32 + j0 / 2, lw);
                 }
@@ -731,9 +947,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_S]);
 
-                const float *fd = reinterpret_cast<const float *>(sm + OFF_RING) + ring * 2 * kC + kC + half * 32;
+                const float *fd = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + SC_FD + half * 32;
                 uint32_t ub[2][8];
-                wait(&bar[B_U], cc & 1, ok);
+                wwait(&bar[B_U], cc & 1, ok);
                 tc_fence_after();
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -742,13 +958,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     tmem_wait_ld_into(r);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
-                        const float4 f = *reinterpret_cast<const float4 *>(fd + q * 16 + j);
-                        const float a = __uint_as_float(r[j]), b = __uint_as_float(r[j + 1]), d = __uint_as_float(r[j + 2]),
-                                    e = __uint_as_float(r[j + 3]);
-                        ub[q][j / 2] = pack_bf16(a, b);
-                        ub[q][j / 2 + 1] = pack_bf16(d, e);
-                        split2(a * f.x, b * f.y, hi[j / 2], lw[j / 2]);
-                        split2(d * f.z, e * f.w, hi[j / 2 + 1], lw[j / 2 + 1]);
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(fd + q * 16 + j);
+                        ub[q][j / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                        ub[q][j / 2 + 1] = pack_bf16(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                        split2(mul2(pair(r[j], r[j + 1]), f.x), hi[j / 2], lw[j / 2]);
+                        split2(mul2(pair(r[j + 2], r[j + 3]), f.y), hi[j / 2 + 1], lw[j / 2 + 1]);
                     }
                     tmem_st8(tmem + lanes + TM_UHI + half * 16 + q * 8, hi);
                     tmem_st8(tmem + lanes + TM_ULO + half * 16 + q * 8, lw);
@@ -757,10 +971,29 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_UST]);
-                wait(&bar[B_SQ], cc & 1, ok);
+                wwait(&bar[B_SQ], cc & 1, ok);
                 tc_fence_after();
+                // U over S hi; S Q^T times scale e^gamma, in place, before U^T Y^T is added
+                const float *eg = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + SC_EG + half * 32;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) tmem_st8(tmem + lanes + TM_UBF + half * 16 + q * 8, ub[q]);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t r[16], a[8], b[8];
+                    tmem_ld16_nowait(tmem + lanes + TM_O + half * 32 + q * 16, r);
+                    tmem_st8(tmem + lanes + TM_UBF + half * 16 + q * 8, ub[q]);
+                    tmem_wait_ld_into(r);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(eg + q * 16 + j);
+                        const float2 v0 = parts(mul2(e.x, pair(r[j], r[j + 1]))), v1 = parts(mul2(e.y, pair(r[j + 2], r[j + 3])));
+                        uint32_t *to = (j < 8 ? a : b) + (j & 7);
+                        to[0] = __float_as_uint(v0.x);
+                        to[1] = __float_as_uint(v0.y);
+                        to[2] = __float_as_uint(v1.x);
+                        to[3] = __float_as_uint(v1.y);
+                    }
+                    tmem_st8(tmem + lanes + TM_O + half * 32 + q * 16, a);
+                    tmem_st8(tmem + lanes + TM_O + half * 32 + q * 16 + 8, b);
+                }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -768,8 +1001,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             if (x.chunks > 0) advance(cc - 1);
 #pragma unroll
-            for (int j = 0; j < 64; j += 4)
-                *reinterpret_cast<float4 *>(p.S_new + mine + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+            for (int j = 0; j < 32; j += 2)
+                *reinterpret_cast<ulonglong2 *>(p.S_new + mine + 2 * j) = make_ulonglong2(s[j], s[j + 1]);
         }
     }
     if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
