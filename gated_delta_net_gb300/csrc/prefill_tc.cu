@@ -84,6 +84,8 @@ constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32, TM_UBF = TM_SHI;
 
 struct Params {
     int hk_n, hv_n, total, max_tokens, n_states, items, probe;
+    int step_b, step_h;    // blocks of the grid, in whole requests and heads
+    uint32_t group_inv;    // ceil(2^32 / heads that share a key head), 0 for one
     float scale;
     const int32_t *offsets, *slots, *fresh;
     const float *g, *beta, *S0;
@@ -98,34 +100,47 @@ struct Item {
     bool zero;      // starts from zero
 };
 
-__device__ __forceinline__ Item item_of(const Params &p, int idx) {
-    Item x;
-    const int b = idx / p.hv_n;
-    x.h = idx % p.hv_n;
-    x.hk = x.h / (p.hv_n / p.hk_n);
-    x.lo = __ldg(p.offsets + b);
-    x.n = __ldg(p.offsets + b + 1) - x.lo;
-    const int slot = p.slots ? __ldg(p.slots + b) : b;
-    x.err = 0;
-    if (x.n < 0 || x.lo < 0 || x.lo + x.n > p.total) x.err = GDN_DEV_BAD_DESC;
-    else if (x.n > p.max_tokens) x.err = GDN_DEV_TOO_MANY;
-    else if (slot < 0 || slot >= p.n_states) x.err = GDN_DEV_BAD_SLOT;
-    x.zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
-    x.state = ((int64_t)slot * p.hv_n + x.h) * (kD * kD);
-    x.chunks = x.err ? 0 : (x.n + kC - 1) / kC;
-    return x;
-}
+// a block's items: (request, head) pairs, a grid apart
+struct Walk {
+    int idx, b, h;
+    __device__ __forceinline__ void next(const Params &p) {
+        idx += gridDim.x;
+        b += p.step_b;
+        h += p.step_h;
+        if (h >= p.hv_n) {
+            h -= p.hv_n;
+            ++b;
+        }
+    }
+    __device__ __forceinline__ Item item(const Params &p) const {
+        Item x;
+        x.h = h;
+        x.hk = p.group_inv ? __umulhi((uint32_t)h, p.group_inv) : h;
+        x.lo = __ldg(p.offsets + b);
+        x.n = __ldg(p.offsets + b + 1) - x.lo;
+        const int slot = p.slots ? __ldg(p.slots + b) : b;
+        x.err = 0;
+        if (x.n < 0 || x.lo < 0 || x.lo + x.n > p.total) x.err = GDN_DEV_BAD_DESC;
+        else if (x.n > p.max_tokens) x.err = GDN_DEV_TOO_MANY;
+        else if (slot < 0 || slot >= p.n_states) x.err = GDN_DEV_BAD_SLOT;
+        x.zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
+        x.state = ((int64_t)slot * p.hv_n + h) * (kD * kD);
+        x.chunks = x.err ? 0 : (x.n + kC - 1) / kC;
+        return x;
+    }
+};
 
 // Bounded wait: about a second; after a first one that ran out the others only look once, so that a
 // block whose pipeline broke still ends soon.  A phase is waited for before the one after it can
 // complete, or the parity would alias: what runs two chunks ahead or behind has two barriers.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
-    if (mbar_try_wait(bar, parity)) return;
-    const long long t0 = clock64();
+    const uint32_t limit = ok ? 1u << 19 : 1u;
 #pragma unroll 1
-    for (uint32_t i = 0; ok && i < (1u << 24); ++i) {
-        if (mbar_try_wait(bar, parity)) return;
-        if (clock64() - t0 > (1ll << 31)) break;
+    for (uint32_t i = 0; i < limit; ++i) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 2000;\n\t"
+                     "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+        if (done) return;
     }
     ok = false;
 }
@@ -295,16 +310,14 @@ __device__ __forceinline__ void put_block(uint8_t *tt, const float *sc, int bi, 
         }
     }
 }
-__device__ __forceinline__ void put_diag(uint8_t *tt, const float *sc, int bi, int lane, uint32_t addr) {
+__device__ __forceinline__ void diag_block(uint32_t addr, float (&v)[2][4]) {
     Frag f;
     load_left(addr, f);
-    float v[2][4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[e >> 1][2 * (e & 1)] = bf16_lo(f.hi[e]) + bf16_lo(f.lo[e]);
         v[e >> 1][2 * (e & 1) + 1] = bf16_hi(f.hi[e]) + bf16_hi(f.lo[e]);
     }
-    put_block(tt, sc, bi, bi, lane, v);
 }
 
 // sum of two double-floats
@@ -349,6 +362,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *slot;
     bool ok = true;
+    Walk at = {(int)blockIdx.x, (int)blockIdx.x / p.hv_n, (int)blockIdx.x % p.hv_n};
 
     if (warp < 4) {
         reg_dealloc<40>();
@@ -359,8 +373,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (p.probe > 0) ok = mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe);
             bool go = true;  // the pipeline's own waits
             int cc = 0, kq = 0;
-            for (int idx = blockIdx.x; idx < p.items && go; idx += gridDim.x) {
-                const Item x = item_of(p, idx);
+            for (; at.idx < p.items && go; at.next(p)) {
+                const Item x = at.item(p);
                 if (x.err) flag(p.status, x.err);
                 for (int c = 0; c < x.chunks && go; ++c) {
                     uint8_t *dst = sm + OFF_KQ + kq * 4 * kTile;
@@ -382,8 +396,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // ---------------------------------------------------------------- [K;Q] K^T
             const uint32_t id = idesc_bf16_f32(128, kC);
             int cc = 0, kq = 0;
-            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-                const Item x = item_of(p, idx);
+            for (; at.idx < p.items; at.next(p)) {
+                const Item x = at.item(p);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_FULL + kq], (cc / kKQ) & 1, ok);
@@ -414,11 +428,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t id_ds = idesc_bf16_f32(128, kD) | (1u << 16); // U' K, K MN-major
             uint8_t *vt = sm + OFF_V;
             const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
-            int cc = 0, kq = 0, idx = blockIdx.x;
-            auto seek = [&](int i) {  // the first item from i on that has chunks
-                for (; i < p.items; i += gridDim.x)
-                    if (item_of(p, i).chunks > 0) break;
-                return i;
+            int cc = 0, kq = 0;
+            Item x = {}, nx = {};
+            auto seek = [&]() {  // nx: the next item that has chunks
+                for (nx.chunks = 0; at.idx < p.items && nx.chunks == 0; at.next(p)) nx = at.item(p);
             };
             int loads = 0;
             auto load_v = [&](const Item &x, int c) {
@@ -427,16 +440,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int half = 0; half < 2; ++half)
                     tma_load_3d(vt + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
             };
-            idx = seek(idx);
-            Item x = {}, nx = {};
-            if (idx < p.items) {
-                nx = item_of(p, idx);
-                if (lead) load_v(nx, 0);
-            }
-            while (idx < p.items) {
+            seek();
+            if (lead && nx.chunks > 0) load_v(nx, 0);
+            while (nx.chunks > 0) {
                 x = nx;
-                idx = seek(idx + gridDim.x);
-                if (idx < p.items) nx = item_of(p, idx);
+                seek();
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
@@ -487,7 +495,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     commit(lead, &bar[B_UPD]);
                     if (lead && ok) {
                         if (c + 1 < x.chunks) load_v(x, c + 1);
-                        else if (idx < p.items) load_v(nx, 0);
+                        else if (nx.chunks > 0) load_v(nx, 0);
                     }
                     __syncwarp();
                     // O^T += U^T Y^T, once S Q^T has its factors
@@ -506,8 +514,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // ---------------------------------------------------------------- gates, ahead of everything
             float *el = reinterpret_cast<float *>(sm + OFF_EL);
             int cc = 0, kq = 0;
-            for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-                const Item x = item_of(p, idx);
+            for (; at.idx < p.items; at.next(p)) {
+                const Item x = at.item(p);
                 float g[2], b[2];  // of tokens 2 lane, 2 lane + 1 of the next chunk
                 auto fetch = [&](int c) {
 #pragma unroll
@@ -596,8 +604,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         int cc = 0, kq = 0;
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const Item x = item_of(p, idx);
+        for (; at.idx < p.items; at.next(p)) {
+            const Item x = at.item(p);
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
@@ -609,16 +617,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], (cc / kKQ - 1) & 1, ok);
                 wwait(&bar[B_G], cc & 1, ok);
                 tc_fence_after();
-#pragma unroll
-                for (int cb2 = 0; cb2 < 4; cb2 += 2) {
-                  if (cb2 == 0 || (quad & 1)) {  // rows 0..31 have nothing right of column 31
-                    uint32_t rr[32];
-                    tmem_ld32_nowait(tmem + lanes + TM_G + cb2 * 16, rr);
-                    tmem_wait_ld_into(rr);
-#pragma unroll
-                    for (int cb = cb2; cb < cb2 + 2; ++cb) {
-                        const uint32_t *r = rr + (cb & 1) * 16;
+#pragma unroll 1
+                for (int cb = 0; cb < ((quad & 1) ? 4 : 2); ++cb) {  // rows 0..31 have nothing right of column 31
+                    {
+                        uint32_t r[16];
                         f2 m[8];
+                        tmem_ld16_nowait(tmem + lanes + TM_G + cb * 16, r);
+                        tmem_wait_ld_into(r);
                         if (cb < own) {  // left of the own block: e^(gamma_i - gamma_r) e^(gamma_r - gamma_j)
                             const float *col = sc + SC_COL + 8 * own * (own - 1) + cb * 16;
                             const f2 F = pair(fr, fr);
@@ -672,7 +677,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         }
                         __syncwarp();
                     }
-                  }
                 }
                 tc_fence_before();
                 if (is_y) fence_proxy_async_smem();
@@ -729,8 +733,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t id_w = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
         const uint32_t lane_at = blk((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
         int cc = 0, kq = 0;
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const Item x = item_of(p, idx);
+        for (; at.idx < p.items; at.next(p)) {
+            const Item x = at.item(p);
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
@@ -741,68 +745,41 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 wwait(&bar[B_BLK + (cc & 1)], (cc / 2) & 1, ok);
                 wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
                 float t0[2][4] = {}, t1[2][4] = {};
-                if (quad == 0) {
-                    float a[2][4] = {};
-                    Frag f, n;
-                    load_left(base + 7 * 1024, f);
-                    mul_block(a, f.hi, f.lo, base);
-                    to_left_neg(a, n);
-                    mul_block(t0, n.hi, n.lo, base + 6 * 1024);  // T10 = -T11 A10 T00
-                    put_plain(blocks, t0, lane);
-                    named_sync(2, 128);
-                    float b[2][4] = {};
-                    load_left(base + 8 * 1024, f);
-                    mul_block(b, f.hi, f.lo, base + 2 * 1024);
-                    to_left_neg(b, n);
-                    mul_block(t1, n.hi, n.lo, base + 7 * 1024);  // T21 = -T22 A21 T11
-                } else if (quad == 1) {
+                {
                     float a[2][4] = {}, b[2][4] = {};
                     Frag f, n;
-                    load_left(base + 9 * 1024, f);
-                    mul_block(a, f.hi, f.lo, base + 5 * 1024);
-                    to_left_neg(a, n);
-                    mul_block(t0, n.hi, n.lo, base + 8 * 1024);  // T32 = -T33 A32 T22
-                    __syncwarp();
-                    put_plain(blocks + 5 * 1024, t0, lane);
-                    named_sync(2, 128);
-                    mul_block(b, f.hi, f.lo, base + 4 * 1024);
-                    load_left(base + 5 * 1024, f);
-                    mul_block(b, f.hi, f.lo, base + 2 * 1024);
-                    to_left_neg(b, n);
-                    mul_block(t1, n.hi, n.lo, base + 7 * 1024);  // T31 = -(T32 A21 + T33 A31) T11
-                } else {
-                    // quad 2: row 2, quad 3: row 3 of T21's left half, -(P0 T00 + P1 T10)
-                    float a[2][4] = {}, b[2][4] = {};
-                    Frag f;
-                    load_left(base + (quad == 2 ? 8 : 9) * 1024, f);
-                    mul_block(a, f.hi, f.lo, base + (quad == 2 ? 1 : 3) * 1024);
-                    mul_block(b, f.hi, f.lo, base + (quad == 2 ? 2 : 4) * 1024);
-                    named_sync(2, 128);
-                    if (quad == 3) {
-                        load_left(base + 5 * 1024, f);
-                        mul_block(a, f.hi, f.lo, base + 1 * 1024);
-                        mul_block(b, f.hi, f.lo, base + 2 * 1024);
+                    load_left(base + (quad == 0 ? 7 : quad == 2 ? 8 : 9) * 1024, f);
+                    mul_block(a, f.hi, f.lo, base + (quad == 0 ? 0 : quad == 1 ? 5 : quad == 2 ? 1 : 3) * 1024);
+                    if (quad < 2) {
+                        to_left_neg(a, n);
+                        mul_block(t0, n.hi, n.lo, base + (quad == 0 ? 6 : 8) * 1024);  // T10 = -T11 A10 T00, T32 = -T33 A32 T22
+                        put_plain(blocks + (quad == 0 ? 0 : 5) * 1024, t0, lane);
+                        if (quad == 0) load_left(base + 8 * 1024, f);
+                        mul_block(b, f.hi, f.lo, base + (quad == 0 ? 2 : 4) * 1024);   // T22 A21; T33 A31 of T32 A21 + T33 A31
+                    } else {
+                        mul_block(b, f.hi, f.lo, base + (quad == 2 ? 2 : 4) * 1024);
                     }
-                    to_left_neg(a, f);
-                    mul_block(t0, f.hi, f.lo, base + 6 * 1024);
-                    to_left_neg(b, f);
-                    mul_block(t0, f.hi, f.lo, base);
+                    named_sync(2, 128);
+                    if (quad & 1) {
+                        load_left(base + 5 * 1024, f);
+                        mul_block(b, f.hi, f.lo, base + 2 * 1024);
+                        if (quad == 3) mul_block(a, f.hi, f.lo, base + 1 * 1024);
+                    }
+                    to_left_neg(b, n);
+                    mul_block(t1, n.hi, n.lo, base + (quad < 2 ? 7 : 0) * 1024);  // T21, T31: times T11; the left half's: T10
+                    if (quad >= 2) {
+                        to_left_neg(a, n);
+                        mul_block(t1, n.hi, n.lo, base + 6 * 1024);
+                        diag_block(base + (quad == 2 ? 8 : 9) * 1024, t0);
+                    }
                 }
                 if (cc > 0) wwait(&bar[B_TFREE], (cc - 1) & 1, ok);
-                if (quad == 0) {
-                    put_block(tt, sc, 1, 0, lane, t0);
-                    put_block(tt, sc, 2, 1, lane, t1);
-                    put_diag(tt, sc, 0, lane, base + 6 * 1024);
-                } else if (quad == 1) {
-                    put_block(tt, sc, 3, 2, lane, t0);
-                    put_block(tt, sc, 3, 1, lane, t1);
-                } else if (quad == 2) {
-                    put_block(tt, sc, 2, 0, lane, t0);
-                    put_diag(tt, sc, 1, lane, base + 7 * 1024);
-                    put_diag(tt, sc, 2, lane, base + 8 * 1024);
-                } else {
-                    put_block(tt, sc, 3, 0, lane, t0);
-                    put_diag(tt, sc, 3, lane, base + 9 * 1024);
+                // quad 0: T10, T21, T00; 1: T32, T31, T11; 2: T22, T20; 3: T33, T30
+                put_block(tt, sc, quad == 0 ? 1 : quad == 1 ? 3 : quad, quad == 0 ? 0 : quad == 1 ? 2 : quad, lane, t0);
+                put_block(tt, sc, quad == 0 || quad == 2 ? 2 : 3, quad < 2 ? 1 : 0, lane, t1);
+                if (quad < 2) {
+                    diag_block(base + (6 + quad) * 1024, t0);
+                    put_block(tt, sc, quad, quad, lane, t0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -849,25 +826,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             if (lane == 0) mbar_arrive(&bar[B_OFREE]);
             uint16_t *dst = reinterpret_cast<uint16_t *>(p.o) + ((int64_t)tok * p.hv_n + h) * kD + row;
             const int64_t step = (int64_t)p.hv_n * kD;
-            if (nv >= kC) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    dst[(2 * j) * step] = (uint16_t)w[j];
-                    dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    if (2 * j < nv) dst[(2 * j) * step] = (uint16_t)w[j];
-                    if (2 * j + 1 < nv) dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
-                }
+            for (int j = 0; j < 32; ++j) {
+                if (2 * j < nv) dst[(2 * j) * step] = (uint16_t)w[j];
+                if (2 * j + 1 < nv) dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
             }
         };
-        int cc = 0, kq = 0;
-        int p_tok = 0, p_nv = 0, p_h = 0;  // the chunk whose outputs are still to come
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const Item x = item_of(p, idx);
-            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+        int cc = 0;
+        // the chunk in work (x, c), and the one before it, whose outputs are still to come
+        Item x = {};
+        int c = 0, p_tok = 0, p_nv = 0, p_h = 0;
+        while (true) {
+            while (c == x.chunks && at.idx < p.items) {
+                x = at.item(p);
+                c = 0;
+                at.next(p);
+            }
+            const bool more = c < x.chunks;
+            if (more) {
                 wwait(&bar[B_W], cc & 1, ok);
                 if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // S W^T of the chunk before has read W
                 tc_fence_after();
@@ -891,13 +867,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_WRDY]);
-                if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
-                p_tok = x.lo + c * kC;
-                p_nv = x.n - c * kC;
-                p_h = x.h;
             }
+            if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
+            if (!more) break;
+            p_tok = x.lo + c * kC;
+            p_nv = x.n - c * kC;
+            p_h = x.h;
+            ++c;
+            ++cc;
         }
-        if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
     } else {
         // -------------------------------------------------------------------- the state
         reg_alloc<120>();
@@ -905,16 +883,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const float *el = reinterpret_cast<const float *>(sm + OFF_EL);
         int cc = 0, kq = 0;
-        for (int idx = blockIdx.x; idx < p.items; idx += gridDim.x) {
-            const Item x = item_of(p, idx);
+        for (; at.idx < p.items; at.next(p)) {
+            const Item x = at.item(p);
             if (x.err) continue;
             const int64_t mine = x.state + row * kD + half * 64;
             f2 s[32];
 #pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-                const ulonglong2 v = x.zero ? make_ulonglong2(0, 0) : *reinterpret_cast<const ulonglong2 *>(p.S0 + mine + 2 * j);
-                s[j] = v.x;
-                s[j + 1] = v.y;
+            for (int j = 0; j < 32; j += 4) {
+                s[j] = s[j + 1] = s[j + 2] = s[j + 3] = 0;
+                if (!x.zero)
+                    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                                 : "=l"(s[j]), "=l"(s[j + 1]), "=l"(s[j + 2]), "=l"(s[j + 3]) : "l"(p.S0 + mine + 2 * j));
             }
             // s = e^gamma_63 s + dS of chunk number n
             auto advance = [&](int n) {
@@ -930,8 +909,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int j = 0; j < 16; j += 2) s[(j0 + j) / 2] = fma2(a, s[(j0 + j) / 2], pair(r[j], r[j + 1]));
                 }
             };
-            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+            for (int c = 0;; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 if (c > 0) advance(cc - 1);
+                if (c == x.chunks) break;
                 if (cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);  // U of the chunk before lies over S hi
                 tc_fence_after();
 #pragma unroll
@@ -999,10 +979,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_UBF]);
             }
-            if (x.chunks > 0) advance(cc - 1);
 #pragma unroll
-            for (int j = 0; j < 32; j += 2)
-                *reinterpret_cast<ulonglong2 *>(p.S_new + mine + 2 * j) = make_ulonglong2(s[j], s[j + 1]);
+            for (int j = 0; j < 32; j += 4)
+                asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};"
+                             ::"l"(p.S_new + mine + 2 * j), "l"(s[j]), "l"(s[j + 1]), "l"(s[j + 2]), "l"(s[j + 3]) : "memory");
         }
     }
     if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
@@ -1025,6 +1005,8 @@ bool encode(CUtensorMap *map, const void *base, int heads, int total, int64_t st
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 int64_t token_stride(int64_t given, int heads) { return given ? given : (int64_t)heads * kD; }
 
 }  // namespace
@@ -1033,9 +1015,9 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
     const int64_t qs = token_stride(a.q_stride, a.n_k_heads), ks = token_stride(a.k_stride, a.n_k_heads),
                   vs = token_stride(a.v_stride, a.n_v_heads);
     return a.qkv_dtype == GDN_BF16 && a.out_dtype == GDN_BF16 && a.d_k == kD && a.d_v == kD && a.total_tokens > 0 &&
-           tiles::aligned16(a.q) && tiles::aligned16(a.k) && tiles::aligned16(a.v) && tiles::aligned16(a.S0) &&
-           tiles::aligned16(a.S_new) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0 && std::max(qs, std::max(ks, vs)) < (1ll << 38) &&
-           (int64_t)a.batch * a.n_v_heads <= 0x7fffffff && tensor_map_encoder() != nullptr;
+           tiles::aligned16(a.q) && tiles::aligned16(a.k) && tiles::aligned16(a.v) && aligned32(a.S0) &&
+           aligned32(a.S_new) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0 && std::max(qs, std::max(ks, vs)) < (1ll << 38) &&
+           (int64_t)a.batch * a.n_v_heads <= 0x7fffffff - 65536 && a.n_v_heads <= 65535 && tensor_map_encoder() != nullptr;
 }
 
 cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
@@ -1047,6 +1029,9 @@ cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     Params p = {};
     p.hk_n = a.n_k_heads; p.hv_n = a.n_v_heads; p.total = a.total_tokens; p.max_tokens = a.max_tokens;
     p.n_states = a.n_states; p.items = a.batch * a.n_v_heads; p.probe = wait_probe_polls();
+    const int grid = std::min(p.items, sm_count()), group = a.n_v_heads / a.n_k_heads;
+    p.step_b = grid / p.hv_n; p.step_h = grid % p.hv_n;
+    p.group_inv = group == 1 ? 0u : (uint32_t)(((1ull << 32) + group - 1) / group);
     p.scale = a.scale;
     p.offsets = a.token_offsets; p.slots = a.slots; p.fresh = a.fresh;
     p.g = a.g; p.beta = a.beta; p.S0 = a.S0;
@@ -1054,7 +1039,7 @@ cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     static int have[16];
     cudaError_t e = ensure_smem(prefill_tc_kernel, kSmem, have);
     if (e != cudaSuccess) return e;
-    prefill_tc_kernel<<<(unsigned)std::min(p.items, sm_count()), kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
+    prefill_tc_kernel<<<(unsigned)grid, kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
     return cudaGetLastError();
 }
 
