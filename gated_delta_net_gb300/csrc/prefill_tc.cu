@@ -20,11 +20,11 @@
 // One block an SM (all 512 tensor-memory columns), 24 warps:
 //     warp 0        loads K and Q of three chunks by TMA
 //     warp 1        issues [K;Q] K^T
-//     warp 2        issues U, O and dS: the chain; loads V
+//     warp 2        issues U, O and dS: the chain
 //     warp 3        the chunk's gates: gamma by a scan, and its exponentials
 //     warps 4-7     A and Y; T = (I + A)^-1 in blocks of 16, the diagonal ones
 //     warps 8-11    T's other blocks, T', T'', issue W
-//     warps 12-15   W to shared memory, the outputs to global memory
+//     warps 12-15   load V, W to shared memory, the outputs to global memory
 //     warps 16-23   the state in registers (a row of 64 entries each), its hi + lo operand in
 //                   tensor memory, and U's
 // The chain for a chunk is: S split -> S W^T -> U split -> dS -> S.
@@ -405,7 +405,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     const int nv = x.n - c * kC;
                     if (nv < kC) {  // keys past the prompt's end: zero, whatever the next prompt holds
                         for (int half = 0; half < 2; ++half)
-                            for (int i = nv * 8 + lane; i < kC * 8; i += 32)
+                            _Pragma("unroll 1") for (int i = nv * 8 + lane; i < kC * 8; i += 32)
                                 *reinterpret_cast<uint4 *>(kt + half * 2 * kTile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -429,29 +429,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             uint8_t *vt = sm + OFF_V;
             const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
             int cc = 0, kq = 0;
-            Item x = {}, nx = {};
-            auto seek = [&]() {  // nx: the next item that has chunks
-                for (nx.chunks = 0; at.idx < p.items && nx.chunks == 0; at.next(p)) nx = at.item(p);
-            };
-            int loads = 0;
-            auto load_v = [&](const Item &x, int c) {
-                ++loads;
-                mbar_arrive_expect_tx(&bar[B_VFULL], 2 * kTile);
-                for (int half = 0; half < 2; ++half)
-                    tma_load_3d(vt + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
-            };
-            seek();
-            if (lead && nx.chunks > 0) load_v(nx, 0);
-            while (nx.chunks > 0) {
-                x = nx;
-                seek();
+            for (; at.idx < p.items; at.next(p)) {
+                const Item x = at.item(p);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
                     const int nv = x.n - c * kC;
                     if (nv < kC) {
                         for (int half = 0; half < 2; ++half)
-                            for (int i = nv * 8 + lane; i < kC * 8; i += 32)
+                            _Pragma("unroll 1") for (int i = nv * 8 + lane; i < kC * 8; i += 32)
                                 *reinterpret_cast<uint4 *>(vt + half * kTile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                         fence_proxy_async_smem();
                     }
@@ -459,22 +445,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     // U^T = V^T T'^T
                     wwait(&bar[B_T], cc & 1, ok);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + ((part * kTile + ks * 32) >> 4), id_u, part > 0 || ks > 0);
+                            mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + part * (kTile >> 4) + ks * 2, id_u, part + ks > 0);
                     commit(lead, &bar[B_TFREE]);
                     // U^T += S (-W)^T: hi hi, lo hi, hi lo
                     wwait(&bar[B_WRDY], cc & 1, ok);
                     wwait(&bar[B_S], cc & 1, ok);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 3; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(lead, tm + TM_U, tm + (part == 1 ? TM_SLO : TM_SHI) + ks * 8,
-                                   d_w + (((part == 2 ? 2 * kTile : 0) + ks * 2048) >> 4), id_sw, true);
+                            mma_ts(lead, tm + TM_U, tm + TM_SHI + (part & 1) * (TM_SLO - TM_SHI) + ks * 8,
+                                   d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, true);
                     commit(lead, &bar[B_U]);
                     // O^T = S Q^T
                     if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
@@ -484,20 +470,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int ks = 0; ks < 8; ++ks)
                         mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
                     commit(lead, &bar[B_SQ]);
-                    // dS = U'^T K; U' is made of U^T's sum, so V has been read: the next chunk's may come
+                    // dS = U'^T K
                     wwait(&bar[B_UST], cc & 1, ok);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(lead, tm + TM_DS, tm + (part ? TM_ULO : TM_UHI) + ks * 8, d_k + ks * 128, id_ds, part > 0 || ks > 0);
+                            mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, part + ks > 0);
                     commit(lead, &bar[B_UPD]);
-                    if (lead && ok) {
-                        if (c + 1 < x.chunks) load_v(x, c + 1);
-                        else if (nx.chunks > 0) load_v(nx, 0);
-                    }
-                    __syncwarp();
                     // O^T += U^T Y^T, once S Q^T has its factors
                     wwait(&bar[B_UBF], cc & 1, ok);
                     tc_fence_after();
@@ -509,7 +490,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     commit(lead, &bar[B_EMPTY + kq]);
                 }
             }
-            if (lead && loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
         } else if (warp == 3) {
             // ---------------------------------------------------------------- gates, ahead of everything
             float *el = reinterpret_cast<float *>(sm + OFF_EL);
@@ -537,7 +517,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (c + 1 < x.chunks) fetch(c + 1);
                     float h = g0, l = 0.f;
                     dd_add(h, l, g1, 0.f);
-#pragma unroll
+#pragma unroll 1
                     for (int o = 1; o < 32; o <<= 1) {
                         float h2 = __shfl_up_sync(0xffffffffu, h, o), l2 = __shfl_up_sync(0xffffffffu, l, o);
                         if (lane >= o) {
@@ -775,11 +755,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
                 if (cc > 0) wwait(&bar[B_TFREE], (cc - 1) & 1, ok);
                 // quad 0: T10, T21, T00; 1: T32, T31, T11; 2: T22, T20; 3: T33, T30
-                put_block(tt, sc, quad == 0 ? 1 : quad == 1 ? 3 : quad, quad == 0 ? 0 : quad == 1 ? 2 : quad, lane, t0);
-                put_block(tt, sc, quad == 0 || quad == 2 ? 2 : 3, quad < 2 ? 1 : 0, lane, t1);
-                if (quad < 2) {
-                    diag_block(base + (6 + quad) * 1024, t0);
-                    put_block(tt, sc, quad, quad, lane, t0);
+#pragma unroll 1
+                for (int w = 0; w < (quad < 2 ? 3 : 2); ++w) {
+                    const int bi = w == 0 ? (quad == 0 ? 1 : quad == 1 ? 3 : quad) : w == 1 ? 2 + (quad & 1) : quad;
+                    const int bj = w == 0 ? (quad == 0 ? 0 : quad == 1 ? 2 : quad) : w == 1 ? (quad < 2 ? 1 : 0) : quad;
+                    put_block(tt, sc, bi, bj, lane, t0);
+                    if (w == 0) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) t0[e >> 2][e & 3] = t1[e >> 2][e & 3];
+                    } else {
+                        diag_block(base + (6 + quad) * 1024, t0);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -812,26 +798,28 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         auto outputs = [&](int cc, int tok, int nv, int h) {
             wwait(&bar[B_O], cc & 1, ok);
             tc_fence_after();
-            uint32_t w[32];
-#pragma unroll
+            uint16_t *dst = reinterpret_cast<uint16_t *>(p.o) + ((int64_t)tok * p.hv_n + h) * kD + row;
+            const int64_t step = (int64_t)p.hv_n * kD;
+#pragma unroll 1
             for (int j0 = 0; j0 < 64; j0 += 16) {
                 uint32_t r[16];
                 tmem_ld16_nowait(tmem + lanes + TM_O + j0, r);
                 tmem_wait_ld_into(r);
+                if (j0 == 48) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[B_OFREE]);
+                }
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) w[(j0 + j) / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar[B_OFREE]);
-            uint16_t *dst = reinterpret_cast<uint16_t *>(p.o) + ((int64_t)tok * p.hv_n + h) * kD + row;
-            const int64_t step = (int64_t)p.hv_n * kD;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (2 * j < nv) dst[(2 * j) * step] = (uint16_t)w[j];
-                if (2 * j + 1 < nv) dst[(2 * j + 1) * step] = (uint16_t)(w[j] >> 16);
+                for (int j = 0; j < 16; j += 2) {
+                    const uint32_t w = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                    if (j0 + j < nv) dst[0] = (uint16_t)w;
+                    if (j0 + j + 1 < nv) dst[step] = (uint16_t)(w >> 16);
+                    dst += 2 * step;
+                }
             }
         };
+        int loads = 0;
         int cc = 0;
         // the chunk in work (x, c), and the one before it, whose outputs are still to come
         Item x = {};
@@ -844,11 +832,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             const bool more = c < x.chunks;
             if (more) {
+                if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // the chunk before has its U: V and W have been read
+                if (warp == 12 && lane == 0 && ok) {
+                    ++loads;
+                    mbar_arrive_expect_tx(&bar[B_VFULL], 2 * kTile);
+                    for (int half = 0; half < 2; ++half)
+                        tma_load_3d(sm + OFF_V + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
+                }
+                __syncwarp();
                 wwait(&bar[B_W], cc & 1, ok);
-                if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // S W^T of the chunk before has read W
                 tc_fence_after();
                 uint8_t *wt = sm + OFF_W;
-#pragma unroll
+#pragma unroll 1
                 for (int j0 = 0; j0 < 64; j0 += 16) {
                     uint32_t r[16];
                     tmem_ld16_nowait(tmem + lanes + TM_W + j0, r);
@@ -876,6 +871,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             ++c;
             ++cc;
         }
+        if (loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
     } else {
         // -------------------------------------------------------------------- the state
         reg_alloc<120>();
