@@ -25,9 +25,12 @@
 //     warps 4-7     A and Y; T = (I + A)^-1 in blocks of 16, the diagonal ones
 //     warps 8-11    T's other blocks, T', T'', issue W
 //     warps 12-15   load V, W to shared memory, the outputs to global memory
-//     warps 16-23   the state in registers (a row of 64 entries each), its hi + lo operand in
-//                   tensor memory, and U's
-// The chain for a chunk is: S split -> S W^T -> U split -> dS -> S.
+//     warps 16-23   the state's hi + lo operand and its decay, U's operands, S Q^T's factors
+// The state stays in tensor memory as the sum that dS is added to.  The chain for a chunk is
+// S split -> S W^T -> U split -> dS.
+//
+// The roles run different code at the same time, and what it costs to fetch bounds them as much as
+// what they compute: loops stay rolled where their steps are alike.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -47,7 +50,7 @@ using tiles::pack_bf16;
 constexpr int kC = 64;         // tokens a chunk
 constexpr int kThreads = 768;  // 24 warps
 constexpr int kKQ = 3;         // chunks of K and Q, of Y and of gates held at a time
-constexpr int kDecays = 8;
+constexpr int kDecays = 4;
 
 // shared memory (bytes from a 1024-aligned base)
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: half of a token tile
@@ -60,12 +63,13 @@ constexpr int OFF_A = OFF_Y + kKQ * kTile;   // [2] ten 16 x 16 blocks, bf16 hi 
                                              // it (4; before T is known, A's diagonal blocks in fp32)
 constexpr int kBlocks = 10 * 1024;
 constexpr int OFF_SC = OFF_A + 2 * kBlocks;  // [kKQ] gates of a chunk, floats:
-constexpr int SC_HI = 0, SC_LO = 64, SC_BETA = 128, SC_BG = 192;  // -gamma log2 e hi, lo; beta; beta e^gamma
-constexpr int SC_ROW = 256, SC_COL = 320;    // e^(gamma_i - gamma_r), r the first token of i's block of 16; e^(gamma_r - gamma_j)
-                                             // for the blocks' r = 16, 32, 48 and j < r
-constexpr int SC_EG = 416, SC_FD = 480;      // scale e^gamma, e^(gamma_63 - gamma)
-constexpr int kGates = 544 * 4;
-constexpr int OFF_EL = OFF_SC + kKQ * kGates;  // [kDecays] e^gamma_63
+constexpr int SC_REL = 0, SC_BETA = 64, SC_BG = 128;  // (gamma_r - gamma_j) log2 e, r the first token of j's block of 16; beta;
+                                             // -beta e^gamma
+constexpr int SC_COL = 192;                  // e^(gamma_r - gamma_j) for r = 16, 32, 48 and j < r
+constexpr int SC_EG = 288, SC_FD = 352;      // scale e^gamma, e^(gamma_63 - gamma)
+constexpr int kGates = 416 * 4;
+constexpr int OFF_MASK = OFF_SC + kKQ * kGates;  // fp32 [17][16]: row n is 0 in its first n columns, -10^30 after them
+constexpr int OFF_EL = OFF_MASK + 17 * 64;      // [kDecays] e^gamma_63
 constexpr int OFF_SLOT = OFF_EL + kDecays * 4;
 constexpr int OFF_BAR = OFF_SLOT + 16;
 enum Bar {
@@ -202,6 +206,15 @@ __device__ __forceinline__ float2 parts(f2 x) {
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
     return r;
 }
+__device__ __forceinline__ void unpair(f2 x, uint32_t &a, uint32_t &b) { asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(x)); }
+// 8 floats from and to global memory, 32-byte aligned (a null source reads as zero)
+__device__ __forceinline__ void load8(const float *p, f2 (&v)[4]) {
+    v[0] = v[1] = v[2] = v[3] = 0;
+    if (p) asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(v[0]), "=l"(v[1]), "=l"(v[2]), "=l"(v[3]) : "l"(p) : "memory");
+}
+__device__ __forceinline__ void store8(float *p, const f2 (&v)[4]) {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]) : "memory");
+}
 __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     f2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -247,6 +260,10 @@ __device__ __forceinline__ void ldm_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+__device__ __forceinline__ void stm(uint32_t addr, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -277,37 +294,28 @@ __device__ __forceinline__ void to_left_neg(const float (&d)[2][4], Frag &f) {
     for (int e = 0; e < 4; ++e) split2(pair(-d[e >> 1][2 * (e & 1)], -d[e >> 1][2 * (e & 1) + 1]), f.hi[e], f.lo[e]);
 }
 
-// accumulators to a block in shared memory
-__device__ __forceinline__ void put_plain(uint8_t *at, const float (&d)[2][4], int lane) {
+// accumulators to a block in shared memory, `addr` this lane's row address
+__device__ __forceinline__ void put_plain(uint32_t addr, const float (&d)[2][4]) {
+    uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t hi, lo;
-        split2(pair(d[e >> 1][2 * (e & 1)], d[e >> 1][2 * (e & 1) + 1]), hi, lo);
-        uint8_t *to = at + blk((lane >> 2) + 8 * (e & 1), e >> 1) + (lane & 3) * 4;
-        *reinterpret_cast<uint32_t *>(to) = hi;
-        *reinterpret_cast<uint32_t *>(to + 512) = lo;
-    }
+    for (int e = 0; e < 4; ++e) split2(pair(d[e >> 1][2 * (e & 1)], d[e >> 1][2 * (e & 1) + 1]), hi[e], lo[e]);
+    stm(addr, hi);
+    stm(addr + 512, lo);
 }
 
 // T's block (bi, bj) as T' and -T'', hi and lo, into the tiles the tensor cores read
-__device__ __forceinline__ void put_block(uint8_t *tt, const float *sc, int bi, int bj, int lane, const float (&v)[2][4]) {
+__device__ __forceinline__ void put_block(uint32_t tt, const float *sc, int bi, int bj, int lane, const float (&v)[2][4]) {
+    const uint32_t addr = tt + sw(16 * bi + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * bj + (lane >> 4));
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-        const int col = 16 * bj + 8 * nt + (lane & 3) * 2;
-        const f2 b = *reinterpret_cast<const f2 *>(sc + SC_BETA + col), bg = *reinterpret_cast<const f2 *>(sc + SC_BG + col);
+    for (int w = 0; w < 2; ++w) {
+        uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            const int row = 16 * bi + (lane >> 2) + 8 * hh;
-            const f2 t = pair(v[nt][2 * hh], v[nt][2 * hh + 1]);
-            uint8_t *at = tt + sw(row, 2 * bj + nt) + (lane & 3) * 4;
-            uint32_t hi, lo;
-            split2(mul2(t, b), hi, lo);
-            *reinterpret_cast<uint32_t *>(at) = hi;
-            *reinterpret_cast<uint32_t *>(at + kTile) = lo;
-            split2(mul2(t, bg), hi, lo);
-            *reinterpret_cast<uint32_t *>(at + 2 * kTile) = hi ^ 0x80008000u;
-            *reinterpret_cast<uint32_t *>(at + 3 * kTile) = lo ^ 0x80008000u;
+        for (int e = 0; e < 4; ++e) {
+            const f2 f = *reinterpret_cast<const f2 *>(sc + (w ? SC_BG : SC_BETA) + 16 * bj + 8 * (e >> 1) + (lane & 3) * 2);
+            split2(mul2(pair(v[e >> 1][2 * (e & 1)], v[e >> 1][2 * (e & 1) + 1]), f), hi[e], lo[e]);
         }
+        stm(addr + 2 * w * kTile, hi);
+        stm(addr + (2 * w + 1) * kTile, lo);
     }
 }
 __device__ __forceinline__ void diag_block(uint32_t addr, float (&v)[2][4]) {
@@ -352,6 +360,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     // T's and Y's tiles stay zero above the blocks that are written
     for (int i = tid; i < (4 + kKQ) * kTile / 16; i += kThreads)
         *reinterpret_cast<uint4 *>(sm + (i < 4 * kTile / 16 ? OFF_T : OFF_Y - 4 * kTile) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < 17 * 16; i += kThreads)
+        reinterpret_cast<float *>(sm + OFF_MASK)[diag_at(i >> 4, (i >> 2) & 3) + (i & 3)] = (i & 15) < (i >> 4) ? 0.f : -1e30f;
     fence_proxy_async_smem();
     if (warp == 2) {
         tmem_alloc(slot, 512);
@@ -362,10 +372,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *slot;
     bool ok = true;
+    float *el = reinterpret_cast<float *>(sm + OFF_EL);
     Walk at = {(int)blockIdx.x, (int)blockIdx.x / p.hv_n, (int)blockIdx.x % p.hv_n};
 
     if (warp < 4) {
-        reg_dealloc<40>();
         const uint32_t lead = elect();
         const uint32_t tm = uniform(tmem);
         if (warp == 0 && lane == 0) {
@@ -477,7 +487,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, part + ks > 0);
+                            mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, true);
                     commit(lead, &bar[B_UPD]);
                     // O^T += U^T Y^T, once S Q^T has its factors
                     wwait(&bar[B_UBF], cc & 1, ok);
@@ -492,7 +502,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
         } else if (warp == 3) {
             // ---------------------------------------------------------------- gates, ahead of everything
-            float *el = reinterpret_cast<float *>(sm + OFF_EL);
             int cc = 0, kq = 0;
             for (; at.idx < p.items; at.next(p)) {
                 const Item x = at.item(p);
@@ -511,7 +520,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 if (x.chunks > 0) fetch(0);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     // gamma: a scan in pairs of floats, so that a decay that forgets everything leaves the
-                    // differences after it exact.  e^-200 is zero, whatever lies below it
+                    // differences between later tokens as they were.  e^-200 is zero, whatever lies below it
                     const float g0 = g[0] < -200.f ? -200.f : g[0], g1 = g[1] < -200.f ? -200.f : g[1];
                     const float b0 = b[0], b1 = b[1];
                     if (c + 1 < x.chunks) fetch(c + 1);
@@ -530,25 +539,22 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     dd_add(h0, l0, -g1, 0.f);
                     const float hl = __shfl_sync(0xffffffffu, h, 31), ll = __shfl_sync(0xffffffffu, l, 31);
                     const float hh[2] = {h0, h}, lw[2] = {l0, l}, bb[2] = {b0, b1};
-                    float nh[2], nl[2], bg[2], eg[2], fd[2], rc[2][4];
+                    float rel[2], bg[2], eg[2], fd[2], rc[2][4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float kLog2e = 1.4426950408889634f, kLog2eLo = 1.4426950408889634 - (double)1.4426950408889634f;
-                        nh[e] = -hh[e] * kLog2e;
-                        nl[e] = -(fmaf(hh[e], kLog2e, nh[e]) + fmaf(lw[e], kLog2e, hh[e] * kLog2eLo));
                         const float x0 = __expf(hh[e] + lw[e]);
-                        bg[e] = bb[e] * x0;
+                        bg[e] = -bb[e] * x0;
                         eg[e] = p.scale * x0;
                         fd[e] = __expf((hl - hh[e]) + (ll - lw[e]));
                     }
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {  // from the blocks' first tokens r = 16 q, held by lane 8 q
                         const float rh = __shfl_sync(0xffffffffu, h0, 8 * q), rl = __shfl_sync(0xffffffffu, l0, 8 * q);
-                        const bool own = (lane >> 3) == q;
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float d = (hh[e] - rh) + (lw[e] - rl);
-                            rc[e][q] = __expf(own ? d : -d);
+                            rc[e][q] = __expf(-d);
+                            if ((lane >> 3) == q) rel[e] = -1.4426950408889634f * d;
                         }
                     }
                     const float last = __expf(hl + ll);
@@ -559,16 +565,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                     float *sc = reinterpret_cast<float *>(sm + OFF_SC + kq * kGates);
                     auto put = [&](int at, float v0, float v1) { *reinterpret_cast<float2 *>(sc + at + 2 * lane) = make_float2(v0, v1); };
-                    put(SC_HI, nh[0], nh[1]);
-                    put(SC_LO, nl[0], nl[1]);
+                    put(SC_REL, rel[0], rel[1]);
                     put(SC_BETA, b0, b1);
                     put(SC_BG, bg[0], bg[1]);
                     put(SC_EG, eg[0], eg[1]);
                     put(SC_FD, fd[0], fd[1]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if ((lane >> 3) == q) put(SC_ROW, rc[0][q], rc[1][q]);
-                        else if (lane < 8 * q) put(SC_COL + 8 * q * (q - 1), rc[0][q], rc[1][q]);
+                    for (int q = 1; q < 4; ++q) {
+                        if (lane < 8 * q) put(SC_COL + 8 * q * (q - 1), rc[0][q], rc[1][q]);
                     }
                     if (lane == 0) el[cc & (kDecays - 1)] = last;
                     __syncwarp();
@@ -578,11 +582,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
     } else if (warp < 8) {
         // -------------------------------------------------------------------- A, Y, T's diagonal blocks
-        reg_dealloc<72>();
         const int row = quad * 32 + lane, i = row & 63, own = i >> 4;  // own: the row's block of 16
         const bool is_y = row >= 64;
         const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        const float *mask = reinterpret_cast<const float *>(sm + OFF_MASK);
         int cc = 0, kq = 0;
         for (; at.idx < p.items; at.next(p)) {
             const Item x = at.item(p);
@@ -591,19 +595,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
                 float *diag = reinterpret_cast<float *>(blocks + 6 * 1024);
                 wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
-                const f2 gh = pair(-sc[SC_HI + i], -sc[SC_HI + i]), gl = pair(-sc[SC_LO + i], -sc[SC_LO + i]);
-                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * sc[SC_ROW + i];
+                const f2 rel = pair(-sc[SC_REL + i], -sc[SC_REL + i]);
+                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * exp2_approx(-sc[SC_REL + i]);
                 if (cc >= 2) wwait(&bar[B_BLKFREE + (cc & 1)], (cc / 2 - 1) & 1, ok);
                 if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], (cc / kKQ - 1) & 1, ok);
                 wwait(&bar[B_G], cc & 1, ok);
                 tc_fence_after();
+                uint32_t nr[16];  // the next 16 columns
+                tmem_ld16_nowait(tmem + lanes + TM_G, nr);
+                const int cbs = (quad & 1) ? 4 : 2;  // rows 0..31 have nothing right of column 31
 #pragma unroll 1
-                for (int cb = 0; cb < ((quad & 1) ? 4 : 2); ++cb) {  // rows 0..31 have nothing right of column 31
+                for (int cb = 0; cb < cbs; ++cb) {
                     {
                         uint32_t r[16];
                         f2 m[8];
-                        tmem_ld16_nowait(tmem + lanes + TM_G + cb * 16, r);
-                        tmem_wait_ld_into(r);
+                        tmem_wait_ld_into(nr);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) r[j] = nr[j];
+                        if (cb + 1 < cbs) tmem_ld16_nowait(tmem + lanes + TM_G + (cb + 1) * 16, nr);
                         if (cb < own) {  // left of the own block: e^(gamma_i - gamma_r) e^(gamma_r - gamma_j)
                             const float *col = sc + SC_COL + 8 * own * (own - 1) + cb * 16;
                             const f2 F = pair(fr, fr);
@@ -617,14 +626,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                             const f2 F = pair(f, f);
 #pragma unroll
                             for (int j = 0; j < 16; j += 4) {
-                                const ulonglong2 h4 = *reinterpret_cast<const ulonglong2 *>(sc + SC_HI + cb * 16 + j);
-                                const ulonglong2 l4 = *reinterpret_cast<const ulonglong2 *>(sc + SC_LO + cb * 16 + j);
-                                const float2 d0 = parts(add2(add2(gh, h4.x), add2(gl, l4.x)));
-                                const float2 d1 = parts(add2(add2(gh, h4.y), add2(gl, l4.y)));
-                                const float2 m0 = parts(mul2(pair(exp2_approx(d0.x), exp2_approx(d0.y)), mul2(F, pair(r[j], r[j + 1]))));
-                                const float2 m1 = parts(mul2(pair(exp2_approx(d1.x), exp2_approx(d1.y)), mul2(F, pair(r[j + 2], r[j + 3]))));
-                                m[j / 2] = pair(j < last ? m0.x : 0.f, j + 1 < last ? m0.y : 0.f);
-                                m[j / 2 + 1] = pair(j + 2 < last ? m1.x : 0.f, j + 3 < last ? m1.y : 0.f);
+                                const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(sc + SC_REL + cb * 16 + j);
+                                const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(mask + diag_at(last, j >> 2));
+                                const float2 d0 = parts(add2(add2(rel, x.x), k.x)), d1 = parts(add2(add2(rel, x.y), k.y));
+                                m[j / 2] = mul2(pair(exp2_approx(d0.x), exp2_approx(d0.y)), mul2(F, pair(r[j], r[j + 1])));
+                                m[j / 2 + 1] = mul2(pair(exp2_approx(d1.x), exp2_approx(d1.y)), mul2(F, pair(r[j + 2], r[j + 3])));
                             }
                         }
                         if (cb <= own) {
@@ -708,8 +714,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         }
     } else if (warp < 12) {
         // -------------------------------------------------------------------- the rest of T, T', T''
-        reg_dealloc<72>();
-        uint8_t *tt = sm + OFF_T;
+        const uint32_t tt = smem_u32(sm + OFF_T);
         const uint32_t id_w = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
         const uint32_t lane_at = blk((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
         int cc = 0, kq = 0;
@@ -733,7 +738,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (quad < 2) {
                         to_left_neg(a, n);
                         mul_block(t0, n.hi, n.lo, base + (quad == 0 ? 6 : 8) * 1024);  // T10 = -T11 A10 T00, T32 = -T33 A32 T22
-                        put_plain(blocks + (quad == 0 ? 0 : 5) * 1024, t0, lane);
+                        put_plain(base + (quad == 0 ? 0 : 5) * 1024, t0);
                         if (quad == 0) load_left(base + 8 * 1024, f);
                         mul_block(b, f.hi, f.lo, base + (quad == 0 ? 2 : 4) * 1024);   // T22 A21; T33 A31 of T32 A21 + T33 A31
                     } else {
@@ -778,7 +783,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     wwait(&bar[B_T], cc & 1, ok);
                     if (cc > 0) wwait(&bar[B_WRDY], (cc - 1) & 1, ok);
                     tc_fence_after();
-                    const uint32_t d_k = uniform(desc_lo(sm + OFF_KQ + kq * 4 * kTile, 2 * kTile)), d_t = uniform(desc_lo(tt, 0));
+                    const uint32_t d_k = uniform(desc_lo(sm + OFF_KQ + kq * 4 * kTile, 2 * kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0));
                     const uint32_t tm = uniform(tmem), lead = elect();
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
@@ -794,7 +799,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // -------------------------------------------------------------------- W to shared memory, outputs
         const int row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        reg_dealloc<56>();
         auto outputs = [&](int cc, int tok, int nv, int h) {
             wwait(&bar[B_O], cc & 1, ok);
             tc_fence_after();
@@ -874,74 +878,76 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
     } else {
         // -------------------------------------------------------------------- the state
-        reg_alloc<120>();
         const int row = quad * 32 + lane, half = (warp - 16) >> 2;
-        const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-        const float *el = reinterpret_cast<const float *>(sm + OFF_EL);
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         int cc = 0, kq = 0;
         for (; at.idx < p.items; at.next(p)) {
             const Item x = at.item(p);
             if (x.err) continue;
-            const int64_t mine = x.state + row * kD + half * 64;
-            f2 s[32];
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-                s[j] = s[j + 1] = s[j + 2] = s[j + 3] = 0;
-                if (!x.zero)
-                    asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
-                                 : "=l"(s[j]), "=l"(s[j + 1]), "=l"(s[j + 2]), "=l"(s[j + 3]) : "l"(p.S0 + mine + 2 * j));
+            const float *from = x.zero ? nullptr : p.S0 + x.state + row * kD + half * 64;
+            float *to = p.S_new + x.state + row * kD + half * 64;
+            if (x.chunks == 0) {
+#pragma unroll 1
+                for (int j = 0; j < 64; j += 8) {
+                    f2 v[4];
+                    load8(from ? from + j : nullptr, v);
+                    store8(to + j, v);
+                }
+                continue;
             }
-            // s = e^gamma_63 s + dS of chunk number n
-            auto advance = [&](int n) {
-                wwait(&bar[B_UPD], n & 1, ok);
-                tc_fence_after();
-                const f2 a = pair(el[n & (kDecays - 1)], el[n & (kDecays - 1)]);
+            // S into tensor memory: its sum's last reader was this thread
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 8) {
+                f2 v[4];
+                load8(from ? from + j : nullptr, v);
+                uint32_t r[8];
 #pragma unroll
+                for (int e = 0; e < 4; ++e) unpair(v[e], r[2 * e], r[2 * e + 1]);
+                tmem_st8(lanes + TM_DS + half * 64 + j, r);
+            }
+            tmem_wait_st();
+            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + half * 32;
+                if (cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);  // dS is in; U of the chunk before lay over S hi
+                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
+                tc_fence_after();
+                // S as hi + lo, and its sum times e^gamma_63, ready for dS
+                const f2 decay = pair(el[cc & (kDecays - 1)], el[cc & (kDecays - 1)]);
+#pragma unroll 1
                 for (int j0 = 0; j0 < 64; j0 += 16) {
-                    uint32_t r[16];
-                    tmem_ld16_nowait(tmem + lanes + TM_DS + half * 64 + j0, r);
+                    uint32_t r[16], hi[8], lw[8];
+                    tmem_ld16_nowait(lanes + TM_DS + half * 64 + j0, r);
                     tmem_wait_ld_into(r);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) s[(j0 + j) / 2] = fma2(a, s[(j0 + j) / 2], pair(r[j], r[j + 1]));
-                }
-            };
-            for (int c = 0;; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
-                if (c > 0) advance(cc - 1);
-                if (c == x.chunks) break;
-                if (cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);  // U of the chunk before lies over S hi
-                tc_fence_after();
-#pragma unroll
-                for (int j0 = 0; j0 < 64; j0 += 16) {
-                    uint32_t hi[8], lw[8];
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) split2(s[(j0 + j) / 2], hi[j / 2], lw[j / 2]);
-                    tmem_st8(tmem + lanes + TM_SHI + half * 32 + j0 / 2, hi);
-                    tmem_st8(tmem + lanes + TM_SLO + half * 32 + j0 / 2, lw);
+                    for (int j = 0; j < 16; j += 2) {
+                        const f2 v = pair(r[j], r[j + 1]);
+                        split2(v, hi[j / 2], lw[j / 2]);
+                        unpair(mul2(v, decay), r[j], r[j + 1]);
+                    }
+                    tmem_st8(lanes + TM_SHI + half * 32 + j0 / 2, hi);
+                    tmem_st8(lanes + TM_SLO + half * 32 + j0 / 2, lw);
+                    tmem_st16(lanes + TM_DS + half * 64 + j0, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_S]);
 
-                const float *fd = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + SC_FD + half * 32;
-                uint32_t ub[2][8];
                 wwait(&bar[B_U], cc & 1, ok);
                 tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
+#pragma unroll 1
+                for (int j0 = 0; j0 < 32; j0 += 16) {
                     uint32_t r[16], hi[8], lw[8];
-                    tmem_ld16_nowait(tmem + lanes + TM_U + half * 32 + q * 16, r);
+                    tmem_ld16_nowait(lanes + TM_U + half * 32 + j0, r);
                     tmem_wait_ld_into(r);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(fd + q * 16 + j);
-                        ub[q][j / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                        ub[q][j / 2 + 1] = pack_bf16(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + SC_FD + j0 + j);
                         split2(mul2(pair(r[j], r[j + 1]), f.x), hi[j / 2], lw[j / 2]);
                         split2(mul2(pair(r[j + 2], r[j + 3]), f.y), hi[j / 2 + 1], lw[j / 2 + 1]);
                     }
-                    tmem_st8(tmem + lanes + TM_UHI + half * 16 + q * 8, hi);
-                    tmem_st8(tmem + lanes + TM_ULO + half * 16 + q * 8, lw);
+                    tmem_st8(lanes + TM_UHI + half * 16 + j0 / 2, hi);
+                    tmem_st8(lanes + TM_ULO + half * 16 + j0 / 2, lw);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -950,35 +956,44 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 wwait(&bar[B_SQ], cc & 1, ok);
                 tc_fence_after();
                 // U over S hi; S Q^T times scale e^gamma, in place, before U^T Y^T is added
-                const float *eg = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + SC_EG + half * 32;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t r[16], a[8], b[8];
-                    tmem_ld16_nowait(tmem + lanes + TM_O + half * 32 + q * 16, r);
-                    tmem_st8(tmem + lanes + TM_UBF + half * 16 + q * 8, ub[q]);
+#pragma unroll 1
+                for (int j0 = 0; j0 < 32; j0 += 16) {
+                    uint32_t u[16], r[16], ub[8];
+                    tmem_ld16_nowait(lanes + TM_U + half * 32 + j0, u);
+                    tmem_ld16_nowait(lanes + TM_O + half * 32 + j0, r);
                     tmem_wait_ld_into(r);
+                    tmem_wait_ld_into(u);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
-                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(eg + q * 16 + j);
-                        const float2 v0 = parts(mul2(e.x, pair(r[j], r[j + 1]))), v1 = parts(mul2(e.y, pair(r[j + 2], r[j + 3])));
-                        uint32_t *to = (j < 8 ? a : b) + (j & 7);
-                        to[0] = __float_as_uint(v0.x);
-                        to[1] = __float_as_uint(v0.y);
-                        to[2] = __float_as_uint(v1.x);
-                        to[3] = __float_as_uint(v1.y);
+                        ub[j / 2] = pack_bf16(__uint_as_float(u[j]), __uint_as_float(u[j + 1]));
+                        ub[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
+                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(sc + SC_EG + j0 + j);
+                        unpair(mul2(e.x, pair(r[j], r[j + 1])), r[j], r[j + 1]);
+                        unpair(mul2(e.y, pair(r[j + 2], r[j + 3])), r[j + 2], r[j + 3]);
                     }
-                    tmem_st8(tmem + lanes + TM_O + half * 32 + q * 16, a);
-                    tmem_st8(tmem + lanes + TM_O + half * 32 + q * 16 + 8, b);
+                    tmem_st8(lanes + TM_UBF + half * 16 + j0 / 2, ub);
+                    tmem_st16(lanes + TM_O + half * 32 + j0, r);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_UBF]);
             }
+            wwait(&bar[B_UPD], (cc - 1) & 1, ok);
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 16) {
+                uint32_t r[16];
+                tmem_ld16_nowait(lanes + TM_DS + half * 64 + j, r);
+                tmem_wait_ld_into(r);
+                f2 v[4];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-                asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};"
-                             ::"l"(p.S_new + mine + 2 * j), "l"(s[j]), "l"(s[j + 1]), "l"(s[j + 2]), "l"(s[j + 3]) : "memory");
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = pair(r[8 * q + 2 * e], r[8 * q + 2 * e + 1]);
+                    store8(to + j + 8 * q, v);
+                }
+            }
         }
     }
     if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
