@@ -17,15 +17,16 @@
 // out (2^-18).  The state comes out about 5e-6 (norm-wise) from exact.  The output's own
 // products take S, U and Y rounded once to bf16, like the output itself.
 //
-// One block an SM (all 512 tensor-memory columns), 24 warps:
+// One block an SM (all 512 tensor-memory columns), 28 warps:
 //     warp 0        loads K and Q of three chunks by TMA
 //     warp 1        issues [K;Q] K^T
 //     warp 2        issues U, O and dS: the chain
 //     warp 3        the chunk's gates: gamma by a scan, and its exponentials
-//     warps 4-7     A and Y; T = (I + A)^-1 in blocks of 16, the diagonal ones
-//     warps 8-11    T's other blocks, T', T'', issue W
-//     warps 12-15   load V, W to shared memory, the outputs to global memory
-//     warps 16-23   the state's hi + lo operand and its decay, U's operands, S Q^T's factors
+//     warps 4-7, 9, 11  A and Y; T = (I + A)^-1 is then found in blocks of 16:
+//     warps 8, 10   T's diagonal blocks
+//     warps 12-15   T's other blocks, T', T'', issue W
+//     warps 16-19   load V, W to shared memory, the outputs to global memory
+//     warps 20-27   the state's hi + lo operand and its decay, U's operands, S Q^T's factors
 // The state stays in tensor memory as the sum that dS is added to.  The chain for a chunk is
 // S split -> S W^T -> U split -> dS.
 //
@@ -48,7 +49,7 @@ using tiles::named_sync;
 using tiles::pack_bf16;
 
 constexpr int kC = 64;         // tokens a chunk
-constexpr int kThreads = 768;  // 24 warps
+constexpr int kThreads = 896;  // 28 warps
 constexpr int kKQ = 3;         // chunks of K and Q, of Y and of gates held at a time
 constexpr int kDecays = 4;
 
@@ -74,7 +75,7 @@ constexpr int OFF_SLOT = OFF_EL + kDecays * 4;
 constexpr int OFF_BAR = OFF_SLOT + 16;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
-    B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_VFULL = B_BLKFREE + 2,
+    B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
     B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_UBF, B_SQ, B_UPD, B_O, B_OFREE, B_PROBE, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
@@ -350,9 +351,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            const bool four = i == B_GFREE || i == B_T || i == B_WRDY || i == B_OFREE ||
-                              (i >= B_SCFREE && i < B_GATES) || (i >= B_BLK && i < B_VFULL);
-            const uint32_t n = four ? 4 : i == B_S || i == B_UST || i == B_UBF ? 8 : i == B_TFREE ? 2 : 1;
+            const bool four = i == B_T || i == B_WRDY || i == B_OFREE || (i >= B_SCFREE && i < B_GATES) ||
+                              (i >= B_BLKFREE && i < B_DIAG);
+            const uint32_t n = four ? 4 : i == B_GFREE ? 6 : i >= B_BLK && i < B_BLKFREE ? 7 : i == B_S || i == B_UST || i == B_UBF ? 8 : i == B_TFREE ? 2 : 1;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -439,8 +440,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             uint8_t *vt = sm + OFF_V;
             const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
             int cc = 0, kq = 0;
-            for (; at.idx < p.items; at.next(p)) {
-                const Item x = at.item(p);
+            Item nx = {};
+            if (at.idx < p.items) nx = at.item(p);
+            while (at.idx < p.items) {
+                const Item x = nx;  // the next one's parameters arrive meanwhile
+                at.next(p);
+                if (at.idx < p.items) nx = at.item(p);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
@@ -580,9 +585,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
             }
         }
-    } else if (warp < 8) {
-        // -------------------------------------------------------------------- A, Y, T's diagonal blocks
+    } else if (warp < 12 && (warp < 8 || (quad & 1))) {
+        // -------------------------------------------------------------------- A, Y: 32 rows, 32 columns a warp
         const int row = quad * 32 + lane, i = row & 63, own = i >> 4;  // own: the row's block of 16
+        const int cb0 = warp < 8 ? 0 : 2;             // its first block of columns; rows 0..31 have two only
         const bool is_y = row >= 64;
         const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -602,17 +608,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 wwait(&bar[B_G], cc & 1, ok);
                 tc_fence_after();
                 uint32_t nr[16];  // the next 16 columns
-                tmem_ld16_nowait(tmem + lanes + TM_G, nr);
-                const int cbs = (quad & 1) ? 4 : 2;  // rows 0..31 have nothing right of column 31
+                tmem_ld16_nowait(tmem + lanes + TM_G + cb0 * 16, nr);
 #pragma unroll 1
-                for (int cb = 0; cb < cbs; ++cb) {
+                for (int cb = cb0; cb < cb0 + 2; ++cb) {
                     {
                         uint32_t r[16];
                         f2 m[8];
                         tmem_wait_ld_into(nr);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) r[j] = nr[j];
-                        if (cb + 1 < cbs) tmem_ld16_nowait(tmem + lanes + TM_G + (cb + 1) * 16, nr);
+                        if (cb == cb0) tmem_ld16_nowait(tmem + lanes + TM_G + (cb + 1) * 16, nr);
                         if (cb < own) {  // left of the own block: e^(gamma_i - gamma_r) e^(gamma_r - gamma_j)
                             const float *col = sc + SC_COL + 8 * own * (own - 1) + cb * 16;
                             const f2 F = pair(fr, fr);
@@ -667,12 +672,26 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_before();
                 if (is_y) fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_GFREE]);
-                named_sync(1, 128);
-                // T, diagonal blocks of 16: warp w block w, lane r row r (the upper half-warp repeats it).  From
-                // T (I + A) = I, t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling k
+                if (lane == 0) {
+                    mbar_arrive(&bar[B_GFREE]);
+                    // rows 0..31 hold the first two diagonal blocks, the right half of rows 32..63 the others
+                    if (!is_y && (quad == 0 || cb0 == 2)) mbar_arrive(&bar[B_DIAG + quad * 2 + (cc & 1)]);
+                    if (quad != 0) mbar_arrive(&bar[B_BLK + (cc & 1)]);
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // -------------------------------------------------------------------- T's diagonal blocks, two a warp
+        // Lane l row l mod 16 of one.  From T (I + A) = I, t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling k
+        int cc = 0;
+        for (; at.idx < p.items; at.next(p)) {
+            const Item x = at.item(p);
+            for (int c = 0; c < x.chunks; ++c, ++cc) {
+                uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
+                const float *diag = reinterpret_cast<const float *>(blocks + 6 * 1024);
+                wwait(&bar[B_DIAG + quad + (cc & 1)], (cc / 2) & 1, ok);
                 {
-                    const int r = lane & 15, b0 = quad * 16;
+                    const int r = lane & 15, b0 = quad * 16 + (lane & 16);
                     f2 t[8];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -699,20 +718,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         split2(pair(2 * j < r ? v.x : 2 * j == r ? 1.f : 0.f, 2 * j + 1 < r ? v.y : 2 * j + 1 == r ? 1.f : 0.f), hi[j], lo[j]);
                     }
                     __syncwarp();  // the block has been read: T's takes its place
-                    uint8_t *at = blocks + (6 + quad) * 1024;
-                    if (lane < 16) {
+                    uint8_t *to = blocks + (6 + (b0 >> 4)) * 1024;
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            *reinterpret_cast<uint4 *>(at + blk(r, q)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                            *reinterpret_cast<uint4 *>(at + 512 + blk(r, q)) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-                        }
+                    for (int q = 0; q < 2; ++q) {
+                        *reinterpret_cast<uint4 *>(to + blk(r, q)) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                        *reinterpret_cast<uint4 *>(to + 512 + blk(r, q)) = make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_BLK + (cc & 1)]);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // -------------------------------------------------------------------- the rest of T, T', T''
         const uint32_t tt = smem_u32(sm + OFF_T);
         const uint32_t id_w = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
@@ -795,7 +812,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // -------------------------------------------------------------------- W to shared memory, outputs
         const int row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
@@ -837,7 +854,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const bool more = c < x.chunks;
             if (more) {
                 if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // the chunk before has its U: V and W have been read
-                if (warp == 12 && lane == 0 && ok) {
+                if (warp == 16 && lane == 0 && ok) {
                     ++loads;
                     mbar_arrive_expect_tx(&bar[B_VFULL], 2 * kTile);
                     for (int half = 0; half < 2; ++half)
@@ -878,33 +895,37 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         if (loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
     } else {
         // -------------------------------------------------------------------- the state
-        const int row = quad * 32 + lane, half = (warp - 16) >> 2;
+        const int row = quad * 32 + lane, half = (warp - 20) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         int cc = 0, kq = 0;
-        for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.item(p);
+        Item nx = {};
+        if (at.idx < p.items) nx = at.item(p);
+        while (at.idx < p.items) {
+            const Item x = nx;  // the next one's parameters arrive meanwhile
+            at.next(p);
+            if (at.idx < p.items) nx = at.item(p);
             if (x.err) continue;
             const float *from = x.zero ? nullptr : p.S0 + x.state + row * kD + half * 64;
             float *to = p.S_new + x.state + row * kD + half * 64;
-            if (x.chunks == 0) {
+            // S into tensor memory, whose last reader was this thread (or, without tokens, straight on)
 #pragma unroll 1
-                for (int j = 0; j < 64; j += 8) {
-                    f2 v[4];
-                    load8(from ? from + j : nullptr, v);
-                    store8(to + j, v);
-                }
-                continue;
-            }
-            // S into tensor memory: its sum's last reader was this thread
-#pragma unroll 1
-            for (int j = 0; j < 64; j += 8) {
-                f2 v[4];
-                load8(from ? from + j : nullptr, v);
-                uint32_t r[8];
+            for (int j = 0; j < 64; j += 32) {
+                f2 v[4][4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) unpair(v[e], r[2 * e], r[2 * e + 1]);
-                tmem_st8(lanes + TM_DS + half * 64 + j, r);
+                for (int q = 0; q < 4; ++q) load8(from ? from + j + 8 * q : nullptr, v[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (x.chunks == 0) {
+                        store8(to + j + 8 * q, v[q]);
+                    } else {
+                        uint32_t r[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) unpair(v[q][e], r[2 * e], r[2 * e + 1]);
+                        tmem_st8(lanes + TM_DS + half * 64 + j + 8 * q, r);
+                    }
+                }
             }
+            if (x.chunks == 0) continue;
             tmem_wait_st();
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + half * 32;
