@@ -418,43 +418,74 @@ def gdn_tree_commit_verify(prev: dict, S0, max_nodes_prev: int, max_path: int,
 # the layer around the tree (gdn_layer.h)
 # ----------------------------------------------------------------------------
 
+# These calls serve single tokens, where the host's time counts: one pass over each tensor's
+# attributes, pointers as plain integers, the current stream's handle without its object.
+
 def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
-    """The distance between the tokens of ``t`` in elements (its other dimensions contiguous),
-    after a check of its type and shape."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.is_contiguous():
-        return 0
-    if not t[0].is_contiguous():
-        raise ValueError(f"{name} must be contiguous inside a token")
-    stride = t.stride(0)
-    if shape[0] > 1 and stride < t[0].numel():
-        raise ValueError(f"the tokens of {name} overlap")
-    return stride if shape[0] > 1 else 0
+    """The distance between the tokens of ``t`` in elements (0: contiguous), after a check of its
+    type and shape; its other dimensions are contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+            if t.is_contiguous():
+                return 0
+            stride, row = t.stride(), 1
+            for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
+                if st != row and n != 1:
+                    raise ValueError(f"{name} must be contiguous inside a token")
+                row *= n
+            if stride[0] < row:
+                raise ValueError(f"the tokens of {name} overlap")
+            return stride[0]
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape)
 
 
-def _flat(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
-    """``t`` after a check of its type and shape; contiguous."""
+def _flat(t: torch.Tensor, name: str, dtype, shape) -> int:
+    """The address of ``t`` after a check of its type and shape; contiguous."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape)
+
+
+def _refuse(t, name: str, dtype, shape):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+
+
+def _handle(stream, t: torch.Tensor) -> int:
+    """The handle of ``stream``, or of the current stream of the device of ``t``."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _keep(t: torch.Tensor, stream) -> None:
     """Tell torch's allocator of a call's own temporary that it is used on ``stream``."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream),
-                                               device=t.device)
+            stream = torch.cuda.ExternalStream(_handle(stream, t), device=t.device)
         t.record_stream(stream)
+
+
+def _status(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else _flat(t, "dev_status", torch.int32, t.shape)
+
+
+_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+
+
+def _dtype_code(dtype) -> int:
+    code = _CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    return code
 
 
 def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots=None, fresh=None,
@@ -465,52 +496,47 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     g, beta [T, Hv]; max_tokens bounds its length.  Its state is row slots[b] (or b) of the pools
     S0 (None: zero; a prompt with fresh[b] != 0 starts from zero too) and S_new (may be S0)."""
     T, Hk, dk = q.shape
-    Hv, dv = v.shape[1:]
+    _, Hv, dv = v.shape
     dt = q.dtype
     od = out_dtype or dt
+    code, out_code = _dtype_code(dt), _dtype_code(od)
     qs, ks, vs = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk)), _rows(v, "v", dt, (T, Hv, dv))
-    _flat(g, "g", torch.float32, (T, Hv))
-    _flat(beta, "beta", torch.float32, (T, Hv))
-    _dev(token_offsets, "token_offsets", torch.int32)
+    gp, bp = _flat(g, "g", torch.float32, (T, Hv)), _flat(beta, "beta", torch.float32, (T, Hv))
     B = token_offsets.numel() - 1
-    for name, t in (("slots", slots), ("fresh", fresh)):
-        if t is not None:
-            _flat(t, name, torch.int32, (B,))
+    op = _flat(token_offsets, "token_offsets", torch.int32, (B + 1,))
+    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,))
+    fp = 0 if fresh is None else _flat(fresh, "fresh", torch.int32, (B,))
     if S_new is None:
         if slots is not None:
             raise ValueError("slots need S_new: the pool that they point into")
         S_new = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device)
     n_states = S_new.shape[0]
-    _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk))
-    if S0 is not None:
-        _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
     if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are prompts")
+    np_ = _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk))
+    s0 = 0 if S0 is None else _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
     if out is None:
         out = torch.empty((T, Hv, dv), dtype=od, device=q.device)
-    _flat(out, "out", od, (T, Hv, dv))
-    a = PrefillArgs(B, Hk, Hv, dk, dv, T, int(max_tokens), n_states, float(scale), _code(dt), _code(od), qs, ks, vs,
-                    _ptr(token_offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(slots),
-                    _ptr(fresh), _ptr(out), _ptr(S_new), None, 0, _ptr(dev_status))
+    a = PrefillArgs(B, Hk, Hv, dk, dv, T, max_tokens, n_states, scale, code, out_code, qs, ks, vs, op, q.data_ptr(),
+                    k.data_ptr(), v.data_ptr(), gp, bp, s0, sp, fp, _flat(out, "out", od, (T, Hv, dv)), np_, 0, 0,
+                    _status(dev_status))
     if workspace is None:
         need = lib().gdn_prefill_workspace(ctypes.byref(a))
-        if need < 0:
-            _check(GDN_ERR_INVALID_ARG)
-        if need:
+        if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             _keep(workspace, stream)
     if workspace is not None:
-        _dev(workspace, "workspace", torch.uint8)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    _check(lib().gdn_prefill(ctypes.byref(a), _stream(stream)))
+        a.workspace = _flat(workspace, "workspace", torch.uint8, workspace.shape)
+        a.workspace_bytes = workspace.numel()
+    _check(lib().gdn_prefill(ctypes.byref(a), _handle(stream, q)))
     return out, S_new
 
 
 def gdn_prefill_workspace(batch: int, n_k_heads: int, n_v_heads: int, d_k: int, d_v: int, total_tokens: int,
                           max_tokens: int, dtype=torch.bfloat16, out_dtype=None) -> int:
     """Bytes of ``workspace`` with which gdn_prefill takes these sizes (it allocates its own otherwise)."""
-    a = PrefillArgs(batch, n_k_heads, n_v_heads, d_k, d_v, total_tokens, max_tokens, batch, 1.0, _code(dtype),
-                    _code(out_dtype or dtype))
+    a = PrefillArgs(batch, n_k_heads, n_v_heads, d_k, d_v, total_tokens, max_tokens, batch, 1.0, _dtype_code(dtype),
+                    _dtype_code(out_dtype or dtype))
     need = lib().gdn_prefill_workspace(ctypes.byref(a))
     if need < 0:
         _check(GDN_ERR_INVALID_ARG)
@@ -522,25 +548,22 @@ def gdn_decode(q, k, v, g, beta, S, slots=None, scale: float = 1.0, out=None, ou
     """One token a request: o [B, Hv, d_v]; state slots[b] (or b) of the pool S is updated in place.
     A row whose slot is -1 is not in use: its outputs are zero."""
     B, Hk, dk = q.shape
-    Hv, dv = v.shape[1:]
+    _, Hv, dv = v.shape
     dt = q.dtype
     od = out_dtype or dt
+    code, out_code = _dtype_code(dt), _dtype_code(od)
     qs, ks, vs = _rows(q, "q", dt, (B, Hk, dk)), _rows(k, "k", dt, (B, Hk, dk)), _rows(v, "v", dt, (B, Hv, dv))
-    _flat(g, "g", torch.float32, (B, Hv))
-    _flat(beta, "beta", torch.float32, (B, Hv))
+    gp, bp = _flat(g, "g", torch.float32, (B, Hv)), _flat(beta, "beta", torch.float32, (B, Hv))
     n_states = S.shape[0]
-    _flat(S, "S", torch.float32, (n_states, Hv, dv, dk))
-    if slots is not None:
-        _flat(slots, "slots", torch.int32, (B,))
-    elif n_states < B:
+    Sp = _flat(S, "S", torch.float32, (n_states, Hv, dv, dk))
+    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,))
+    if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are requests")
     if out is None:
         out = torch.empty((B, Hv, dv), dtype=od, device=q.device)
-    else:
-        _flat(out, "out", od, (B, Hv, dv))
-    a = DecodeArgs(B, Hk, Hv, dk, dv, n_states, scale, _code(dt), _code(od), qs, ks, vs, _ptr(q), _ptr(k), _ptr(v),
-                   _ptr(g), _ptr(beta), _ptr(S), _ptr(slots), _ptr(out), _ptr(dev_status))
-    _check(lib().gdn_decode(ctypes.byref(a), _stream(stream)))
+    a = DecodeArgs(B, Hk, Hv, dk, dv, n_states, scale, code, out_code, qs, ks, vs, q.data_ptr(), k.data_ptr(),
+                   v.data_ptr(), gp, bp, Sp, sp, _flat(out, "out", od, (B, Hv, dv)), _status(dev_status))
+    _check(lib().gdn_decode(ctypes.byref(a), _handle(stream, q)))
     return out
 
 
@@ -548,19 +571,22 @@ def gdn_qk_gates(q, k, a, b, A_log, dt_bias, eps: float = 1e-6, q_out=None, k_ou
     """Before the rule: (q, k of unit length per head, g [T, Hv], beta [T, Hv]) from a layer's
     projections q, k [T, Hk, d_k] and a, b [T, Hv] (tokens may be strided) and its A_log, dt_bias [Hv]."""
     T, Hk, dk = q.shape
-    Hv = a.shape[1]
-    dt = q.dtype
+    _, Hv = a.shape
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(dt)
     qs, ks = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk))
     as_, bs = _rows(a, "a", dt, (T, Hv)), _rows(b, "b", dt, (T, Hv))
-    _flat(A_log, "A_log", torch.float32, (Hv,))
-    _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
-    q_out = torch.empty((T, Hk, dk), dtype=dt, device=q.device) if q_out is None else _flat(q_out, "q_out", dt, (T, Hk, dk))
-    k_out = torch.empty((T, Hk, dk), dtype=dt, device=q.device) if k_out is None else _flat(k_out, "k_out", dt, (T, Hk, dk))
-    g = torch.empty((T, Hv), dtype=torch.float32, device=q.device)
-    beta = torch.empty((T, Hv), dtype=torch.float32, device=q.device)
-    args = QkGatesArgs(T, Hk, Hv, dk, eps, _code(dt), qs, ks, as_, bs, _ptr(q), _ptr(k), _ptr(a), _ptr(b),
-                       _ptr(A_log), _ptr(dt_bias), _ptr(q_out), _ptr(k_out), _ptr(g), _ptr(beta))
-    _check(lib().gdn_qk_gates(ctypes.byref(args), _stream(stream)))
+    Ap, dp = _flat(A_log, "A_log", torch.float32, (Hv,)), _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
+    if q_out is None:
+        q_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+    g = torch.empty((T, Hv), dtype=torch.float32, device=dev)
+    beta = torch.empty((T, Hv), dtype=torch.float32, device=dev)
+    args = QkGatesArgs(T, Hk, Hv, dk, eps, code, qs, ks, as_, bs, q.data_ptr(), k.data_ptr(), a.data_ptr(),
+                       b.data_ptr(), Ap, dp, _flat(q_out, "q_out", dt, (T, Hk, dk)),
+                       _flat(k_out, "k_out", dt, (T, Hk, dk)), g.data_ptr(), beta.data_ptr())
+    _check(lib().gdn_qk_gates(ctypes.byref(args), _handle(stream, q)))
     return q_out, k_out, g, beta
 
 
@@ -569,13 +595,14 @@ def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, 
     T, Hv, dv = o.shape
     dt = o.dtype
     os_, zs = _rows(o, "o", dt, (T, Hv, dv)), _rows(z, "z", dt, (T, Hv, dv))
-    if act not in GDN_ACTS:
+    kind = GDN_ACTS.get(act)
+    if kind is None:
         raise ValueError(f"act must be one of {sorted(GDN_ACTS)}, got {act!r}")
-    _flat(weight, "weight", weight.dtype, (dv,))
-    out = torch.empty((T, Hv, dv), dtype=dt, device=o.device) if out is None else _flat(out, "out", dt, (T, Hv, dv))
-    a = NormGateArgs(T, Hv, dv, eps, GDN_ACTS[act], _code(dt), _code(weight.dtype), os_, zs, _ptr(o), _ptr(z),
-                     _ptr(weight), _ptr(out))
-    _check(lib().gdn_norm_gate(ctypes.byref(a), _stream(stream)))
+    if out is None:
+        out = torch.empty((T, Hv, dv), dtype=dt, device=o.device)
+    a = NormGateArgs(T, Hv, dv, eps, kind, _dtype_code(dt), _dtype_code(weight.dtype), os_, zs, o.data_ptr(),
+                     z.data_ptr(), _flat(weight, "weight", weight.dtype, (dv,)), _flat(out, "out", dt, (T, Hv, dv)))
+    _check(lib().gdn_norm_gate(ctypes.byref(a), _handle(stream, o)))
     return out
 
 
@@ -584,16 +611,17 @@ def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: f
     """Between two blocks: (h, n) with h = x + scale * y (y normed first where post_weight is given)
     and n = h normed, times weight; x, y [T, width] (tokens may be strided)."""
     T, D = x.shape
-    dt = x.dtype
+    dt, dev = x.dtype, x.device
     xs, ys = _rows(x, "x", dt, (T, D)), _rows(y, "y", dt, (T, D))
-    _flat(weight, "weight", weight.dtype, (D,))
-    if post_weight is not None:
-        _flat(post_weight, "post_weight", weight.dtype, (D,))
-    h = torch.empty((T, D), dtype=dt, device=x.device) if h is None else _flat(h, "h", dt, (T, D))
-    out = torch.empty((T, D), dtype=dt, device=x.device) if out is None else _flat(out, "out", dt, (T, D))
-    a = ResidualNormArgs(T, D, scale, eps, _code(dt), _code(weight.dtype), xs, ys, _ptr(x), _ptr(y), _ptr(weight),
-                         _ptr(post_weight), _ptr(h), _ptr(out))
-    _check(lib().gdn_residual_norm(ctypes.byref(a), _stream(stream)))
+    wp = _flat(weight, "weight", weight.dtype, (D,))
+    pp = 0 if post_weight is None else _flat(post_weight, "post_weight", weight.dtype, (D,))
+    if h is None:
+        h = torch.empty((T, D), dtype=dt, device=dev)
+    if out is None:
+        out = torch.empty((T, D), dtype=dt, device=dev)
+    a = ResidualNormArgs(T, D, scale, eps, _dtype_code(dt), _dtype_code(weight.dtype), xs, ys, x.data_ptr(),
+                         y.data_ptr(), wp, pp, _flat(h, "h", dt, (T, D)), _flat(out, "out", dt, (T, D)))
+    _check(lib().gdn_residual_norm(ctypes.byref(a), _handle(stream, x)))
     return h, out
 
 

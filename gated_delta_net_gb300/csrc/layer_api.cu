@@ -18,6 +18,7 @@ bool valid_dtype(int t) { return t == GDN_F32 || t == GDN_BF16; }
 int check_heads(int hk, int hv) {
     if (hk < 1 || hv < 1) return fail(GDN_ERR_INVALID_ARG, "head counts must be >= 1");
     if (hv % hk) return fail(GDN_ERR_INVALID_ARG, "n_v_heads %d not a multiple of n_k_heads %d", hv, hk);
+    if (hv > 65536) return fail(GDN_ERR_UNSUPPORTED, "n_v_heads %d > 65536", hv);
     return GDN_OK;
 }
 
@@ -115,7 +116,7 @@ int gdn_norm_gate(const gdn_norm_gate_args *a, void *stream) {
     gdn::clear_error();
     if (!a) return fail(GDN_ERR_INVALID_ARG, "args is NULL");
     if (a->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "total_tokens %d < 0", a->total_tokens);
-    if (a->n_v_heads < 1) return fail(GDN_ERR_INVALID_ARG, "head counts must be >= 1");
+    if (int st = check_heads(a->n_v_heads, a->n_v_heads)) return st;
     if (!supported_dim(a->d_v)) return fail(GDN_ERR_UNSUPPORTED, "d_v=%d: supported sizes are 16, 32, 64, 128", a->d_v);
     if (!valid_dtype(a->dtype) || !valid_dtype(a->weight_dtype))
         return fail(GDN_ERR_UNSUPPORTED, "unknown dtype (%d, weight %d)", a->dtype, a->weight_dtype);
