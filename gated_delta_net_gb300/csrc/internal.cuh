@@ -72,6 +72,7 @@ cudaError_t launch_states_tc(const gdn_states_args &a, cudaStream_t stream);
 cudaError_t launch_prefill_simt(const gdn_prefill_args &a, cudaStream_t stream);
 // chunked tensor-core prompts for bf16, d_k = d_v = 128
 bool prefill_tc_supported(const gdn_prefill_args &a);
+int64_t prefill_tc_workspace(const gdn_prefill_args &a);  // bytes, 256-byte aligned
 cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream);
 cudaError_t launch_decode(const gdn_decode_args &a, cudaStream_t stream);
 cudaError_t launch_qk_gates(const gdn_qk_gates_args &a, cudaStream_t stream);

@@ -58,6 +58,9 @@ int check_prefill(const gdn_prefill_args *a) {
     return GDN_OK;
 }
 
+// whether the chunked kernel runs (shorter prompts are done sooner token by token)
+bool chunked(const gdn_prefill_args &a) { return a.max_tokens >= 16 && gdn::prefill_tc_supported(a); }
+
 }  // namespace
 
 extern "C" {
@@ -65,7 +68,7 @@ extern "C" {
 int64_t gdn_prefill_workspace(const gdn_prefill_args *a) {
     gdn::clear_error();
     if (check_prefill(a)) return -1;
-    return 0;
+    return a->batch > 0 && chunked(*a) ? gdn::prefill_tc_workspace(*a) : 0;
 }
 
 int gdn_prefill(const gdn_prefill_args *a, void *stream) {
@@ -75,8 +78,14 @@ int gdn_prefill(const gdn_prefill_args *a, void *stream) {
     if (!a->token_offsets || !a->S_new) return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a->total_tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->o))
         return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
-    if (a->max_tokens >= 16 && gdn::prefill_tc_supported(*a))
+    if (chunked(*a)) {
+        const int64_t need = gdn::prefill_tc_workspace(*a);
+        if (need > 0 && (!a->workspace || a->workspace_bytes < need))
+            return fail(GDN_ERR_INVALID_ARG, "workspace of %lld bytes: %lld are needed", (long long)(a->workspace ? a->workspace_bytes : 0), (long long)need);
+        if (need > 0 && (reinterpret_cast<uintptr_t>(a->workspace) & 255))
+            return fail(GDN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
         return done(gdn::launch_prefill_tc(*a, (cudaStream_t)stream), "prefill launch");
+    }
     return done(gdn::launch_prefill_simt(*a, (cudaStream_t)stream), "prefill launch");
 }
 

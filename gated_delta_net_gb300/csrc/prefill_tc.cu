@@ -76,7 +76,7 @@ constexpr int OFF_BAR = OFF_SLOT + 16;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
     B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
-    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_UBF, B_SQ, B_UPD, B_O, B_OFREE, B_PROBE, B_COUNT
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_PROBE, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -84,39 +84,56 @@ static_assert(kSmem <= 232448, "one block an SM");
 // tensor-memory columns
 constexpr uint32_t TM_DS = 0, TM_S = 128, TM_U = 256, TM_O = 320, TM_G = 384, TM_W = 448;
 constexpr uint32_t TM_SHI = TM_S, TM_SLO = TM_S + 64;
-// U' hi, lo lie over S lo (free once S W^T is done), U over S hi (free once S Q^T is done)
-constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32, TM_UBF = TM_SHI;
+// U' hi, lo lie over S lo, which is free once S W^T is done.  U in bf16 lies over its own sum: tokens 0..31 in the
+// first 16 columns of their half of it, tokens 32..63 in the first 16 of theirs
+constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32;
 
 struct Params {
-    int hk_n, hv_n, total, max_tokens, n_states, items, probe;
-    int step_b, step_h;    // blocks of the grid, in whole requests and heads
-    uint32_t group_inv;    // ceil(2^32 / heads that share a key head), 0 for one
+    int hk_n, hv_n, total, max_tokens, n_states, batch, items, probe;
+    int seg, segs;                  // tokens of a segment, a multiple of 64; segments a prompt can have
+    int step_h, step_b, step_s;     // blocks of the grid, in heads, requests and slices
+    uint32_t group_inv;             // ceil(2^32 / heads that share a key head), 0 for one
     float scale;
     const int32_t *offsets, *slots, *fresh;
     const float *g, *beta, *S0;
     __nv_bfloat16 *o;
-    float *S_new;
+    float *S_new, *ws;
     int32_t *status;
 };
 
+// Few prompts do not fill the GPU, so a prompt is cut into segments.  A first pass over all segments but the last
+// finds, without outputs, each one's state from zero (from S0 for the first) and its effect on a state before it
+// (the same from the identity and with v = 0: rows of the state do not meet, so S -> S M + L).  A small kernel
+// joins them, and a second pass runs every segment from the state before it.  Workspace of a (request, head), in
+// states: S before segments 0 .. segs - 1 (after the first pass: S0, L of segments 0 .. segs - 2), M of segments
+// 1 .. segs - 2.
 struct Item {
     int h, hk, lo, n, chunks, err;
-    int64_t state;  // first entry of its state in the pools
-    bool zero;      // starts from zero
+    bool skip;          // has no such segment, or is refused
+    bool unit;          // from the identity, without v
+    const float *from;  // the state before it, null for zero
+    float *to;          // where the one after it goes, null for nowhere
 };
 
-// a block's items: (request, head) pairs, a grid apart
+// a block's items: (slice, request, head), a grid apart.  A slice is a segment; in the first pass, the slices
+// from segs - 1 on are segments 1.. from the identity.
 struct Walk {
-    int idx, b, h;
+    int idx, h, b, s;
     __device__ __forceinline__ void next(const Params &p) {
         idx += gridDim.x;
-        b += p.step_b;
         h += p.step_h;
+        b += p.step_b;
+        s += p.step_s;
         if (h >= p.hv_n) {
             h -= p.hv_n;
             ++b;
         }
+        if (b >= p.batch) {
+            b -= p.batch;
+            ++s;
+        }
     }
+    template <bool OUT>
     __device__ __forceinline__ Item item(const Params &p) const {
         Item x;
         x.h = h;
@@ -128,9 +145,23 @@ struct Walk {
         if (x.n < 0 || x.lo < 0 || x.lo + x.n > p.total) x.err = GDN_DEV_BAD_DESC;
         else if (x.n > p.max_tokens) x.err = GDN_DEV_TOO_MANY;
         else if (slot < 0 || slot >= p.n_states) x.err = GDN_DEV_BAD_SLOT;
-        x.zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
-        x.state = ((int64_t)slot * p.hv_n + h) * (kD * kD);
-        x.chunks = x.err ? 0 : (x.n + kC - 1) / kC;
+        const int64_t state = ((int64_t)slot * p.hv_n + h) * (kD * kD);
+        float *ws = p.ws + ((int64_t)b * p.hv_n + h) * (2 * p.segs - 2) * (kD * kD);
+        x.unit = !OUT && s >= p.segs - 1;
+        const int seg = x.unit ? s - (p.segs - 2) : s, off = seg * p.seg;
+        const bool last = x.n - off <= p.seg, one = x.n <= p.seg;
+        x.skip = x.err || (seg > 0 && x.n <= off) || (!OUT && last);
+        const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
+        if (OUT) {
+            x.from = one ? (zero ? nullptr : p.S0 + state) : ws + seg * (kD * kD);
+            x.to = last ? p.S_new + state : nullptr;
+        } else {
+            x.from = seg == 0 && !zero ? p.S0 + state : nullptr;
+            x.to = ws + (x.unit ? p.segs + seg - 1 : seg + 1) * (kD * kD);
+        }
+        x.lo += off;
+        x.n = min(x.n - off, p.seg);
+        x.chunks = x.skip ? 0 : (x.n + kC - 1) / kC;
         return x;
     }
 };
@@ -338,6 +369,8 @@ __device__ __forceinline__ void dd_add(float &ah, float &al, float bh, float bl)
     al = __fsub_rn(e, __fsub_rn(ah, s));
 }
 
+// OUT: outputs and final states; otherwise the first pass over segments
+template <bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, Params p) {
@@ -351,9 +384,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            const bool four = i == B_T || i == B_WRDY || i == B_OFREE || (i >= B_SCFREE && i < B_GATES) ||
+            const bool four = i == B_T || i == B_WRDY || i == B_OFREE || i == B_SQRD || (i >= B_SCFREE && i < B_GATES) ||
                               (i >= B_BLKFREE && i < B_DIAG);
-            const uint32_t n = four ? 4 : i == B_GFREE ? 6 : i >= B_BLK && i < B_BLKFREE ? 7 : i == B_S || i == B_UST || i == B_UBF ? 8 : i == B_TFREE ? 2 : 1;
+            const uint32_t n = four ? 4 : i == B_GFREE ? (OUT ? 6 : 3) : i >= B_BLK && i < B_BLKFREE ? (OUT ? 7 : 4)
+                               : i == B_S || i == B_UST ? 8 : i == B_TFREE ? 2 : 1;
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
@@ -374,7 +408,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const uint32_t tmem = *slot;
     bool ok = true;
     float *el = reinterpret_cast<float *>(sm + OFF_EL);
-    Walk at = {(int)blockIdx.x, (int)blockIdx.x / p.hv_n, (int)blockIdx.x % p.hv_n};
+    Walk at;
+    at.idx = blockIdx.x;
+    at.h = at.idx % p.hv_n;
+    at.b = at.idx / p.hv_n % p.batch;
+    at.s = at.idx / p.hv_n / p.batch;
 
     if (warp < 4) {
         const uint32_t lead = elect();
@@ -385,16 +423,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             bool go = true;  // the pipeline's own waits
             int cc = 0, kq = 0;
             for (; at.idx < p.items && go; at.next(p)) {
-                const Item x = at.item(p);
-                if (x.err) flag(p.status, x.err);
+                const Item x = at.template item<OUT>(p);
+                if (OUT && x.err) flag(p.status, x.err);
                 for (int c = 0; c < x.chunks && go; ++c) {
                     uint8_t *dst = sm + OFF_KQ + kq * 4 * kTile;
                     if (cc >= kKQ) wait(&bar[B_EMPTY + kq], (cc / kKQ - 1) & 1, go);
                     if (!go) break;  // nothing is loaded over a stage that may be in use
-                    mbar_arrive_expect_tx(&bar[B_FULL + kq], 4 * kTile);
+                    mbar_arrive_expect_tx(&bar[B_FULL + kq], (OUT ? 4 : 2) * kTile);
                     for (int half = 0; half < 2; ++half) {
                         tma_load_3d(dst + half * 2 * kTile, &tmK, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
-                        tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
+                        if (OUT) tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
                     }
                     ++cc;
                     kq = kq + 1 == kKQ ? 0 : kq + 1;
@@ -408,7 +446,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t id = idesc_bf16_f32(128, kC);
             int cc = 0, kq = 0;
             for (; at.idx < p.items; at.next(p)) {
-                const Item x = at.item(p);
+                const Item x = at.template item<OUT>(p);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_FULL + kq], (cc / kKQ) & 1, ok);
@@ -441,11 +479,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
             int cc = 0, kq = 0;
             Item nx = {};
-            if (at.idx < p.items) nx = at.item(p);
+            if (at.idx < p.items) nx = at.template item<OUT>(p);
             while (at.idx < p.items) {
                 const Item x = nx;  // the next one's parameters arrive meanwhile
                 at.next(p);
-                if (at.idx < p.items) nx = at.item(p);
+                if (at.idx < p.items) nx = at.template item<OUT>(p);
                 for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
@@ -457,14 +495,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    // U^T = V^T T'^T
+                    // U^T = V^T T'^T, once the U before it has been read
                     wwait(&bar[B_T], cc & 1, ok);
+                    if (OUT && cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);
                     tc_fence_after();
+                    if (!x.unit) {
 #pragma unroll 1
-                    for (int part = 0; part < 2; ++part)
+                        for (int part = 0; part < 2; ++part)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + part * (kTile >> 4) + ks * 2, id_u, part + ks > 0);
+                            for (int ks = 0; ks < 4; ++ks)
+                                mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + part * (kTile >> 4) + ks * 2, id_u, part + ks > 0);
+                    }
                     commit(lead, &bar[B_TFREE]);
                     // U^T += S (-W)^T: hi hi, lo hi, hi lo
                     wwait(&bar[B_WRDY], cc & 1, ok);
@@ -475,17 +516,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             mma_ts(lead, tm + TM_U, tm + TM_SHI + (part & 1) * (TM_SLO - TM_SHI) + ks * 8,
-                                   d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, true);
+                                   d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, OUT || !x.unit || part + ks > 0);
                     commit(lead, &bar[B_U]);
-                    // O^T = S Q^T
-                    if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
-                    tc_fence_after();
                     const uint32_t d_q = uniform(desc_lo(kt + kTile, 0)), d_k = uniform(desc_lo(kt, 2 * kTile));
+                    if (OUT) {  // O^T = S Q^T
+                        if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
+                        tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
-                    commit(lead, &bar[B_SQ]);
-                    // dS = U'^T K
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
+                        commit(lead, &bar[B_SQ]);
+                    }
+                    // S += U'^T K
                     wwait(&bar[B_UST], cc & 1, ok);
                     tc_fence_after();
 #pragma unroll 1
@@ -494,14 +536,16 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         for (int ks = 0; ks < 4; ++ks)
                             mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, true);
                     commit(lead, &bar[B_UPD]);
-                    // O^T += U^T Y^T, once S Q^T has its factors
-                    wwait(&bar[B_UBF], cc & 1, ok);
-                    tc_fence_after();
-                    const uint32_t d_y = uniform(desc_lo(sm + OFF_Y + kq * kTile, 0));
+                    if (OUT) {  // O^T += U^T Y^T, once S Q^T has its factors
+                        wwait(&bar[B_SQRD], cc & 1, ok);
+                        tc_fence_after();
+                        const uint32_t d_y = uniform(desc_lo(sm + OFF_Y + kq * kTile, 0));
 #pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) mma_ts(lead, tm + TM_O, tm + TM_UBF + ks * 8, d_y + ((ks * 32) >> 4), id_k, true);
-                    commit(lead, &bar[B_O]);
-                    commit(lead, &bar[B_YFREE + kq]);
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_ts(lead, tm + TM_O, tm + TM_U + (ks >> 1) * 32 + (ks & 1) * 8, d_y + ((ks * 32) >> 4), id_k, true);
+                        commit(lead, &bar[B_O]);
+                        commit(lead, &bar[B_YFREE + kq]);
+                    }
                     commit(lead, &bar[B_EMPTY + kq]);
                 }
             }
@@ -509,7 +553,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // ---------------------------------------------------------------- gates, ahead of everything
             int cc = 0, kq = 0;
             for (; at.idx < p.items; at.next(p)) {
-                const Item x = at.item(p);
+                const Item x = at.template item<OUT>(p);
                 float g[2], b[2];  // of tokens 2 lane, 2 lane + 1 of the next chunk
                 auto fetch = [&](int c) {
 #pragma unroll
@@ -589,13 +633,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // -------------------------------------------------------------------- A, Y: 32 rows, 32 columns a warp
         const int row = quad * 32 + lane, i = row & 63, own = i >> 4;  // own: the row's block of 16
         const int cb0 = warp < 8 ? 0 : 2;             // its first block of columns; rows 0..31 have two only
-        const bool is_y = row >= 64;
+        const bool is_y = row >= 64;                  // of Y (none in a pass without outputs)
         const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const float *mask = reinterpret_cast<const float *>(sm + OFF_MASK);
         int cc = 0, kq = 0;
-        for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.item(p);
+        for (; at.idx < p.items && (OUT || !is_y); at.next(p)) {
+            const Item x = at.template item<OUT>(p);
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
@@ -685,7 +729,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // Lane l row l mod 16 of one.  From T (I + A) = I, t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling k
         int cc = 0;
         for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.item(p);
+            const Item x = at.template item<OUT>(p);
             for (int c = 0; c < x.chunks; ++c, ++cc) {
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
                 const float *diag = reinterpret_cast<const float *>(blocks + 6 * 1024);
@@ -736,7 +780,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t lane_at = blk((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
         int cc = 0, kq = 0;
         for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.item(p);
+            const Item x = at.template item<OUT>(p);
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
@@ -816,6 +860,28 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // -------------------------------------------------------------------- W to shared memory, outputs
         const int row = quad * 32 + lane;
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+        auto factors = [&](int cc, int kq) {  // S Q^T times scale e^gamma, in place, before U^T Y^T is added
+            const float *eg = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + SC_EG;
+            wwait(&bar[B_SQ], cc & 1, ok);
+            tc_fence_after();
+#pragma unroll 1
+            for (int j0 = 0; j0 < 64; j0 += 16) {
+                uint32_t r[16];
+                tmem_ld16_nowait(tmem + lanes + TM_O + j0, r);
+                tmem_wait_ld_into(r);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(eg + j0 + j);
+                    unpair(mul2(e.x, pair(r[j], r[j + 1])), r[j], r[j + 1]);
+                    unpair(mul2(e.y, pair(r[j + 2], r[j + 3])), r[j + 2], r[j + 3]);
+                }
+                tmem_st16(tmem + lanes + TM_O + j0, r);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar[B_SQRD]);
+        };
         auto outputs = [&](int cc, int tok, int nv, int h) {
             wwait(&bar[B_O], cc & 1, ok);
             tc_fence_after();
@@ -844,14 +910,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         int cc = 0;
         // the chunk in work (x, c), and the one before it, whose outputs are still to come
         Item x = {};
-        int c = 0, p_tok = 0, p_nv = 0, p_h = 0;
+        int c = 0, kq = 0, p_tok = 0, p_nv = 0, p_h = 0;
         while (true) {
             while (c == x.chunks && at.idx < p.items) {
-                x = at.item(p);
+                x = at.template item<OUT>(p);
                 c = 0;
                 at.next(p);
             }
             const bool more = c < x.chunks;
+            bool w_first = false;
             if (more) {
                 if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // the chunk before has its U: V and W have been read
                 if (warp == 16 && lane == 0 && ok) {
@@ -861,36 +928,46 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         tma_load_3d(sm + OFF_V + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
                 }
                 __syncwarp();
-                wwait(&bar[B_W], cc & 1, ok);
-                tc_fence_after();
-                uint8_t *wt = sm + OFF_W;
-#pragma unroll 1
-                for (int j0 = 0; j0 < 64; j0 += 16) {
-                    uint32_t r[16];
-                    tmem_ld16_nowait(tmem + lanes + TM_W + j0, r);
-                    tmem_wait_ld_into(r);
-                    uint32_t hi[8], lw[8];
-#pragma unroll
-                    for (int j = 0; j < 16; j += 2) split2(pair(r[j], r[j + 1]), hi[j / 2], lw[j / 2]);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint32_t off = sw(row, j0 / 8 + q);
-                        *reinterpret_cast<uint4 *>(wt + off) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-                        *reinterpret_cast<uint4 *>(wt + 2 * kTile + off) = make_uint4(lw[4 * q], lw[4 * q + 1], lw[4 * q + 2], lw[4 * q + 3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_WRDY]);
+                w_first = __shfl_sync(0xffffffffu, mbar_test_wait(&bar[B_W], cc & 1), 0);
             }
-            if (cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
+            // W of this chunk and the factors of the one before: what is there first
+#pragma unroll 1
+            for (int step = 0; step < 2; ++step) {
+                if ((step == 0) != w_first) {
+                    if (OUT && cc > 0) factors(cc - 1, kq == 0 ? kKQ - 1 : kq - 1);
+                } else if (more) {
+                    wwait(&bar[B_W], cc & 1, ok);
+                    tc_fence_after();
+                    uint8_t *wt = sm + OFF_W;
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 64; j0 += 16) {
+                        uint32_t r[16];
+                        tmem_ld16_nowait(tmem + lanes + TM_W + j0, r);
+                        tmem_wait_ld_into(r);
+                        uint32_t hi[8], lw[8];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) split2(pair(r[j], r[j + 1]), hi[j / 2], lw[j / 2]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const uint32_t off = sw(row, j0 / 8 + q);
+                            *reinterpret_cast<uint4 *>(wt + off) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+                            *reinterpret_cast<uint4 *>(wt + 2 * kTile + off) = make_uint4(lw[4 * q], lw[4 * q + 1], lw[4 * q + 2], lw[4 * q + 3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[B_WRDY]);
+                }
+            }
+            if (OUT && cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
             if (!more) break;
             p_tok = x.lo + c * kC;
             p_nv = x.n - c * kC;
             p_h = x.h;
             ++c;
             ++cc;
+            kq = kq + 1 == kKQ ? 0 : kq + 1;
         }
         if (loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
     } else {
@@ -899,24 +976,30 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         int cc = 0, kq = 0;
         Item nx = {};
-        if (at.idx < p.items) nx = at.item(p);
+        if (at.idx < p.items) nx = at.template item<OUT>(p);
         while (at.idx < p.items) {
             const Item x = nx;  // the next one's parameters arrive meanwhile
             at.next(p);
-            if (at.idx < p.items) nx = at.item(p);
-            if (x.err) continue;
-            const float *from = x.zero ? nullptr : p.S0 + x.state + row * kD + half * 64;
-            float *to = p.S_new + x.state + row * kD + half * 64;
+            if (at.idx < p.items) nx = at.template item<OUT>(p);
+            if (x.skip) continue;
+            const int64_t mine = row * kD + half * 64;
             // S into tensor memory, whose last reader was this thread (or, without tokens, straight on)
 #pragma unroll 1
             for (int j = 0; j < 64; j += 32) {
                 f2 v[4][4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) load8(from ? from + j + 8 * q : nullptr, v[q]);
+                for (int q = 0; q < 4; ++q) {
+                    load8(x.from ? x.from + mine + j + 8 * q : nullptr, v[q]);
+                    if (!OUT && x.unit && (row >> 3) == (half * 64 + j) / 8 + q) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (((row & 7) >> 1) == e) v[q][e] = (row & 1) ? pair(0.f, 1.f) : pair(1.f, 0.f);
+                    }
+                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (x.chunks == 0) {
-                        store8(to + j + 8 * q, v[q]);
+                        if (x.to) store8(x.to + mine + j + 8 * q, v[q]);
                     } else {
                         uint32_t r[8];
 #pragma unroll
@@ -929,7 +1012,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             tmem_wait_st();
             for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + half * 32;
-                if (cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);  // dS is in; U of the chunk before lay over S hi
+                if (cc > 0) wwait(&bar[B_UPD], (cc - 1) & 1, ok);  // the chunk before is in the sum, and U' has been read
                 wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
                 tc_fence_after();
                 // S as hi + lo, and its sum times e^gamma_63, ready for dS
@@ -958,52 +1041,30 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_after();
 #pragma unroll 1
                 for (int j0 = 0; j0 < 32; j0 += 16) {
-                    uint32_t r[16], hi[8], lw[8];
+                    uint32_t r[16], hi[8], lw[8], ub[8];
                     tmem_ld16_nowait(lanes + TM_U + half * 32 + j0, r);
                     tmem_wait_ld_into(r);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + SC_FD + j0 + j);
+                        ub[j / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                        ub[j / 2 + 1] = pack_bf16(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
                         split2(mul2(pair(r[j], r[j + 1]), f.x), hi[j / 2], lw[j / 2]);
                         split2(mul2(pair(r[j + 2], r[j + 3]), f.y), hi[j / 2 + 1], lw[j / 2 + 1]);
                     }
                     tmem_st8(lanes + TM_UHI + half * 16 + j0 / 2, hi);
                     tmem_st8(lanes + TM_ULO + half * 16 + j0 / 2, lw);
+                    if (OUT) tmem_st8(lanes + TM_U + half * 32 + j0 / 2, ub);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_UST]);
-                wwait(&bar[B_SQ], cc & 1, ok);
-                tc_fence_after();
-                // U over S hi; S Q^T times scale e^gamma, in place, before U^T Y^T is added
-#pragma unroll 1
-                for (int j0 = 0; j0 < 32; j0 += 16) {
-                    uint32_t u[16], r[16], ub[8];
-                    tmem_ld16_nowait(lanes + TM_U + half * 32 + j0, u);
-                    tmem_ld16_nowait(lanes + TM_O + half * 32 + j0, r);
-                    tmem_wait_ld_into(r);
-                    tmem_wait_ld_into(u);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        ub[j / 2] = pack_bf16(__uint_as_float(u[j]), __uint_as_float(u[j + 1]));
-                        ub[j / 2 + 1] = pack_bf16(__uint_as_float(u[j + 2]), __uint_as_float(u[j + 3]));
-                        const ulonglong2 e = *reinterpret_cast<const ulonglong2 *>(sc + SC_EG + j0 + j);
-                        unpair(mul2(e.x, pair(r[j], r[j + 1])), r[j], r[j + 1]);
-                        unpair(mul2(e.y, pair(r[j + 2], r[j + 3])), r[j + 2], r[j + 3]);
-                    }
-                    tmem_st8(lanes + TM_UBF + half * 16 + j0 / 2, ub);
-                    tmem_st16(lanes + TM_O + half * 32 + j0, r);
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar[B_UBF]);
             }
             wwait(&bar[B_UPD], (cc - 1) & 1, ok);
             tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; j < 64; j += 16) {
+            for (int j = 0; x.to && j < 64; j += 16) {
                 uint32_t r[16];
                 tmem_ld16_nowait(lanes + TM_DS + half * 64 + j, r);
                 tmem_wait_ld_into(r);
@@ -1012,7 +1073,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int q = 0; q < 2; ++q) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = pair(r[8 * q + 2 * e], r[8 * q + 2 * e + 1]);
-                    store8(to + j + 8 * q, v);
+                    store8(x.to + mine + j + 8 * q, v);
                 }
             }
         }
@@ -1021,6 +1082,48 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     tc_fence_before();
     __syncthreads();
     if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// The states before the segments of prompts that have several, in place of the first pass's: S before segment s + 1
+// is S_s M_s + L_s, in fp32.  A block takes 16 rows of one (request, head); a thread 8 rows of one column.
+constexpr int kJoinRows = 16;
+__global__ void __launch_bounds__(256) prefill_join_kernel(Params p) {
+    __shared__ __align__(16) float S[kJoinRows][kD];
+    const int part = blockIdx.x % (kD / kJoinRows), item = blockIdx.x / (kD / kJoinRows), h = item % p.hv_n, b = item / p.hv_n;
+    const int lo = __ldg(p.offsets + b), n = __ldg(p.offsets + b + 1) - lo, slot = p.slots ? __ldg(p.slots + b) : b;
+    if (n <= p.seg || lo < 0 || lo + n > p.total || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
+    const int col = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * (kJoinRows / 2), segs = (n + p.seg - 1) / p.seg;
+    float *ws = p.ws + (int64_t)item * (2 * p.segs - 2) * (kD * kD);
+    const int64_t at = (int64_t)(part * kJoinRows + r0) * kD + col;
+    const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
+    const float *S0 = p.S0 + ((int64_t)slot * p.hv_n + h) * (kD * kD);
+    float x[kJoinRows / 2];
+#pragma unroll
+    for (int r = 0; r < kJoinRows / 2; ++r) {
+        ws[at + r * kD] = zero ? 0.f : S0[at + r * kD];  // the final state may go to S0's place while segment 0 runs
+        x[r] = ws[kD * kD + at + r * kD];
+    }
+    for (int s = 1; s < segs - 1; ++s) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kJoinRows / 2; ++r) S[r0 + r][col] = x[r];
+        __syncthreads();
+        const float *M = ws + (int64_t)(p.segs + s - 1) * (kD * kD) + col;
+        float *L = ws + (int64_t)(s + 1) * (kD * kD) + at;
+#pragma unroll
+        for (int r = 0; r < kJoinRows / 2; ++r) x[r] = L[r * kD];
+#pragma unroll 4
+        for (int k = 0; k < kD; k += 4) {
+            const float m0 = M[k * kD], m1 = M[(k + 1) * kD], m2 = M[(k + 2) * kD], m3 = M[(k + 3) * kD];
+#pragma unroll
+            for (int r = 0; r < kJoinRows / 2; ++r) {
+                const float4 v = *reinterpret_cast<const float4 *>(&S[r0 + r][k]);
+                x[r] = fmaf(v.x, m0, fmaf(v.y, m1, fmaf(v.z, m2, fmaf(v.w, m3, x[r]))));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kJoinRows / 2; ++r) L[r * kD] = x[r];
+    }
 }
 
 // [T][H][128] bf16 tokens `stride` elements apart as a 3-D tensor (d, head, token); boxes of 64 x 1 x 64,
@@ -1052,6 +1155,50 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
            (int64_t)a.batch * a.n_v_heads <= 0x7fffffff - 65536 && a.n_v_heads <= 65535 && tensor_map_encoder() != nullptr;
 }
 
+// How many segments a prompt is cut into (1: none), and their length.  In units of a chunk's time on an SM: a pass over
+// segments of L chunks takes L for every wave of blocks, the first pass (2 segs - 3 slices) about 0.8 of that; a join
+// step and the launches are estimated at 1.5 and 8.
+// One prompt of 16384 tokens with 32 heads: TIMES.
+int plan_segments(const gdn_prefill_args &a, int &seg) {
+    const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads, chunks = std::max(1, (a.max_tokens + kC - 1) / kC);
+    double best = (double)chunks * ((items + sms - 1) / sms) * 0.9;  // worth a tenth at least
+    int segs = 1;
+    seg = (int)std::min<int64_t>(chunks * kC, 0x7fffffc0);
+    for (int64_t s = 2; s <= 24 && s <= chunks && items < sms; ++s) {
+        const int64_t len = (chunks + s - 1) / s;
+        // segments that have tokens: those of every prompt, or as many as all the tokens fill
+        const double pieces = std::min<double>((double)a.batch * s, (double)a.total_tokens / (len * kC) + a.batch) * a.n_v_heads;
+        const double firsts = std::max(0.0, (pieces - items) + std::max(0.0, pieces - 2 * items));
+        const double cost = len * (std::ceil(pieces / sms) + 0.8 * std::ceil(firsts / sms)) + 1.5 * (s - 2) + 8;
+        if (cost < best && (chunks + len - 1) / len == s) {
+            best = cost;
+            segs = (int)s;
+            seg = (int)(len * kC);
+        }
+    }
+    return segs;
+}
+
+int64_t prefill_tc_workspace(const gdn_prefill_args &a) {
+    int seg;
+    const int segs = plan_segments(a, seg);
+    return segs == 1 ? 0 : (int64_t)a.batch * a.n_v_heads * (2 * segs - 2) * (kD * kD * 4);
+}
+
+template <bool OUT>
+cudaError_t launch_pass(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV, Params p, int slices, cudaStream_t stream) {
+    p.items = p.batch * p.hv_n * slices;
+    const int grid = std::min(p.items, sm_count());
+    p.step_h = grid % p.hv_n;
+    p.step_b = grid / p.hv_n % p.batch;
+    p.step_s = grid / p.hv_n / p.batch;
+    static int have[16];
+    cudaError_t e = ensure_smem(prefill_tc_kernel<OUT>, kSmem, have);
+    if (e != cudaSuccess) return e;
+    prefill_tc_kernel<OUT><<<(unsigned)grid, kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     CUtensorMap tmQ, tmK, tmV;
     if (!encode(&tmQ, a.q, a.n_k_heads, a.total_tokens, token_stride(a.q_stride, a.n_k_heads)) ||
@@ -1060,19 +1207,22 @@ cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     Params p = {};
     p.hk_n = a.n_k_heads; p.hv_n = a.n_v_heads; p.total = a.total_tokens; p.max_tokens = a.max_tokens;
-    p.n_states = a.n_states; p.items = a.batch * a.n_v_heads; p.probe = wait_probe_polls();
-    const int grid = std::min(p.items, sm_count()), group = a.n_v_heads / a.n_k_heads;
-    p.step_b = grid / p.hv_n; p.step_h = grid % p.hv_n;
+    p.n_states = a.n_states; p.batch = a.batch; p.probe = wait_probe_polls();
+    const int group = a.n_v_heads / a.n_k_heads;
     p.group_inv = group == 1 ? 0u : (uint32_t)(((1ull << 32) + group - 1) / group);
     p.scale = a.scale;
     p.offsets = a.token_offsets; p.slots = a.slots; p.fresh = a.fresh;
     p.g = a.g; p.beta = a.beta; p.S0 = a.S0;
-    p.o = static_cast<__nv_bfloat16 *>(a.o); p.S_new = a.S_new; p.status = a.dev_status;
-    static int have[16];
-    cudaError_t e = ensure_smem(prefill_tc_kernel, kSmem, have);
-    if (e != cudaSuccess) return e;
-    prefill_tc_kernel<<<(unsigned)grid, kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
-    return cudaGetLastError();
+    p.o = static_cast<__nv_bfloat16 *>(a.o); p.S_new = a.S_new; p.ws = static_cast<float *>(a.workspace); p.status = a.dev_status;
+    p.segs = plan_segments(a, p.seg);
+    if (p.segs > 1) {
+        cudaError_t e = launch_pass<false>(tmQ, tmK, tmV, p, 2 * p.segs - 3, stream);
+        if (e != cudaSuccess) return e;
+        prefill_join_kernel<<<(unsigned)(p.batch * p.hv_n * (kD / kJoinRows)), 256, 0, stream>>>(p);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pass<true>(tmQ, tmK, tmV, p, p.segs, stream);
 }
 
 }  // namespace gdn

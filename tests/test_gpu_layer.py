@@ -137,6 +137,29 @@ def test_prefill_long_prompt_many_segments(hv, length):
     close(S, rS, TOL_STATE[BF])
 
 
+def test_prefill_segments_in_place():
+    # prompts of several segments and of one, states in their pool's places, some of them not read
+    lengths, hv, n = [700, 64, 0, 2000, 129], 2, 6
+    x = tokens(19, sum(lengths), 1, hv, 128, 128, BF, slow=True)
+    off = offsets(lengths)
+    S = pool(8, n, hv, 128, 128)
+    before = f64(S)
+    slots = torch.tensor([4, 1, 0, 3, 5], dtype=torch.int32, device="cuda")
+    fresh = torch.tensor([0, 0, 0, 0, 1], dtype=torch.int32, device="cuda")
+    assert gb.gdn_prefill_workspace(5, 1, hv, 128, 128, sum(lengths), 2000) > 0
+    ro, rS = OL.prefill(*map(f64, x), off.cpu().numpy(), S0=before, slots=slots.cpu().numpy(), fresh=fresh.cpu().numpy())
+    for _ in range(3):
+        S.copy_(torch.from_numpy(before).float())
+        st = gb.new_status()
+        o, _ = gb.gdn_prefill(*x, off, 2000, S0=S, S_new=S, slots=slots, fresh=fresh, dev_status=st)
+        gb.check_status(st)
+        close(o, ro, TOL[BF])
+        close(S, rS, TOL_STATE[BF])
+    assert np.array_equal(f64(S)[2], before[2])
+    with pytest.raises(gb.GdnError):
+        gb.gdn_prefill(*x, off, 2000, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
 def test_prefill_correlated_unnormalised_keys():
     # neighbouring keys almost alike and longer than one: the chunk's system is far from the identity
     T = 192
