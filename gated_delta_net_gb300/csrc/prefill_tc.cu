@@ -1155,21 +1155,22 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
            (int64_t)a.batch * a.n_v_heads <= 0x7fffffff - 65536 && a.n_v_heads <= 65535 && tensor_map_encoder() != nullptr;
 }
 
-// How many segments a prompt is cut into (1: none), and their length.  In units of a chunk's time on an SM: a pass over
-// segments of L chunks takes L for every wave of blocks, the first pass (2 segs - 3 slices) about 0.8 of that; a join
-// step and the launches are estimated at 1.5 and 8.
-// One prompt of 16384 tokens with 32 heads: TIMES.
+// How many segments a prompt is cut into (1: none), and their length.  In units of a chunk's time on a full GPU (4.2 us;
+// with few blocks running it is down to 0.77 of that): a pass over segments of L chunks takes L + 3 for every wave of
+// blocks, the first pass over its 2 segs - 3 slices 0.7 of that; a join step takes 1.5, the launches 3.  One prompt of
+// 16384 tokens with 32 heads, measured with 1, 2, 3, 4, 6, 8, 9, 16 segments: 842, 795, 571, 622, 643, 658, 675, 790 us.
 int plan_segments(const gdn_prefill_args &a, int &seg) {
     const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads, chunks = std::max(1, (a.max_tokens + kC - 1) / kC);
-    double best = (double)chunks * ((items + sms - 1) / sms) * 0.9;  // worth a tenth at least
+    auto waves = [&](double blocks) { return std::ceil(blocks / sms) * (0.715 + 0.285 * std::min(1.0, blocks / sms)); };
+    double best = 0.9 * (chunks + 3) * waves((double)items);  // worth a tenth at least
     int segs = 1;
     seg = (int)std::min<int64_t>(chunks * kC, 0x7fffffc0);
     for (int64_t s = 2; s <= 24 && s <= chunks && items < sms; ++s) {
         const int64_t len = (chunks + s - 1) / s;
         // segments that have tokens: those of every prompt, or as many as all the tokens fill
         const double pieces = std::min<double>((double)a.batch * s, (double)a.total_tokens / (len * kC) + a.batch) * a.n_v_heads;
-        const double firsts = std::max(0.0, (pieces - items) + std::max(0.0, pieces - 2 * items));
-        const double cost = len * (std::ceil(pieces / sms) + 0.8 * std::ceil(firsts / sms)) + 1.5 * (s - 2) + 8;
+        const double firsts = std::max(0.0, pieces - items) + std::max(0.0, pieces - 2 * items);
+        const double cost = (len + 3) * (waves(pieces) + 0.7 * waves(firsts)) + 1.5 * (s - 2) + 3;
         if (cost < best && (chunks + len - 1) / len == s) {
             best = cost;
             segs = (int)s;
