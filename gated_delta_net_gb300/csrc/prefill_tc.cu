@@ -18,13 +18,13 @@
 // products take S, U and Y rounded once to bf16, like the output itself.
 //
 // One block an SM (all 512 tensor-memory columns), 28 warps:
-//     warp 0        loads K and Q of three chunks by TMA
+//     warp 0        issues W
 //     warp 1        issues [K;Q] K^T
 //     warp 2        issues U, O and dS: the chain
-//     warp 3        the chunk's gates: gamma by a scan, and its exponentials
+//     warp 3        walks the items, loads K and Q of three chunks, the chunk's gates: gamma by a scan, and its exponentials
 //     warps 4-7, 9, 11  A and Y; T = (I + A)^-1 is then found in blocks of 16:
 //     warps 8, 10   T's diagonal blocks
-//     warps 12-15   T's other blocks, T', T'', issue W
+//     warps 12-15   T's other blocks, T', T''
 //     warps 16-19   load V, W to shared memory, the outputs to global memory
 //     warps 20-27   the state's hi + lo operand and its decay, U's operands, S Q^T's factors
 // The state stays in tensor memory as the sum that dS is added to.  The chain for a chunk is
@@ -68,7 +68,8 @@ constexpr int SC_REL = 0, SC_BETA = 64, SC_BG = 128;  // (gamma_r - gamma_j) log
                                              // -beta e^gamma
 constexpr int SC_COL = 192;                  // e^(gamma_r - gamma_j) for r = 16, 32, 48 and j < r
 constexpr int SC_EG = 288, SC_FD = 352;      // scale e^gamma, e^(gamma_63 - gamma)
-constexpr int kGates = 416 * 4;
+constexpr int SC_JOB = 416;                  // the chunk itself (Job)
+constexpr int kGates = 432 * 4;
 constexpr int OFF_MASK = OFF_SC + kKQ * kGates;  // fp32 [17][16]: row n is 0 in its first n columns, -10^30 after them
 constexpr int OFF_EL = OFF_MASK + 17 * 64;      // [kDecays] e^gamma_63
 constexpr int OFF_SLOT = OFF_EL + kDecays * 4;
@@ -76,7 +77,7 @@ constexpr int OFF_BAR = OFF_SLOT + 16;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
     B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
-    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_PROBE, B_COUNT
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_PROBE, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -133,14 +134,28 @@ struct Walk {
             ++s;
         }
     }
+    // what an item's parameters are made of, asked for one item ahead: nothing waits for it until then
+    struct Raw {
+        int lo, hi, slot, fresh;
+    };
+    __device__ __forceinline__ Raw raw(const Params &p) const {
+        Raw r = {0, 0, b, 0};
+        if (idx < p.items) {
+            r.lo = __ldg(p.offsets + b);
+            r.hi = __ldg(p.offsets + b + 1);
+            if (p.slots) r.slot = __ldg(p.slots + b);
+            if (p.fresh) r.fresh = __ldg(p.fresh + b);
+        }
+        return r;
+    }
     template <bool OUT>
-    __device__ __forceinline__ Item item(const Params &p) const {
+    __device__ __forceinline__ Item item(const Params &p, const Raw &raw) const {
         Item x;
         x.h = h;
         x.hk = p.group_inv ? __umulhi((uint32_t)h, p.group_inv) : h;
-        x.lo = __ldg(p.offsets + b);
-        x.n = __ldg(p.offsets + b + 1) - x.lo;
-        const int slot = p.slots ? __ldg(p.slots + b) : b;
+        x.lo = raw.lo;
+        x.n = raw.hi - raw.lo;
+        const int slot = raw.slot;
         x.err = 0;
         if (x.n < 0 || x.lo < 0 || x.lo + x.n > p.total) x.err = GDN_DEV_BAD_DESC;
         else if (x.n > p.max_tokens) x.err = GDN_DEV_TOO_MANY;
@@ -151,7 +166,7 @@ struct Walk {
         const int seg = x.unit ? s - (p.segs - 2) : s, off = seg * p.seg;
         const bool last = x.n - off <= p.seg, one = x.n <= p.seg;
         x.skip = x.err || (seg > 0 && x.n <= off) || (!OUT && last);
-        const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
+        const bool zero = !p.S0 || raw.fresh != 0;
         if (OUT) {
             x.from = one ? (zero ? nullptr : p.S0 + state) : ws + seg * (kD * kD);
             x.to = last ? p.S_new + state : nullptr;
@@ -166,8 +181,29 @@ struct Walk {
     }
 };
 
-// Bounded wait: about a second; after a first one that ran out the others only look once, so that a
-// block whose pipeline broke still ends soon.  A phase is waited for before the one after it can
+// A chunk as the roles see it, put beside its gates by the warp that makes them.
+struct Job {
+    int tok, nv, h, flags;  // its first token; tokens of the segment from there on; value head; kFirst ..
+    const float *from;      // state before the segment, null for zero
+    float *to;              // place for the state after it, null for none
+};
+constexpr int kFirst = 1, kLast = 2, kUnit = 4, kEnd = 8;  // first, last chunk of a segment; from the identity; no more
+
+// A chunk's number, its place in the rings of three, and the parity of their round.
+struct Ring {
+    int cc = 0, kq = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next() {
+        ++cc;
+        if (++kq == kKQ) {
+            kq = 0;
+            ph ^= 1;
+        }
+    }
+};
+
+// Bounded wait: about a second; after a first one that ran out the others only look once, and the role
+// ends before its next chunk, so that a block whose pipeline broke still ends soon.  A phase is waited for before the one after it can
 // complete, or the parity would alias: what runs two chunks ahead or behind has two barriers.
 __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
     const uint32_t limit = ok ? 1u << 19 : 1u;
@@ -185,6 +221,14 @@ __device__ __forceinline__ void wait(uint64_t *bar, uint32_t parity, bool &ok) {
 __device__ __forceinline__ void wwait(uint64_t *bar, uint32_t parity, bool &ok) {
     wait(bar, parity, ok);
     __syncwarp();
+}
+
+// the warp's next chunk, or false after the last one (or a wait that ran out)
+__device__ __forceinline__ bool take(const uint8_t *sm, uint64_t *bar, const Ring &r, Job &j, bool &ok) {
+    wait(&bar[B_GATES + r.kq], r.ph, ok);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    j = *reinterpret_cast<const Job *>(sm + OFF_SC + r.kq * kGates + SC_JOB * 4);
+    return !(j.flags & kEnd);
 }
 
 __device__ __forceinline__ uint32_t sw(int row, int chunk16) {  // byte offset in a tile of 128-byte rows
@@ -369,6 +413,18 @@ __device__ __forceinline__ void dd_add(float &ah, float &al, float bh, float bl)
     al = __fsub_rn(e, __fsub_rn(ah, s));
 }
 
+// zeros in rows nv.. of a tile's two halves, `apart` bytes from each other, for the tensor core to read
+__device__ __forceinline__ void zero_tail(uint8_t *tile, int apart, int nv, int lane) {
+    if (nv >= kC) return;
+#pragma unroll 1
+    for (int i = nv * 8 + lane; i < kC * 8; i += 32) {
+        *reinterpret_cast<uint4 *>(tile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(tile + apart + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // OUT: outputs and final states; otherwise the first pass over segments
 template <bool OUT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -384,7 +440,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     }
     if (tid == 0) {
         for (int i = 0; i < B_COUNT; ++i) {
-            const bool four = i == B_T || i == B_WRDY || i == B_OFREE || i == B_SQRD || (i >= B_SCFREE && i < B_GATES) ||
+            const bool four = i == B_T || i == B_MID || i == B_WRDY || i == B_OFREE || i == B_SQRD || (i >= B_SCFREE && i < B_GATES) ||
                               (i >= B_BLKFREE && i < B_DIAG);
             const uint32_t n = four ? 4 : i == B_GFREE ? (OUT ? 6 : 3) : i >= B_BLK && i < B_BLKFREE ? (OUT ? 7 : 4)
                                : i == B_S || i == B_UST ? 8 : i == B_TFREE ? 2 : 1;
@@ -408,66 +464,47 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
     const uint32_t tmem = *slot;
     bool ok = true;
     float *el = reinterpret_cast<float *>(sm + OFF_EL);
-    Walk at;
-    at.idx = blockIdx.x;
-    at.h = at.idx % p.hv_n;
-    at.b = at.idx / p.hv_n % p.batch;
-    at.s = at.idx / p.hv_n / p.batch;
+    Ring at;
+    Job j;
 
     if (warp < 4) {
         const uint32_t lead = elect();
         const uint32_t tm = uniform(tmem);
-        if (warp == 0 && lane == 0) {
-            // ---------------------------------------------------------------- loads
-            if (p.probe > 0) ok = mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe);
-            bool go = true;  // the pipeline's own waits
-            int cc = 0, kq = 0;
-            for (; at.idx < p.items && go; at.next(p)) {
-                const Item x = at.template item<OUT>(p);
-                if (OUT && x.err) flag(p.status, x.err);
-                for (int c = 0; c < x.chunks && go; ++c) {
-                    uint8_t *dst = sm + OFF_KQ + kq * 4 * kTile;
-                    if (cc >= kKQ) wait(&bar[B_EMPTY + kq], (cc / kKQ - 1) & 1, go);
-                    if (!go) break;  // nothing is loaded over a stage that may be in use
-                    mbar_arrive_expect_tx(&bar[B_FULL + kq], (OUT ? 4 : 2) * kTile);
-                    for (int half = 0; half < 2; ++half) {
-                        tma_load_3d(dst + half * 2 * kTile, &tmK, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
-                        if (OUT) tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + kq], half * 64, x.hk, x.lo + c * kC);
-                    }
-                    ++cc;
-                    kq = kq + 1 == kKQ ? 0 : kq + 1;
-                }
+        if (warp == 0) {
+            // ---------------------------------------------------------------- W^T = K^T T''^T
+            const uint32_t id = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
+            const uint32_t d_t = uniform(desc_lo(sm + OFF_T, 0));
+            if (p.probe > 0 && lead && !mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe)) flag(p.status, GDN_DEV_TIMEOUT);
+            __syncwarp();
+            for (; take(sm, bar, at, j, ok); at.next()) {
+                wwait(&bar[B_T], at.cc & 1, ok);
+                if (at.cc > 0) wwait(&bar[B_WRDY], (at.cc - 1) & 1, ok);  // the W before it has been read
+                tc_fence_after();
+                const uint32_t d_k = uniform(desc_lo(sm + OFF_KQ + at.kq * 4 * kTile, 2 * kTile));
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ss(lead, tm + TM_W, d_k + ks * 128, d_t + (2 + part) * (kTile >> 4) + ks * 2, id, part + ks > 0);
+                commit(lead, &bar[B_W]);
+                commit(lead, &bar[B_TFREE]);
             }
-            // every load has landed before the block ends, whatever became of its reader
-            for (int i = 0; i < kKQ && i < cc; ++i) mbar_wait(&bar[B_FULL + i], ((cc - 1 - i) / kKQ) & 1, 1u << 16);
-            ok = ok && go;
         } else if (warp == 1) {
             // ---------------------------------------------------------------- [K;Q] K^T
             const uint32_t id = idesc_bf16_f32(128, kC);
-            int cc = 0, kq = 0;
-            for (; at.idx < p.items; at.next(p)) {
-                const Item x = at.template item<OUT>(p);
-                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
-                    uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
-                    wwait(&bar[B_FULL + kq], (cc / kKQ) & 1, ok);
-                    if (cc > 0) wwait(&bar[B_GFREE], (cc - 1) & 1, ok);
-                    const int nv = x.n - c * kC;
-                    if (nv < kC) {  // keys past the prompt's end: zero, whatever the next prompt holds
-                        for (int half = 0; half < 2; ++half)
-                            _Pragma("unroll 1") for (int i = nv * 8 + lane; i < kC * 8; i += 32)
-                                *reinterpret_cast<uint4 *>(kt + half * 2 * kTile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                    }
-                    tc_fence_after();
-                    const uint32_t d = uniform(desc_lo(kt, 0));
+            for (; take(sm, bar, at, j, ok); at.next()) {
+                uint8_t *kt = sm + OFF_KQ + at.kq * 4 * kTile;
+                wwait(&bar[B_FULL + at.kq], at.ph, ok);
+                if (at.cc > 0) wwait(&bar[B_GFREE], (at.cc - 1) & 1, ok);
+                zero_tail(kt, 2 * kTile, j.nv, lane);  // keys past the prompt's end, whatever the next prompt holds
+                tc_fence_after();
+                const uint32_t d = uniform(desc_lo(kt, 0));
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t o = ((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4;
-                        mma_ss(lead, tm + TM_G, d + o, d + o, id, ks > 0);
-                    }
-                    commit(lead, &bar[B_G]);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t o = ((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4;
+                    mma_ss(lead, tm + TM_G, d + o, d + o, id, ks > 0);
                 }
+                commit(lead, &bar[B_G]);
             }
         } else if (warp == 2) {
             // ---------------------------------------------------------------- the chain's products
@@ -475,31 +512,18 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t id_sw = idesc_bf16_f32(128, kC) | (1u << 16); // S (tensor memory) W^T, W MN-major
             const uint32_t id_k = idesc_bf16_f32(128, kC);               // K-major right-hand side
             const uint32_t id_ds = idesc_bf16_f32(128, kD) | (1u << 16); // U' K, K MN-major
-            uint8_t *vt = sm + OFF_V;
-            const uint32_t d_v = uniform(desc_lo(vt, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
-            int cc = 0, kq = 0;
-            Item nx = {};
-            if (at.idx < p.items) nx = at.template item<OUT>(p);
-            while (at.idx < p.items) {
-                const Item x = nx;  // the next one's parameters arrive meanwhile
-                at.next(p);
-                if (at.idx < p.items) nx = at.template item<OUT>(p);
-                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+            const uint32_t d_v = uniform(desc_lo(sm + OFF_V, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
+            for (; take(sm, bar, at, j, ok); at.next()) {
+                    const int cc = at.cc, kq = at.kq;
+                    const bool unit = !OUT && (j.flags & kUnit);
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
-                    const int nv = x.n - c * kC;
-                    if (nv < kC) {
-                        for (int half = 0; half < 2; ++half)
-                            _Pragma("unroll 1") for (int i = nv * 8 + lane; i < kC * 8; i += 32)
-                                *reinterpret_cast<uint4 *>(vt + half * kTile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
+                    zero_tail(sm + OFF_V, kTile, j.nv, lane);
                     // U^T = V^T T'^T, once the U before it has been read
                     wwait(&bar[B_T], cc & 1, ok);
                     if (OUT && cc > 0) wwait(&bar[B_O], (cc - 1) & 1, ok);
                     tc_fence_after();
-                    if (!x.unit) {
+                    if (!unit) {
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -516,7 +540,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             mma_ts(lead, tm + TM_U, tm + TM_SHI + (part & 1) * (TM_SLO - TM_SHI) + ks * 8,
-                                   d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, OUT || !x.unit || part + ks > 0);
+                                   d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, !unit || part + ks > 0);
                     commit(lead, &bar[B_U]);
                     const uint32_t d_q = uniform(desc_lo(kt + kTile, 0)), d_k = uniform(desc_lo(kt, 2 * kTile));
                     if (OUT) {  // O^T = S Q^T
@@ -547,13 +571,33 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         commit(lead, &bar[B_YFREE + kq]);
                     }
                     commit(lead, &bar[B_EMPTY + kq]);
-                }
             }
         } else if (warp == 3) {
-            // ---------------------------------------------------------------- gates, ahead of everything
-            int cc = 0, kq = 0;
-            for (; at.idx < p.items; at.next(p)) {
-                const Item x = at.template item<OUT>(p);
+            // ---------------------------------------------------------------- items, gates, K and Q
+            Walk walk;
+            walk.idx = blockIdx.x;
+            walk.h = walk.idx % p.hv_n;
+            walk.b = walk.idx / p.hv_n % p.batch;
+            walk.s = walk.idx / p.hv_n / p.batch;
+            // a place in the rings was last read by T and the chain of three chunks before
+            auto place = [&]() {
+                if (at.cc >= kKQ) {
+                    wwait(&bar[B_SCFREE + at.kq], at.ph ^ 1, ok);
+                    wwait(&bar[B_EMPTY + at.kq], at.ph ^ 1, ok);
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                return reinterpret_cast<float *>(sm + OFF_SC + at.kq * kGates);
+            };
+            Walk::Raw raw = walk.raw(p);
+            while (ok && walk.idx < p.items) {
+                const Item x = walk.template item<OUT>(p, raw);
+                walk.next(p);
+                raw = walk.raw(p);
+                if (OUT && lane == 0 && x.err) flag(p.status, x.err);
+                if (x.chunks == 0 && !x.skip && x.from != x.to) {  // no tokens: the state as it is
+                    for (int i = lane; i < kD * kD / 4; i += 32)
+                        reinterpret_cast<float4 *>(x.to)[i] = x.from ? reinterpret_cast<const float4 *>(x.from)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
                 float g[2], b[2];  // of tokens 2 lane, 2 lane + 1 of the next chunk
                 auto fetch = [&](int c) {
 #pragma unroll
@@ -567,7 +611,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     }
                 };
                 if (x.chunks > 0) fetch(0);
-                for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+                for (int c = 0; c < x.chunks && ok; ++c, at.next()) {
                     // gamma: a scan in pairs of floats, so that a decay that forgets everything leaves the
                     // differences between later tokens as they were.  e^-200 is zero, whatever lies below it
                     const float g0 = g[0] < -200.f ? -200.f : g[0], g1 = g[1] < -200.f ? -200.f : g[1];
@@ -607,13 +651,27 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         }
                     }
                     const float last = __expf(hl + ll);
-                    // the place was last read by T and the chain of three chunks before
-                    if (cc >= kKQ) {
-                        wwait(&bar[B_SCFREE + kq], (cc / kKQ - 1) & 1, ok);
-                        wwait(&bar[B_EMPTY + kq], (cc / kKQ - 1) & 1, ok);
+                    float *sc = place();
+                    if (!ok) break;
+                    if (lane == 0) {
+                        uint8_t *dst = sm + OFF_KQ + at.kq * 4 * kTile;
+                        mbar_arrive_expect_tx(&bar[B_FULL + at.kq], (OUT ? 4 : 2) * kTile);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            tma_load_3d(dst + half * 2 * kTile, &tmK, &bar[B_FULL + at.kq], half * 64, x.hk, x.lo + c * kC);
+                            if (OUT) tma_load_3d(dst + half * 2 * kTile + kTile, &tmQ, &bar[B_FULL + at.kq], half * 64, x.hk, x.lo + c * kC);
+                        }
+                        Job *job = reinterpret_cast<Job *>(sc + SC_JOB);
+                        job->tok = x.lo + c * kC;
+                        job->nv = x.n - c * kC;
+                        job->h = x.h;
+                        job->flags = (c == 0 ? kFirst : 0) | (c == x.chunks - 1 ? kLast : 0) | (x.unit ? kUnit : 0);
+                        job->from = x.from;
+                        job->to = x.to;
+                        el[at.cc & (kDecays - 1)] = last;
                     }
-                    float *sc = reinterpret_cast<float *>(sm + OFF_SC + kq * kGates);
-                    auto put = [&](int at, float v0, float v1) { *reinterpret_cast<float2 *>(sc + at + 2 * lane) = make_float2(v0, v1); };
+                    __syncwarp();
+                    auto put = [&](int to, float v0, float v1) { *reinterpret_cast<float2 *>(sc + to + 2 * lane) = make_float2(v0, v1); };
                     put(SC_REL, rel[0], rel[1]);
                     put(SC_BETA, b0, b1);
                     put(SC_BG, bg[0], bg[1]);
@@ -623,11 +681,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int q = 1; q < 4; ++q) {
                         if (lane < 8 * q) put(SC_COL + 8 * q * (q - 1), rc[0][q], rc[1][q]);
                     }
-                    if (lane == 0) el[cc & (kDecays - 1)] = last;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar[B_GATES + kq]);
+                    if (lane == 0) mbar_arrive(&bar[B_GATES + at.kq]);
                 }
             }
+            float *sc = place();
+            if (ok) {
+                if (lane == 0) {
+                    reinterpret_cast<Job *>(sc + SC_JOB)->flags = kEnd;
+                    mbar_arrive(&bar[B_GATES + at.kq]);
+                }
+            }
+            // every load has landed before the block ends, whatever became of its reader
+            for (int i = 0; i < kKQ && i < at.cc; ++i) mbar_wait(&bar[B_FULL + i], ((at.cc - 1 - i) / kKQ) & 1, 1u << 16);
         }
     } else if (warp < 12 && (warp < 8 || (quad & 1))) {
         // -------------------------------------------------------------------- A, Y: 32 rows, 32 columns a warp
@@ -637,18 +703,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int last = (i & 15) + (is_y ? 1 : 0);  // columns of the own block that count
         const uint32_t lanes = (uint32_t)(quad * 32) << 16;
         const float *mask = reinterpret_cast<const float *>(sm + OFF_MASK);
-        int cc = 0, kq = 0;
-        for (; at.idx < p.items && (OUT || !is_y); at.next(p)) {
-            const Item x = at.template item<OUT>(p);
-            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+        for (; (OUT || !is_y) && take(sm, bar, at, j, ok); at.next()) {
+                const int cc = at.cc, kq = at.kq;
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
                 float *diag = reinterpret_cast<float *>(blocks + 6 * 1024);
-                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
                 const f2 rel = pair(-sc[SC_REL + i], -sc[SC_REL + i]);
                 const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * exp2_approx(-sc[SC_REL + i]);
                 if (cc >= 2) wwait(&bar[B_BLKFREE + (cc & 1)], (cc / 2 - 1) & 1, ok);
-                if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], (cc / kKQ - 1) & 1, ok);
+                if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], at.ph ^ 1, ok);
                 wwait(&bar[B_G], cc & 1, ok);
                 tc_fence_after();
                 uint32_t nr[16];  // the next 16 columns
@@ -699,14 +762,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                                 for (int q = 0; q < 4; ++q)
                                     *reinterpret_cast<ulonglong2 *>(diag + diag_at(i, q)) = make_ulonglong2(m[2 * q], m[2 * q + 1]);
                             } else {
-                                uint8_t *at = blocks + (own * (own - 1) / 2 + cb) * 1024;
+                                uint8_t *to = blocks + (own * (own - 1) / 2 + cb) * 1024;
 #pragma unroll
                                 for (int q = 0; q < 2; ++q) {
                                     uint32_t hi[4], lo[4];
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) split2(m[4 * q + e], hi[e], lo[e]);
-                                    *reinterpret_cast<uint4 *>(at + blk(i & 15, q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                                    *reinterpret_cast<uint4 *>(at + 512 + blk(i & 15, q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                    *reinterpret_cast<uint4 *>(to + blk(i & 15, q)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                    *reinterpret_cast<uint4 *>(to + 512 + blk(i & 15, q)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                                 }
                             }
                         }
@@ -722,15 +785,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (!is_y && (quad == 0 || cb0 == 2)) mbar_arrive(&bar[B_DIAG + quad * 2 + (cc & 1)]);
                     if (quad != 0) mbar_arrive(&bar[B_BLK + (cc & 1)]);
                 }
-            }
         }
     } else if (warp < 12) {
         // -------------------------------------------------------------------- T's diagonal blocks, two a warp
         // Lane l row l mod 16 of one.  From T (I + A) = I, t_j = -A_rj - sum_{j < k < r} t_k A_kj, for falling k
-        int cc = 0;
-        for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.template item<OUT>(p);
-            for (int c = 0; c < x.chunks; ++c, ++cc) {
+        for (; take(sm, bar, at, j, ok); at.next()) {
+                const int cc = at.cc;
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
                 const float *diag = reinterpret_cast<const float *>(blocks + 6 * 1024);
                 wwait(&bar[B_DIAG + quad + (cc & 1)], (cc / 2) & 1, ok);
@@ -771,17 +831,13 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_BLK + (cc & 1)]);
-            }
         }
     } else if (warp < 16) {
         // -------------------------------------------------------------------- the rest of T, T', T''
         const uint32_t tt = smem_u32(sm + OFF_T);
-        const uint32_t id_w = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
         const uint32_t lane_at = blk((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4);
-        int cc = 0, kq = 0;
-        for (; at.idx < p.items; at.next(p)) {
-            const Item x = at.template item<OUT>(p);
-            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
+        for (; take(sm, bar, at, j, ok); at.next()) {
+                const int cc = at.cc, kq = at.kq;
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks;
                 const uint32_t base = smem_u32(blocks) + lane_at;
@@ -789,7 +845,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 // By blocks of 32, T21 = -T22 A21 T11: two warps take the two inner blocks T10 and T32 (into the
                 // places of A10 and A32) and the right half of T21, two its left half
                 wwait(&bar[B_BLK + (cc & 1)], (cc / 2) & 1, ok);
-                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
                 float t0[2][4] = {}, t1[2][4] = {};
                 {
                     float a[2][4] = {}, b[2][4] = {};
@@ -805,7 +860,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     } else {
                         mul_block(b, f.hi, f.lo, base + (quad == 2 ? 2 : 4) * 1024);
                     }
-                    named_sync(2, 128);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar[B_MID]);
+                    wwait(&bar[B_MID], cc & 1, ok);
                     if (quad & 1) {
                         load_left(base + 5 * 1024, f);
                         mul_block(b, f.hi, f.lo, base + 2 * 1024);
@@ -840,21 +897,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     mbar_arrive(&bar[B_SCFREE + kq]);
                     mbar_arrive(&bar[B_BLKFREE + (cc & 1)]);
                 }
-                if (quad == 3) {  // W^T = K^T T''^T, once the W before it has been read
-                    wwait(&bar[B_T], cc & 1, ok);
-                    if (cc > 0) wwait(&bar[B_WRDY], (cc - 1) & 1, ok);
-                    tc_fence_after();
-                    const uint32_t d_k = uniform(desc_lo(sm + OFF_KQ + kq * 4 * kTile, 2 * kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0));
-                    const uint32_t tm = uniform(tmem), lead = elect();
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ss(lead, tm + TM_W, d_k + ks * 128, d_t + (((2 + part) * kTile + ks * 32) >> 4), id_w, part > 0 || ks > 0);
-                    commit(lead, &bar[B_W]);
-                    commit(lead, &bar[B_TFREE]);
-                }
-            }
         }
     } else if (warp < 20) {
         // -------------------------------------------------------------------- W to shared memory, outputs
@@ -907,17 +949,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
         };
         int loads = 0;
-        int cc = 0;
-        // the chunk in work (x, c), and the one before it, whose outputs are still to come
-        Item x = {};
-        int c = 0, kq = 0, p_tok = 0, p_nv = 0, p_h = 0;
-        while (true) {
-            while (c == x.chunks && at.idx < p.items) {
-                x = at.template item<OUT>(p);
-                c = 0;
-                at.next(p);
-            }
-            const bool more = c < x.chunks;
+        int p_tok = 0, p_nv = 0, p_h = 0;  // the chunk before, whose outputs are still to come
+        for (bool more = true; more; at.next()) {
+            more = take(sm, bar, at, j, ok);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const int cc = at.cc;
             bool w_first = false;
             if (more) {
                 if (cc > 0) wwait(&bar[B_U], (cc - 1) & 1, ok);  // the chunk before has its U: V and W have been read
@@ -925,7 +961,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     ++loads;
                     mbar_arrive_expect_tx(&bar[B_VFULL], 2 * kTile);
                     for (int half = 0; half < 2; ++half)
-                        tma_load_3d(sm + OFF_V + half * kTile, &tmV, &bar[B_VFULL], half * 64, x.h, x.lo + c * kC);
+                        tma_load_3d(sm + OFF_V + half * kTile, &tmV, &bar[B_VFULL], half * 64, j.h, j.tok);
                 }
                 __syncwarp();
                 w_first = __shfl_sync(0xffffffffu, mbar_test_wait(&bar[B_W], cc & 1), 0);
@@ -934,7 +970,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 #pragma unroll 1
             for (int step = 0; step < 2; ++step) {
                 if ((step == 0) != w_first) {
-                    if (OUT && cc > 0) factors(cc - 1, kq == 0 ? kKQ - 1 : kq - 1);
+                    if (OUT && cc > 0) factors(cc - 1, at.kq == 0 ? kKQ - 1 : at.kq - 1);
                 } else if (more) {
                     wwait(&bar[B_W], cc & 1, ok);
                     tc_fence_after();
@@ -961,59 +997,45 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 }
             }
             if (OUT && cc > 0) outputs(cc - 1, p_tok, p_nv, p_h);
-            if (!more) break;
-            p_tok = x.lo + c * kC;
-            p_nv = x.n - c * kC;
-            p_h = x.h;
-            ++c;
-            ++cc;
-            kq = kq + 1 == kKQ ? 0 : kq + 1;
+            p_tok = j.tok;
+            p_nv = j.nv;
+            p_h = j.h;
         }
         if (loads > 0) mbar_wait(&bar[B_VFULL], (loads - 1) & 1, 1u << 16);  // landed, read or not
     } else {
         // -------------------------------------------------------------------- the state
         const int row = quad * 32 + lane, half = (warp - 20) >> 2;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        int cc = 0, kq = 0;
-        Item nx = {};
-        if (at.idx < p.items) nx = at.template item<OUT>(p);
-        while (at.idx < p.items) {
-            const Item x = nx;  // the next one's parameters arrive meanwhile
-            at.next(p);
-            if (at.idx < p.items) nx = at.template item<OUT>(p);
-            if (x.skip) continue;
-            const int64_t mine = row * kD + half * 64;
-            // S into tensor memory, whose last reader was this thread (or, without tokens, straight on)
+        const int64_t mine = row * kD + half * 64;
+        for (; take(sm, bar, at, j, ok); at.next()) {
+            const int cc = at.cc, kq = at.kq;
+            if (j.flags & kFirst) {
+                // S into tensor memory, whose last reader was this thread
 #pragma unroll 1
-            for (int j = 0; j < 64; j += 32) {
-                f2 v[4][4];
+                for (int i = 0; i < 64; i += 32) {
+                    f2 v[4][4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    load8(x.from ? x.from + mine + j + 8 * q : nullptr, v[q]);
-                    if (!OUT && x.unit && (row >> 3) == (half * 64 + j) / 8 + q) {
+                    for (int q = 0; q < 4; ++q) {
+                        load8(j.from ? j.from + mine + i + 8 * q : nullptr, v[q]);
+                        if (!OUT && (j.flags & kUnit) && (row >> 3) == (half * 64 + i) / 8 + q) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (((row & 7) >> 1) == e) v[q][e] = (row & 1) ? pair(0.f, 1.f) : pair(1.f, 0.f);
+                            for (int e = 0; e < 4; ++e)
+                                if (((row & 7) >> 1) == e) v[q][e] = (row & 1) ? pair(0.f, 1.f) : pair(1.f, 0.f);
+                        }
                     }
-                }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (x.chunks == 0) {
-                        if (x.to) store8(x.to + mine + j + 8 * q, v[q]);
-                    } else {
+                    for (int q = 0; q < 4; ++q) {
                         uint32_t r[8];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) unpair(v[q][e], r[2 * e], r[2 * e + 1]);
-                        tmem_st8(lanes + TM_DS + half * 64 + j + 8 * q, r);
+                        tmem_st8(lanes + TM_DS + half * 64 + i + 8 * q, r);
                     }
                 }
+                tmem_wait_st();
+            } else {
+                wwait(&bar[B_UPD], (cc - 1) & 1, ok);  // the chunk before is in the sum, and U' has been read
             }
-            if (x.chunks == 0) continue;
-            tmem_wait_st();
-            for (int c = 0; c < x.chunks; ++c, ++cc, kq = kq + 1 == kKQ ? 0 : kq + 1) {
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates) + half * 32;
-                if (cc > 0) wwait(&bar[B_UPD], (cc - 1) & 1, ok);  // the chunk before is in the sum, and U' has been read
-                wwait(&bar[B_GATES + kq], (cc / kKQ) & 1, ok);
                 tc_fence_after();
                 // S as hi + lo, and its sum times e^gamma_63, ready for dS
                 const f2 decay = pair(el[cc & (kDecays - 1)], el[cc & (kDecays - 1)]);
@@ -1060,20 +1082,20 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[B_UST]);
-            }
-            wwait(&bar[B_UPD], (cc - 1) & 1, ok);
+            if (!(j.flags & kLast)) continue;
+            wwait(&bar[B_UPD], cc & 1, ok);
             tc_fence_after();
 #pragma unroll 1
-            for (int j = 0; x.to && j < 64; j += 16) {
+            for (int i = 0; j.to && i < 64; i += 16) {
                 uint32_t r[16];
-                tmem_ld16_nowait(lanes + TM_DS + half * 64 + j, r);
+                tmem_ld16_nowait(lanes + TM_DS + half * 64 + i, r);
                 tmem_wait_ld_into(r);
                 f2 v[4];
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = pair(r[8 * q + 2 * e], r[8 * q + 2 * e + 1]);
-                    store8(x.to + mine + j + 8 * q, v);
+                    store8(j.to + mine + i + 8 * q, v);
                 }
             }
         }
