@@ -73,11 +73,12 @@ constexpr int kGates = 432 * 4;
 constexpr int OFF_MASK = OFF_SC + kKQ * kGates;  // fp32 [17][16]: row n is 0 in its first n columns, -10^30 after them
 constexpr int OFF_EL = OFF_MASK + 17 * 64;      // [kDecays] e^gamma_63
 constexpr int OFF_SLOT = OFF_EL + kDecays * 4;
-constexpr int OFF_BAR = OFF_SLOT + 16;
+constexpr int OFF_NEXT = OFF_SLOT + 16;      // answer to a request for the next item
+constexpr int OFF_BAR = OFF_NEXT + 16;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
     B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
-    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_PROBE, B_COUNT
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_NEXT, B_PROBE, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -92,7 +93,6 @@ constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32;
 struct Params {
     int hk_n, hv_n, total, max_tokens, n_states, batch, items, probe;
     int seg, segs;                  // tokens of a segment, a multiple of 64; segments a prompt can have
-    int step_h, step_b, step_s;     // blocks of the grid, in heads, requests and slices
     uint32_t group_inv;             // ceil(2^32 / heads that share a key head), 0 for one
     float scale;
     const int32_t *offsets, *slots, *fresh;
@@ -116,36 +116,25 @@ struct Item {
     float *to;          // where the one after it goes, null for nowhere
 };
 
-// a block's items: (slice, request, head), a grid apart.  A slice is a segment; in the first pass, the slices
+// Item number idx of the grid: (slice, request, head).  A slice is a segment; in the first pass, the slices
 // from segs - 1 on are segments 1.. from the identity.
 struct Walk {
     int idx, h, b, s;
-    __device__ __forceinline__ void next(const Params &p) {
-        idx += gridDim.x;
-        h += p.step_h;
-        b += p.step_b;
-        s += p.step_s;
-        if (h >= p.hv_n) {
-            h -= p.hv_n;
-            ++b;
-        }
-        if (b >= p.batch) {
-            b -= p.batch;
-            ++s;
-        }
+    __device__ __forceinline__ void set(const Params &p, int i) {
+        idx = i;
+        const int u = (unsigned)i / (unsigned)p.hv_n;
+        h = i - u * p.hv_n;
+        s = (unsigned)u / (unsigned)p.batch;
+        b = u - s * p.batch;
     }
-    // what an item's parameters are made of, asked for one item ahead: nothing waits for it until then
+    // what an item's parameters are made of
     struct Raw {
         int lo, hi, slot, fresh;
     };
     __device__ __forceinline__ Raw raw(const Params &p) const {
-        Raw r = {0, 0, b, 0};
-        if (idx < p.items) {
-            r.lo = __ldg(p.offsets + b);
-            r.hi = __ldg(p.offsets + b + 1);
-            if (p.slots) r.slot = __ldg(p.slots + b);
-            if (p.fresh) r.fresh = __ldg(p.fresh + b);
-        }
+        Raw r = {__ldg(p.offsets + b), __ldg(p.offsets + b + 1), b, 0};
+        if (p.slots) r.slot = __ldg(p.slots + b);
+        if (p.fresh) r.fresh = __ldg(p.fresh + b);
         return r;
     }
     template <bool OUT>
@@ -515,7 +504,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             const uint32_t d_v = uniform(desc_lo(sm + OFF_V, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
             for (; take(sm, bar, at, j, ok); at.next()) {
                     const int cc = at.cc, kq = at.kq;
-                    const bool unit = !OUT && (j.flags & kUnit);
+                    const bool unit = !OUT && (j.flags & kUnit), zero = (j.flags & kFirst) && !j.from && !unit;
                     uint8_t *kt = sm + OFF_KQ + kq * 4 * kTile;
                     wwait(&bar[B_VFULL], cc & 1, ok);
                     zero_tail(sm + OFF_V, kTile, j.nv, lane);
@@ -535,20 +524,24 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     wwait(&bar[B_WRDY], cc & 1, ok);
                     wwait(&bar[B_S], cc & 1, ok);
                     tc_fence_after();
+                    if (!zero) {  // from zero, S W^T and S Q^T are left out
 #pragma unroll 1
                     for (int part = 0; part < 3; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             mma_ts(lead, tm + TM_U, tm + TM_SHI + (part & 1) * (TM_SLO - TM_SHI) + ks * 8,
                                    d_w + (part >> 1) * (2 * kTile >> 4) + ks * 128, id_sw, !unit || part + ks > 0);
+                    }
                     commit(lead, &bar[B_U]);
                     const uint32_t d_q = uniform(desc_lo(kt + kTile, 0)), d_k = uniform(desc_lo(kt, 2 * kTile));
                     if (OUT) {  // O^T = S Q^T
                         if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
                         tc_fence_after();
+                        if (!zero) {
 #pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
+                            for (int ks = 0; ks < 8; ++ks)
+                                mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
+                        }
                         commit(lead, &bar[B_SQ]);
                     }
                     // S += U'^T K
@@ -558,7 +551,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, true);
+                            mma_ts(lead, tm + TM_DS, tm + TM_UHI + part * (TM_ULO - TM_UHI) + ks * 8, d_k + ks * 128, id_ds, !zero || part + ks > 0);
                     commit(lead, &bar[B_UPD]);
                     if (OUT) {  // O^T += U^T Y^T, once S Q^T has its factors
                         wwait(&bar[B_SQRD], cc & 1, ok);
@@ -566,7 +559,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         const uint32_t d_y = uniform(desc_lo(sm + OFF_Y + kq * kTile, 0));
 #pragma unroll
                         for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(lead, tm + TM_O, tm + TM_U + (ks >> 1) * 32 + (ks & 1) * 8, d_y + ((ks * 32) >> 4), id_k, true);
+                            mma_ts(lead, tm + TM_O, tm + TM_U + (ks >> 1) * 32 + (ks & 1) * 8, d_y + ((ks * 32) >> 4), id_k, !zero || ks > 0);
                         commit(lead, &bar[B_O]);
                         commit(lead, &bar[B_YFREE + kq]);
                     }
@@ -574,11 +567,32 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
         } else if (warp == 3) {
             // ---------------------------------------------------------------- items, gates, K and Q
+            // The grid has a block for each item; a running block takes the items of blocks that have not begun (they
+            // are cancelled then), so that prompts of different lengths spread evenly
             Walk walk;
-            walk.idx = blockIdx.x;
-            walk.h = walk.idx % p.hv_n;
-            walk.b = walk.idx / p.hv_n % p.batch;
-            walk.s = walk.idx / p.hv_n / p.batch;
+            walk.set(p, blockIdx.x);
+            uint32_t asked = 0;
+            auto ask = [&]() {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar[B_NEXT], 16);
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                                 ::"r"(smem_u32(sm + OFF_NEXT)), "r"(smem_u32(&bar[B_NEXT])) : "memory");
+                }
+                ++asked;
+            };
+            auto answer = [&]() {  // the next item's number, or -1
+                wwait(&bar[B_NEXT], (asked - 1) & 1, ok);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) return -1;
+                uint32_t got, first;
+                asm volatile("{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+                             "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\t"
+                             "mov.u32 %1, 0;\n\t@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+                             : "=r"(got), "=r"(first) : "r"(smem_u32(sm + OFF_NEXT)) : "memory");
+                fence_proxy_async_smem();  // read, before the next answer is written there
+                __syncwarp();
+                return got ? (int)first : -1;
+            };
             // a place in the rings was last read by T and the chain of three chunks before
             auto place = [&]() {
                 if (at.cc >= kKQ) {
@@ -588,11 +602,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 ok = __all_sync(0xffffffffu, ok);
                 return reinterpret_cast<float *>(sm + OFF_SC + at.kq * kGates);
             };
-            Walk::Raw raw = walk.raw(p);
-            while (ok && walk.idx < p.items) {
-                const Item x = walk.template item<OUT>(p, raw);
-                walk.next(p);
-                raw = walk.raw(p);
+            while (ok && walk.idx >= 0) {
+                const Item x = walk.template item<OUT>(p, walk.raw(p));
+                if (x.chunks == 0) ask();
                 if (OUT && lane == 0 && x.err) flag(p.status, x.err);
                 if (x.chunks == 0 && !x.skip && x.from != x.to) {  // no tokens: the state as it is
                     for (int i = lane; i < kD * kD / 4; i += 32)
@@ -617,6 +629,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     const float g0 = g[0] < -200.f ? -200.f : g[0], g1 = g[1] < -200.f ? -200.f : g[1];
                     const float b0 = b[0], b1 = b[1];
                     if (c + 1 < x.chunks) fetch(c + 1);
+                    else ask();
                     float h = g0, l = 0.f;
                     dd_add(h, l, g1, 0.f);
 #pragma unroll 1
@@ -684,6 +697,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar[B_GATES + at.kq]);
                 }
+                const int next = ok ? answer() : -1;
+                if (next < 0) break;
+                walk.set(p, next);
             }
             float *sc = place();
             if (ok) {
@@ -694,6 +710,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
             // every load has landed before the block ends, whatever became of its reader
             for (int i = 0; i < kKQ && i < at.cc; ++i) mbar_wait(&bar[B_FULL + i], ((at.cc - 1 - i) / kKQ) & 1, 1u << 16);
+            if (asked > 0) mbar_wait(&bar[B_NEXT], (asked - 1) & 1, 1u << 16);
         }
     } else if (warp < 12 && (warp < 8 || (quad & 1))) {
         // -------------------------------------------------------------------- A, Y: 32 rows, 32 columns a warp
@@ -1009,7 +1026,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const int64_t mine = row * kD + half * 64;
         for (; take(sm, bar, at, j, ok); at.next()) {
             const int cc = at.cc, kq = at.kq;
-            if (j.flags & kFirst) {
+            const bool zero = (j.flags & kFirst) && !j.from && (OUT || !(j.flags & kUnit));  // nothing to split, nor to add to
+            if (zero) {
+            } else if (j.flags & kFirst) {
                 // S into tensor memory, whose last reader was this thread
 #pragma unroll 1
                 for (int i = 0; i < 64; i += 32) {
@@ -1040,7 +1059,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 // S as hi + lo, and its sum times e^gamma_63, ready for dS
                 const f2 decay = pair(el[cc & (kDecays - 1)], el[cc & (kDecays - 1)]);
 #pragma unroll 1
-                for (int j0 = 0; j0 < 64; j0 += 16) {
+                for (int j0 = 0; !zero && j0 < 64; j0 += 16) {
                     uint32_t r[16], hi[8], lw[8];
                     tmem_ld16_nowait(lanes + TM_DS + half * 64 + j0, r);
                     tmem_wait_ld_into(r);
@@ -1211,14 +1230,10 @@ int64_t prefill_tc_workspace(const gdn_prefill_args &a) {
 template <bool OUT>
 cudaError_t launch_pass(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV, Params p, int slices, cudaStream_t stream) {
     p.items = p.batch * p.hv_n * slices;
-    const int grid = std::min(p.items, sm_count());
-    p.step_h = grid % p.hv_n;
-    p.step_b = grid / p.hv_n % p.batch;
-    p.step_s = grid / p.hv_n / p.batch;
     static int have[16];
     cudaError_t e = ensure_smem(prefill_tc_kernel<OUT>, kSmem, have);
     if (e != cudaSuccess) return e;
-    prefill_tc_kernel<OUT><<<(unsigned)grid, kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
+    prefill_tc_kernel<OUT><<<(unsigned)p.items, kThreads, kSmem, stream>>>(tmQ, tmK, tmV, p);
     return cudaGetLastError();
 }
 
