@@ -78,6 +78,8 @@ int gdn_prefill(const gdn_prefill_args *a, void *stream) {
     if (!a->token_offsets || !a->S_new) return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
     if (a->total_tokens > 0 && (!a->q || !a->k || !a->v || !a->g || !a->beta || !a->o))
         return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
+    if ((reinterpret_cast<uintptr_t>(a->S0) | reinterpret_cast<uintptr_t>(a->S_new)) & 15)
+        return fail(GDN_ERR_INVALID_ARG, "S0 and S_new must be 16-byte aligned");
     if (chunked(*a)) {
         const int64_t need = gdn::prefill_tc_workspace(*a);
         if (need > 0 && (!a->workspace || a->workspace_bytes < need))

@@ -15,8 +15,32 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens a tile
+constexpr int kRpt = 1;    // rows a thread has part of
+
+// two fp32 values in a register pair, for the packed fp32 instructions
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float sum(f2 x) {
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+    return a + b;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
 struct Params {
     int hk, hv, dv, total, max_tokens, n_states, slabs;
@@ -32,12 +56,12 @@ struct Params {
 
 template <typename T, typename O, int DK>
 __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
-    constexpr int LPR = DK / 16, kRows = kThreads / LPR;  // rows a block
+    constexpr int LPR = DK / 16, kGroups = kThreads / LPR, kRows = kGroups * kRpt;  // rows a block
     constexpr int kLoadK = kTile * DK / kThreads, kLoadV = kTile * (kRows < 128 ? kRows : 128) / kThreads;
     static_assert(kTile * DK % kThreads == 0, "whole loads");
     constexpr int kCols = kRows < 128 ? kRows : 128;  // value columns a block can use
     __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
-    __shared__ float sv[2][kTile][kCols], so[kTile][kCols], skq[kTile], salpha[kTile], sbeta[kTile];
+    __shared__ float sv[2][kTile][kCols], so[kTile][kCols], skq[kTile], salpha[2][kTile], sbeta[2][kTile];
 
     const int tid = threadIdx.x, sub = tid % LPR, warp = tid >> 5, lane = tid & 31;
     const int slab = blockIdx.x % p.slabs, item = blockIdx.x / p.slabs;
@@ -52,21 +76,28 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         if (tid == 0) flag(p.status, err);
         return;
     }
-    const int lrow = tid / LPR, row = slab * kRows + lrow;
-    const bool live = row < p.dv;
+    const int lrow = tid / LPR;  // and kGroups further on
     const int ncols = min(kCols, p.dv - slab * kRows);
-    const int64_t state = ((int64_t)slot * p.hv + h) * p.dv * DK + (int64_t)row * DK;
-    float s[4][4];
-    const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0) || !live;
+    const int64_t state = (((int64_t)slot * p.hv + h) * p.dv + slab * kRows + lrow) * DK + sub * 4;
+    const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
+    bool live[kRpt];
+    f2 s[kRpt][8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int i = 0; i < kRpt; ++i) {
+        live[i] = lrow + i * kGroups < ncols;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[c][e] = zero ? 0.f : p.S0[state + (c * LPR + sub) * 4 + e];
+        for (int c = 0; c < 4; ++c) {
+            const float *from = p.S0 + state + i * kGroups * DK + c * LPR * 4;
+            const bool z = zero || !live[i];
+            s[i][2 * c] = z ? 0 : pair(from[0], from[1]);
+            s[i][2 * c + 1] = z ? 0 : pair(from[2], from[3]);
+        }
+    }
 
     const T *qb = static_cast<const T *>(p.q) + (int64_t)lo * p.qs + hk * DK;
     const T *kb = static_cast<const T *>(p.k) + (int64_t)lo * p.ks + hk * DK;
     const T *vb = static_cast<const T *>(p.v) + (int64_t)lo * p.vs + h * p.dv + slab * kRows;
-    float rk[kLoadK], rq[kLoadK], rv[kLoadV];
+    float rk[kLoadK], rq[kLoadK], rv[kLoadV], rg = 0.f, rb = 0.f;
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kLoadK; ++i) {
@@ -79,6 +110,10 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         for (int i = 0; i < kLoadV; ++i) {
             const int x = tid + i * kThreads, t = x / kCols, d = x % kCols;
             rv[i] = t0 + t < n && d < ncols ? load_f(vb, (int64_t)(t0 + t) * p.vs + d) : 0.f;
+        }
+        if (tid < kTile && t0 + tid < n) {
+            rg = __ldg(p.g + (int64_t)(lo + t0 + tid) * p.hv + h);
+            rb = __ldg(p.beta + (int64_t)(lo + t0 + tid) * p.hv + h);
         }
     };
     auto put = [&](int buf) {
@@ -93,6 +128,10 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
             const int x = tid + i * kThreads;
             sv[buf][x / kCols][x % kCols] = rv[i];
         }
+        if (tid < kTile) {
+            salpha[buf][tid] = expf(rg);
+            sbeta[buf][tid] = rb;
+        }
     };
     if (n > 0) {
         fetch(0);
@@ -105,40 +144,66 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
             float x = 0.f;
             for (int d = lane; d < DK; d += 32) x = fmaf(sk[buf][t][d], sq[buf][t][d], x);
             x = warp_sum(x);
-            if (lane == 0) {
-                const int64_t at = (int64_t)(lo + t0 + t) * p.hv + h;
-                skq[t] = x;
-                salpha[t] = expf(__ldg(p.g + at));
-                sbeta[t] = __ldg(p.beta + at);
-            }
+            if (lane == 0) skq[t] = x;
         }
         if (t0 + kTile < n) fetch(t0 + kTile);
         __syncthreads();
-        for (int t = 0; t < nt; ++t) {
-            float4 k4[4], q4[4];
-            float xk = 0.f, xq = 0.f;
+        // a token's k and q are read while the one before it is reduced
+        f2 k0[8], q0[8];
+        auto read = [&](int t, f2 (&k)[8], f2 (&q)[8]) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                k4[c] = *reinterpret_cast<const float4 *>(&sk[buf][t][(c * LPR + sub) * 4]);
-                q4[c] = *reinterpret_cast<const float4 *>(&sq[buf][t][(c * LPR + sub) * 4]);
-                xk = fmaf(s[c][0], k4[c].x, fmaf(s[c][1], k4[c].y, fmaf(s[c][2], k4[c].z, fmaf(s[c][3], k4[c].w, xk))));
-                xq = fmaf(s[c][0], q4[c].x, fmaf(s[c][1], q4[c].y, fmaf(s[c][2], q4[c].z, fmaf(s[c][3], q4[c].w, xq))));
+                const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(&sk[buf][t][(c * LPR + sub) * 4]);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sq[buf][t][(c * LPR + sub) * 4]);
+                k[2 * c] = a.x;
+                k[2 * c + 1] = a.y;
+                q[2 * c] = b.x;
+                q[2 * c + 1] = b.y;
+            }
+        };
+        auto step = [&](int t, const f2 (&k)[8], const f2 (&q)[8]) {
+            float xk[kRpt], xq[kRpt];
+#pragma unroll
+            for (int i = 0; i < kRpt; ++i) {
+                f2 a0 = mul2(s[i][0], k[0]), a1 = mul2(s[i][1], k[1]), b0 = mul2(s[i][0], q[0]), b1 = mul2(s[i][1], q[1]);
+#pragma unroll
+                for (int e = 2; e < 8; e += 2) {
+                    a0 = fma2(s[i][e], k[e], a0);
+                    a1 = fma2(s[i][e + 1], k[e + 1], a1);
+                    b0 = fma2(s[i][e], q[e], b0);
+                    b1 = fma2(s[i][e + 1], q[e + 1], b1);
+                }
+                xk[i] = sum(a0) + sum(a1);
+                xq[i] = sum(b0) + sum(b1);
             }
 #pragma unroll
             for (int w = LPR / 2; w > 0; w >>= 1) {
-                xk += __shfl_xor_sync(0xffffffffu, xk, w);
-                xq += __shfl_xor_sync(0xffffffffu, xq, w);
-            }
-            const float alpha = salpha[t];
-            const float u = live ? sbeta[t] * (sv[buf][t][lrow % kCols] - alpha * xk) : 0.f;
-            if (live && sub == 0) so[t][lrow] = p.scale * fmaf(u, skq[t], alpha * xq);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                s[c][0] = fmaf(u, k4[c].x, alpha * s[c][0]);
-                s[c][1] = fmaf(u, k4[c].y, alpha * s[c][1]);
-                s[c][2] = fmaf(u, k4[c].z, alpha * s[c][2]);
-                s[c][3] = fmaf(u, k4[c].w, alpha * s[c][3]);
+                for (int i = 0; i < kRpt; ++i) {
+                    xk[i] += __shfl_xor_sync(0xffffffffu, xk[i], w);
+                    xq[i] += __shfl_xor_sync(0xffffffffu, xq[i], w);
+                }
             }
+            const float alpha = salpha[buf][t], beta = sbeta[buf][t], kq = skq[t];
+            const f2 alpha2 = pair(alpha, alpha);
+#pragma unroll
+            for (int i = 0; i < kRpt; ++i) {
+                const float u = live[i] ? beta * (sv[buf][t][(lrow + i * kGroups) % kCols] - alpha * xk[i]) : 0.f;
+                if (live[i] && sub == 0) so[t][lrow + i * kGroups] = p.scale * fmaf(u, kq, alpha * xq[i]);
+                const f2 u2 = pair(u, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[i][e] = fma2(u2, k[e], mul2(alpha2, s[i][e]));
+            }
+        };
+        read(0, k0, q0);
+#pragma unroll 1
+        for (int t = 0; t < nt; t += 2) {
+            f2 k1[8], q1[8];
+            const bool second = t + 1 < nt;
+            if (second) read(t + 1, k1, q1);
+            step(t, k0, q0);
+            if (t + 2 < nt) read(t + 2, k0, q0);
+            if (second) step(t + 1, k1, q1);
         }
         if (t0 + kTile < n) put(buf ^ 1);
         __syncthreads();
@@ -149,17 +214,21 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         }
         // the next tile's first __syncthreads() stands between these reads and its writes of so
     }
-    if (live) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+    for (int i = 0; i < kRpt; ++i) {
+        if (!live[i]) continue;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p.S_new[state + (c * LPR + sub) * 4 + e] = s[c][e];
+        for (int c = 0; c < 4; ++c) {
+            f2 *to = reinterpret_cast<f2 *>(p.S_new + state + i * kGroups * DK + c * LPR * 4);
+            to[0] = s[i][2 * c];
+            to[1] = s[i][2 * c + 1];
+        }
     }
 }
 
 template <typename T, typename O, int DK>
 cudaError_t run(Params p, int batch, cudaStream_t stream) {
-    constexpr int rows = kThreads / (DK / 16);
+    constexpr int rows = kThreads / (DK / 16) * kRpt;
     p.slabs = (p.dv + rows - 1) / rows;
     const int64_t blocks = (int64_t)batch * p.hv * p.slabs;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;

@@ -16,7 +16,7 @@
  *     Inside a token the heads are contiguous.  Every other array is contiguous.
  *   - States lie in a pool [n_states][Hv][d_v][d_k]; request b uses the state
  *     slots[b], or state b where slots is NULL.  Two requests of one call must not
- *     share a slot.
+ *     share a slot.  The pools are 16-byte aligned.
  *   - Supported: d_k, d_v in {16, 32, 64, 128}, Hv a multiple of Hk, tokens in fp32
  *     or bf16.  Sums, norms and states are fp32.
  */

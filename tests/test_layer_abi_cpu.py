@@ -52,7 +52,7 @@ RULE = [(dict(batch=-1), INVALID), (dict(n_k_heads=0), INVALID), (dict(n_k_heads
 CASES = ([("gdn_prefill", gb.PrefillArgs, PREFILL, kw, code) for kw, code in RULE]
          + [("gdn_prefill", gb.PrefillArgs, PREFILL, kw, code) for kw, code in
             [(dict(total_tokens=-1), INVALID), (dict(max_tokens=-1), INVALID), (dict(token_offsets=None), INVALID),
-             (dict(S_new=None), INVALID)]]
+             (dict(S_new=None), INVALID), (dict(S0=FAKE + 8), INVALID), (dict(S_new=FAKE + 4), INVALID)]]
          + [("gdn_decode", gb.DecodeArgs, DECODE, kw, code) for kw, code in
             RULE + [(dict(S=None), INVALID), (dict(S=FAKE + 4), INVALID)]]
          + [("gdn_qk_gates", gb.QkGatesArgs, GATES, kw, code) for kw, code in
