@@ -1,15 +1,18 @@
-// prefill_simt.cu -- prompts through the gated delta rule, one token after another:
-// the general kernel, any supported widths, types and strides.
+// prefill_simt.cu -- prompts through the gated delta rule, four tokens at a time: the
+// general kernel, any supported widths, types and strides.
 //
 // A block takes a slab of state rows of one (prompt, value head); rows of S do not
 // meet, so slabs are independent.  A row's d_k entries lie in the registers of d_k / 16
-// lanes for the whole prompt.  Per token, with the old state,
-//     u = beta (v - e^g S k),  o = scale (e^g S q + u (k . q)),  S <- e^g S + u k^T,
-// so that both products are reduced together and the step's chain is one reduction
-// and one update.  Tokens come in tiles of 16 through shared memory: the next tile's
-// values are loaded into registers before the present tile is worked off.  The chain
-// over the tokens bounds it: about 0.1 us a token whatever the number of heads, until
-// the heads' blocks fill the GPU.
+// lanes for the whole prompt.  For four tokens with the state S before them, a_i the
+// decay from there to token i and e_ij that from token j to token i,
+//     u_i = beta_i (v_i - a_i S k_i - sum_{j < i} e_ij (k_i.k_j) u_j)
+//     o_i = scale (a_i S q_i + sum_{j <= i} e_ij (q_i.k_j) u_j)
+//     S  <- a_3 S + sum_j e_3j u_j k_j^T,
+// so that eight products with S are reduced together and the chain over the tokens is one
+// reduction and one update for four of them.  The token products, which all rows share,
+// are made by a warp for each four.  Tokens come in tiles of 16 through shared memory:
+// the next tile's values are loaded into registers before the present tile is worked off.
+// The chain bounds it, until the heads' blocks fill the GPU: TIMES.
 #include "internal.cuh"
 
 namespace gdn {
@@ -17,7 +20,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens a tile
-constexpr int kRpt = 1;    // rows a thread has part of
+constexpr int kStep = 4;   // tokens a step
+static_assert(kThreads / 32 * kStep == kTile, "a warp for each step's token products");
 
 // two fp32 values in a register pair, for the packed fp32 instructions
 using f2 = unsigned long long;
@@ -42,7 +46,34 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     return r;
 }
 
+// 16 bytes of a row as they are (vec: 16-byte aligned), and as floats in shared memory
+template <typename T>
+__device__ __forceinline__ uint4 raw16(const T *p, bool vec) {
+    if (vec) return __ldg(reinterpret_cast<const uint4 *>(p));
+    uint32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            r[i] = __float_as_uint(p[i]);
+        } else {
+            const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+            r[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+        }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+template <typename T>
+__device__ __forceinline__ void put16(float *to, const uint4 &w) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<uint4 *>(to) = w;
+    } else {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w.x << 16, w.x & 0xFFFF0000u, w.y << 16, w.y & 0xFFFF0000u);
+        *reinterpret_cast<uint4 *>(to + 4) = make_uint4(w.z << 16, w.z & 0xFFFF0000u, w.w << 16, w.w & 0xFFFF0000u);
+    }
+}
+
 struct Params {
+    bool vec;  // rows of q, k and v start on 16 bytes
     int hk, hv, dv, total, max_tokens, n_states, slabs;
     int64_t qs, ks, vs;
     float scale;
@@ -56,12 +87,15 @@ struct Params {
 
 template <typename T, typename O, int DK>
 __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
-    constexpr int LPR = DK / 16, kGroups = kThreads / LPR, kRows = kGroups * kRpt;  // rows a block
-    constexpr int kLoadK = kTile * DK / kThreads, kLoadV = kTile * (kRows < 128 ? kRows : 128) / kThreads;
-    static_assert(kTile * DK % kThreads == 0, "whole loads");
+    constexpr int LPR = DK / 16, kRows = kThreads / LPR;  // rows a block
     constexpr int kCols = kRows < 128 ? kRows : 128;  // value columns a block can use
+    constexpr int VE = 16 / sizeof(T), kPer = kThreads * VE;  // entries of 16 bytes, of one load of the block
+    constexpr int kLoadK = (kTile * DK + kPer - 1) / kPer, kLoadV = (kTile * kCols + kPer - 1) / kPer;
     __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
-    __shared__ float sv[2][kTile][kCols], so[kTile][kCols], skq[kTile], salpha[2][kTile], sbeta[2][kTile];
+    __shared__ __align__(16) float sv[2][kTile][kCols];
+    __shared__ float so[kTile][kCols], salpha[2][kTile], sbeta[2][kTile];
+    // of each step: beta_i e_ij k_i.k_j (10, 20, 21, 30, 31, 32), e_ij q_i.k_j (00, 10, 11, 20, ..), a_i, beta_i, e_3i, pad
+    __shared__ __align__(16) float scoef[kTile / kStep][32];
 
     const int tid = threadIdx.x, sub = tid % LPR, warp = tid >> 5, lane = tid & 31;
     const int slab = blockIdx.x % p.slabs, item = blockIdx.x / p.slabs;
@@ -76,41 +110,41 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         if (tid == 0) flag(p.status, err);
         return;
     }
-    const int lrow = tid / LPR;  // and kGroups further on
+    const int lrow = tid / LPR;
     const int ncols = min(kCols, p.dv - slab * kRows);
+    const bool live = lrow < ncols;
     const int64_t state = (((int64_t)slot * p.hv + h) * p.dv + slab * kRows + lrow) * DK + sub * 4;
-    const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
-    bool live[kRpt];
-    f2 s[kRpt][8];
+    const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0) || !live;
+    f2 s[8];
 #pragma unroll
-    for (int i = 0; i < kRpt; ++i) {
-        live[i] = lrow + i * kGroups < ncols;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const float *from = p.S0 + state + i * kGroups * DK + c * LPR * 4;
-            const bool z = zero || !live[i];
-            s[i][2 * c] = z ? 0 : pair(from[0], from[1]);
-            s[i][2 * c + 1] = z ? 0 : pair(from[2], from[3]);
-        }
+    for (int c = 0; c < 4; ++c) {
+        const float *from = p.S0 + state + c * LPR * 4;
+        s[2 * c] = zero ? 0 : pair(from[0], from[1]);
+        s[2 * c + 1] = zero ? 0 : pair(from[2], from[3]);
     }
 
     const T *qb = static_cast<const T *>(p.q) + (int64_t)lo * p.qs + hk * DK;
     const T *kb = static_cast<const T *>(p.k) + (int64_t)lo * p.ks + hk * DK;
     const T *vb = static_cast<const T *>(p.v) + (int64_t)lo * p.vs + h * p.dv + slab * kRows;
-    float rk[kLoadK], rq[kLoadK], rv[kLoadV], rg = 0.f, rb = 0.f;
+    uint4 rk[kLoadK], rq[kLoadK], rv[kLoadV];
+    float rg = 0.f, rb = 0.f;
     auto fetch = [&](int t0) {
 #pragma unroll
         for (int i = 0; i < kLoadK; ++i) {
-            const int x = tid + i * kThreads, t = x / DK, d = x % DK;
-            const bool in = t0 + t < n;
-            rk[i] = in ? load_f(kb, (int64_t)(t0 + t) * p.ks + d) : 0.f;
-            rq[i] = in ? load_f(qb, (int64_t)(t0 + t) * p.qs + d) : 0.f;
+            const int x = (tid + i * kThreads) * VE, t = x / DK, d = x % DK;
+            rk[i] = rq[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < kTile && t0 + t < n) {
+                rk[i] = raw16(kb + (int64_t)(t0 + t) * p.ks + d, p.vec);
+                rq[i] = raw16(qb + (int64_t)(t0 + t) * p.qs + d, p.vec);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kLoadV; ++i) {
-            const int x = tid + i * kThreads, t = x / kCols, d = x % kCols;
-            rv[i] = t0 + t < n && d < ncols ? load_f(vb, (int64_t)(t0 + t) * p.vs + d) : 0.f;
+            const int x = (tid + i * kThreads) * VE, t = x / kCols, d = x % kCols;
+            rv[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (t < kTile && t0 + t < n && d < ncols) rv[i] = raw16(vb + (int64_t)(t0 + t) * p.vs + d, p.vec);
         }
+        rg = rb = 0.f;  // tokens past the end: no decay, nothing written
         if (tid < kTile && t0 + tid < n) {
             rg = __ldg(p.g + (int64_t)(lo + t0 + tid) * p.hv + h);
             rb = __ldg(p.beta + (int64_t)(lo + t0 + tid) * p.hv + h);
@@ -119,14 +153,16 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     auto put = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < kLoadK; ++i) {
-            const int x = tid + i * kThreads;
-            sk[buf][x / DK][x % DK] = rk[i];
-            sq[buf][x / DK][x % DK] = rq[i];
+            const int x = (tid + i * kThreads) * VE;
+            if (x / DK < kTile) {
+                put16<T>(&sk[buf][x / DK][x % DK], rk[i]);
+                put16<T>(&sq[buf][x / DK][x % DK], rq[i]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kLoadV; ++i) {
-            const int x = tid + i * kThreads;
-            sv[buf][x / kCols][x % kCols] = rv[i];
+            const int x = (tid + i * kThreads) * VE;
+            if (x / kCols < kTile) put16<T>(&sv[buf][x / kCols][x % kCols], rv[i]);
         }
         if (tid < kTile) {
             salpha[buf][tid] = expf(rg);
@@ -140,38 +176,87 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     __syncthreads();
     for (int t0 = 0, buf = 0; t0 < n; t0 += kTile, buf ^= 1) {
         const int nt = min(kTile, n - t0);
-        for (int t = warp; t < nt; t += kThreads / 32) {
-            float x = 0.f;
-            for (int d = lane; d < DK; d += 32) x = fmaf(sk[buf][t][d], sq[buf][t][d], x);
-            x = warp_sum(x);
-            if (lane == 0) skq[t] = x;
+        {
+            // step number `warp`: its 16 token products, summed over the warp by halves so that lane 2 m ends with
+            // number m
+            const int g0 = warp * kStep;
+            float x[16];
+#pragma unroll
+            for (int m = 0; m < 16; ++m) x[m] = 0.f;
+            if (lane * 4 < DK) {
+                float4 k[kStep], q[kStep];
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                    k[i] = *reinterpret_cast<const float4 *>(&sk[buf][g0 + i][lane * 4]);
+                    q[i] = *reinterpret_cast<const float4 *>(&sq[buf][g0 + i][lane * 4]);
+                }
+                auto dot = [](const float4 &a, const float4 &b) { return fmaf(a.x, b.x, a.y * b.y) + fmaf(a.z, b.z, a.w * b.w); };
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) {
+                        if (j < i) x[i * (i - 1) / 2 + j] = dot(k[i], k[j]);
+                        x[6 + i * (i + 1) / 2 + j] = dot(q[i], k[j]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int w = 16, m = 8; w >= 2; w >>= 1, m >>= 1) {
+#pragma unroll
+                for (int e = 0; e < m; ++e) {
+                    const bool up = lane & w;
+                    const float send = up ? x[e] : x[e + m], keep = up ? x[e + m] : x[e];
+                    x[e] = keep + __shfl_xor_sync(0xffffffffu, send, w);
+                }
+            }
+            x[0] += __shfl_xor_sync(0xffffffffu, x[0], 1);
+            const int m = lane >> 1;
+            int i = 0, j = 0;  // of product number m
+            if (m < 6) {
+                i = m < 1 ? 1 : m < 3 ? 2 : 3;
+                j = m - i * (i - 1) / 2;
+            } else {
+                i = m < 7 ? 0 : m < 9 ? 1 : m < 12 ? 2 : 3;
+                j = m - 6 - i * (i + 1) / 2;
+            }
+            float e = 1.f;
+            for (int t = j + 1; t <= i; ++t) e *= salpha[buf][g0 + t];
+            if (!(lane & 1)) {
+                scoef[warp][m] = e * x[0] * (m < 6 ? sbeta[buf][g0 + i] : 1.f);
+            } else if (m < 12) {  // a_i, beta_i, e_3i
+                const int t0i = m & 3;
+                float y = 1.f;
+                if (m < 4) for (int t = 0; t <= t0i; ++t) y *= salpha[buf][g0 + t];
+                else if (m < 8) y = sbeta[buf][g0 + t0i];
+                else for (int t = t0i + 1; t < kStep; ++t) y *= salpha[buf][g0 + t];
+                scoef[warp][16 + m] = y;
+            }
         }
         if (t0 + kTile < n) fetch(t0 + kTile);
         __syncthreads();
-        // a token's k and q are read while the one before it is reduced
-        f2 k0[8], q0[8];
-        auto read = [&](int t, f2 (&k)[8], f2 (&q)[8]) {
+#pragma unroll 1
+        for (int t = 0; t < nt; t += kStep) {
+            float cf[28];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(&sk[buf][t][(c * LPR + sub) * 4]);
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(&sq[buf][t][(c * LPR + sub) * 4]);
-                k[2 * c] = a.x;
-                k[2 * c + 1] = a.y;
-                q[2 * c] = b.x;
-                q[2 * c + 1] = b.y;
+            for (int c = 0; c < 28; c += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(&scoef[t / kStep][c]);
+                cf[c] = v.x; cf[c + 1] = v.y; cf[c + 2] = v.z; cf[c + 3] = v.w;
             }
-        };
-        auto step = [&](int t, const f2 (&k)[8], const f2 (&q)[8]) {
-            float xk[kRpt], xq[kRpt];
+            f2 k[kStep][8];
+            float xk[kStep], xq[kStep];
 #pragma unroll
-            for (int i = 0; i < kRpt; ++i) {
-                f2 a0 = mul2(s[i][0], k[0]), a1 = mul2(s[i][1], k[1]), b0 = mul2(s[i][0], q[0]), b1 = mul2(s[i][1], q[1]);
+            for (int i = 0; i < kStep; ++i) {
+                f2 a0 = 0, a1 = 0, b0 = 0, b1 = 0;
 #pragma unroll
-                for (int e = 2; e < 8; e += 2) {
-                    a0 = fma2(s[i][e], k[e], a0);
-                    a1 = fma2(s[i][e + 1], k[e + 1], a1);
-                    b0 = fma2(s[i][e], q[e], b0);
-                    b1 = fma2(s[i][e + 1], q[e + 1], b1);
+                for (int c = 0; c < 4; ++c) {
+                    const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(&sk[buf][t + i][(c * LPR + sub) * 4]);
+                    const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(&sq[buf][t + i][(c * LPR + sub) * 4]);
+                    k[i][2 * c] = a.x;
+                    k[i][2 * c + 1] = a.y;
+                    a0 = fma2(s[2 * c], a.x, a0);
+                    a1 = fma2(s[2 * c + 1], a.y, a1);
+                    b0 = fma2(s[2 * c], q.x, b0);
+                    b1 = fma2(s[2 * c + 1], q.y, b1);
                 }
                 xk[i] = sum(a0) + sum(a1);
                 xq[i] = sum(b0) + sum(b1);
@@ -179,31 +264,34 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
 #pragma unroll
             for (int w = LPR / 2; w > 0; w >>= 1) {
 #pragma unroll
-                for (int i = 0; i < kRpt; ++i) {
+                for (int i = 0; i < kStep; ++i) {
                     xk[i] += __shfl_xor_sync(0xffffffffu, xk[i], w);
                     xq[i] += __shfl_xor_sync(0xffffffffu, xq[i], w);
                 }
             }
-            const float alpha = salpha[buf][t], beta = sbeta[buf][t], kq = skq[t];
-            const f2 alpha2 = pair(alpha, alpha);
+            float u[kStep];
 #pragma unroll
-            for (int i = 0; i < kRpt; ++i) {
-                const float u = live[i] ? beta * (sv[buf][t][(lrow + i * kGroups) % kCols] - alpha * xk[i]) : 0.f;
-                if (live[i] && sub == 0) so[t][lrow + i * kGroups] = p.scale * fmaf(u, kq, alpha * xq[i]);
-                const f2 u2 = pair(u, u);
+            for (int i = 0; i < kStep; ++i) {
+                const float *a = cf + 16, *beta = cf + 20;
+                float x = beta[i] * (sv[buf][t + i][lrow % kCols] - a[i] * xk[i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[i][e] = fma2(u2, k[e], mul2(alpha2, s[i][e]));
+                for (int j = 0; j < i; ++j) x = fmaf(-cf[i * (i - 1) / 2 + j], u[j], x);
+                u[i] = live ? x : 0.f;
+                float o = a[i] * xq[i];
+#pragma unroll
+                for (int j = 0; j <= i; ++j) o = fmaf(cf[6 + i * (i + 1) / 2 + j], u[j], o);
+                if (live && sub == 0) so[t + i][lrow] = p.scale * o;
             }
-        };
-        read(0, k0, q0);
-#pragma unroll 1
-        for (int t = 0; t < nt; t += 2) {
-            f2 k1[8], q1[8];
-            const bool second = t + 1 < nt;
-            if (second) read(t + 1, k1, q1);
-            step(t, k0, q0);
-            if (t + 2 < nt) read(t + 2, k0, q0);
-            if (second) step(t + 1, k1, q1);
+            const f2 a3 = pair(cf[19], cf[19]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] = mul2(a3, s[e]);
+#pragma unroll
+            for (int j = 0; j < kStep; ++j) {
+                const float w = cf[24 + j] * u[j];
+                const f2 w2 = pair(w, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[e] = fma2(w2, k[j][e], s[e]);
+            }
         }
         if (t0 + kTile < n) put(buf ^ 1);
         __syncthreads();
@@ -214,21 +302,19 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         }
         // the next tile's first __syncthreads() stands between these reads and its writes of so
     }
-#pragma unroll
-    for (int i = 0; i < kRpt; ++i) {
-        if (!live[i]) continue;
+    if (live) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            f2 *to = reinterpret_cast<f2 *>(p.S_new + state + i * kGroups * DK + c * LPR * 4);
-            to[0] = s[i][2 * c];
-            to[1] = s[i][2 * c + 1];
+            f2 *to = reinterpret_cast<f2 *>(p.S_new + state + c * LPR * 4);
+            to[0] = s[2 * c];
+            to[1] = s[2 * c + 1];
         }
     }
 }
 
 template <typename T, typename O, int DK>
 cudaError_t run(Params p, int batch, cudaStream_t stream) {
-    constexpr int rows = kThreads / (DK / 16) * kRpt;
+    constexpr int rows = kThreads / (DK / 16);
     p.slabs = (p.dv + rows - 1) / rows;
     const int64_t blocks = (int64_t)batch * p.hv * p.slabs;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
@@ -257,6 +343,9 @@ cudaError_t launch_prefill_simt(const gdn_prefill_args &a, cudaStream_t stream) 
     p.ks = a.k_stride ? a.k_stride : (int64_t)a.n_k_heads * a.d_k;
     p.vs = a.v_stride ? a.v_stride : (int64_t)a.n_v_heads * a.d_v;
     p.scale = a.scale;
+    const int e = a.qkv_dtype == GDN_BF16 ? 2 : 4;
+    p.vec = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v)) & 15) == 0 &&
+            p.qs * e % 16 == 0 && p.ks * e % 16 == 0 && p.vs * e % 16 == 0;
     p.offsets = a.token_offsets; p.slots = a.slots; p.fresh = a.fresh;
     p.q = a.q; p.k = a.k; p.v = a.v; p.g = a.g; p.beta = a.beta; p.S0 = a.S0; p.o = a.o; p.S_new = a.S_new;
     p.status = a.dev_status;
