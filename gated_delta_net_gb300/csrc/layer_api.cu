@@ -58,8 +58,13 @@ int check_prefill(const gdn_prefill_args *a) {
     return GDN_OK;
 }
 
-// whether the chunked kernel runs (shorter prompts are done sooner token by token)
-bool chunked(const gdn_prefill_args &a) { return a.max_tokens >= 16 && gdn::prefill_tc_supported(a); }
+// Whether the chunked kernel runs.  A chunk takes it 12 us whatever it holds, four tokens take the recurrent one
+// 1.5 us once their heads' blocks are spread over idle SMs (32 heads, 16 / 24 / 32 / 64 tokens: 12.1, 12.1, 12.0, 12.4 us
+// against 7.5, 10.9, 12.8, 23.1); with a (prompt, head) for every SM the chunked one is ahead from one token on (8
+// prompts of 1 / 32 tokens: 17 us against 20 / 67).
+bool chunked(const gdn_prefill_args &a) {
+    return gdn::prefill_tc_supported(a) && (a.max_tokens > 28 || (int64_t)a.batch * a.n_v_heads >= gdn::sm_count());
+}
 
 }  // namespace
 

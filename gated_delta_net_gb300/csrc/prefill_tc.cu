@@ -78,7 +78,7 @@ constexpr int OFF_BAR = OFF_NEXT + 16;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
     B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
-    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_NEXT, B_PROBE, B_COUNT
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_NEXT, B_DRAIN, B_PROBE = B_DRAIN + 3, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -436,6 +436,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             mbar_init(&bar[i], n);
         }
         fence_mbar_init();
+        // test hook: a wait that runs out, before the roles' own waits begin
+        if (p.probe > 0 && !mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe)) flag(p.status, GDN_DEV_TIMEOUT);
     }
     // T's and Y's tiles stay zero above the blocks that are written
     for (int i = tid; i < (4 + kKQ) * kTile / 16; i += kThreads)
@@ -463,8 +465,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // ---------------------------------------------------------------- W^T = K^T T''^T
             const uint32_t id = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
             const uint32_t d_t = uniform(desc_lo(sm + OFF_T, 0));
-            if (p.probe > 0 && lead && !mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe)) flag(p.status, GDN_DEV_TIMEOUT);
-            __syncwarp();
             for (; take(sm, bar, at, j, ok); at.next()) {
                 wwait(&bar[B_T], at.cc & 1, ok);
                 if (at.cc > 0) wwait(&bar[B_WRDY], (at.cc - 1) & 1, ok);  // the W before it has been read
@@ -711,6 +711,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             // every load has landed before the block ends, whatever became of its reader
             for (int i = 0; i < kKQ && i < at.cc; ++i) mbar_wait(&bar[B_FULL + i], ((at.cc - 1 - i) / kKQ) & 1, 1u << 16);
             if (asked > 0) mbar_wait(&bar[B_NEXT], (asked - 1) & 1, 1u << 16);
+        }
+        if (warp < 3) {  // what this warp issued is done before the block ends, whatever became of its reader
+            commit(lead, &bar[B_DRAIN + warp]);
+            mbar_wait(&bar[B_DRAIN + warp], 0, 1u << 16);
         }
     } else if (warp < 12 && (warp < 8 || (quad & 1))) {
         // -------------------------------------------------------------------- A, Y: 32 rows, 32 columns a warp

@@ -377,6 +377,92 @@ def test_residual_norm(T, D, pad, dtype, wtype, post):
         assert torch.equal(x2, h) and torch.equal(y2, n)
 
 
+def test_example_serves_a_layer():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "layer_serving.py")
+    spec = importlib.util.spec_from_file_location("layer_serving", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    stream, states = example.run()
+    # the rule's bf16 outputs differ by their rounding, then pass a bf16 product and sum; q, k, v are the same bits
+    # up to the products' own rounding of another batch
+    assert stream <= 2.0 ** -5 and states <= 2.0 ** -6
+
+
+def test_prefill_many_more_prompts_than_sms():
+    rng = np.random.default_rng(3)
+    lengths = rng.integers(0, 150, 230).tolist()
+    x = tokens(22, sum(lengths), 1, 2, 128, 128, BF)
+    off = offsets(lengths)
+    st = gb.new_status()
+    o, S = gb.gdn_prefill(*x, off, 150, dev_status=st)
+    gb.check_status(st)
+    ro, rS = OL.prefill(*map(f64, x), off.cpu().numpy())
+    close(o, ro, TOL[BF])
+    close(S, rS, TOL_STATE[BF])
+
+
+@pytest.mark.parametrize("lengths", [[1] * 90, [3, 20, 28, 1] * 25])
+def test_prefill_short_prompts_fill_the_gpu(lengths):
+    x = tokens(23, sum(lengths), 1, 2, 128, 128, BF)
+    off = offsets(lengths)
+    S0 = pool(9, len(lengths), 2, 128, 128)
+    o, S = gb.gdn_prefill(*x, off, 28, S0=S0)
+    ro, rS = OL.prefill(*map(f64, x), off.cpu().numpy(), S0=f64(S0))
+    close(o, ro, TOL[BF])
+    close(S, rS, TOL_STATE[BF])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_rows_and_states_past_2_to_the_31(dtype):
+    # rows so far apart, and a slot so far into the pool, that offsets pass 32 bits
+    T, hv, d = 90, 2, 128
+    q, k, v, g, beta = tokens(24, T, 1, hv, d, d, dtype, slow=True)
+    stride = 1 << 25
+    rows = torch.empty(T * stride, dtype=dtype, device="cuda").view(T, stride)
+    qs, ks, vs = rows[:, :d].view(T, 1, d), rows[:, d:2 * d].view(T, 1, d), rows[:, 2 * d:(2 + hv) * d].view(T, hv, d)
+    qs.copy_(q), ks.copy_(k), vs.copy_(v)
+    n = 70000
+    S = torch.empty(n, hv, d, d, device="cuda")
+    S0 = pool(10, 1, hv, d, d)
+    S[n - 1] = S0[0]
+    slots = torch.tensor([n - 1], dtype=torch.int32, device="cuda")
+    o, _ = gb.gdn_prefill(qs[:80], ks[:80], vs[:80], g[:80], beta[:80], offsets([80]), 80, S0=S, S_new=S, slots=slots)
+    outs = [gb.gdn_decode(qs[t:t + 1], ks[t:t + 1], vs[t:t + 1], g[t:t + 1], beta[t:t + 1], S, slots=slots) for t in range(80, T)]
+    ro, rS = OL.prefill(*map(f64, (q, k, v, g, beta)), [0, T], S0=f64(S0))
+    close(torch.cat([o] + outs), ro, TOL[dtype])
+    close(S[n - 1:], rS, TOL_STATE[dtype])
+    y = gb.gdn_norm_gate(vs, vs, torch.ones(d, device="cuda"))
+    assert torch.equal(y, gb.gdn_norm_gate(v, v, torch.ones(d, device="cuda")))
+    rest = (v[:, :, 0].contiguous(), v[:, :, 1].contiguous(), torch.zeros(hv, device="cuda"), torch.zeros(hv, device="cuda"))
+    for got, ref in zip(gb.gdn_qk_gates(qs, ks, *rest), gb.gdn_qk_gates(q, k, *rest)):
+        assert torch.equal(got, ref)
+
+
+def test_prefill_wait_probe_reports_and_still_computes():
+    x = tokens(25, 100, 1, 2, 128, 128, BF)
+    ref, rS = gb.gdn_prefill(*x, offsets([100]), 100)
+    st = gb.new_status()
+    gb.gdn_test_set_wait_probe(1000)
+    try:
+        o, S = gb.gdn_prefill(*x, offsets([100]), 100, dev_status=st)
+        torch.cuda.synchronize()
+    finally:
+        gb.gdn_test_set_wait_probe(0)
+    assert int(st.item()) == 16
+    assert torch.equal(o, ref) and torch.equal(S, rS)
+
+
+def test_same_inputs_same_bits():
+    lengths = [700, 64, 300, 1]
+    x = tokens(26, sum(lengths), 2, 4, 128, 128, BF)
+    first = gb.gdn_prefill(*x, offsets(lengths), 700)
+    for _ in range(3):
+        again = gb.gdn_prefill(*x, offsets(lengths), 700)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_binding_refusals():
     x = tokens(1, 4, 1, 2, 16, 16, F32)
     off = offsets([4])
