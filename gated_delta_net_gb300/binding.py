@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -135,11 +136,10 @@ def lib():
         L.gdn_tree_relabel.restype = ctypes.c_int
         L.gdn_gather_rows.argtypes = [_P, _P, _P, _P, _I, _I, ctypes.c_int64, _P, _P]
         L.gdn_gather_rows.restype = ctypes.c_int
-        for fn, args in ((L.gdn_prefill, PrefillArgs), (L.gdn_decode, DecodeArgs), (L.gdn_qk_gates, QkGatesArgs),
-                         (L.gdn_norm_gate, NormGateArgs), (L.gdn_residual_norm, ResidualNormArgs)):
-            fn.argtypes = [ctypes.POINTER(args), _P]
+        for fn in (L.gdn_prefill, L.gdn_decode, L.gdn_qk_gates, L.gdn_norm_gate, L.gdn_residual_norm):
+            fn.argtypes = [_P, _P]
             fn.restype = ctypes.c_int
-        L.gdn_prefill_workspace.argtypes = [ctypes.POINTER(PrefillArgs)]
+        L.gdn_prefill_workspace.argtypes = [_P]
         L.gdn_prefill_workspace.restype = _L
         L.gdn_last_error.restype = ctypes.c_char_p
         L.gdn_tree_version.restype = ctypes.c_int
@@ -419,7 +419,20 @@ def gdn_tree_commit_verify(prev: dict, S0, max_nodes_prev: int, max_path: int,
 # ----------------------------------------------------------------------------
 
 # These calls serve single tokens, where the host's time counts: one pass over each tensor's
-# attributes, pointers as plain integers, the current stream's handle without its object.
+# attributes and none over the outputs made here, pointers as plain integers, the current stream's
+# handle without its object, the arguments packed in one go (0.3 us against the Structure's 0.8).
+
+_FORMATS = {_I: "i", _F: "f", _L: "q", _P: "P"}
+
+
+def _packer(args):
+    """What lays the values of a Structure's fields out as the Structure does."""
+    return struct.Struct("@" + "".join(_FORMATS[kind] for _, kind in args._fields_)).pack
+
+
+_prefill_args, _decode_args, _qk_gates_args, _norm_gate_args, _residual_norm_args = map(
+    _packer, (PrefillArgs, DecodeArgs, QkGatesArgs, NormGateArgs, ResidualNormArgs))
+
 
 def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
     """The distance between the tokens of ``t`` in elements (0: contiguous), after a check of its
@@ -517,18 +530,22 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     s0 = 0 if S0 is None else _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
     if out is None:
         out = torch.empty((T, Hv, dv), dtype=od, device=q.device)
-    a = PrefillArgs(B, Hk, Hv, dk, dv, T, max_tokens, n_states, scale, code, out_code, qs, ks, vs, op, q.data_ptr(),
-                    k.data_ptr(), v.data_ptr(), gp, bp, s0, sp, fp, _flat(out, "out", od, (T, Hv, dv)), np_, 0, 0,
-                    _status(dev_status))
+        outp = out.data_ptr()
+    else:
+        outp = _flat(out, "out", od, (T, Hv, dv))
+    a = (B, Hk, Hv, dk, dv, T, max_tokens, n_states, scale, code, out_code, qs, ks, vs, op, q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), gp, bp, s0, sp, fp, outp, np_)
+    st, stream_handle, L = _status(dev_status), _handle(stream, q), lib()
+    packed = None
     if workspace is None:
-        need = lib().gdn_prefill_workspace(ctypes.byref(a))
+        packed = _prefill_args(*a, 0, 0, st)
+        need = L.gdn_prefill_workspace(packed)
         if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
             _keep(workspace, stream)
     if workspace is not None:
-        a.workspace = _flat(workspace, "workspace", torch.uint8, workspace.shape)
-        a.workspace_bytes = workspace.numel()
-    _check(lib().gdn_prefill(ctypes.byref(a), _handle(stream, q)))
+        packed = _prefill_args(*a, _flat(workspace, "workspace", torch.uint8, workspace.shape), workspace.numel(), st)
+    _check(L.gdn_prefill(packed, stream_handle))
     return out, S_new
 
 
@@ -561,9 +578,12 @@ def gdn_decode(q, k, v, g, beta, S, slots=None, scale: float = 1.0, out=None, ou
         raise ValueError("the pool has fewer states than there are requests")
     if out is None:
         out = torch.empty((B, Hv, dv), dtype=od, device=q.device)
-    a = DecodeArgs(B, Hk, Hv, dk, dv, n_states, scale, code, out_code, qs, ks, vs, q.data_ptr(), k.data_ptr(),
-                   v.data_ptr(), gp, bp, Sp, sp, _flat(out, "out", od, (B, Hv, dv)), _status(dev_status))
-    _check(lib().gdn_decode(ctypes.byref(a), _handle(stream, q)))
+        outp = out.data_ptr()
+    else:
+        outp = _flat(out, "out", od, (B, Hv, dv))
+    _check(lib().gdn_decode(
+        _decode_args(B, Hk, Hv, dk, dv, n_states, scale, code, out_code, qs, ks, vs, q.data_ptr(), k.data_ptr(),
+                     v.data_ptr(), gp, bp, Sp, sp, outp, _status(dev_status)), _handle(stream, q)))
     return out
 
 
@@ -579,14 +599,19 @@ def gdn_qk_gates(q, k, a, b, A_log, dt_bias, eps: float = 1e-6, q_out=None, k_ou
     Ap, dp = _flat(A_log, "A_log", torch.float32, (Hv,)), _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
     if q_out is None:
         q_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+        qp = q_out.data_ptr()
+    else:
+        qp = _flat(q_out, "q_out", dt, (T, Hk, dk))
     if k_out is None:
         k_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+        kp = k_out.data_ptr()
+    else:
+        kp = _flat(k_out, "k_out", dt, (T, Hk, dk))
     g = torch.empty((T, Hv), dtype=torch.float32, device=dev)
     beta = torch.empty((T, Hv), dtype=torch.float32, device=dev)
-    args = QkGatesArgs(T, Hk, Hv, dk, eps, code, qs, ks, as_, bs, q.data_ptr(), k.data_ptr(), a.data_ptr(),
-                       b.data_ptr(), Ap, dp, _flat(q_out, "q_out", dt, (T, Hk, dk)),
-                       _flat(k_out, "k_out", dt, (T, Hk, dk)), g.data_ptr(), beta.data_ptr())
-    _check(lib().gdn_qk_gates(ctypes.byref(args), _handle(stream, q)))
+    _check(lib().gdn_qk_gates(
+        _qk_gates_args(T, Hk, Hv, dk, eps, code, qs, ks, as_, bs, q.data_ptr(), k.data_ptr(), a.data_ptr(),
+                       b.data_ptr(), Ap, dp, qp, kp, g.data_ptr(), beta.data_ptr()), _handle(stream, q)))
     return q_out, k_out, g, beta
 
 
@@ -600,9 +625,12 @@ def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, 
         raise ValueError(f"act must be one of {sorted(GDN_ACTS)}, got {act!r}")
     if out is None:
         out = torch.empty((T, Hv, dv), dtype=dt, device=o.device)
-    a = NormGateArgs(T, Hv, dv, eps, kind, _dtype_code(dt), _dtype_code(weight.dtype), os_, zs, o.data_ptr(),
-                     z.data_ptr(), _flat(weight, "weight", weight.dtype, (dv,)), _flat(out, "out", dt, (T, Hv, dv)))
-    _check(lib().gdn_norm_gate(ctypes.byref(a), _handle(stream, o)))
+        outp = out.data_ptr()
+    else:
+        outp = _flat(out, "out", dt, (T, Hv, dv))
+    _check(lib().gdn_norm_gate(
+        _norm_gate_args(T, Hv, dv, eps, kind, _dtype_code(dt), _dtype_code(weight.dtype), os_, zs, o.data_ptr(),
+                        z.data_ptr(), _flat(weight, "weight", weight.dtype, (dv,)), outp), _handle(stream, o)))
     return out
 
 
@@ -617,11 +645,17 @@ def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: f
     pp = 0 if post_weight is None else _flat(post_weight, "post_weight", weight.dtype, (D,))
     if h is None:
         h = torch.empty((T, D), dtype=dt, device=dev)
+        hp = h.data_ptr()
+    else:
+        hp = _flat(h, "h", dt, (T, D))
     if out is None:
         out = torch.empty((T, D), dtype=dt, device=dev)
-    a = ResidualNormArgs(T, D, scale, eps, _dtype_code(dt), _dtype_code(weight.dtype), xs, ys, x.data_ptr(),
-                         y.data_ptr(), wp, pp, _flat(h, "h", dt, (T, D)), _flat(out, "out", dt, (T, D)))
-    _check(lib().gdn_residual_norm(ctypes.byref(a), _handle(stream, x)))
+        outp = out.data_ptr()
+    else:
+        outp = _flat(out, "out", dt, (T, D))
+    _check(lib().gdn_residual_norm(
+        _residual_norm_args(T, D, scale, eps, _dtype_code(dt), _dtype_code(weight.dtype), xs, ys, x.data_ptr(),
+                            y.data_ptr(), wp, pp, hp, outp), _handle(stream, x)))
     return h, out
 
 
