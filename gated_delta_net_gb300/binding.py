@@ -441,7 +441,13 @@ def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
         if t.dtype is dtype and t.shape == shape and t.is_cuda:
             if t.is_contiguous():
                 return 0
-            stride, row = t.stride(), 1
+            stride = t.stride()
+            if len(shape) == 3:
+                if stride[2] == 1 and stride[1] == shape[2] and stride[0] >= shape[1] * shape[2]:
+                    return stride[0]
+            elif stride[1] == 1 and stride[0] >= shape[1]:
+                return stride[0]
+            row = 1  # sizes of one, whose strides do not count, or a mistake
             for n, st in zip(reversed(shape[1:]), reversed(stride[1:])):
                 if st != row and n != 1:
                     raise ValueError(f"{name} must be contiguous inside a token")
