@@ -148,10 +148,11 @@ struct Walk {
         x.h = h;
         x.hk = p.group_inv ? __umulhi((uint32_t)h, p.group_inv) : h;
         x.lo = raw.lo;
-        x.n = raw.hi - raw.lo;
+        const bool inside = raw.lo >= 0 && raw.hi >= raw.lo && raw.hi <= p.total;
+        x.n = inside ? raw.hi - raw.lo : 0;
         const int slot = raw.slot;
         x.err = 0;
-        if (x.n < 0 || x.lo < 0 || x.lo + x.n > p.total) x.err = GDN_DEV_BAD_DESC;
+        if (!inside) x.err = GDN_DEV_BAD_DESC;
         else if (x.n > p.max_tokens) x.err = GDN_DEV_TOO_MANY;
         else if (slot < 0 || slot >= p.n_states) x.err = GDN_DEV_BAD_SLOT;
         const int64_t state = ((int64_t)slot * p.hv_n + h) * (kD * kD);
@@ -404,9 +405,12 @@ __device__ __forceinline__ void dd_add(float &ah, float &al, float bh, float bl)
 __device__ __forceinline__ void zero_tail(uint8_t *tile, int apart, int nv, int lane) {
     if (nv >= kC) return;
 #pragma unroll 1
-    for (int i = nv * 8 + lane; i < kC * 8; i += 32) {
-        *reinterpret_cast<uint4 *>(tile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(tile + apart + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i0 = nv * 8; i0 < kC * 8; i0 += 32) {  // the same steps in every lane: the warp issues products
+        const int i = i0 + lane;
+        if (i < kC * 8) {
+            *reinterpret_cast<uint4 *>(tile + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(tile + apart + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -602,7 +606,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             };
             while (ok && walk.idx >= 0) {
                 const Item x = walk.template item<OUT>(p, walk.raw(p));
-                if (x.chunks == 0) ask();
+                if (x.chunks <= 0) ask();
                 if (OUT && lane == 0 && x.err) flag(p.status, x.err);
                 if (x.chunks == 0 && !x.skip && x.from != x.to) {  // no tokens: the state as it is
                     for (int i = lane; i < kD * kD / 4; i += 32)
@@ -1133,8 +1137,9 @@ constexpr int kJoinRows = 16;
 __global__ void __launch_bounds__(256) prefill_join_kernel(Params p) {
     __shared__ __align__(16) float S[kJoinRows][kD];
     const int part = blockIdx.x % (kD / kJoinRows), item = blockIdx.x / (kD / kJoinRows), h = item % p.hv_n, b = item / p.hv_n;
-    const int lo = __ldg(p.offsets + b), n = __ldg(p.offsets + b + 1) - lo, slot = p.slots ? __ldg(p.slots + b) : b;
-    if (n <= p.seg || lo < 0 || lo + n > p.total || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
+    const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), slot = p.slots ? __ldg(p.slots + b) : b;
+    const int n = lo >= 0 && hi >= lo && hi <= p.total ? hi - lo : 0;
+    if (n <= p.seg || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
     const int col = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * (kJoinRows / 2), segs = (n + p.seg - 1) / p.seg;
     float *ws = p.ws + (int64_t)item * (2 * p.segs - 2) * (kD * kD);
     const int64_t at = (int64_t)(part * kJoinRows + r0) * kD + col;
@@ -1203,7 +1208,8 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
 // blocks, the first pass over its 2 segs - 3 slices 0.7 of that; a join step takes 1.5, the launches 3.  One prompt of
 // 16384 tokens with 32 heads, measured with 1, 2, 3, 4, 6, 8, 9, 16 segments: 842, 795, 571, 622, 643, 658, 675, 790 us.
 int plan_segments(const gdn_prefill_args &a, int &seg) {
-    const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads, chunks = std::max(1, (a.max_tokens + kC - 1) / kC);
+    const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads;
+    const int64_t chunks = std::max<int64_t>(1, ((int64_t)std::min(a.max_tokens, a.total_tokens) + kC - 1) / kC);
     auto waves = [&](double blocks) { return std::ceil(blocks / sms) * (0.715 + 0.285 * std::min(1.0, blocks / sms)); };
     double best = 0.9 * (chunks + 3) * waves((double)items);  // worth a tenth at least
     int segs = 1;

@@ -228,6 +228,24 @@ def test_prefill_skips_bad_requests(dtype):
         close(S[:1], rS, TOL_STATE[dtype])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_prefill_skips_offsets_at_the_ends_of_their_type(dtype):
+    least, most = -2 ** 31, 2 ** 31 - 1
+    x = tokens(17, 80, 1, 2, 128, 128, dtype)
+    for off in ([0, 70, least, 80], [0, 70, most, 80], [least, 70, 70, 80], [most, least, 70, 80]):
+        st = gb.new_status()
+        S = torch.full((3, 2, 128, 128), 7.0, device="cuda")
+        gb.gdn_prefill(*x, torch.tensor(off, dtype=torch.int32, device="cuda"), most, S_new=S, dev_status=st,
+                       workspace=torch.empty(1 << 28, dtype=torch.uint8, device="cuda"))
+        assert int(st.item()) == 32, off
+        for i, (lo, hi) in enumerate(zip(off, off[1:])):
+            if not 0 <= lo <= hi <= 80:
+                assert bool((S[i] == 7.0).all()), (off, i)
+                continue
+            _, rS = OL.prefill(*[f64(t)[lo:hi] for t in x], [0, hi - lo])
+            close(S[i:i + 1], rS, TOL_STATE[dtype])
+
+
 def test_prefill_on_another_stream_and_in_a_graph():
     lengths = [300, 40]
     x = tokens(16, 340, 2, 4, 128, 128, BF)
