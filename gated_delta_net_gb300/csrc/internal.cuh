@@ -82,6 +82,20 @@ cudaError_t launch_residual_norm(const gdn_residual_norm_args &a, cudaStream_t s
 // driver entry point for TMA descriptors (nullptr when the driver lacks it)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Prompts longest first, so that none begins when the others are nearly done: the length of prompt b (-1 where its
+// offsets are not a prompt's), and the place of number i among n lengths.
+__device__ __forceinline__ int prompt_length(const int32_t *offsets, int b) {
+    const int lo = __ldg(offsets + b), hi = __ldg(offsets + b + 1);
+    return lo >= 0 && hi >= lo ? hi - lo : -1;
+}
+__device__ __forceinline__ int length_rank(const int *len, int n, int i) {
+    const int mine = len[i];
+    int r = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) r += len[j] > mine || (len[j] == mine && j < i);
+    return r;
+}
+
 // streaming multiprocessors on the current device (1 if the query fails)
 int sm_count();
 

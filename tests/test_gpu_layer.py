@@ -502,3 +502,29 @@ def test_binding_refusals():
         gb.gdn_residual_norm(torch.ones(4, 8, device="cuda").t(), torch.ones(8, 4, device="cuda"), torch.ones(4, device="cuda"))
     with pytest.raises(gb.GdnError):
         gb.gdn_qk_gates(x[0][:, :, :8].contiguous(), x[1][:, :, :8].contiguous(), x[3], x[4], x[3][0], x[3][0])
+
+
+@pytest.mark.parametrize("dtype,dv", [(F32, 128), (BF, 128), (BF, 64)])
+@pytest.mark.parametrize("batch", [2, 40, 128, 200, 256, 257])
+def test_prefill_takes_prompts_in_any_order(dtype, dv, batch):
+    # more items than the GPU holds at once, lengths with ties, empty and refused prompts among them
+    lengths = [(7 * b * b + 3) % 90 if b % 5 else 0 for b in range(batch)]
+    hv = 16 if batch < 40 else 8
+    T = sum(lengths)
+    x = tokens(31, T, 2, hv, 128, dv, dtype)
+    off = offsets(lengths)
+    slots = torch.arange(batch, dtype=torch.int32).flip(0).cuda()
+    slots[0] = batch
+    st = gb.new_status()
+    S = torch.zeros(batch, hv, dv, 128, device="cuda")
+    o, _ = gb.gdn_prefill(*x, off, 90, slots=slots, S_new=S, dev_status=st)
+    assert int(st.item()) == 128
+    at = off.tolist()
+    for b in {1, batch // 2, batch - 2, batch - 1} - {0}:
+        ro, rS = OL.prefill(*[f64(t)[at[b]:at[b + 1]] for t in x], [0, lengths[b]])
+        close(o[at[b]:at[b + 1]], ro, TOL[dtype])
+        i = int(slots[b])
+        close(S[i:i + 1], rS, TOL_STATE[dtype])
+    alone, _ = gb.gdn_prefill(*[t[at[1]:] for t in x], torch.tensor([0, lengths[1]], dtype=torch.int32, device="cuda"), 90)
+    if batch >= 40:  # neither cut into segments: the same bits
+        assert torch.equal(alone[:lengths[1]], o[at[1]:at[2]])
