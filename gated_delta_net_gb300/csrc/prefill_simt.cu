@@ -12,9 +12,9 @@
 // reduction and one update for four of them.  The token products, which all rows share,
 // are made by a warp for each four.  Tokens come in tiles of 16 through shared memory:
 // the next tile's values are loaded into registers before the present tile is worked off.
-// The chain over the steps bounds it, at about 0.3 us a token (300 tokens of 16 heads in fp32:
-// 88 us; one warp a scheduler, 127 instructions a token, 4.5 cycles each), until the heads'
-// blocks fill the GPU.
+// The chain over the steps bounds it, at 0.22 us a token (300 tokens of 16 heads in fp32:
+// 68 us; one warp a scheduler), until the heads' blocks fill the GPU: 16865 tokens of 32
+// heads take 3540 us, three blocks an SM, bound by what they issue.
 #include "internal.cuh"
 
 namespace gdn {
@@ -23,6 +23,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kTile = 16;  // tokens a tile
 constexpr int kStep = 4;   // tokens a step
+constexpr int kCoefA = 8, kCoefQ = 20, kCoef = 36;  // a step's coefficients
 static_assert(kThreads / 32 * kStep == kTile, "a warp for each step's token products");
 
 // two fp32 values in a register pair, for the packed fp32 instructions
@@ -36,6 +37,11 @@ __device__ __forceinline__ float sum(f2 x) {
     float a, b;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
     return a + b;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     f2 r;
@@ -76,7 +82,8 @@ __device__ __forceinline__ void put16(float *to, const uint4 &w) {
 
 struct Params {
     bool vec;  // rows of q, k and v start on 16 bytes
-    int hk, hv, dv, total, max_tokens, n_states, slabs;
+    int hk, hv, dv, total, max_tokens, n_states, slabs, batch;
+    bool sorted;  // prompts longest first
     int64_t qs, ks, vs;
     float scale;
     const int32_t *offsets, *slots, *fresh;
@@ -96,12 +103,22 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     __shared__ __align__(16) float sk[2][kTile][DK], sq[2][kTile][DK];
     __shared__ __align__(16) float sv[2][kTile][kCols];
     __shared__ float so[kTile][kCols], salpha[2][kTile], sbeta[2][kTile];
-    // of each step: beta_i e_ij k_i.k_j (10, 20, 21, 30, 31, 32), e_ij q_i.k_j (00, 10, 11, 20, ..), a_i, beta_i, e_3i, pad
-    __shared__ __align__(16) float scoef[kTile / kStep][32];
+    // of each step: beta_i e_ij k_i.k_j (10, 20, 21, 30, 31, 32), two of padding, a_i, beta_i, e_3i, and e_ij q_i.k_j in
+    // rows i of four, zero above the diagonal
+    __shared__ __align__(16) float scoef[kTile / kStep][kCoef];
 
     const int tid = threadIdx.x, sub = tid % LPR, warp = tid >> 5, lane = tid & 31;
     const int slab = blockIdx.x % p.slabs, item = blockIdx.x / p.slabs;
-    const int h = item % p.hv, b = item / p.hv, hk = h / (p.hv / p.hk);
+    const int h = item % p.hv, hk = h / (p.hv / p.hk);
+    int b = item / p.hv;
+    if (p.sorted) {
+        __shared__ int slen[kThreads], pick;
+        if (tid < p.batch) slen[tid] = prompt_length(p.offsets, tid);
+        __syncthreads();
+        if (tid < p.batch && length_rank(slen, p.batch, tid) == b) pick = tid;
+        __syncthreads();
+        b = pick;
+    }
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1);
     const bool inside = lo >= 0 && hi >= lo && hi <= p.total;
     const int n = inside ? hi - lo : 0;
@@ -117,6 +134,11 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     const int lrow = tid / LPR;
     const int ncols = min(kCols, p.dv - slab * kRows);
     const bool live = lrow < ncols;
+    // of the eight sums of a step (S k_i, S q_i) each lane of a row ends with kHeld; S q_i of tokens out0 on lies in its
+    // entries from kFirst on, in the upper half of the lanes
+    constexpr int kHeld = 2 * kStep / LPR, kFirst = LPR > 1 ? 0 : kStep;
+    const int out0 = (sub * kHeld + kFirst) & (kStep - 1);
+    const bool writes = live && sub * kHeld + kFirst >= kStep;
     const int64_t state = (((int64_t)slot * p.hv + h) * p.dv + slab * kRows + lrow) * DK + sub * 4;
     const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0) || !live;
     f2 s[8];
@@ -176,6 +198,9 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     if (n > 0) {
         fetch(0);
         put(0);
+        scoef[warp][lane] = 0.f;
+        if (lane < kCoef - 32) scoef[warp][32 + lane] = 0.f;
+        __syncwarp();
     }
     __syncthreads();
     for (int t0 = 0, buf = 0; t0 < n; t0 += kTile, buf ^= 1) {
@@ -226,72 +251,95 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
             float e = 1.f;
             for (int t = j + 1; t <= i; ++t) e *= salpha[buf][g0 + t];
             if (!(lane & 1)) {
-                scoef[warp][m] = e * x[0] * (m < 6 ? sbeta[buf][g0 + i] : 1.f);
+                scoef[warp][m < 6 ? m : kCoefQ + 4 * i + j] = e * x[0] * (m < 6 ? sbeta[buf][g0 + i] : 1.f);
             } else if (m < 12) {  // a_i, beta_i, e_3i
                 const int t0i = m & 3;
                 float y = 1.f;
                 if (m < 4) for (int t = 0; t <= t0i; ++t) y *= salpha[buf][g0 + t];
                 else if (m < 8) y = sbeta[buf][g0 + t0i];
                 else for (int t = t0i + 1; t < kStep; ++t) y *= salpha[buf][g0 + t];
-                scoef[warp][16 + m] = y;
+                scoef[warp][kCoefA + m] = y;
             }
         }
         if (t0 + kTile < n) fetch(t0 + kTile);
         __syncthreads();
 #pragma unroll 1
         for (int t = 0; t < nt; t += kStep) {
-            float cf[28];
+            const float *coef = scoef[t / kStep];
+            float cf[kCoefQ];
 #pragma unroll
-            for (int c = 0; c < 28; c += 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(&scoef[t / kStep][c]);
+            for (int c = 0; c < kCoefQ; c += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(coef + c);
                 cf[c] = v.x; cf[c + 1] = v.y; cf[c + 2] = v.z; cf[c + 3] = v.w;
             }
+            float4 qc[kHeld - kFirst];
+            float qa[kHeld - kFirst];
+#pragma unroll
+            for (int e = 0; e < kHeld - kFirst; ++e) {
+                qc[e] = *reinterpret_cast<const float4 *>(coef + kCoefQ + 4 * (out0 + e));
+                qa[e] = coef[kCoefA + out0 + e];
+            }
             f2 k[kStep][8];
-            float xk[kStep], xq[kStep];
+            float x[2 * kStep];  // S k_i, S q_i
 #pragma unroll
             for (int i = 0; i < kStep; ++i) {
-                f2 a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+                f2 a0, a1, b0, b1;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(&sk[buf][t + i][(c * LPR + sub) * 4]);
                     const ulonglong2 q = *reinterpret_cast<const ulonglong2 *>(&sq[buf][t + i][(c * LPR + sub) * 4]);
                     k[i][2 * c] = a.x;
                     k[i][2 * c + 1] = a.y;
-                    a0 = fma2(s[2 * c], a.x, a0);
-                    a1 = fma2(s[2 * c + 1], a.y, a1);
-                    b0 = fma2(s[2 * c], q.x, b0);
-                    b1 = fma2(s[2 * c + 1], q.y, b1);
+                    a0 = c ? fma2(s[2 * c], a.x, a0) : mul2(s[0], a.x);
+                    a1 = c ? fma2(s[2 * c + 1], a.y, a1) : mul2(s[1], a.y);
+                    b0 = c ? fma2(s[2 * c], q.x, b0) : mul2(s[0], q.x);
+                    b1 = c ? fma2(s[2 * c + 1], q.y, b1) : mul2(s[1], q.y);
                 }
-                xk[i] = sum(a0) + sum(a1);
-                xq[i] = sum(b0) + sum(b1);
+                x[i] = sum(add2(a0, a1));
+                x[kStep + i] = sum(add2(b0, b1));
             }
+            // summed over the row's lanes by halves, lane `sub` ends with number sub kHeld on; S k_i then goes to all of
+            // them, S q_i stays where it makes token i's output
 #pragma unroll
-            for (int w = LPR / 2; w > 0; w >>= 1) {
+            for (int w = LPR / 2, m = 4; w > 0; w >>= 1, m >>= 1) {
+                const bool up = sub & w;
 #pragma unroll
-                for (int i = 0; i < kStep; ++i) {
-                    xk[i] += __shfl_xor_sync(0xffffffffu, xk[i], w);
-                    xq[i] += __shfl_xor_sync(0xffffffffu, xq[i], w);
+                for (int e = 0; e < m; ++e) {
+                    const float send = up ? x[e] : x[e + m], keep = up ? x[e + m] : x[e];
+                    x[e] = keep + __shfl_xor_sync(0xffffffffu, send, w);
                 }
             }
             float u[kStep];
 #pragma unroll
             for (int i = 0; i < kStep; ++i) {
-                const float *a = cf + 16, *beta = cf + 20;
-                float x = beta[i] * (sv[buf][t + i][lrow % kCols] - a[i] * xk[i]);
+                const float *a = cf + kCoefA, *beta = a + kStep;
+                const float xk = LPR > 1 ? __shfl_sync(0xffffffffu, x[i % kHeld], i / kHeld, LPR) : x[i];
+                u[i] = beta[i] * (sv[buf][t + i][lrow % kCols] - a[i] * xk);
 #pragma unroll
-                for (int j = 0; j < i; ++j) x = fmaf(-cf[i * (i - 1) / 2 + j], u[j], x);
-                u[i] = live ? x : 0.f;
-                float o = a[i] * xq[i];
-#pragma unroll
-                for (int j = 0; j <= i; ++j) o = fmaf(cf[6 + i * (i + 1) / 2 + j], u[j], o);
-                if (live && sub == 0) so[t + i][lrow] = p.scale * o;
+                for (int j = 0; j < i; ++j) u[i] = fmaf(-cf[i * (i - 1) / 2 + j], u[j], u[i]);
             }
-            const f2 a3 = pair(cf[19], cf[19]);
+#pragma unroll
+            for (int e = kFirst; e < kHeld; ++e) {
+                const float4 c = qc[e - kFirst];
+                const int i = out0 + e - kFirst;
+                float o = fmaf(c.x, u[0], qa[e - kFirst] * x[e]);
+                if constexpr (LPR <= 2) {  // i is known
+                    if (i >= 1) o = fmaf(c.y, u[1], o);
+                    if (i >= 2) o = fmaf(c.z, u[2], o);
+                    if (i >= 3) o = fmaf(c.w, u[3], o);
+                } else {  // a later token's NaN is not this one's
+                    o = fmaf(c.y, i >= 1 ? u[1] : 0.f, o);
+                    o = fmaf(c.z, i >= 2 ? u[2] : 0.f, o);
+                    o = fmaf(c.w, i >= 3 ? u[3] : 0.f, o);
+                }
+                if (writes) so[t + i][lrow] = p.scale * o;
+            }
+            const f2 a3 = pair(cf[kCoefA + 3], cf[kCoefA + 3]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = mul2(a3, s[e]);
 #pragma unroll
             for (int j = 0; j < kStep; ++j) {
-                const float w = cf[24 + j] * u[j];
+                const float w = cf[kCoefA + 8 + j] * u[j];
                 const f2 w2 = pair(w, w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[e] = fma2(w2, k[j][e], s[e]);
@@ -316,12 +364,16 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     }
 }
 
+// Prompts are taken longest first where not all blocks are resident at once (about three an SM) and a block has a
+// thread for each prompt: 24 prompts of 1 to 400 tokens of 32 heads 1020 us, in their own order 1063.
 template <typename T, typename O, int DK>
 cudaError_t run(Params p, int batch, cudaStream_t stream) {
     constexpr int rows = kThreads / (DK / 16);
     p.slabs = (p.dv + rows - 1) / rows;
     const int64_t blocks = (int64_t)batch * p.hv * p.slabs;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    p.batch = batch;
+    p.sorted = batch > 1 && batch <= kThreads && blocks > 3 * sm_count();
     prefill_simt_kernel<T, O, DK><<<(unsigned)blocks, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
