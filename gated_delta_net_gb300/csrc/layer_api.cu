@@ -58,12 +58,14 @@ int check_prefill(const gdn_prefill_args *a) {
     return GDN_OK;
 }
 
-// Whether the chunked kernel runs.  A chunk takes it 12 us whatever it holds, four tokens take the recurrent one
-// 1.5 us once their heads' blocks are spread over idle SMs (32 heads, 16 / 24 / 32 / 64 tokens: 12.1, 12.1, 12.0, 12.4 us
-// against 7.5, 10.9, 12.8, 23.1); with a (prompt, head) for every SM the chunked one is ahead from one token on (8
-// prompts of 1 / 32 tokens: 17 us against 20 / 67).
+// Whether the chunked kernel runs.  A chunk takes it 12 us whatever it holds.  The recurrent one takes four tokens in
+// about 1.3 us while its blocks are spread over idle SMs (one prompt of 32 heads, 8 / 16 / 28 / 32 / 64 tokens: 5.5,
+// 7.1, 11.2, 11.9, 21.6 us against 12), longer where there are more of them (four prompts of 1 / 4 / 8 / 16 tokens:
+// 12.3, 12.5, 15.4, 20.7 against 12.3), and with a (prompt, head) for every SM the chunked one is ahead from one token
+// on (eight prompts of 1 / 16 tokens: 20.5, 34.7 against 18).
 bool chunked(const gdn_prefill_args &a) {
-    return gdn::prefill_tc_supported(a) && (a.max_tokens > 28 || (int64_t)a.batch * a.n_v_heads >= gdn::sm_count());
+    const int64_t items = (int64_t)a.batch * a.n_v_heads;
+    return gdn::prefill_tc_supported(a) && (a.max_tokens > 28 || items >= gdn::sm_count() || items * a.max_tokens > 28 * 32);
 }
 
 }  // namespace

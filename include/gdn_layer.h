@@ -65,8 +65,8 @@ typedef struct {
  * g = -infinity forgets the state.  A NaN or infinity in q, k or v may reach any
  * output of its own 64-token chunk, and of the tokens after it.
  * bf16 q/k/v/o with d_k = d_v = 128, 16-byte aligned rows and 32-byte aligned pools
- * run the chunked tensor-core kernel, unless the prompts are few and max_tokens is at
- * most 28; everything else runs the recurrent one.  Where few prompts are long, the
+ * run the chunked tensor-core kernel, unless the prompts are few and short (max_tokens
+ * at most 28); everything else runs the recurrent one.  Where few prompts are long, the
  * chunked kernel cuts them into segments and needs the workspace.
  * State errors: about 4e-6 of the state's norm (chunked), 3e-7 (recurrent).
  */
