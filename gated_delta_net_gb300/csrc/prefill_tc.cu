@@ -100,7 +100,7 @@ constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32;
 struct Params {
     int hk_n, hv_n, total, max_tokens, n_states, batch, items, probe;
     bool sorted;                    // prompts longest first
-    int seg, segs;                  // tokens of a segment, a multiple of 64; segments a prompt can have
+    int seg0, seg, segs;            // tokens of the first segment and of the others, multiples of 64; segments a prompt can have
     uint32_t group_inv;             // ceil(2^32 / heads that share a key head), 0 for one
     float scale;
     const int32_t *offsets, *slots, *fresh;
@@ -124,8 +124,8 @@ struct Item {
     float *to;          // where the one after it goes, null for nowhere
 };
 
-// Item number idx of the grid: (slice, request, head).  A slice is a segment; in the first pass, the slices
-// from segs - 1 on are segments 1.. from the identity.
+// Item number idx of the grid: (slice, request, head).  A slice is a segment, the first one last, as it may be
+// shorter; in the first pass the slices are the inner segments, the same from the identity, and the first segment.
 struct Walk {
     const uint8_t *order;  // of the prompts, null for their own
     int idx, h, b, s;
@@ -162,9 +162,11 @@ struct Walk {
         else if (slot < 0 || slot >= p.n_states) x.err = GDN_DEV_BAD_SLOT;
         const int64_t state = ((int64_t)slot * p.hv_n + h) * (kD * kD);
         float *ws = p.ws + ((int64_t)b * p.hv_n + h) * (2 * p.segs - 2) * (kD * kD);
-        x.unit = !OUT && s >= p.segs - 1;
-        const int seg = x.unit ? s - (p.segs - 2) : s, off = seg * p.seg;
-        const bool last = x.n - off <= p.seg, one = x.n <= p.seg;
+        x.unit = !OUT && s >= p.segs - 2 && s < 2 * p.segs - 4;
+        const bool first = s == (OUT ? p.segs - 1 : 2 * p.segs - 4);
+        const int seg = first ? 0 : x.unit ? s - (p.segs - 3) : s + 1;
+        const int off = first ? 0 : p.seg0 + (seg - 1) * p.seg, len = first ? p.seg0 : p.seg;
+        const bool last = x.n - off <= len, one = x.n <= p.seg0;
         x.skip = x.err || (seg > 0 && x.n <= off) || (!OUT && last);
         const bool zero = !p.S0 || raw.fresh != 0;
         if (OUT) {
@@ -175,7 +177,7 @@ struct Walk {
             x.to = ws + (x.unit ? p.segs + seg - 1 : seg + 1) * (kD * kD);
         }
         x.lo += off;
-        x.n = min(x.n - off, p.seg);
+        x.n = min(x.n - off, len);
         x.chunks = x.skip ? 0 : (x.n + kC - 1) / kC;
         return x;
     }
@@ -1151,8 +1153,8 @@ __global__ void __launch_bounds__(256) prefill_join_kernel(Params p) {
     const int part = blockIdx.x % (kD / kJoinRows), item = blockIdx.x / (kD / kJoinRows), h = item % p.hv_n, b = item / p.hv_n;
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), slot = p.slots ? __ldg(p.slots + b) : b;
     const int n = lo >= 0 && hi >= lo && hi <= p.total ? hi - lo : 0;
-    if (n <= p.seg || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
-    const int col = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * (kJoinRows / 2), segs = (n + p.seg - 1) / p.seg;
+    if (n <= p.seg0 || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
+    const int col = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * (kJoinRows / 2), segs = 1 + (n - p.seg0 + p.seg - 1) / p.seg;
     float *ws = p.ws + (int64_t)item * (2 * p.segs - 2) * (kD * kD);
     const int64_t at = (int64_t)(part * kJoinRows + r0) * kD + col;
     const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
@@ -1215,35 +1217,57 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
            (int64_t)a.batch * a.n_v_heads <= 0x7fffffff - 65536 && a.n_v_heads <= 65535 && tensor_map_encoder() != nullptr;
 }
 
-// How many segments a prompt is cut into (1: none), and their length.  In units of a chunk's time on a full GPU (4.2 us;
-// with few blocks running it is down to 0.77 of that): a pass over segments of L chunks takes L + 3 for every wave of
-// blocks, the first pass over its 2 segs - 3 slices 0.7 of that; a join step takes 1.5, the launches 3.  One prompt of
-// 16384 tokens with 32 heads, measured with 1, 2, 3, 4, 6, 8, 9, 16 segments: 842, 795, 571, 622, 643, 658, 675, 790 us.
-int plan_segments(const gdn_prefill_args &a, int &seg) {
+// How many segments a prompt is cut into (1: none), and their lengths.  In units of a chunk's time on a full GPU (4.1 us;
+// with few blocks running it is down to 0.72 of that): a pass takes L + 3 for a wave of blocks with segments of L chunks,
+// the first pass 0.7 of that; a join step takes 1.5, the launches 3.  The first pass has an item for each first segment
+// and two for each inner one: where it would leave a few first segments over, these are made a half or a third as long,
+// and two or three of them go one after the other beside the inner ones.  One prompt of 16384 tokens with 32 heads,
+// measured with 1, 2, 3, 4, 6, 8, 9, 16 equal segments: 842, 795, 571, 622, 643, 658, 675, 790 us; with three and one of
+// half the length: HALF us.
+int plan_segments(const gdn_prefill_args &a, int &seg0, int &seg) {
     const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads;
     const int64_t chunks = std::max<int64_t>(1, ((int64_t)std::min(a.max_tokens, a.total_tokens) + kC - 1) / kC);
-    auto waves = [&](double blocks) { return std::ceil(blocks / sms) * (0.715 + 0.285 * std::min(1.0, blocks / sms)); };
-    double best = 0.9 * (chunks + 3) * waves((double)items);  // worth a tenth at least
+    // time of `count` items of `len`, then `count0` shorter ones of `len0`
+    auto pass = [&](double count, double len, double count0, double len0) {
+        const double full = std::floor(count / sms), rest = count - full * sms;
+        double t = full * len;
+        if (rest > 0) {
+            count0 -= (sms - std::ceil(rest)) * std::floor(len / len0);
+            t += len;
+        }
+        t += std::ceil(std::max(0.0, count0) / sms) * len0;
+        return t;
+    };
+    auto speed = [&](double blocks) { return 0.715 + 0.285 * std::min(1.0, blocks / sms); };
+    double best = 0.9 * pass((double)items, (double)chunks + 3, 0, 1) * speed((double)items);  // worth a tenth at least
     int segs = 1;
-    seg = (int)std::min<int64_t>(chunks * kC, 0x7fffffc0);
+    seg0 = seg = (int)std::min<int64_t>(chunks * kC, 0x7fffffc0);
     for (int64_t s = 2; s <= 24 && s <= chunks && items < sms; ++s) {
-        const int64_t len = (chunks + s - 1) / s;
-        // segments that have tokens: those of every prompt, or as many as all the tokens fill
-        const double pieces = std::min<double>((double)a.batch * s, (double)a.total_tokens / (len * kC) + a.batch) * a.n_v_heads;
-        const double firsts = std::max(0.0, pieces - items) + std::max(0.0, pieces - 2 * items);
-        const double cost = (len + 3) * (waves(pieces) + 0.7 * waves(firsts)) + 1.5 * (s - 2) + 3;
-        if (cost < best && (chunks + len - 1) / len == s) {
-            best = cost;
-            segs = (int)s;
-            seg = (int)(len * kC);
+        for (int part = 1; part <= 3; ++part) {
+            // len0 + 3 = (len + 3) / part and len0 + (s - 1) len = chunks, as far as whole chunks go
+            const int64_t len = (part * (chunks + 3) - 3 + part * (s - 1)) / (part * (s - 1) + 1), len0 = chunks - (s - 1) * len;
+            if (len0 < 1) continue;
+            // segments that have tokens: those of every prompt, or as many as all the tokens fill
+            const double pieces = std::min<double>((double)a.batch * s, (double)a.total_tokens / (len * kC) + a.batch) * a.n_v_heads;
+            const double inner = std::max(0.0, pieces - 2 * items), more = std::max(0.0, pieces - items);
+            const double firsts = std::min((double)items, more);
+            const double cost = pass(more, (double)len + 3, (double)items, (double)len0 + 3) * speed(pieces) +
+                                0.7 * pass(2 * inner, (double)len + 3, firsts, (double)len0 + 3) * speed(2 * inner + firsts) +
+                                1.5 * (s - 2) + 3;
+            if (cost < best) {
+                best = cost;
+                segs = (int)s;
+                seg0 = (int)(len0 * kC);
+                seg = (int)(len * kC);
+            }
         }
     }
     return segs;
 }
 
 int64_t prefill_tc_workspace(const gdn_prefill_args &a) {
-    int seg;
-    const int segs = plan_segments(a, seg);
+    int seg0, seg;
+    const int segs = plan_segments(a, seg0, seg);
     return segs == 1 ? 0 : (int64_t)a.batch * a.n_v_heads * (2 * segs - 2) * (kD * kD * 4);
 }
 
@@ -1274,7 +1298,7 @@ cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     p.offsets = a.token_offsets; p.slots = a.slots; p.fresh = a.fresh;
     p.g = a.g; p.beta = a.beta; p.S0 = a.S0;
     p.o = static_cast<__nv_bfloat16 *>(a.o); p.S_new = a.S_new; p.ws = static_cast<float *>(a.workspace); p.status = a.dev_status;
-    p.segs = plan_segments(a, p.seg);
+    p.segs = plan_segments(a, p.seg0, p.seg);
     if (p.segs > 1) {
         cudaError_t e = launch_pass<false>(tmQ, tmK, tmV, p, 2 * p.segs - 3, stream);
         if (e != cudaSuccess) return e;
