@@ -34,7 +34,7 @@
 // what they compute: loops stay rolled where their steps are alike.
 //
 // 64 prompts of 16 to 512 tokens, 32 value heads, states gathered from a pool: 256 us for 597 MB that have
-// to move (88 us); one prompt of 16384 tokens in three segments, 32 heads: 565 us.  What bounds it is the
+// to move (88 us); one prompt of 16384 tokens in four segments, 32 heads: 505 us.  What bounds it is the
 // vector work that surrounds the products (Gram matrix to A, Y and T, sums to bf16 pairs) and its issue: the
 // schedulers issue in 47 % of cycles with 7 warps each, the tensor pipe is busy for a third.
 #include <algorithm>
@@ -1146,47 +1146,86 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
 }
 
 // The states before the segments of prompts that have several, in place of the first pass's: S before segment s + 1
-// is S_s M_s + L_s, in fp32.  A block takes 16 rows of one (request, head); a thread 8 rows of one column.
-constexpr int kJoinRows = 16;
+// is S_s M_s + L_s, in fp32.  A block takes R rows of one (request, head).  M comes to shared memory a step ahead, as
+// it does not depend on the chain; each of the eight warps takes 16 rows of M, so that M is read there once, and the
+// warps' sums are added up over M's place.
+constexpr int join_smem(int rows) { return (2 * kD * kD + rows * kD) * 4; }
+template <int R>
 __global__ void __launch_bounds__(256) prefill_join_kernel(Params p) {
-    __shared__ __align__(16) float S[kJoinRows][kD];
-    const int part = blockIdx.x % (kD / kJoinRows), item = blockIdx.x / (kD / kJoinRows), h = item % p.hv_n, b = item / p.hv_n;
+    extern __shared__ __align__(16) float join[];
+    float *S = join + 2 * kD * kD;  // [R][kD]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int part = blockIdx.x % (kD / R), item = blockIdx.x / (kD / R), h = item % p.hv_n, b = item / p.hv_n;
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1), slot = p.slots ? __ldg(p.slots + b) : b;
     const int n = lo >= 0 && hi >= lo && hi <= p.total ? hi - lo : 0;
     if (n <= p.seg0 || n > p.max_tokens || slot < 0 || slot >= p.n_states) return;
-    const int col = threadIdx.x & 127, r0 = (threadIdx.x >> 7) * (kJoinRows / 2), segs = 1 + (n - p.seg0 + p.seg - 1) / p.seg;
+    const int segs = 1 + (n - p.seg0 + p.seg - 1) / p.seg;
     float *ws = p.ws + (int64_t)item * (2 * p.segs - 2) * (kD * kD);
-    const int64_t at = (int64_t)(part * kJoinRows + r0) * kD + col;
+    auto fetch = [&](int s) {
+        if (s < segs - 1) {
+            const float *M = ws + (int64_t)(p.segs + s - 1) * (kD * kD);
+            const uint32_t to = smem_u32(join + (s & 1) * kD * kD);
+#pragma unroll
+            for (int i = tid * 4; i < kD * kD; i += 1024)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + i * 4), "l"(M + i) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    fetch(1);
     const bool zero = !p.S0 || (p.fresh && __ldg(p.fresh + b) != 0);
     const float *S0 = p.S0 + ((int64_t)slot * p.hv_n + h) * (kD * kD);
-    float x[kJoinRows / 2];
+    const int64_t rows = (int64_t)part * R * kD;
 #pragma unroll
-    for (int r = 0; r < kJoinRows / 2; ++r) {
-        ws[at + r * kD] = zero ? 0.f : S0[at + r * kD];  // the final state may go to S0's place while segment 0 runs
-        x[r] = ws[kD * kD + at + r * kD];
+    for (int i = tid * 4; i < R * kD; i += 1024) {
+        // the final state may go to S0's place while segment 0 runs
+        *reinterpret_cast<float4 *>(ws + rows + i) = zero ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(S0 + rows + i);
+        *reinterpret_cast<float4 *>(S + i) = *reinterpret_cast<const float4 *>(ws + kD * kD + rows + i);
     }
     for (int s = 1; s < segs - 1; ++s) {
+        float *L = ws + (int64_t)(s + 1) * (kD * kD) + rows, *M = join + (s & 1) * kD * kD;
+        float4 x[R / 8];
+#pragma unroll
+        for (int i = 0; i < R / 8; ++i) x[i] = *reinterpret_cast<const float4 *>(L + tid * 4 + i * 1024);
+        fetch(s + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
+        f2 acc[R][2];
 #pragma unroll
-        for (int r = 0; r < kJoinRows / 2; ++r) S[r0 + r][col] = x[r];
-        __syncthreads();
-        const float *M = ws + (int64_t)(p.segs + s - 1) * (kD * kD) + col;
-        float *L = ws + (int64_t)(s + 1) * (kD * kD) + at;
+        for (int r = 0; r < R; ++r) acc[r][0] = acc[r][1] = 0;
+#pragma unroll 1
+        for (int k = warp * 16; k < warp * 16 + 16; k += 4) {
+            ulonglong2 m[4];
 #pragma unroll
-        for (int r = 0; r < kJoinRows / 2; ++r) x[r] = L[r * kD];
-#pragma unroll 4
-        for (int k = 0; k < kD; k += 4) {
-            const float m0 = M[k * kD], m1 = M[(k + 1) * kD], m2 = M[(k + 2) * kD], m3 = M[(k + 3) * kD];
+            for (int e = 0; e < 4; ++e) m[e] = *reinterpret_cast<const ulonglong2 *>(M + (k + e) * kD + lane * 4);
 #pragma unroll
-            for (int r = 0; r < kJoinRows / 2; ++r) {
-                const float4 v = *reinterpret_cast<const float4 *>(&S[r0 + r][k]);
-                x[r] = fmaf(v.x, m0, fmaf(v.y, m1, fmaf(v.z, m2, fmaf(v.w, m3, x[r]))));
+            for (int r = 0; r < R; ++r) {
+                const float4 v = *reinterpret_cast<const float4 *>(S + r * kD + k);
+                const float y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[r][0] = fma2(pair(y[e], y[e]), m[e].x, acc[r][0]);
+                    acc[r][1] = fma2(pair(y[e], y[e]), m[e].y, acc[r][1]);
+                }
             }
         }
+        __syncthreads();  // M has been read
 #pragma unroll
-        for (int r = 0; r < kJoinRows / 2; ++r) L[r * kD] = x[r];
+        for (int r = 0; r < R; ++r) *reinterpret_cast<ulonglong2 *>(M + (warp * R + r) * kD + lane * 4) = make_ulonglong2(acc[r][0], acc[r][1]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < R / 8; ++i) {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(M + w * R * kD + tid * 4 + i * 1024);
+                x[i] = make_float4(x[i].x + y.x, x[i].y + y.y, x[i].z + y.z, x[i].w + y.w);
+            }
+            *reinterpret_cast<float4 *>(L + tid * 4 + i * 1024) = x[i];
+            *reinterpret_cast<float4 *>(S + tid * 4 + i * 1024) = x[i];
+        }
+        __syncthreads();  // the sums have been read: the M after the next may come
     }
 }
+
 
 // [T][H][128] bf16 tokens `stride` elements apart as a 3-D tensor (d, head, token); boxes of 64 x 1 x 64,
 // 128-byte swizzle
@@ -1219,11 +1258,11 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
 
 // How many segments a prompt is cut into (1: none), and their lengths.  In units of a chunk's time on a full GPU (4.1 us;
 // with few blocks running it is down to 0.72 of that): a pass takes L + 3 for a wave of blocks with segments of L chunks,
-// the first pass 0.7 of that; a join step takes 1.5, the launches 3.  The first pass has an item for each first segment
+// the first pass 0.7 of that; a join step takes 0.4, the launches 3.  The first pass has an item for each first segment
 // and two for each inner one: where it would leave a few first segments over, these are made a half or a third as long,
-// and two or three of them go one after the other beside the inner ones.  One prompt of 16384 tokens with 32 heads,
-// measured with 1, 2, 3, 4, 6, 8, 9, 16 equal segments: 842, 795, 571, 622, 643, 658, 675, 790 us; with three and one of
-// half the length: HALF us.
+// and two or three of them go one after the other beside the inner ones.  One prompt of 16384 tokens with 32 heads:
+// 842 us in one piece, with 2, 3, 4, 6, 8, 16 equal segments 795, 571, 622, 643, 658, 790 (all at one build); 565 with
+// three and 504 with four, the first of them of half the length (at a later one).
 int plan_segments(const gdn_prefill_args &a, int &seg0, int &seg) {
     const int64_t sms = sm_count(), items = (int64_t)a.batch * a.n_v_heads;
     const int64_t chunks = std::max<int64_t>(1, ((int64_t)std::min(a.max_tokens, a.total_tokens) + kC - 1) / kC);
@@ -1242,7 +1281,7 @@ int plan_segments(const gdn_prefill_args &a, int &seg0, int &seg) {
     double best = 0.9 * pass((double)items, (double)chunks + 3, 0, 1) * speed((double)items);  // worth a tenth at least
     int segs = 1;
     seg0 = seg = (int)std::min<int64_t>(chunks * kC, 0x7fffffc0);
-    for (int64_t s = 2; s <= 24 && s <= chunks && items < sms; ++s) {
+    for (int64_t s = 2; s <= std::min<int64_t>(chunks, 128) && items < sms && items * (2 * s - 3) <= 6 * sms; ++s) {
         for (int part = 1; part <= 3; ++part) {
             // len0 + 3 = (len + 3) / part and len0 + (s - 1) len = chunks, as far as whole chunks go
             const int64_t len = (part * (chunks + 3) - 3 + part * (s - 1)) / (part * (s - 1) + 1), len0 = chunks - (s - 1) * len;
@@ -1253,7 +1292,7 @@ int plan_segments(const gdn_prefill_args &a, int &seg0, int &seg) {
             const double firsts = std::min((double)items, more);
             const double cost = pass(more, (double)len + 3, (double)items, (double)len0 + 3) * speed(pieces) +
                                 0.7 * pass(2 * inner, (double)len + 3, firsts, (double)len0 + 3) * speed(2 * inner + firsts) +
-                                1.5 * (s - 2) + 3;
+                                0.4 * (s - 2) + 3;
             if (cost < best) {
                 best = cost;
                 segs = (int)s;
@@ -1283,6 +1322,15 @@ cudaError_t launch_pass(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CU
     return cudaGetLastError();
 }
 
+template <int R>
+cudaError_t launch_join(const Params &p, cudaStream_t stream) {
+    static int have[16];
+    cudaError_t e = ensure_smem(prefill_join_kernel<R>, join_smem(R), have);
+    if (e != cudaSuccess) return e;
+    prefill_join_kernel<R><<<(unsigned)(p.batch * p.hv_n * (kD / R)), 256, join_smem(R), stream>>>(p);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     CUtensorMap tmQ, tmK, tmV;
     if (!encode(&tmQ, a.q, a.n_k_heads, a.total_tokens, token_stride(a.q_stride, a.n_k_heads)) ||
@@ -1302,8 +1350,7 @@ cudaError_t launch_prefill_tc(const gdn_prefill_args &a, cudaStream_t stream) {
     if (p.segs > 1) {
         cudaError_t e = launch_pass<false>(tmQ, tmK, tmV, p, 2 * p.segs - 3, stream);
         if (e != cudaSuccess) return e;
-        prefill_join_kernel<<<(unsigned)(p.batch * p.hv_n * (kD / kJoinRows)), 256, 0, stream>>>(p);
-        e = cudaGetLastError();
+        e = p.batch * p.hv_n * 8 >= sm_count() ? launch_join<16>(p, stream) : launch_join<8>(p, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_pass<true>(tmQ, tmK, tmV, p, p.segs, stream);
