@@ -7,7 +7,9 @@
 // memory.  A row of S takes d_k / 16 lanes with four 16-byte pieces each (128
 // contiguous bytes an instruction for d_k = 128); a warp has two sets of rows in
 // flight, and a block takes an eighth of the heads' rows or more, so that a single
-// request still spreads over the GPU.
+// request still spreads over the GPU.  A head's blocks are neighbours, so that its state is
+// read and written in one run, and it passes the cache as something not needed again soon:
+// 256 requests of 32 heads take 156 us, 6.7 TB/s (169 with neither, 160 with the order alone).
 #include "internal.cuh"
 
 namespace gdn {
@@ -17,7 +19,7 @@ constexpr int kThreads = 128;
 constexpr int kSets = 2;  // row sets a warp has in flight
 
 struct DecodeParams {
-    int hk, hv, dv, n_states;
+    int hk, hv, dv, n_states, slab_bits;  // blocks a head takes, a power of two
     int64_t qs, ks, vs;
     float scale;
     bool vec;  // q and k rows start on 16 bytes
@@ -50,8 +52,9 @@ template <typename T, typename O, int DK>
 __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
     constexpr int LPR = DK / 16, kRowsPerSet = 32 / LPR, kRowsPerBlock = kThreads / 32 * kSets * kRowsPerSet;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % LPR;
-    const int b = blockIdx.x / p.hv, h = blockIdx.x % p.hv, hk = h / (p.hv / p.hk);
-    const int row0 = blockIdx.y * kRowsPerBlock + warp * (kSets * kRowsPerSet) + lane / LPR;
+    const int item = blockIdx.x >> p.slab_bits, slab = blockIdx.x & ((1 << p.slab_bits) - 1);
+    const int b = item / p.hv, h = item % p.hv, hk = h / (p.hv / p.hk);
+    const int row0 = slab * kRowsPerBlock + warp * (kSets * kRowsPerSet) + lane / LPR;
     const int slot = p.slots ? __ldg(p.slots + b) : b;
     O *o = static_cast<O *>(p.o) + ((int64_t)b * p.hv + h) * p.dv;
     if (slot < 0 || slot >= p.n_states) {
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
         const int row = row0 + i * kRowsPerSet;
         if (row < p.dv) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][c] = *reinterpret_cast<const float4 *>(S + (int64_t)row * DK + (c * LPR + sub) * 4);
+            for (int c = 0; c < 4; ++c) s[i][c] = __ldcs(reinterpret_cast<const float4 *>(S + (int64_t)row * DK + (c * LPR + sub) * 4));
         } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -127,18 +130,19 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
             x.y = fmaf(u, k[c][1], alpha * x.y);
             x.z = fmaf(u, k[c][2], alpha * x.z);
             x.w = fmaf(u, k[c][3], alpha * x.w);
-            *reinterpret_cast<float4 *>(S + (int64_t)row * DK + (c * LPR + sub) * 4) = x;
+            __stcs(reinterpret_cast<float4 *>(S + (int64_t)row * DK + (c * LPR + sub) * 4), x);
         }
         if (sub == 0) store_f(o, row, p.scale * fmaf(u, kq, alpha * sq[i]));
     }
 }
 
 template <typename T, typename O, int DK>
-cudaError_t run(const DecodeParams &p, int batch, cudaStream_t stream) {
+cudaError_t run(DecodeParams p, int batch, cudaStream_t stream) {
     constexpr int rows = kThreads / 32 * kSets * (32 / (DK / 16));
     const int64_t items = (int64_t)batch * p.hv;
-    if (items > 0x7fffffff) return cudaErrorInvalidValue;
-    decode_kernel<T, O, DK><<<dim3((unsigned)items, (p.dv + rows - 1) / rows), kThreads, 0, stream>>>(p);
+    while (rows << p.slab_bits < p.dv) ++p.slab_bits;
+    if (items << p.slab_bits > 0x7fffffff) return cudaErrorInvalidValue;
+    decode_kernel<T, O, DK><<<(unsigned)(items << p.slab_bits), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
