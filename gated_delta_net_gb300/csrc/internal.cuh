@@ -82,6 +82,26 @@ cudaError_t launch_residual_norm(const gdn_residual_norm_args &a, cudaStream_t s
 // driver entry point for TMA descriptors (nullptr when the driver lacks it)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// A launch whose blocks may take their places while the kernel before it in the stream ends: the kernel calls
+// after_previous() before it reads or writes global memory, which waits for that kernel to be done and lets the next
+// one do the same.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // Prompts longest first, so that none begins when the others are nearly done: the length of prompt b (-1 where its
 // offsets are not a prompt's), and the place of number i among n lengths.
 __device__ __forceinline__ int prompt_length(const int32_t *offsets, int b) {

@@ -528,3 +528,46 @@ def test_prefill_takes_prompts_in_any_order(dtype, dv, batch):
     alone, _ = gb.gdn_prefill(*[t[at[1]:] for t in x], torch.tensor([0, lengths[1]], dtype=torch.int32, device="cuda"), 90)
     if batch >= 40:  # neither cut into segments: the same bits
         assert torch.equal(alone[:lengths[1]], o[at[1]:at[2]])
+
+
+@pytest.mark.parametrize("T", [3, 5000])
+def test_calls_one_after_the_other_eager_and_in_a_graph(T):
+    # each call reads what the one before wrote, in a stream that ends and begins with torch's own kernels
+    hk, hv, d = 2, 4, 128
+    x = torch.randn(T, (2 * hk + 2 * hv) * d + 2 * hv, generator=torch.Generator().manual_seed(41)).to(BF).cuda()
+    cut = [0, hk * d, 2 * hk * d, (2 * hk + hv) * d, (2 * hk + 2 * hv) * d, (2 * hk + 2 * hv) * d + hv, x.shape[1]]
+    A_log, dt_bias = torch.linspace(-1, 1, hv).cuda(), torch.linspace(-2, 0, hv).cuda()
+    w, wr = torch.linspace(.5, 1.5, d).to(BF).cuda(), torch.linspace(.5, 1.5, hv * d).to(BF).cuda()
+    S0 = pool(42, T, hv, d, d)
+    slots = torch.arange(T, dtype=torch.int32, device="cuda").flip(0)
+
+    def chain(S, wait):
+        S.copy_(S0)
+        y = x
+        for _ in range(3):
+            parts = [y[:, a:b] for a, b in zip(cut, cut[1:])]
+            q, k = parts[0].view(T, hk, d), parts[1].view(T, hk, d)
+            v, z = parts[2].view(T, hv, d), parts[3].view(T, hv, d)
+            q, k, g, beta = gb.gdn_qk_gates(q, k, parts[4], parts[5], A_log, dt_bias)
+            wait()
+            o = gb.gdn_decode(q, k, v, g, beta, S, slots)
+            wait()
+            o = gb.gdn_norm_gate(o, z, w)
+            wait()
+            h, n = gb.gdn_residual_norm(o.view(T, hv * d), parts[2], wr)
+            wait()
+            y = torch.cat([n, h, n, y[:, cut[4]:]], dim=1)
+        return y
+
+    S1, S2, S3 = torch.empty_like(S0), torch.empty_like(S0), torch.empty_like(S0)
+    ref = chain(S1, torch.cuda.synchronize)
+    got = chain(S2, lambda: None)
+    assert torch.equal(ref, got) and torch.equal(S1, S2)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        y = chain(S3, lambda: None)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ref, y) and torch.equal(S1, S3)
