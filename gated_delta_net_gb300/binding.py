@@ -182,6 +182,32 @@ def _code(dtype: torch.dtype) -> int:
     raise TypeError(f"unsupported dtype {dtype}")
 
 
+def _on(stream, device):
+    """``stream`` (torch's, or a handle) as one that torch can allocate for."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device=device)
+
+
+def _scratch(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory that only a launch on ``stream`` (None: the current one) uses.  It is allocated for that stream:
+    a block of another one's may still be in use there by what that stream has yet to do."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_on(stream, device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a result of a launch on ``stream``: as above, and recorded on the current stream, where the
+    caller may use it after a wait of its own."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    t = _scratch(shape, dtype, device, stream)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def gdn_test_set_wait_probe(polls: int) -> None:
     """Test hook: later tensor-core verify/commit launches make one bounded wait of
     ``polls`` polls that runs out (GDN_DEV_TIMEOUT); 0 turns it off."""
@@ -485,14 +511,6 @@ def _handle(stream, t: torch.Tensor) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _keep(t: torch.Tensor, stream) -> None:
-    """Tell torch's allocator of a call's own temporary that it is used on ``stream``."""
-    if stream is not None:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(_handle(stream, t), device=t.device)
-        t.record_stream(stream)
-
-
 def _status(t: Optional[torch.Tensor]) -> int:
     return 0 if t is None else _flat(t, "dev_status", torch.int32, t.shape)
 
@@ -528,14 +546,14 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     if S_new is None:
         if slots is not None:
             raise ValueError("slots need S_new: the pool that they point into")
-        S_new = torch.empty((B, Hv, dv, dk), dtype=torch.float32, device=q.device)
+        S_new = _empty((B, Hv, dv, dk), torch.float32, q.device, stream)
     n_states = S_new.shape[0]
     if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are prompts")
     np_ = _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk))
     s0 = 0 if S0 is None else _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=od, device=q.device)
+        out = _empty((T, Hv, dv), od, q.device, stream)
         outp = out.data_ptr()
     else:
         outp = _flat(out, "out", od, (T, Hv, dv))
@@ -547,8 +565,7 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
         packed = _prefill_args(*a, 0, 0, st)
         need = L.gdn_prefill_workspace(packed)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-            _keep(workspace, stream)
+            workspace = _scratch(need, torch.uint8, q.device, stream)
     if workspace is not None:
         packed = _prefill_args(*a, _flat(workspace, "workspace", torch.uint8, workspace.shape), workspace.numel(), st)
     _check(L.gdn_prefill(packed, stream_handle))
@@ -583,7 +600,7 @@ def gdn_decode(q, k, v, g, beta, S, slots=None, scale: float = 1.0, out=None, ou
     if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are requests")
     if out is None:
-        out = torch.empty((B, Hv, dv), dtype=od, device=q.device)
+        out = _empty((B, Hv, dv), od, q.device, stream)
         outp = out.data_ptr()
     else:
         outp = _flat(out, "out", od, (B, Hv, dv))
@@ -604,17 +621,17 @@ def gdn_qk_gates(q, k, a, b, A_log, dt_bias, eps: float = 1e-6, q_out=None, k_ou
     as_, bs = _rows(a, "a", dt, (T, Hv)), _rows(b, "b", dt, (T, Hv))
     Ap, dp = _flat(A_log, "A_log", torch.float32, (Hv,)), _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
     if q_out is None:
-        q_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+        q_out = _empty((T, Hk, dk), dt, dev, stream)
         qp = q_out.data_ptr()
     else:
         qp = _flat(q_out, "q_out", dt, (T, Hk, dk))
     if k_out is None:
-        k_out = torch.empty((T, Hk, dk), dtype=dt, device=dev)
+        k_out = _empty((T, Hk, dk), dt, dev, stream)
         kp = k_out.data_ptr()
     else:
         kp = _flat(k_out, "k_out", dt, (T, Hk, dk))
-    g = torch.empty((T, Hv), dtype=torch.float32, device=dev)
-    beta = torch.empty((T, Hv), dtype=torch.float32, device=dev)
+    g = _empty((T, Hv), torch.float32, dev, stream)
+    beta = _empty((T, Hv), torch.float32, dev, stream)
     _check(lib().gdn_qk_gates(
         _qk_gates_args(T, Hk, Hv, dk, eps, code, qs, ks, as_, bs, q.data_ptr(), k.data_ptr(), a.data_ptr(),
                        b.data_ptr(), Ap, dp, qp, kp, g.data_ptr(), beta.data_ptr()), _handle(stream, q)))
@@ -630,7 +647,7 @@ def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, 
     if kind is None:
         raise ValueError(f"act must be one of {sorted(GDN_ACTS)}, got {act!r}")
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=dt, device=o.device)
+        out = _empty((T, Hv, dv), dt, o.device, stream)
         outp = out.data_ptr()
     else:
         outp = _flat(out, "out", dt, (T, Hv, dv))
@@ -650,12 +667,12 @@ def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: f
     wp = _flat(weight, "weight", weight.dtype, (D,))
     pp = 0 if post_weight is None else _flat(post_weight, "post_weight", weight.dtype, (D,))
     if h is None:
-        h = torch.empty((T, D), dtype=dt, device=dev)
+        h = _empty((T, D), dt, dev, stream)
         hp = h.data_ptr()
     else:
         hp = _flat(h, "h", dt, (T, D))
     if out is None:
-        out = torch.empty((T, D), dtype=dt, device=dev)
+        out = _empty((T, D), dt, dev, stream)
         outp = out.data_ptr()
     else:
         outp = _flat(out, "out", dt, (T, D))
