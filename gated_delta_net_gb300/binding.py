@@ -183,19 +183,22 @@ def _code(dtype: torch.dtype) -> int:
 
 
 def _on(stream, device):
-    """``stream`` (torch's, or a handle) as one that torch can allocate for."""
+    """``stream`` (torch's, or a handle) as one that torch can allocate for.  The handles 0 to 2 are the default
+    stream's names; the one for each thread (2) is ordered with it."""
     if isinstance(stream, torch.cuda.Stream):
         return stream
-    return torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device=device)
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    return torch.cuda.default_stream(device) if handle <= 2 else torch.cuda.ExternalStream(handle, device=device)
 
 
-def _scratch(shape, dtype, device, stream) -> torch.Tensor:
+def _scratch(shape, dtype, device, stream, zero: bool = False) -> torch.Tensor:
     """Memory that only a launch on ``stream`` (None: the current one) uses.  It is allocated for that stream:
     a block of another one's may still be in use there by what that stream has yet to do."""
+    make = torch.zeros if zero else torch.empty
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
     with torch.cuda.stream(_on(stream, device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return make(shape, dtype=dtype, device=device)
 
 
 def _empty(shape, dtype, device, stream) -> torch.Tensor:
@@ -235,9 +238,9 @@ def gdn_tree_build_desc(parent: torch.Tensor, node_offsets: torch.Tensor, max_no
     T = parent.numel()
     words = mask_words or max(1, (max_nodes + 31) // 32)
     if anc_mask is None:
-        anc_mask = torch.empty((T, words), dtype=torch.int32, device=parent.device)
+        anc_mask = _empty((T, words), torch.int32, parent.device, stream)
     if depth is None:
-        depth = torch.empty(T, dtype=torch.int32, device=parent.device)
+        depth = _empty(T, torch.int32, parent.device, stream)
     _dev(anc_mask, "anc_mask", torch.int32)
     _dev(depth, "depth", torch.int32)
     if anc_mask.shape != (T, words) or depth.numel() != T:
@@ -265,7 +268,7 @@ def gdn_tree_states(k, v, g, beta, S0, node_offsets, parent, anc_mask, sel_reque
     if sel_node.numel() != n_sel or S0.shape != (B, Hv, dv, dk):
         raise ValueError("inconsistent selection / S0 shapes")
     if out is None:
-        out = torch.empty((n_sel, Hv, dv, dk), dtype=torch.float32, device=S0.device)
+        out = _empty((n_sel, Hv, dv, dk), torch.float32, S0.device, stream)
     _dev(out, "out", torch.float32)
     if out.shape != (n_sel, Hv, dv, dk):
         raise ValueError("out must be [n_sel, Hv, d_v, d_k]")
@@ -287,9 +290,9 @@ def gdn_tree_grow(node_offsets: torch.Tensor, n_children: torch.Tensor, draws: t
     if draws.dim() != 2 or draws.shape[0] != T or not draws.is_contiguous():
         raise ValueError("draws must be a contiguous [T, max_children] tensor")
     B = node_offsets.numel() - 1
-    parent = torch.empty(T, dtype=torch.int32, device=draws.device)
-    score = torch.empty(T, dtype=torch.float32, device=draws.device)
-    n_nodes = torch.empty(B, dtype=torch.int32, device=draws.device)
+    parent = _empty(T, torch.int32, draws.device, stream)
+    score = _empty(T, torch.float32, draws.device, stream)
+    n_nodes = _empty(B, torch.int32, draws.device, stream)
     _check(lib().gdn_tree_grow(_ptr(node_offsets), B, T, int(width), int(max_depth), draws.shape[1],
                                _ptr(n_children), _ptr(draws), _ptr(parent), _ptr(score), _ptr(n_nodes),
                                _ptr(dev_status), _stream(stream)))
@@ -303,9 +306,9 @@ def gdn_tree_relabel(parent: torch.Tensor, node_offsets: torch.Tensor, max_nodes
     _dev(parent, "parent", torch.int32)
     _dev(node_offsets, "node_offsets", torch.int32)
     T = parent.numel()
-    order = torch.empty(T, dtype=torch.int32, device=parent.device)
-    rank = torch.empty_like(order)
-    parent_out = torch.empty_like(order)
+    order = _empty(T, torch.int32, parent.device, stream)
+    rank = _empty(T, torch.int32, parent.device, stream)
+    parent_out = _empty(T, torch.int32, parent.device, stream)
     _check(lib().gdn_tree_relabel(_ptr(parent), _ptr(node_offsets), node_offsets.numel() - 1, T,
                                   int(max_nodes), _ptr(order), _ptr(rank), _ptr(parent_out),
                                   _ptr(dev_status), _stream(stream)))
@@ -325,7 +328,7 @@ def gdn_gather_rows(src: torch.Tensor, index: torch.Tensor, node_offsets: torch.
     if index.numel() != T:
         raise ValueError("index must have one entry per row")
     if out is None:
-        out = torch.empty_like(src)
+        out = _empty(src.shape, src.dtype, src.device, stream)
     _dev(out, "out", src.dtype)
     if out.shape != src.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped like src")
@@ -337,7 +340,7 @@ def gdn_gather_rows(src: torch.Tensor, index: torch.Tensor, node_offsets: torch.
 
 
 def _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, max_nodes,
-                 max_depth, scale, out, out_dtype, dev_status):
+                 max_depth, scale, out, out_dtype, dev_status, stream):
     for name, t in (("q", q), ("k", k), ("v", v)):
         _dev(t, name)
     if not (q.dtype == k.dtype == v.dtype):
@@ -356,7 +359,7 @@ def _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, ma
         raise ValueError("inconsistent S0 / tree shapes")
     od = out_dtype or q.dtype
     if out is None:
-        out = torch.empty((T, Hv, dv), dtype=od, device=q.device)
+        out = _empty((T, Hv, dv), od, q.device, stream)
     _dev(out, "out", od)
     if out.shape != (T, Hv, dv):
         raise ValueError("out must be [T, Hv, d_v]")
@@ -372,7 +375,7 @@ def gdn_tree_verify(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth,
                     dev_status=None, stream=None) -> torch.Tensor:
     """Every node's output o [T, Hv, d_v]; S0 is only read."""
     a, out = _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, max_nodes,
-                          max_depth, scale, out, out_dtype, dev_status)
+                          max_depth, scale, out, out_dtype, dev_status, stream)
     _check(lib().gdn_tree_verify(ctypes.byref(a), _stream(stream)))
     return out
 
@@ -382,13 +385,13 @@ def gdn_tree_verify_branches(q, k, v, g, beta, S0, node_offsets, parent, anc_mas
                              out_dtype=None, dev_status=None, stream=None) -> torch.Tensor:
     """Per-branch recurrent baseline; same results as gdn_tree_verify up to rounding."""
     a, out = _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, max_nodes,
-                          max_depth, scale, out, out_dtype, dev_status)
+                          max_depth, scale, out, out_dtype, dev_status, stream)
     _check(lib().gdn_tree_verify_branches(ctypes.byref(a), _stream(stream)))
     return out
 
 
 def _commit_args(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_idx, max_nodes,
-                 max_path, out, dev_status):
+                 max_path, out, dev_status, stream):
     for name, t in (("k", k), ("v", v)):
         _dev(t, name)
     for name, t in (("g", g), ("beta", beta), ("S0", S0)):
@@ -402,11 +405,11 @@ def _commit_args(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_idx
     if S0.shape != (B, Hv, dv, dk) or path_offsets.numel() != B + 1:
         raise ValueError("inconsistent S0 / path shapes")
     if out is None:
-        out = torch.empty_like(S0)
+        out = _empty(S0.shape, torch.float32, S0.device, stream)
     _dev(out, "out", torch.float32)
     if out.shape != S0.shape:
         raise ValueError("out must match S0")
-    pidx = path_idx if path_idx.numel() else torch.zeros(1, dtype=torch.int32, device=k.device)
+    pidx = path_idx if path_idx.numel() else _scratch(1, torch.int32, k.device, stream, zero=True)
     a = CommitArgs(B, Hk, Hv, dk, dv, T, int(max_nodes), int(max_path), _code(k.dtype),
                    _ptr(node_offsets), _ptr(k),
                    _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(parent), _ptr(path_offsets),
@@ -419,7 +422,7 @@ def gdn_tree_commit(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_
                     stream=None) -> torch.Tensor:
     """State after each request's accepted path [B, Hv, d_v, d_k]; ``out`` may be ``S0``."""
     a, out, _keep = _commit_args(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_idx,
-                                 max_nodes, max_path, out, dev_status)
+                                 max_nodes, max_path, out, dev_status, stream)
     _check(lib().gdn_tree_commit(ctypes.byref(a), _stream(stream)))
     return out
 
@@ -433,9 +436,9 @@ def gdn_tree_commit_verify(prev: dict, S0, max_nodes_prev: int, max_path: int,
     ``S0``), and verify the new tree from it.  Returns (o, S_new)."""
     c, S_new, _keep = _commit_args(prev["k"], prev["v"], prev["g"], prev["beta"], S0,
                                    prev["node_offsets"], prev["parent"], prev["path_offsets"],
-                                   prev["path_idx"], max_nodes_prev, max_path, S_new, dev_status)
+                                   prev["path_idx"], max_nodes_prev, max_path, S_new, dev_status, stream)
     a, out = _verify_args(q, k, v, g, beta, S_new, node_offsets, parent, anc_mask, depth, max_nodes,
-                          max_depth, scale, out, out_dtype, dev_status)
+                          max_depth, scale, out, out_dtype, dev_status, stream)
     _check(lib().gdn_tree_commit_verify(ctypes.byref(c), ctypes.byref(a), _stream(stream)))
     return out, S_new
 

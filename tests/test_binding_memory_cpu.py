@@ -76,6 +76,7 @@ def device(monkeypatch):
     monkeypatch.setattr(torch, "empty_like", empty_like)
     monkeypatch.setattr(torch.cuda, "Stream", Stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
@@ -109,11 +110,36 @@ LAYER = {
 }
 
 
+NODES, PARENT = [0, T], [-1, 0, 1, 2, 3, 4]
+
+
+def tree():
+    return ints(*NODES), ints(*PARENT), dev(T, 1, dtype=I32), dev(T, dtype=I32)
+
+
+PREV = dict(zip("k v g beta".split(), rule()[1:]), node_offsets=ints(*NODES), parent=ints(*PARENT),
+            path_offsets=ints(0, 1), path_idx=ints(0))
+TREE = {
+    "build_desc": lambda s: gb.gdn_tree_build_desc(ints(*PARENT), ints(*NODES), T, stream=s),
+    "states": lambda s: gb.gdn_tree_states(*rule()[1:], dev(1, HV, D, D), *tree()[:3], ints(0), ints(1), T, stream=s),
+    "grow": lambda s: gb.gdn_tree_grow(ints(*NODES), dev(T, dtype=I32), dev(T, 2), 3, stream=s),
+    "relabel": lambda s: gb.gdn_tree_relabel(ints(*PARENT), ints(*NODES), T, stream=s),
+    "gather_rows": lambda s: gb.gdn_gather_rows(dev(T, 4), dev(T, dtype=I32), ints(*NODES), stream=s),
+    "verify": lambda s: gb.gdn_tree_verify(*rule(), dev(1, HV, D, D), *tree(), T, stream=s),
+    "verify_branches": lambda s: gb.gdn_tree_verify_branches(*rule(), dev(1, HV, D, D), *tree(), T, stream=s),
+    "commit": lambda s: gb.gdn_tree_commit(*rule()[1:], dev(1, HV, D, D), *tree()[:2], ints(0, 1), ints(0), T, stream=s),
+    "commit_nothing": lambda s: gb.gdn_tree_commit(*rule()[1:], dev(1, HV, D, D), *tree()[:2], ints(0, 0),
+                                                   dev(0, dtype=I32), T, stream=s),
+    "commit_verify": lambda s: gb.gdn_tree_commit_verify(PREV, dev(1, HV, D, D), T, 1, *rule(), *tree(), T, stream=s),
+}
+CALLS = {**LAYER, **TREE}
+
+
 @pytest.mark.parametrize("side", [Stream(9), 9], ids=["stream", "handle"])
-@pytest.mark.parametrize("name", sorted(LAYER))
+@pytest.mark.parametrize("name", sorted(CALLS))
 def test_memory_of_a_call_on_another_stream(device, name, side):
     library, made = device
-    got = LAYER[name](side)
+    got = CALLS[name](side)
     got = got if isinstance(got, tuple) else (got,)
     assert library.streams == [9]
     assert made and [owner for _, owner in made] == [9] * len(made)
@@ -122,9 +148,16 @@ def test_memory_of_a_call_on_another_stream(device, name, side):
         assert t.data_ptr() in mine and t.recorded == [7]
 
 
-@pytest.mark.parametrize("name", sorted(LAYER))
+@pytest.mark.parametrize("name", sorted(CALLS))
 def test_memory_of_a_call_on_the_current_stream(device, name):
     library, made = device
-    LAYER[name](None)
+    CALLS[name](None)
     assert library.streams == [7]
     assert made and all(owner == 7 and not hasattr(t, "recorded") for t, owner in made)
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2])
+def test_names_of_the_default_stream(device, handle):
+    library, made = device
+    gb.gdn_norm_gate(dev(T, HV, D), dev(T, HV, D), dev(D), stream=handle)
+    assert library.streams == [handle] and [owner for _, owner in made] == [0]

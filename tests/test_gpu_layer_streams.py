@@ -52,3 +52,14 @@ def test_results_of_another_stream_that_are_dropped_at_once():
         got = gb.gdn_norm_gate(x[2], x[2], w, stream=side)
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got, ref) and np.all(ones.float().cpu().numpy() == 1.0)
+
+
+def test_names_of_the_default_stream():
+    x = tokens(53, 5, 1, 2, 64, 64, BF)
+    w = torch.ones(64, device="cuda")
+    ref = gb.gdn_norm_gate(x[2], x[2], w)
+    torch.cuda.synchronize()
+    for handle in (0, 1, 2):
+        got = gb.gdn_norm_gate(x[2], x[2], w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
