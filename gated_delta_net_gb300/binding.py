@@ -463,11 +463,22 @@ _prefill_args, _decode_args, _qk_gates_args, _norm_gate_args, _residual_norm_arg
     _packer, (PrefillArgs, DecodeArgs, QkGatesArgs, NormGateArgs, ResidualNormArgs))
 
 
-def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
+def _device(t, name: str) -> int:
+    """The device of a call's first tensor.  It has to be the current one, where kernels are launched, and all
+    other tensors have to be there as well."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
     """The distance between the tokens of ``t`` in elements (0: contiguous), after a check of its
-    type and shape; its other dimensions are contiguous."""
+    type, shape and device; its other dimensions are contiguous."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_cuda:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
             if t.is_contiguous():
                 return 0
             stride = t.stride()
@@ -486,36 +497,38 @@ def _rows(t: torch.Tensor, name: str, dtype, shape) -> int:
             return stride[0]
     except AttributeError:
         pass
-    _refuse(t, name, dtype, shape)
+    _refuse(t, name, dtype, shape, dev)
 
 
-def _flat(t: torch.Tensor, name: str, dtype, shape) -> int:
-    """The address of ``t`` after a check of its type and shape; contiguous."""
+def _flat(t: torch.Tensor, name: str, dtype, shape, dev: int) -> int:
+    """The address of ``t`` after a check of its type, shape and device; contiguous."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
             return t.data_ptr()
     except AttributeError:
         pass
-    _refuse(t, name, dtype, shape)
+    _refuse(t, name, dtype, shape, dev)
 
 
-def _refuse(t, name: str, dtype, shape):
+def _refuse(t, name: str, dtype, shape, dev: int):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the first tensor on cuda:{dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
 
 
-def _handle(stream, t: torch.Tensor) -> int:
-    """The handle of ``stream``, or of the current stream of the device of ``t``."""
+def _handle(stream, dev: int) -> int:
+    """The handle of ``stream``, or of the current stream of device ``dev``."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _status(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else _flat(t, "dev_status", torch.int32, t.shape)
+def _status(t: Optional[torch.Tensor], dev: int) -> int:
+    return 0 if t is None else _flat(t, "dev_status", torch.int32, t.shape, dev)
 
 
 _CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
@@ -537,15 +550,15 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     S0 (None: zero; a prompt with fresh[b] != 0 starts from zero too) and S_new (may be S0)."""
     T, Hk, dk = q.shape
     _, Hv, dv = v.shape
-    dt = q.dtype
+    dt, dev = q.dtype, _device(q, "q")
     od = out_dtype or dt
     code, out_code = _dtype_code(dt), _dtype_code(od)
-    qs, ks, vs = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk)), _rows(v, "v", dt, (T, Hv, dv))
-    gp, bp = _flat(g, "g", torch.float32, (T, Hv)), _flat(beta, "beta", torch.float32, (T, Hv))
+    qs, ks, vs = _rows(q, "q", dt, (T, Hk, dk), dev), _rows(k, "k", dt, (T, Hk, dk), dev), _rows(v, "v", dt, (T, Hv, dv), dev)
+    gp, bp = _flat(g, "g", torch.float32, (T, Hv), dev), _flat(beta, "beta", torch.float32, (T, Hv), dev)
     B = token_offsets.numel() - 1
-    op = _flat(token_offsets, "token_offsets", torch.int32, (B + 1,))
-    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,))
-    fp = 0 if fresh is None else _flat(fresh, "fresh", torch.int32, (B,))
+    op = _flat(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
+    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,), dev)
+    fp = 0 if fresh is None else _flat(fresh, "fresh", torch.int32, (B,), dev)
     if S_new is None:
         if slots is not None:
             raise ValueError("slots need S_new: the pool that they point into")
@@ -553,16 +566,16 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     n_states = S_new.shape[0]
     if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are prompts")
-    np_ = _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk))
-    s0 = 0 if S0 is None else _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk))
+    np_ = _flat(S_new, "S_new", torch.float32, (n_states, Hv, dv, dk), dev)
+    s0 = 0 if S0 is None else _flat(S0, "S0", torch.float32, (n_states, Hv, dv, dk), dev)
     if out is None:
         out = _empty((T, Hv, dv), od, q.device, stream)
         outp = out.data_ptr()
     else:
-        outp = _flat(out, "out", od, (T, Hv, dv))
+        outp = _flat(out, "out", od, (T, Hv, dv), dev)
     a = (B, Hk, Hv, dk, dv, T, max_tokens, n_states, scale, code, out_code, qs, ks, vs, op, q.data_ptr(), k.data_ptr(),
          v.data_ptr(), gp, bp, s0, sp, fp, outp, np_)
-    st, stream_handle, L = _status(dev_status), _handle(stream, q), lib()
+    st, stream_handle, L = _status(dev_status, dev), _handle(stream, dev), lib()
     packed = None
     if workspace is None:
         packed = _prefill_args(*a, 0, 0, st)
@@ -570,7 +583,7 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
         if need > 0:
             workspace = _scratch(need, torch.uint8, q.device, stream)
     if workspace is not None:
-        packed = _prefill_args(*a, _flat(workspace, "workspace", torch.uint8, workspace.shape), workspace.numel(), st)
+        packed = _prefill_args(*a, _flat(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel(), st)
     _check(L.gdn_prefill(packed, stream_handle))
     return out, S_new
 
@@ -592,24 +605,24 @@ def gdn_decode(q, k, v, g, beta, S, slots=None, scale: float = 1.0, out=None, ou
     A row whose slot is -1 is not in use: its outputs are zero."""
     B, Hk, dk = q.shape
     _, Hv, dv = v.shape
-    dt = q.dtype
+    dt, dev = q.dtype, _device(q, "q")
     od = out_dtype or dt
     code, out_code = _dtype_code(dt), _dtype_code(od)
-    qs, ks, vs = _rows(q, "q", dt, (B, Hk, dk)), _rows(k, "k", dt, (B, Hk, dk)), _rows(v, "v", dt, (B, Hv, dv))
-    gp, bp = _flat(g, "g", torch.float32, (B, Hv)), _flat(beta, "beta", torch.float32, (B, Hv))
+    qs, ks, vs = _rows(q, "q", dt, (B, Hk, dk), dev), _rows(k, "k", dt, (B, Hk, dk), dev), _rows(v, "v", dt, (B, Hv, dv), dev)
+    gp, bp = _flat(g, "g", torch.float32, (B, Hv), dev), _flat(beta, "beta", torch.float32, (B, Hv), dev)
     n_states = S.shape[0]
-    Sp = _flat(S, "S", torch.float32, (n_states, Hv, dv, dk))
-    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,))
+    Sp = _flat(S, "S", torch.float32, (n_states, Hv, dv, dk), dev)
+    sp = 0 if slots is None else _flat(slots, "slots", torch.int32, (B,), dev)
     if slots is None and n_states < B:
         raise ValueError("the pool has fewer states than there are requests")
     if out is None:
         out = _empty((B, Hv, dv), od, q.device, stream)
         outp = out.data_ptr()
     else:
-        outp = _flat(out, "out", od, (B, Hv, dv))
+        outp = _flat(out, "out", od, (B, Hv, dv), dev)
     _check(lib().gdn_decode(
         _decode_args(B, Hk, Hv, dk, dv, n_states, scale, code, out_code, qs, ks, vs, q.data_ptr(), k.data_ptr(),
-                     v.data_ptr(), gp, bp, Sp, sp, outp, _status(dev_status)), _handle(stream, q)))
+                     v.data_ptr(), gp, bp, Sp, sp, outp, _status(dev_status, dev)), _handle(stream, dev)))
     return out
 
 
@@ -618,34 +631,34 @@ def gdn_qk_gates(q, k, a, b, A_log, dt_bias, eps: float = 1e-6, q_out=None, k_ou
     projections q, k [T, Hk, d_k] and a, b [T, Hv] (tokens may be strided) and its A_log, dt_bias [Hv]."""
     T, Hk, dk = q.shape
     _, Hv = a.shape
-    dt, dev = q.dtype, q.device
+    dt, dev = q.dtype, _device(q, "q")
     code = _dtype_code(dt)
-    qs, ks = _rows(q, "q", dt, (T, Hk, dk)), _rows(k, "k", dt, (T, Hk, dk))
-    as_, bs = _rows(a, "a", dt, (T, Hv)), _rows(b, "b", dt, (T, Hv))
-    Ap, dp = _flat(A_log, "A_log", torch.float32, (Hv,)), _flat(dt_bias, "dt_bias", torch.float32, (Hv,))
+    qs, ks = _rows(q, "q", dt, (T, Hk, dk), dev), _rows(k, "k", dt, (T, Hk, dk), dev)
+    as_, bs = _rows(a, "a", dt, (T, Hv), dev), _rows(b, "b", dt, (T, Hv), dev)
+    Ap, dp = _flat(A_log, "A_log", torch.float32, (Hv,), dev), _flat(dt_bias, "dt_bias", torch.float32, (Hv,), dev)
     if q_out is None:
-        q_out = _empty((T, Hk, dk), dt, dev, stream)
+        q_out = _empty((T, Hk, dk), dt, q.device, stream)
         qp = q_out.data_ptr()
     else:
-        qp = _flat(q_out, "q_out", dt, (T, Hk, dk))
+        qp = _flat(q_out, "q_out", dt, (T, Hk, dk), dev)
     if k_out is None:
-        k_out = _empty((T, Hk, dk), dt, dev, stream)
+        k_out = _empty((T, Hk, dk), dt, q.device, stream)
         kp = k_out.data_ptr()
     else:
-        kp = _flat(k_out, "k_out", dt, (T, Hk, dk))
-    g = _empty((T, Hv), torch.float32, dev, stream)
-    beta = _empty((T, Hv), torch.float32, dev, stream)
+        kp = _flat(k_out, "k_out", dt, (T, Hk, dk), dev)
+    g = _empty((T, Hv), torch.float32, q.device, stream)
+    beta = _empty((T, Hv), torch.float32, q.device, stream)
     _check(lib().gdn_qk_gates(
         _qk_gates_args(T, Hk, Hv, dk, eps, code, qs, ks, as_, bs, q.data_ptr(), k.data_ptr(), a.data_ptr(),
-                       b.data_ptr(), Ap, dp, qp, kp, g.data_ptr(), beta.data_ptr()), _handle(stream, q)))
+                       b.data_ptr(), Ap, dp, qp, kp, g.data_ptr(), beta.data_ptr()), _handle(stream, dev)))
     return q_out, k_out, g, beta
 
 
 def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, stream=None) -> torch.Tensor:
     """After the rule: o [T, Hv, d_v] normed per head, times weight [d_v] and act(z) (silu or sigmoid)."""
     T, Hv, dv = o.shape
-    dt = o.dtype
-    os_, zs = _rows(o, "o", dt, (T, Hv, dv)), _rows(z, "z", dt, (T, Hv, dv))
+    dt, dev = o.dtype, _device(o, "o")
+    os_, zs = _rows(o, "o", dt, (T, Hv, dv), dev), _rows(z, "z", dt, (T, Hv, dv), dev)
     kind = GDN_ACTS.get(act)
     if kind is None:
         raise ValueError(f"act must be one of {sorted(GDN_ACTS)}, got {act!r}")
@@ -653,10 +666,10 @@ def gdn_norm_gate(o, z, weight, eps: float = 1e-6, act: str = "silu", out=None, 
         out = _empty((T, Hv, dv), dt, o.device, stream)
         outp = out.data_ptr()
     else:
-        outp = _flat(out, "out", dt, (T, Hv, dv))
+        outp = _flat(out, "out", dt, (T, Hv, dv), dev)
     _check(lib().gdn_norm_gate(
         _norm_gate_args(T, Hv, dv, eps, kind, _dtype_code(dt), _dtype_code(weight.dtype), os_, zs, o.data_ptr(),
-                        z.data_ptr(), _flat(weight, "weight", weight.dtype, (dv,)), outp), _handle(stream, o)))
+                        z.data_ptr(), _flat(weight, "weight", weight.dtype, (dv,), dev), outp), _handle(stream, dev)))
     return out
 
 
@@ -665,23 +678,23 @@ def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: f
     """Between two blocks: (h, n) with h = x + scale * y (y normed first where post_weight is given)
     and n = h normed, times weight; x, y [T, width] (tokens may be strided)."""
     T, D = x.shape
-    dt, dev = x.dtype, x.device
-    xs, ys = _rows(x, "x", dt, (T, D)), _rows(y, "y", dt, (T, D))
-    wp = _flat(weight, "weight", weight.dtype, (D,))
-    pp = 0 if post_weight is None else _flat(post_weight, "post_weight", weight.dtype, (D,))
+    dt, dev = x.dtype, _device(x, "x")
+    xs, ys = _rows(x, "x", dt, (T, D), dev), _rows(y, "y", dt, (T, D), dev)
+    wp = _flat(weight, "weight", weight.dtype, (D,), dev)
+    pp = 0 if post_weight is None else _flat(post_weight, "post_weight", weight.dtype, (D,), dev)
     if h is None:
-        h = _empty((T, D), dt, dev, stream)
+        h = _empty((T, D), dt, x.device, stream)
         hp = h.data_ptr()
     else:
-        hp = _flat(h, "h", dt, (T, D))
+        hp = _flat(h, "h", dt, (T, D), dev)
     if out is None:
-        out = _empty((T, D), dt, dev, stream)
+        out = _empty((T, D), dt, x.device, stream)
         outp = out.data_ptr()
     else:
-        outp = _flat(out, "out", dt, (T, D))
+        outp = _flat(out, "out", dt, (T, D), dev)
     _check(lib().gdn_residual_norm(
         _residual_norm_args(T, D, scale, eps, _dtype_code(dt), _dtype_code(weight.dtype), xs, ys, x.data_ptr(),
-                            y.data_ptr(), wp, pp, hp, outp), _handle(stream, x)))
+                            y.data_ptr(), wp, pp, hp, outp), _handle(stream, dev)))
     return h, out
 
 
