@@ -159,19 +159,34 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle without its object
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _dev(t: torch.Tensor, name: str, dtype=None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+def _here() -> int:
+    """The current device, where kernels are launched (-1: there is none)."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -1
+
+
+def _dev(t: torch.Tensor, name: str, here: int, dtype=None) -> torch.Tensor:
+    at = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if at < 0:
         raise TypeError(f"{name} must be a CUDA tensor")
+    if at != here:
+        raise ValueError(f"{name} is on cuda:{at}, which is not the current device")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+def _status_ptr(t: Optional[torch.Tensor], here: int):
+    return None if t is None else _ptr(_dev(t, "dev_status", here))
 
 
 def _code(dtype: torch.dtype) -> int:
@@ -233,34 +248,36 @@ def gdn_tree_build_desc(parent: torch.Tensor, node_offsets: torch.Tensor, max_no
                         depth: Optional[torch.Tensor] = None, mask_words: Optional[int] = None,
                         dev_status: Optional[torch.Tensor] = None, stream=None):
     """Ancestor bitmask [T, mask_words] (int32 storage of uint32 words) and depth [T]."""
-    _dev(parent, "parent", torch.int32)
-    _dev(node_offsets, "node_offsets", torch.int32)
+    here = _here()
+    _dev(parent, "parent", here, torch.int32)
+    _dev(node_offsets, "node_offsets", here, torch.int32)
     T = parent.numel()
     words = mask_words or max(1, (max_nodes + 31) // 32)
     if anc_mask is None:
         anc_mask = _empty((T, words), torch.int32, parent.device, stream)
     if depth is None:
         depth = _empty(T, torch.int32, parent.device, stream)
-    _dev(anc_mask, "anc_mask", torch.int32)
-    _dev(depth, "depth", torch.int32)
+    _dev(anc_mask, "anc_mask", here, torch.int32)
+    _dev(depth, "depth", here, torch.int32)
     if anc_mask.shape != (T, words) or depth.numel() != T:
         raise ValueError("anc_mask must be [T, mask_words] and depth [T]")
     _check(lib().gdn_tree_build_desc(_ptr(parent), _ptr(node_offsets), node_offsets.numel() - 1,
                                      int(max_nodes), _ptr(anc_mask), words, _ptr(depth),
-                                     _ptr(dev_status), _stream(stream)))
+                                     _status_ptr(dev_status, here), _stream(stream)))
     return anc_mask, depth
 
 
 def gdn_tree_states(k, v, g, beta, S0, node_offsets, parent, anc_mask, sel_request, sel_node,
                     max_nodes: int, out=None, dev_status=None, stream=None) -> torch.Tensor:
     """The state at each selected node [n_sel, Hv, d_v, d_k] (fp32)."""
+    here = _here()
     for name, t in (("k", k), ("v", v)):
-        _dev(t, name)
+        _dev(t, name, here)
     for name, t in (("g", g), ("beta", beta), ("S0", S0)):
-        _dev(t, name, torch.float32)
+        _dev(t, name, here, torch.float32)
     for name, t in (("node_offsets", node_offsets), ("parent", parent), ("anc_mask", anc_mask),
                     ("sel_request", sel_request), ("sel_node", sel_node)):
-        _dev(t, name, torch.int32)
+        _dev(t, name, here, torch.int32)
     T, Hk, dk = k.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = node_offsets.numel() - 1
@@ -269,13 +286,13 @@ def gdn_tree_states(k, v, g, beta, S0, node_offsets, parent, anc_mask, sel_reque
         raise ValueError("inconsistent selection / S0 shapes")
     if out is None:
         out = _empty((n_sel, Hv, dv, dk), torch.float32, S0.device, stream)
-    _dev(out, "out", torch.float32)
+    _dev(out, "out", here, torch.float32)
     if out.shape != (n_sel, Hv, dv, dk):
         raise ValueError("out must be [n_sel, Hv, d_v, d_k]")
     a = StatesArgs(B, Hk, Hv, dk, dv, T, int(max_nodes), _code(k.dtype), _ptr(node_offsets), _ptr(k),
                    _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(parent), _ptr(anc_mask),
                    anc_mask.shape[1] if anc_mask.dim() == 2 else 1, n_sel, _ptr(sel_request),
-                   _ptr(sel_node), _ptr(out), _ptr(dev_status))
+                   _ptr(sel_node), _ptr(out), _status_ptr(dev_status, here))
     _check(lib().gdn_tree_states(ctypes.byref(a), _stream(stream)))
     return out
 
@@ -283,9 +300,10 @@ def gdn_tree_states(k, v, g, beta, S0, node_offsets, parent, anc_mask, sel_reque
 def gdn_tree_grow(node_offsets: torch.Tensor, n_children: torch.Tensor, draws: torch.Tensor,
                   width: int, max_depth: int = 16, dev_status=None, stream=None):
     """Top-w best-first trees: (parent [T] int32, score [T] float32, n_nodes [B] int32)."""
-    _dev(node_offsets, "node_offsets", torch.int32)
-    _dev(n_children, "n_children", torch.int32)
-    _dev(draws, "draws", torch.float32)
+    here = _here()
+    _dev(node_offsets, "node_offsets", here, torch.int32)
+    _dev(n_children, "n_children", here, torch.int32)
+    _dev(draws, "draws", here, torch.float32)
     T = n_children.numel()
     if draws.dim() != 2 or draws.shape[0] != T or not draws.is_contiguous():
         raise ValueError("draws must be a contiguous [T, max_children] tensor")
@@ -295,7 +313,7 @@ def gdn_tree_grow(node_offsets: torch.Tensor, n_children: torch.Tensor, draws: t
     n_nodes = _empty(B, torch.int32, draws.device, stream)
     _check(lib().gdn_tree_grow(_ptr(node_offsets), B, T, int(width), int(max_depth), draws.shape[1],
                                _ptr(n_children), _ptr(draws), _ptr(parent), _ptr(score), _ptr(n_nodes),
-                               _ptr(dev_status), _stream(stream)))
+                               _status_ptr(dev_status, here), _stream(stream)))
     return parent, score, n_nodes
 
 
@@ -303,15 +321,16 @@ def gdn_tree_relabel(parent: torch.Tensor, node_offsets: torch.Tensor, max_nodes
                      dev_status: Optional[torch.Tensor] = None, stream=None):
     """Topological relabelling by (depth, old id): (order, rank, parent_out), each [T] int32
     with request-local ids."""
-    _dev(parent, "parent", torch.int32)
-    _dev(node_offsets, "node_offsets", torch.int32)
+    here = _here()
+    _dev(parent, "parent", here, torch.int32)
+    _dev(node_offsets, "node_offsets", here, torch.int32)
     T = parent.numel()
     order = _empty(T, torch.int32, parent.device, stream)
     rank = _empty(T, torch.int32, parent.device, stream)
     parent_out = _empty(T, torch.int32, parent.device, stream)
     _check(lib().gdn_tree_relabel(_ptr(parent), _ptr(node_offsets), node_offsets.numel() - 1, T,
                                   int(max_nodes), _ptr(order), _ptr(rank), _ptr(parent_out),
-                                  _ptr(dev_status), _stream(stream)))
+                                  _status_ptr(dev_status, here), _stream(stream)))
     return order, rank, parent_out
 
 
@@ -319,9 +338,10 @@ def gdn_gather_rows(src: torch.Tensor, index: torch.Tensor, node_offsets: torch.
                     out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """Rows permuted within each request: out[lo + j] = src[lo + index[lo + j]]."""
-    _dev(src, "src")
-    _dev(index, "index", torch.int32)
-    _dev(node_offsets, "node_offsets", torch.int32)
+    here = _here()
+    _dev(src, "src", here)
+    _dev(index, "index", here, torch.int32)
+    _dev(node_offsets, "node_offsets", here, torch.int32)
     if not src.is_contiguous():
         raise ValueError("src must be contiguous")
     T = src.shape[0]
@@ -329,27 +349,28 @@ def gdn_gather_rows(src: torch.Tensor, index: torch.Tensor, node_offsets: torch.
         raise ValueError("index must have one entry per row")
     if out is None:
         out = _empty(src.shape, src.dtype, src.device, stream)
-    _dev(out, "out", src.dtype)
+    _dev(out, "out", here, src.dtype)
     if out.shape != src.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor shaped like src")
     row_bytes = src[0].numel() * src.element_size() if T else 16
     _check(lib().gdn_gather_rows(_ptr(src), _ptr(out), _ptr(index), _ptr(node_offsets),
-                                 node_offsets.numel() - 1, T, row_bytes, _ptr(dev_status),
+                                 node_offsets.numel() - 1, T, row_bytes, _status_ptr(dev_status, here),
                                  _stream(stream)))
     return out
 
 
 def _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, max_nodes,
                  max_depth, scale, out, out_dtype, dev_status, stream):
+    here = _here()
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _dev(t, name)
+        _dev(t, name, here)
     if not (q.dtype == k.dtype == v.dtype):
         raise TypeError("q, k, v must share a dtype")
     for name, t in (("g", g), ("beta", beta), ("S0", S0)):
-        _dev(t, name, torch.float32)
+        _dev(t, name, here, torch.float32)
     for name, t in (("node_offsets", node_offsets), ("parent", parent), ("anc_mask", anc_mask),
                     ("depth", depth)):
-        _dev(t, name, torch.int32)
+        _dev(t, name, here, torch.int32)
     T, Hk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = node_offsets.numel() - 1
@@ -360,13 +381,13 @@ def _verify_args(q, k, v, g, beta, S0, node_offsets, parent, anc_mask, depth, ma
     od = out_dtype or q.dtype
     if out is None:
         out = _empty((T, Hv, dv), od, q.device, stream)
-    _dev(out, "out", od)
+    _dev(out, "out", here, od)
     if out.shape != (T, Hv, dv):
         raise ValueError("out must be [T, Hv, d_v]")
     a = VerifyArgs(B, Hk, Hv, dk, dv, T, int(max_nodes), int(max_depth), float(scale), _code(q.dtype),
                    _code(od), _ptr(node_offsets), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                    _ptr(S0), _ptr(parent), _ptr(anc_mask), anc_mask.shape[1] if anc_mask.dim() == 2 else 1,
-                   _ptr(depth), _ptr(out), _ptr(dev_status))
+                   _ptr(depth), _ptr(out), _status_ptr(dev_status, here))
     return a, out
 
 
@@ -392,13 +413,14 @@ def gdn_tree_verify_branches(q, k, v, g, beta, S0, node_offsets, parent, anc_mas
 
 def _commit_args(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_idx, max_nodes,
                  max_path, out, dev_status, stream):
+    here = _here()
     for name, t in (("k", k), ("v", v)):
-        _dev(t, name)
+        _dev(t, name, here)
     for name, t in (("g", g), ("beta", beta), ("S0", S0)):
-        _dev(t, name, torch.float32)
+        _dev(t, name, here, torch.float32)
     for name, t in (("node_offsets", node_offsets), ("parent", parent),
                     ("path_offsets", path_offsets), ("path_idx", path_idx)):
-        _dev(t, name, torch.int32)
+        _dev(t, name, here, torch.int32)
     T, Hk, dk = k.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = node_offsets.numel() - 1
@@ -406,14 +428,14 @@ def _commit_args(k, v, g, beta, S0, node_offsets, parent, path_offsets, path_idx
         raise ValueError("inconsistent S0 / path shapes")
     if out is None:
         out = _empty(S0.shape, torch.float32, S0.device, stream)
-    _dev(out, "out", torch.float32)
+    _dev(out, "out", here, torch.float32)
     if out.shape != S0.shape:
         raise ValueError("out must match S0")
     pidx = path_idx if path_idx.numel() else _scratch(1, torch.int32, k.device, stream, zero=True)
     a = CommitArgs(B, Hk, Hv, dk, dv, T, int(max_nodes), int(max_path), _code(k.dtype),
                    _ptr(node_offsets), _ptr(k),
                    _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(parent), _ptr(path_offsets),
-                   _ptr(pidx), _ptr(out), _ptr(dev_status))
+                   _ptr(pidx), _ptr(out), _status_ptr(dev_status, here))
     return a, out, pidx
 
 

@@ -30,6 +30,43 @@ def _layer():
     }
 
 
+def _tree():
+    dev, ints, rule = mem.dev, mem.ints, mem.rule
+    nodes, parents = [0, T], [-1, 0, 1, 2, 3, 4]
+    i32 = dict(dtype=torch.int32)
+
+    def tree():
+        return ints(*nodes), ints(*parents), dev(T, 1, **i32), dev(T, **i32)
+
+    def verify(fn):
+        return lambda: fn(*rule(), dev(1, HV, D, D), *tree(), T, out=dev(T, HV, D), dev_status=ints(0))
+
+    def fused():
+        prev = dict(zip("k v g beta".split(), (dev(T, HK, D), dev(T, HV, D), dev(T, HV), dev(T, HV))), node_offsets=ints(*nodes),
+                    parent=ints(*parents), path_offsets=ints(0, 1), path_idx=ints(0))
+        return gb.gdn_tree_commit_verify(prev, dev(1, HV, D, D), T, 1, *rule(), *tree(), T, S_new=dev(1, HV, D, D),
+                                         out=dev(T, HV, D), dev_status=ints(0))
+
+    kv = lambda: (dev(T, HK, D), dev(T, HV, D), dev(T, HV), dev(T, HV))  # noqa: E731
+    return {
+        "build_desc": lambda: gb.gdn_tree_build_desc(ints(*parents), ints(*nodes), T, dev(T, 1, **i32), dev(T, **i32), dev_status=ints(0)),
+        "states": lambda: gb.gdn_tree_states(*kv(), dev(1, HV, D, D), ints(*nodes), ints(*parents), dev(T, 1, **i32), ints(0),
+                                             ints(1), T, out=dev(1, HV, D, D), dev_status=ints(0)),
+        "grow": lambda: gb.gdn_tree_grow(ints(*nodes), dev(T, **i32), dev(T, 2), 3, dev_status=ints(0)),
+        "relabel": lambda: gb.gdn_tree_relabel(ints(*parents), ints(*nodes), T, dev_status=ints(0)),
+        "gather_rows": lambda: gb.gdn_gather_rows(dev(T, 4), dev(T, **i32), ints(*nodes), out=dev(T, 4), dev_status=ints(0)),
+        "verify": verify(gb.gdn_tree_verify),
+        "verify_branches": verify(gb.gdn_tree_verify_branches),
+        "commit": lambda: gb.gdn_tree_commit(*kv(), dev(1, HV, D, D), ints(*nodes), ints(*parents), ints(0, 1), ints(0), T,
+                                             out=dev(1, HV, D, D), dev_status=ints(0)),
+        "commit_verify": fused,
+    }
+
+
+def _calls():
+    return {**_layer(), **_tree()}
+
+
 def _counted(monkeypatch, moved):
     """Make the tensors whose numbers are in ``moved`` (or all) elsewhere; returns the list of those made."""
     made = []
@@ -63,14 +100,14 @@ def _refuses_each(device, monkeypatch, calls, name):
     assert len(library.streams) == 1
 
 
-@pytest.mark.parametrize("name", sorted(_layer()))
+@pytest.mark.parametrize("name", sorted(_calls()))
 def test_a_tensor_on_another_device(device, monkeypatch, name):  # noqa: F811
-    _refuses_each(device, monkeypatch, _layer, name)
+    _refuses_each(device, monkeypatch, _calls, name)
 
 
-@pytest.mark.parametrize("name", sorted(_layer()))
+@pytest.mark.parametrize("name", sorted(_calls()))
 def test_a_device_that_is_not_the_current_one(device, monkeypatch, name):  # noqa: F811
     _counted(monkeypatch, "all")
     with pytest.raises(ValueError):
-        _layer()[name]()
+        _calls()[name]()
     assert device[0].streams == []
