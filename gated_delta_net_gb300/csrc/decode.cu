@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
     const int item = blockIdx.x >> p.slab_bits, slab = blockIdx.x & ((1 << p.slab_bits) - 1);
     const int b = item / p.hv, h = item % p.hv, hk = h / (p.hv / p.hk);
     const int row0 = slab * kRowsPerBlock + warp * (kSets * kRowsPerSet) + lane / LPR;
-    const int slot = p.slots ? __ldg(p.slots + b) : b;
+    const int slot = p.slots ? p.slots[b] : b;
     O *o = static_cast<O *>(p.o) + ((int64_t)b * p.hv + h) * p.dv;
     if (slot < 0 || slot >= p.n_states) {
         if (slot == -1) {
@@ -76,7 +76,10 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
         const int row = row0 + i * kRowsPerSet;
         if (row < p.dv) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][c] = __ldcs(reinterpret_cast<const float4 *>(S + (int64_t)row * DK + (c * LPR + sub) * 4));
+            for (int c = 0; c < 4; ++c) {
+                const uint4 w = load_streaming(S + (int64_t)row * DK + (c * LPR + sub) * 4);
+                s[i][c] = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+            }
         } else {
 #pragma unroll
             for (int c = 0; c < 4; ++c) s[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -89,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) decode_kernel(DecodeParams p) {
         load4(kp + (c * LPR + sub) * 4, p.vec, k[c]);
         load4(qp + (c * LPR + sub) * 4, p.vec, q[c]);
     }
-    const float alpha = expf(__ldg(p.g + (int64_t)b * p.hv + h)), beta = __ldg(p.beta + (int64_t)b * p.hv + h);
+    const float alpha = expf(p.g[(int64_t)b * p.hv + h]), beta = p.beta[(int64_t)b * p.hv + h];
     float v[kSets];
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {

@@ -84,7 +84,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // A launch whose blocks may take their places while the kernel before it in the stream ends: the kernel calls
 // after_previous() before it reads or writes global memory, which waits for that kernel to be done and lets the next
-// one do the same.
+// one do the same.  The kernel before may write in this one's lifetime, so what it may have written is read with
+// ordinary loads: __ldg and the like are for memory that nobody writes while the kernel lives, and the compiler may
+// move them up past the wait.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cudaStream_t stream, A... args) {
     cudaLaunchAttribute attr[1] = {};
@@ -100,6 +102,13 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, cuda
 }
 __device__ __forceinline__ void after_previous() {
     asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// 16 bytes that are not needed again soon, for kernels launched like that: in order with the wait, and coherent.
+__device__ __forceinline__ uint4 load_streaming(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+    return r;
 }
 
 // Prompts longest first, so that none begins when the others are nearly done: the length of prompt b (-1 where its

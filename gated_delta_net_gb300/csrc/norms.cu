@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(kThreads, 16) qk_gates_kernel(QkGates p) {
     const int stride = (gridDim.x - p.row_blocks) * kThreads;
     for (int64_t c = (int)(blockIdx.x - p.row_blocks) * kThreads + threadIdx.x; c < p.cells; c += stride) {
         const int t = p.by_hv.of((uint32_t)c), h = (int)c - t * p.hv;
-        const float x = load_f(static_cast<const T *>(p.a), t * p.as + h) + __ldg(p.dt_bias + h);
-        p.g[c] = -expf(__ldg(p.A_log + h)) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
+        const float x = load_f(static_cast<const T *>(p.a), t * p.as + h) + p.dt_bias[h];
+        p.g[c] = -expf(p.A_log[h]) * (fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))));
         p.beta[c] = sigmoid_f(load_f(static_cast<const T *>(p.b), t * p.bs + h));
     }
 }
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512) residual_norm_kernel(Res
             const int c = threadIdx.x + i * blockDim.x;
             nx[i] = ny[i] = make_uint4(0u, 0u, 0u, 0u);
             if (c < pieces) {
-                nx[i] = __ldcs(reinterpret_cast<const uint4 *>(x + row * p.xs) + c);
-                ny[i] = __ldcs(reinterpret_cast<const uint4 *>(y + row * p.ys) + c);
+                nx[i] = load_streaming(x + row * p.xs + c * N);
+                ny[i] = load_streaming(y + row * p.ys + c * N);
             }
         }
     };
