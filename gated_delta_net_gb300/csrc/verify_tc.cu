@@ -127,6 +127,13 @@ struct Unit {
     bool has2, meta;
 };
 
+// 16 bytes from L2, where the kernel before may have written them in this one's lifetime; in order with griddep_wait()
+__device__ __forceinline__ float4 ld_l2(const float *p) {
+    float4 r;
+    asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p));
+    return r;
+}
+
 __device__ __forceinline__ int hv_of(const Unit &u, int g) { return u.hv0 + (g != 0 && u.has2 ? 1 : 0); }
 
 __device__ __forceinline__ bool unit_ok(int lo, int n, int total) {
@@ -308,6 +315,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     // S0 of value head g of unit u as bf16 (B operand, K-major, 128-byte
     // swizzle) into head g's S space by one warp group; eight rows per batch,
     // double-buffered; lane l holds columns 4l .. 4l + 3 (coalesced row reads).
+    // Read from L2, after a commit S0 is written in this kernel's lifetime.
     auto convert = [&](const Unit &u, int g) {
         const int sw = quad;  // rows 32 sw .. 32 sw + 31 of the state tile
         const float *s0t = p.S0 + ((int64_t)u.b * p.hv_n + hv_of(u, g)) * (kD * kD);
@@ -316,7 +324,7 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         auto s0_load = [&](float4 (&d)[8], int batch) {
 #pragma unroll
             for (int r = 0; r < 8; ++r)
-                d[r] = __ldg(reinterpret_cast<const float4 *>(s0t + (sw * 32 + batch * 8 + r) * kD) + lane);
+                d[r] = ld_l2(s0t + (sw * 32 + batch * 8 + r) * kD + 4 * lane);
         };
         auto s0_put = [&](const float4 (&src)[8], int batch) {
 #pragma unroll

@@ -35,3 +35,13 @@ def test_they_wait_first_and_read_with_ordinary_loads(name):
     assert READ_ONLY.findall(text) == []
     kernels = re.findall(r"__global__[^{;]*\)\s*\{\s*([^\n]*)", text)
     assert kernels and all(first.strip() == "after_previous();" for first in kernels)
+
+
+@pytest.mark.parametrize("name", ["verify_tc.cu", "verify_wide.cu"])
+def test_verification_after_a_commit_reads_its_state_with_coherent_loads(name):
+    # launched while the commit that writes S0 runs; whatever holds S0's address in these files
+    text = _source(name)
+    names = {"S0"} | set(re.findall(r"(\w+) = (?:reinterpret_cast<[^>]*>\()?p\.S0\b", text))
+    assert len(names) > 1
+    for name in names:
+        assert not re.search(r"__ld\w+\([^;]*\b%s\b" % name, text), name
