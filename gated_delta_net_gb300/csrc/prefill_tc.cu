@@ -69,7 +69,7 @@ constexpr int OFF_A = OFF_Y + kKQ * kTile;   // [2] ten 16 x 16 blocks, bf16 hi 
                                              // it (4; before T is known, A's diagonal blocks in fp32)
 constexpr int kBlocks = 10 * 1024;
 constexpr int OFF_SC = OFF_A + 2 * kBlocks;  // [kKQ] gates of a chunk, floats:
-constexpr int SC_REL = 0, SC_BETA = 64, SC_BG = 128;  // (gamma_r - gamma_j) log2 e, r the first token of j's block of 16; beta;
+constexpr int SC_REL = 0, SC_BETA = 64, SC_BG = 128;  // (gamma_e - gamma_j) log2 e, e the last token of j's block of 16; beta;
                                              // -beta e^gamma
 constexpr int SC_COL = 192;                  // e^(gamma_r - gamma_j) for r = 16, 32, 48 and j < r
 constexpr int SC_EG = 288, SC_FD = 352;      // scale e^gamma, e^(gamma_63 - gamma)
@@ -674,11 +674,15 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         const float rh = __shfl_sync(0xffffffffu, h0, 8 * q), rl = __shfl_sync(0xffffffffu, l0, 8 * q);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const float d = (hh[e] - rh) + (lw[e] - rl);
-                            rc[e][q] = __expf(-d);
-                            if ((lane >> 3) == q) rel[e] = -1.4426950408889634f * d;
+                            rc[e][q] = __expf((rh - hh[e]) + (rl - lw[e]));
                         }
                     }
+                    // Within a block from its last token: a difference of two such is good to 2^-24 of the larger one, and
+                    // where that is large, what lies there no longer counts at the block's end.  (From the first token, a
+                    // strong decay early in the block cost all that came after it: 12 tokens that forget, 7e-5 of the state.)
+                    const float eh = __shfl_sync(0xffffffffu, h, lane | 7), elo = __shfl_sync(0xffffffffu, l, lane | 7);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) rel[e] = 1.4426950408889634f * ((eh - hh[e]) + (elo - lw[e]));
                     const float last = __expf(hl + ll);
                     float *sc = place();
                     if (!ok) break;
@@ -746,7 +750,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
                 float *diag = reinterpret_cast<float *>(blocks + 6 * 1024);
                 const f2 rel = pair(-sc[SC_REL + i], -sc[SC_REL + i]);
-                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * exp2_approx(-sc[SC_REL + i]);
+                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * exp2_approx(sc[SC_REL + 16 * own] - sc[SC_REL + i]);
                 if (cc >= 2) wwait(&bar[B_BLKFREE + (cc & 1)], (cc / 2 - 1) & 1, ok);
                 if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], at.ph ^ 1, ok);
                 wwait(&bar[B_G], cc & 1, ok);
