@@ -531,14 +531,23 @@ cudaError_t launch_residual_norm(const gdn_residual_norm_args &a, cudaStream_t s
     p.scale = a.scale;
     p.eps = a.eps;
     p.wvec = aligned16(a.weight) && (!a.post_weight || aligned16(a.post_weight));
-    p.x = a.x; p.y = a.y; p.w = a.weight; p.pw = a.post_weight; p.h = a.h; p.n = a.n;
+    p.w = a.weight; p.pw = a.post_weight;
     const bool vec = vec_rows(a.x, p.xs, e) && vec_rows(a.y, p.ys, e) && vec_rows(a.h, a.width, e) && vec_rows(a.n, a.width, e);
     const bool wb = a.weight_dtype == GDN_BF16;
-    if (a.dtype == GDN_BF16)
-        return wb ? pick_residual_norm<__nv_bfloat16, __nv_bfloat16>(p, a.total_tokens, vec, stream)
-                  : pick_residual_norm<__nv_bfloat16, float>(p, a.total_tokens, vec, stream);
-    return wb ? pick_residual_norm<float, __nv_bfloat16>(p, a.total_tokens, vec, stream)
-              : pick_residual_norm<float, float>(p, a.total_tokens, vec, stream);
+    const int64_t most = 1ll << 30;
+    for (int64_t t = 0; t < a.total_tokens; t += most) {
+        const int n = (int)std::min(most, a.total_tokens - t);
+        p.x = static_cast<const char *>(a.x) + t * p.xs * e;
+        p.y = static_cast<const char *>(a.y) + t * p.ys * e;
+        p.h = static_cast<char *>(a.h) + t * a.width * e;
+        p.n = static_cast<char *>(a.n) + t * a.width * e;
+        const cudaError_t err =
+            a.dtype == GDN_BF16
+                ? (wb ? pick_residual_norm<__nv_bfloat16, __nv_bfloat16>(p, n, vec, stream) : pick_residual_norm<__nv_bfloat16, float>(p, n, vec, stream))
+                : (wb ? pick_residual_norm<float, __nv_bfloat16>(p, n, vec, stream) : pick_residual_norm<float, float>(p, n, vec, stream));
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace gdn
