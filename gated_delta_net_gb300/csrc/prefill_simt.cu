@@ -121,11 +121,11 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     }
     const int lo = __ldg(p.offsets + b), hi = __ldg(p.offsets + b + 1);
     const bool inside = lo >= 0 && hi >= lo && hi <= p.total;
-    const int n = inside ? hi - lo : 0;
+    const unsigned n = inside ? hi - lo : 0;  // with the tokens up to a tile past it more than an int can hold
     const int slot = p.slots ? __ldg(p.slots + b) : b;
     int err = 0;
     if (!inside) err = GDN_DEV_BAD_DESC;
-    else if (n > p.max_tokens) err = GDN_DEV_TOO_MANY;
+    else if (n > (unsigned)p.max_tokens) err = GDN_DEV_TOO_MANY;
     else if (slot < 0 || slot >= p.n_states) err = GDN_DEV_BAD_SLOT;
     if (err) {
         if (tid == 0) flag(p.status, err);
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
     const T *vb = static_cast<const T *>(p.v) + (int64_t)lo * p.vs + h * p.dv + slab * kRows;
     uint4 rk[kLoadK], rq[kLoadK], rv[kLoadV];
     float rg = 0.f, rb = 0.f;
-    auto fetch = [&](int t0) {
+    auto fetch = [&](unsigned t0) {
 #pragma unroll
         for (int i = 0; i < kLoadK; ++i) {
             const int x = (tid + i * kThreads) * VE, t = x / DK, d = x % DK;
@@ -203,8 +203,9 @@ __global__ void __launch_bounds__(kThreads) prefill_simt_kernel(Params p) {
         __syncwarp();
     }
     __syncthreads();
-    for (int t0 = 0, buf = 0; t0 < n; t0 += kTile, buf ^= 1) {
-        const int nt = min(kTile, n - t0);
+    int buf = 0;
+    for (unsigned t0 = 0; t0 < n; t0 += kTile, buf ^= 1) {
+        const int nt = min((unsigned)kTile, n - t0);
         {
             // step number `warp`: its 16 token products, summed over the warp by halves so that lane 2 m ends with
             // number m
