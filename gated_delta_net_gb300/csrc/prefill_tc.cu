@@ -13,9 +13,14 @@
 //     W^T = K^T T''^T, U^T = V^T T'^T - S W^T, O^T = S Q^T and U^T Y^T, dS = U'^T K.
 //
 // Precision: the state's chain keeps fp32 sums, and its operands that are not bf16 already
-// (T', T'', W, S, U') enter as pairs hi + lo of bf16, x = hi + lo to 2^-17; lo x lo is left
-// out (2^-18).  The state comes out about 5e-6 (norm-wise) from exact.  The output's own
-// products take S, U and Y rounded once to bf16, like the output itself.
+// (T', T'', W, S, U') enter as pairs hi + lo of bf16, x = hi + lo to 2^-18; lo x lo is left
+// out (2^-18).  The state comes out about 4e-6 (norm-wise) from exact: bf16 is what the tensor
+// core takes beside the bf16 tokens, and a third part of each operand would not fit.  The output
+// takes the same pairs of S, and Y and U as tf32 (2^-12): 1.68e-3 from exact, of which 1.66e-3
+// are its own rounding to bf16.
+//
+// T and Y are lower triangles: they lie in shared memory, and are multiplied, by strips of 16
+// columns without the rows above them, which is what makes room for Y in 32 bits.
 //
 // One block an SM (all 512 tensor-memory columns), 28 warps:
 //     warp 0        issues W
@@ -25,18 +30,19 @@
 //     warps 4-7, 9, 11  A and Y; T = (I + A)^-1 is then found in blocks of 16:
 //     warps 8, 10   T's diagonal blocks
 //     warps 12-15   T's other blocks, T', T''
-//     warps 16-19   load V, W to shared memory, the outputs to global memory
-//     warps 20-27   the state's hi + lo operand and its decay, U's operands, S Q^T's factors
+//     warps 16-19   load V, W to shared memory, S Q^T's factors, the outputs to global memory
+//     warps 20-27   the state's hi + lo operand and its decay, U' hi + lo
 // The state stays in tensor memory as the sum that dS is added to.  The chain for a chunk is
 // S split -> S W^T -> U split -> dS.
 //
 // The roles run different code at the same time, and what it costs to fetch bounds them as much as
 // what they compute: loops stay rolled where their steps are alike.
 //
-// 64 prompts of 16 to 512 tokens, 32 value heads, states gathered from a pool: 256 us for 597 MB that have
-// to move (88 us); one prompt of 16384 tokens in four segments, 32 heads: 505 us.  What bounds it is the
-// vector work that surrounds the products (Gram matrix to A, Y and T, sums to bf16 pairs) and its issue: the
-// schedulers issue in 47 % of cycles with 7 warps each, the tensor pipe is busy for a third.
+// 64 prompts of 16 to 512 tokens, 32 value heads, states gathered from a pool: 262 us for 597 MB that have
+// to move (88 us); one prompt of 16384 tokens in four segments, 32 heads: 504 us.  (With S, U and Y rounded to bf16 for
+// the outputs 255 and 497, and the outputs 2.8e-3 from exact.)  What bounds it is the latency of the chain, 3.3 us a
+// chunk alone and 4.2 beside the other roles: no pipe is busy for half of the time (issue 47 % of cycles with 7 warps
+// a scheduler, tensor pipe a third).
 #include <algorithm>
 
 #include "internal.cuh"
@@ -62,10 +68,15 @@ constexpr int kDecays = 4;
 constexpr int kTile = kC * 128;              // 64 rows of 128 bytes: half of a token tile
 constexpr int OFF_KQ = 0;                    // [kKQ][2 halves of d][K, Q] tiles
 constexpr int OFF_V = OFF_KQ + kKQ * 4 * kTile;  // [2 halves] tiles
+// Lower triangles, by strips of 16 columns without the rows above them: a strip's 16-byte columns one after the other,
+// rows next to each other (strip s has 64 - 16 s rows, and strip_rows(s) lie in those before it)
+__host__ __device__ constexpr int strip_rows(int s) { return 72 * s - 8 * s * s; }
+constexpr int kTriT = strip_rows(4) * 32;    // T: bf16, two 16-byte columns a strip
+constexpr int kTriY = strip_rows(4) * 64;    // Y: fp32, four
 constexpr int OFF_T = OFF_V + 2 * kTile;     // T' hi, lo, T'' hi, lo (negated): rows i, columns j
-constexpr int OFF_W = OFF_T + 4 * kTile;     // W^T hi, lo: 128 rows of d_k, columns i
+constexpr int OFF_W = OFF_T + 4 * kTriT;     // W^T hi, lo: 128 rows of d_k, columns i
 constexpr int OFF_Y = OFF_W + 4 * kTile;     // [kKQ] Y: rows i, columns j
-constexpr int OFF_A = OFF_Y + kKQ * kTile;   // [2] ten 16 x 16 blocks, bf16 hi and lo: A below the diagonal (6), T on
+constexpr int OFF_A = OFF_Y + kKQ * kTriY;   // [2] ten 16 x 16 blocks, bf16 hi and lo: A below the diagonal (6), T on
                                              // it (4; before T is known, A's diagonal blocks in fp32)
 constexpr int kBlocks = 10 * 1024;
 constexpr int OFF_SC = OFF_A + 2 * kBlocks;  // [kKQ] gates of a chunk, floats:
@@ -85,7 +96,7 @@ constexpr int OFF_BAR = OFF_ORDER + kSorted;
 enum Bar {
     B_FULL = 0, B_EMPTY = B_FULL + kKQ, B_SCFREE = B_EMPTY + kKQ, B_GATES = B_SCFREE + kKQ, B_YFREE = B_GATES + kKQ,
     B_BLK = B_YFREE + kKQ, B_BLKFREE = B_BLK + 2, B_DIAG = B_BLKFREE + 2, B_VFULL = B_DIAG + 4,
-    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_NEXT, B_DRAIN, B_PROBE = B_DRAIN + 3, B_COUNT
+    B_G, B_GFREE, B_T, B_TFREE, B_W, B_WRDY, B_S, B_U, B_SL, B_UST, B_SQ, B_SQRD, B_UPD, B_O, B_OFREE, B_MID, B_NEXT, B_DRAIN, B_PROBE = B_DRAIN + 3, B_COUNT
 };
 constexpr int kSmem = OFF_BAR + B_COUNT * 8;
 static_assert(kSmem <= 232448, "one block an SM");
@@ -93,8 +104,7 @@ static_assert(kSmem <= 232448, "one block an SM");
 // tensor-memory columns
 constexpr uint32_t TM_DS = 0, TM_S = 128, TM_U = 256, TM_O = 320, TM_G = 384, TM_W = 448;
 constexpr uint32_t TM_SHI = TM_S, TM_SLO = TM_S + 64;
-// U' hi, lo lie over S lo, which is free once S W^T is done.  U in bf16 lies over its own sum: tokens 0..31 in the
-// first 16 columns of their half of it, tokens 32..63 in the first 16 of theirs
+// U' hi, lo lie over S lo, which is free once S W^T and S lo Q^T are done.  U's sum is itself the left-hand operand of Y U
 constexpr uint32_t TM_UHI = TM_SLO, TM_ULO = TM_SLO + 32;
 
 struct Params {
@@ -238,6 +248,12 @@ __device__ __forceinline__ uint32_t desc_lo(const void *tile, int lbo_bytes) {
     return ((smem_u32(tile) >> 4) & 0x3FFFu) | ((uint32_t)(lbo_bytes >> 4) << 16);
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// a strip of a triangle: not swizzled, groups of 8 rows after one another, its rows between 16-byte columns
+constexpr uint32_t kStripHi = (128u >> 4) | (1u << 14);
+// low word of columns 16-byte 2 half.. of strip s of a triangle at (smem address >> 4), `columns` of them a strip
+__device__ __forceinline__ constexpr uint32_t strip_lo(uint32_t at, int columns, int s, int half) {
+    return (at + strip_rows(s) * columns + half * 2 * (64 - 16 * s)) | (uint32_t)(64 - 16 * s) << 16;
+}
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 
 __device__ __forceinline__ uint32_t elect() {
@@ -246,17 +262,26 @@ __device__ __forceinline__ uint32_t elect() {
     return r;
 }
 
+// HI: the high word of b
+template <uint32_t HI = kDescHi>
 __device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-                 "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %7};\n\t"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi), "r"(HI) : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
     asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
                  "mov.b64 db, {%2, %6};\n\t"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
                  ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+// tf32 operands: A, 8 columns of tensor memory, times a strip
+__device__ __forceinline__ void mma_ts_tf32(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::tf32 [%0], [%1], db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kStripHi) : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
@@ -301,6 +326,9 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+// A tf32 product cuts both its operands off behind 11 bits, each by 0.36 2^-10 on average (a mantissa from 1 to 2): made up
+// for in one of them, it rounds them.
+constexpr float kTf32Up = 1.f + 0.72f / 1024;
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -376,7 +404,8 @@ __device__ __forceinline__ void put_plain(uint32_t addr, const float (&d)[2][4])
 
 // T's block (bi, bj) as T' and -T'', hi and lo, into the tiles the tensor cores read
 __device__ __forceinline__ void put_block(uint32_t tt, const float *sc, int bi, int bj, int lane, const float (&v)[2][4]) {
-    const uint32_t addr = tt + sw(16 * bi + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * bj + (lane >> 4));
+    const int rows = 64 - 16 * bj;  // of strip bj
+    const uint32_t addr = tt + strip_rows(bj) * 32 + ((lane >> 4) * rows + 16 * (bi - bj) + (lane & 15)) * 16;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         uint32_t hi[4], lo[4];
@@ -385,8 +414,8 @@ __device__ __forceinline__ void put_block(uint32_t tt, const float *sc, int bi, 
             const f2 f = *reinterpret_cast<const f2 *>(sc + (w ? SC_BG : SC_BETA) + 16 * bj + 8 * (e >> 1) + (lane & 3) * 2);
             split2(mul2(pair(v[e >> 1][2 * (e & 1)], v[e >> 1][2 * (e & 1) + 1]), f), hi[e], lo[e]);
         }
-        stm(addr + 2 * w * kTile, hi);
-        stm(addr + (2 * w + 1) * kTile, lo);
+        stm(addr + 2 * w * kTriT, hi);
+        stm(addr + (2 * w + 1) * kTriT, lo);
     }
 }
 __device__ __forceinline__ void diag_block(uint32_t addr, float (&v)[2][4]) {
@@ -448,9 +477,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         // test hook: a wait that runs out, before the roles' own waits begin
         if (p.probe > 0 && !mbar_wait(&bar[B_PROBE], 0, (uint32_t)p.probe)) flag(p.status, GDN_DEV_TIMEOUT);
     }
-    // T's and Y's tiles stay zero above the blocks that are written
-    for (int i = tid; i < (4 + kKQ) * kTile / 16; i += kThreads)
-        *reinterpret_cast<uint4 *>(sm + (i < 4 * kTile / 16 ? OFF_T : OFF_Y - 4 * kTile) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     for (int i = tid; i < 17 * 16; i += kThreads)
         reinterpret_cast<float *>(sm + OFF_MASK)[diag_at(i >> 4, (i >> 2) & 3) + (i & 3)] = (i & 15) < (i >> 4) ? 0.f : -1e30f;
     fence_proxy_async_smem();
@@ -478,8 +504,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         const uint32_t tm = uniform(tmem);
         if (warp == 0) {
             // ---------------------------------------------------------------- W^T = K^T T''^T
-            const uint32_t id = idesc_bf16_f32(128, kC) | (1u << 15);  // K^T is MN-major
-            const uint32_t d_t = uniform(desc_lo(sm + OFF_T, 0));
+            const uint32_t id = idesc_bf16_f32(128, 0) | (1u << 15);  // K^T is MN-major
+            const uint32_t d_t = uniform(smem_u32(sm + OFF_T) >> 4);
             for (; take(sm, bar, at, j, ok); at.next()) {
                 wwait(&bar[B_T], at.cc & 1, ok);
                 if (at.cc > 0) wwait(&bar[B_WRDY], (at.cc - 1) & 1, ok);  // the W before it has been read
@@ -489,7 +515,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 for (int part = 0; part < 2; ++part)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        mma_ss(lead, tm + TM_W, d_k + ks * 128, d_t + (2 + part) * (kTile >> 4) + ks * 2, id, part + ks > 0);
+                        mma_ss<kStripHi>(lead, tm + TM_W + 16 * ks, d_k + ks * 128, strip_lo(d_t + (2 + part) * (kTriT >> 4), 2, ks, 0),
+                                         id | (uint32_t)(8 - 2 * ks) << 17, part + ks > 0);
                 commit(lead, &bar[B_W]);
                 commit(lead, &bar[B_TFREE]);
             }
@@ -512,11 +539,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
             }
         } else if (warp == 2) {
             // ---------------------------------------------------------------- the chain's products
-            const uint32_t id_u = idesc_bf16_f32(128, kC) | (1u << 15);  // V^T (MN-major) T'^T
+            const uint32_t id_u = idesc_bf16_f32(128, 0) | (1u << 15);  // V^T (MN-major) T'^T, by strips
             const uint32_t id_sw = idesc_bf16_f32(128, kC) | (1u << 16); // S (tensor memory) W^T, W MN-major
             const uint32_t id_k = idesc_bf16_f32(128, kC);               // K-major right-hand side
             const uint32_t id_ds = idesc_bf16_f32(128, kD) | (1u << 16); // U' K, K MN-major
-            const uint32_t d_v = uniform(desc_lo(sm + OFF_V, kTile)), d_t = uniform(desc_lo(sm + OFF_T, 0)), d_w = uniform(desc_lo(sm + OFF_W, 0));
+            const uint32_t id_yu = (1u << 4) | (2u << 7) | (2u << 10) | ((128u >> 4) << 24);  // tf32 U^T Y^T, by strips
+            const uint32_t d_v = uniform(desc_lo(sm + OFF_V, kTile)), d_t = uniform(smem_u32(sm + OFF_T) >> 4), d_w = uniform(desc_lo(sm + OFF_W, 0));
             for (; take(sm, bar, at, j, ok); at.next()) {
                     const int cc = at.cc, kq = at.kq;
                     const bool unit = !OUT && (j.flags & kUnit), zero = (j.flags & kFirst) && !j.from && !unit;
@@ -530,9 +558,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (!unit) {
 #pragma unroll 1
                         for (int part = 0; part < 2; ++part)
-#pragma unroll 2
+#pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                mma_ss(lead, tm + TM_U, d_v + ks * 128, d_t + part * (kTile >> 4) + ks * 2, id_u, part + ks > 0);
+                                mma_ss<kStripHi>(lead, tm + TM_U + 16 * ks, d_v + ks * 128, strip_lo(d_t + part * (kTriT >> 4), 2, ks, 0),
+                                                 id_u | (uint32_t)(8 - 2 * ks) << 17, part + ks > 0);
                     }
                     commit(lead, &bar[B_TFREE]);
                     // U^T += S (-W)^T: hi hi, lo hi, hi lo
@@ -552,12 +581,17 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (OUT) {  // O^T = S Q^T
                         if (cc > 0) wwait(&bar[B_OFREE], (cc - 1) & 1, ok);
                         tc_fence_after();
-                        if (!zero) {
+                        // S lo first: U' takes its place
+#pragma unroll 1
+                        for (int part = 0; part < 2; ++part) {
+                            if (!zero) {
 #pragma unroll 2
-                            for (int ks = 0; ks < 8; ++ks)
-                                mma_ts(lead, tm + TM_O, tm + TM_SHI + ks * 8, d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, ks > 0);
+                                for (int ks = 0; ks < 8; ++ks)
+                                    mma_ts(lead, tm + TM_O, tm + (part ? TM_SHI : TM_SLO) + ks * 8,
+                                           d_q + (((ks >> 2) * 2 * kTile + (ks & 3) * 32) >> 4), id_k, part + ks > 0);
+                            }
+                            commit(lead, &bar[part ? B_SQ : B_SL]);
                         }
-                        commit(lead, &bar[B_SQ]);
                     }
                     // S += U'^T K
                     wwait(&bar[B_UST], cc & 1, ok);
@@ -571,10 +605,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                     if (OUT) {  // O^T += U^T Y^T, once S Q^T has its factors
                         wwait(&bar[B_SQRD], cc & 1, ok);
                         tc_fence_after();
-                        const uint32_t d_y = uniform(desc_lo(sm + OFF_Y + kq * kTile, 0));
+                        const uint32_t d_y = uniform(smem_u32(sm + OFF_Y + kq * kTriY) >> 4);
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            mma_ts(lead, tm + TM_O, tm + TM_U + (ks >> 1) * 32 + (ks & 1) * 8, d_y + ((ks * 32) >> 4), id_k, !zero || ks > 0);
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts_tf32(lead, tm + TM_O + 16 * (ks >> 1), tm + TM_U + 8 * ks, strip_lo(d_y, 4, ks >> 1, ks & 1),
+                                        id_yu | (uint32_t)(8 - 2 * (ks >> 1)) << 17, !zero || ks > 0);
                         commit(lead, &bar[B_O]);
                         commit(lead, &bar[B_YFREE + kq]);
                     }
@@ -747,10 +782,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
         for (; (OUT || !is_y) && take(sm, bar, at, j, ok); at.next()) {
                 const int cc = at.cc, kq = at.kq;
                 const float *sc = reinterpret_cast<const float *>(sm + OFF_SC + kq * kGates);
-                uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTile;
+                uint8_t *blocks = sm + OFF_A + (cc & 1) * kBlocks, *yt = sm + OFF_Y + kq * kTriY;
                 float *diag = reinterpret_cast<float *>(blocks + 6 * 1024);
                 const f2 rel = pair(-sc[SC_REL + i], -sc[SC_REL + i]);
-                const float f = is_y ? p.scale : sc[SC_BETA + i], fr = f * exp2_approx(sc[SC_REL + 16 * own] - sc[SC_REL + i]);
+                const float f = is_y ? kTf32Up * p.scale : sc[SC_BETA + i], fr = f * exp2_approx(sc[SC_REL + 16 * own] - sc[SC_REL + i]);
                 if (cc >= 2) wwait(&bar[B_BLKFREE + (cc & 1)], (cc / 2 - 1) & 1, ok);
                 if (is_y && cc >= kKQ) wwait(&bar[B_YFREE + kq], at.ph ^ 1, ok);
                 wwait(&bar[B_G], cc & 1, ok);
@@ -788,15 +823,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                         }
                         if (cb <= own) {
                             if (is_y) {
+                                uint8_t *to = yt + strip_rows(cb) * 64 + (i - 16 * cb) * 16;
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    uint32_t y[4];
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const float2 v = parts(m[4 * q + e]);
-                                        y[e] = pack_bf16(v.x, v.y);
-                                    }
-                                    *reinterpret_cast<uint4 *>(yt + sw(i, 2 * cb + q)) = make_uint4(y[0], y[1], y[2], y[3]);
+                                for (int q = 0; q < 4; ++q) {
+                                    *reinterpret_cast<ulonglong2 *>(to + q * (64 - 16 * cb) * 16) = make_ulonglong2(m[2 * q], m[2 * q + 1]);
                                 }
                             } else if (cb == own) {
 #pragma unroll
@@ -1106,20 +1136,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant
                 tc_fence_after();
 #pragma unroll 1
                 for (int j0 = 0; j0 < 32; j0 += 16) {
-                    uint32_t r[16], hi[8], lw[8], ub[8];
+                    uint32_t r[16], hi[8], lw[8];
                     tmem_ld16_nowait(lanes + TM_U + half * 32 + j0, r);
                     tmem_wait_ld_into(r);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sc + SC_FD + j0 + j);
-                        ub[j / 2] = pack_bf16(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
-                        ub[j / 2 + 1] = pack_bf16(__uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
                         split2(mul2(pair(r[j], r[j + 1]), f.x), hi[j / 2], lw[j / 2]);
                         split2(mul2(pair(r[j + 2], r[j + 3]), f.y), hi[j / 2 + 1], lw[j / 2 + 1]);
                     }
+                    if (OUT && j0 == 0) {  // S lo has been read
+                        wwait(&bar[B_SL], cc & 1, ok);
+                        tc_fence_after();
+                    }
                     tmem_st8(lanes + TM_UHI + half * 16 + j0 / 2, hi);
                     tmem_st8(lanes + TM_ULO + half * 16 + j0 / 2, lw);
-                    if (OUT) tmem_st8(lanes + TM_U + half * 32 + j0 / 2, ub);
                 }
                 tmem_wait_st();
                 tc_fence_before();

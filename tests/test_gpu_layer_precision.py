@@ -59,3 +59,17 @@ def test_prefill_states_and_outputs(lengths):
     assert far(S, rS, (2, 3)) <= 1e-5
     assert far(o, ro, (0, 2)) <= 2.0 ** -7
     assert far(o, ro, 2) <= 2.0 ** -5  # each row of its own, small ones too: a row's terms may cancel to a quarter
+
+
+@pytest.mark.parametrize("lengths", [[64], [300, 1000], [3000]], ids=str)
+def test_prefill_outputs_are_rounded_to_bf16_once(lengths):
+    # rounding to bf16 is 2^-9 / sqrt(3) of a value's leading bit, 1.66e-3 norm-wise over mantissas of 1 to 2.  The
+    # products' operands have 2^-12 of theirs (tf32) or less: two times 2^-12 / sqrt(3), of terms that are up to twice
+    # the sum, leave it below 2^-9
+    hk, hv, d = 2, 4, 128
+    x = tokens(64, sum(lengths), hk, hv, d, d, BF, slow=True)
+    off = offsets(lengths)
+    S0 = pool(65, len(lengths), hv, d, d)
+    o, _ = gb.gdn_prefill(*x, off, max(lengths), S0=S0, scale=d ** -0.5)
+    ro, _ = OL.prefill(*map(f64, x), off.cpu().numpy(), S0=f64(S0), scale=d ** -0.5)
+    assert far(o, ro, (0, 2)) <= 2.0 ** -9
