@@ -2,7 +2,7 @@
 argument marshalling only.
 
 Every function has the name of the C entry point it calls.  Tensors are torch
-tensors on the CUDA device (torch provides memory and streams; every step of
+tensors on the current CUDA device (torch provides memory and streams; every step of
 the computation runs in the library's kernels).  The library is loaded on
 first use from ``_build/libgdn_tree.so``; if it is missing the call raises,
 there is no other implementation to fall back to.
@@ -569,7 +569,9 @@ def gdn_prefill(q, k, v, g, beta, token_offsets, max_tokens: int, S0=None, slots
     """Prompts, packed: (o [T, Hv, d_v], S_new).  Prompt b is rows token_offsets[b] to
     token_offsets[b + 1] of q, k [T, Hk, d_k], v [T, Hv, d_v] (tokens may be strided) and of
     g, beta [T, Hv]; max_tokens bounds its length.  Its state is row slots[b] (or b) of the pools
-    S0 (None: zero; a prompt with fresh[b] != 0 starts from zero too) and S_new (may be S0)."""
+    S0 (None: zero; a prompt with fresh[b] != 0 starts from zero too) and S_new (may be S0).
+    bf16 in and out with heads of 128 take the chunked kernel; other types and widths, out_dtype=float32
+    among them, the recurrent one: fp32 arithmetic, about ten times as long."""
     T, Hk, dk = q.shape
     _, Hv, dv = v.shape
     dt, dev = q.dtype, _device(q, "q")

@@ -9,7 +9,7 @@
 // flight, and a block takes an eighth of the heads' rows or more, so that a single
 // request still spreads over the GPU.  A head's blocks are neighbours, so that its state is
 // read and written in one run, and it passes the cache as something not needed again soon:
-// 256 requests of 32 heads take 153 us, 6.9 TB/s (155 without the early launch, 169 with none of
+// 256 requests of 32 heads take 152 us, 6.9 TB/s (155 without the early launch, 169 with none of
 // this).
 #include "internal.cuh"
 

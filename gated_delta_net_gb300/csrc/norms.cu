@@ -5,8 +5,8 @@
 // once, a row stays in registers between its sum of squares and its result.  Heads
 // are narrow (d <= 128), so a row takes 16 bytes a lane and as few lanes as that
 // needs (a half-warp for 128 bf16 values).  16384 tokens of 16 key and 32 value heads of 128 in bf16
-// take 44 us (qk_gates, 6.3 TB/s) and 59 us (norm_gate, 6.8 TB/s), 8192 rows of 5120 with the post norm
-// 54 us (residual_norm, 6.2 TB/s), 2 us less each than without the early launch.
+// take 43.7 us (qk_gates, 6.3 TB/s) and 59.5 us (norm_gate, 6.8 TB/s), 8192 rows of 5120 with the post norm
+// 53.8 us (residual_norm, 6.2 TB/s), 2 us less each than without the early launch.
 #include <algorithm>
 
 #include "internal.cuh"
@@ -119,8 +119,8 @@ __device__ __forceinline__ float group_sum(float x) {
 __device__ __forceinline__ float sigmoid_f(float x) { return 1.f / (1.f + expf(-x)); }
 
 // x times its gate.  What is rounded to bf16 takes the fast exponential and quotient (a few 2^-21 for the
-// gates that are not negligible); with the exact ones the kernel was bound by arithmetic: 179 us for 16384
-// tokens of 32 heads of 128, against 59 us for its bytes.
+// gates that are not negligible); with the exact ones the kernel is bound by arithmetic: 77 us for 16384
+// tokens of 32 heads of 128, against 59.5.  In fp32, with twice the bytes, they fit beside them: 113 us.
 template <typename T>
 __device__ __forceinline__ float gated(float x, float z, int act) {
     const float num = act == GDN_ACT_SILU ? x * z : x;

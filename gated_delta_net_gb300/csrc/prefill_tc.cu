@@ -1291,7 +1291,7 @@ bool prefill_tc_supported(const gdn_prefill_args &a) {
            (int64_t)a.batch * a.n_v_heads <= 0x7fffffff - 65536 && a.n_v_heads <= 65535 && tensor_map_encoder() != nullptr;
 }
 
-// How many segments a prompt is cut into (1: none), and their lengths.  In units of a chunk's time on a full GPU (4.1 us;
+// How many segments a prompt is cut into (1: none), and their lengths.  In units of a chunk's time on a full GPU (4.2 us;
 // with few blocks running it is down to 0.72 of that): a pass takes L + 3 for a wave of blocks with segments of L chunks,
 // the first pass 0.7 of that; a join step takes 0.4, the launches 3.  The first pass has an item for each first segment
 // and two for each inner one: where it would leave a few first segments over, these are made a half or a third as long,
@@ -1348,7 +1348,8 @@ int64_t prefill_tc_workspace(const gdn_prefill_args &a) {
 template <bool OUT>
 cudaError_t launch_pass(const CUtensorMap &tmQ, const CUtensorMap &tmK, const CUtensorMap &tmV, Params p, int slices, cudaStream_t stream) {
     p.items = p.batch * p.hv_n * slices;
-    // the longest first, so that the blocks end together: 256 us for 64 prompts of 16 to 512 tokens, in their own order 267
+    // the longest first, so that the blocks end together: 256 us for 64 prompts of 16 to 512 tokens, in their own order 267 (at
+    // one build)
     p.sorted = slices == 1 && p.batch > 1 && p.batch <= kSorted && p.items > sm_count();
     static int have[16];
     cudaError_t e = ensure_smem(prefill_tc_kernel<OUT>, kSmem, have);

@@ -62,13 +62,17 @@ typedef struct {
  * initial state.  A prompt longer than max_tokens sets GDN_DEV_TOO_MANY, offsets
  * that descend or pass T set GDN_DEV_BAD_DESC, and a slot outside the pool sets
  * GDN_DEV_BAD_SLOT; that request is skipped, its outputs and state are not written.
- * g = -infinity forgets the state.  A NaN or infinity in q, k or v may reach any
- * output of its own 64-token chunk, and of the tokens after it.
+ * g = -infinity forgets the state.  A NaN or infinity in q, k or v, or a NaN in g or beta,
+ * may reach any output of its own 64-token chunk, and of the tokens after it.
  * bf16 q/k/v/o with d_k = d_v = 128, 16-byte aligned rows and 32-byte aligned pools
  * run the chunked tensor-core kernel, unless the prompts are few and short (max_tokens
  * at most 28); everything else runs the recurrent one.  Where few prompts are long, the
  * chunked kernel cuts them into segments and needs the workspace.
- * State errors: about 4e-6 of the state's norm (chunked), 3e-7 (recurrent).
+ * The recurrent kernel computes in fp32 whatever the types, a token after another: bf16 prompts
+ * with fp32 outputs get that, and take about ten times the chunked kernel's time (one prompt of
+ * 16384 tokens, 32 heads: 5.2 ms, 0.5 ms).
+ * Errors, norm-wise: states about 4e-6 (chunked) or 3e-7 (recurrent), bf16 outputs 1.68e-3
+ * (chunked) or 1.66e-3, which is their own rounding.
  */
 GDN_API int gdn_prefill(const gdn_prefill_args *args, void *stream);
 
