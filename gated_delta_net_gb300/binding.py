@@ -1,5 +1,5 @@
-"""Thin Python binding of ``include/gdn_tree.h`` and ``include/gdn_layer.h``:
-argument marshalling only.
+"""Thin Python binding of ``include/gdn_tree.h``, ``include/gdn_layer.h`` and
+``include/gdn_attention.h``: argument marshalling only.
 
 Every function has the name of the C entry point it calls.  Tensors are torch
 tensors on the current CUDA device (torch provides memory and streams; every step of
@@ -22,7 +22,7 @@ GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED = 0, 1, 2
 GDN_ERR_INVALID_TREE, GDN_ERR_INVALID_PATH, GDN_ERR_CUDA, GDN_ERR_DEVICE = 3, 4, 5, 6
 GDN_F32, GDN_BF16 = 0, 1
 DEV_BITS = {1: "BAD_TREE", 2: "BAD_PATH", 4: "TOO_MANY", 8: "TOO_DEEP", 16: "TIMEOUT", 64: "INTERNAL",
-            32: "BAD_DESC", 128: "BAD_SLOT"}
+            32: "BAD_DESC", 128: "BAD_SLOT", 256: "BAD_PAGE", 512: "BAD_POSITION"}
 GDN_ACTS = {"silu": 0, "sigmoid": 1}
 
 _P = ctypes.c_void_p
@@ -91,6 +91,29 @@ class ResidualNormArgs(ctypes.Structure):
                 ("post_weight", _P), ("h", _P), ("n", _P)]
 
 
+_CACHE = [("batch", _I), ("n_pages", _I), ("page_size", _I), ("max_pages", _I), ("n_kv_heads", _I), ("d", _I), ("dtype", _I),
+          ("page_stride", _L), ("slot_stride", _L), ("head_stride", _L), ("k_cache", _P), ("v_cache", _P), ("page_table", _P),
+          ("lens", _P), ("dev_status", _P)]  # gdn_kv_cache, which every struct of gdn_attention.h begins with
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = _CACHE + [("total_tokens", _I), ("n_q_heads", _I), ("rot_dim", _I), ("interleaved", _I), ("n_positions", _I),
+                         ("weight_dtype", _I), ("eps", _F), ("q_stride", _L), ("k_stride", _L), ("v_stride", _L), ("q", _P),
+                         ("k", _P), ("v", _P), ("token_offsets", _P), ("depth", _P), ("cos_sin", _P), ("q_weight", _P),
+                         ("k_weight", _P), ("q_out", _P)]
+
+
+class KvAttendArgs(ctypes.Structure):
+    _fields_ = _CACHE + [("total_tokens", _I), ("max_tokens", _I), ("n_q_heads", _I), ("mask_words", _I), ("out_dtype", _I),
+                         ("scale", _F), ("q_stride", _L), ("q", _P), ("token_offsets", _P), ("anc_mask", _P), ("o", _P),
+                         ("workspace", _P), ("workspace_bytes", _L)]
+
+
+class KvCommitArgs(ctypes.Structure):
+    _fields_ = _CACHE + [("node_offsets", _P), ("path_offsets", _P), ("path_idx", _P), ("total_path", _I),
+                         ("new_lens", _P)]
+
+
 class GdnError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"gdn status {code}: {msg}")
@@ -139,6 +162,11 @@ def lib():
         for fn in (L.gdn_prefill, L.gdn_decode, L.gdn_qk_gates, L.gdn_norm_gate, L.gdn_residual_norm):
             fn.argtypes = [_P, _P]
             fn.restype = ctypes.c_int
+        for fn in (L.gdn_kv_append, L.gdn_kv_attend, L.gdn_kv_decode, L.gdn_kv_commit):
+            fn.argtypes = [_P, _P]
+            fn.restype = ctypes.c_int
+        L.gdn_kv_attend_workspace.argtypes = [_P, _I]
+        L.gdn_kv_attend_workspace.restype = _L
         L.gdn_prefill_workspace.argtypes = [_P]
         L.gdn_prefill_workspace.restype = _L
         L.gdn_last_error.restype = ctypes.c_char_p
@@ -720,6 +748,176 @@ def gdn_residual_norm(x, y, weight, scale: float = 1.0, post_weight=None, eps: f
         _residual_norm_args(T, D, scale, eps, _dtype_code(dt), _dtype_code(weight.dtype), xs, ys, x.data_ptr(),
                             y.data_ptr(), wp, pp, hp, outp), _handle(stream, dev)))
     return h, out
+
+
+# ----------------------------------------------------------------------------
+# the attention layers' paged cache (gdn_attention.h)
+# ----------------------------------------------------------------------------
+
+_kv_append_args, _kv_attend_args, _kv_commit_args = map(_packer, (KvAppendArgs, KvAttendArgs, KvCommitArgs))
+
+
+def _cache(k_cache, v_cache, page_table, lens, dev_status, dev: int, dt) -> tuple:
+    """The values of gdn_kv_cache: pools [n_pages, page_size, Hkv, d] of any strides over the first three dimensions, the
+    same for both, page_table [B, max_pages], lens [B]."""
+    try:
+        shape, stride = k_cache.shape, k_cache.stride()
+        n_pages, page_size, hkv, d = shape
+        B, max_pages = page_table.shape
+        fine = (k_cache.dtype is dt and v_cache.dtype is dt and v_cache.shape == shape and v_cache.stride() == stride
+                and (stride[3] == 1 or d == 1) and k_cache.get_device() == dev and v_cache.get_device() == dev)
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _refuse_cache(k_cache, v_cache, page_table, dt, dev)
+    return (B, n_pages, page_size, max_pages, hkv, d, _dtype_code(dt), stride[0], stride[1], stride[2], k_cache.data_ptr(), v_cache.data_ptr(),
+            _flat(page_table, "page_table", torch.int32, (B, max_pages), dev), _flat(lens, "lens", torch.int32, (B,), dev),
+            _status(dev_status, dev))
+
+
+def _refuse_cache(k_cache, v_cache, page_table, dt, dev: int):
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("page_table", page_table)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the first tensor on cuda:{dev}")
+    if k_cache.dtype is not dt or v_cache.dtype is not dt:
+        raise TypeError(f"the cache must be {dt}, got {k_cache.dtype} and {v_cache.dtype}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    raise ValueError("k_cache and v_cache must be [n_pages, page_size, Hkv, d] with the same strides, d contiguous, got "
+                     f"{list(k_cache.shape)}, {list(v_cache.shape)}")
+
+
+def gdn_kv_append(q, k, v, k_cache, v_cache, page_table, lens, token_offsets=None, depth=None, cos_sin=None,
+                  interleaved: bool = False, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None, dev_status=None, stream=None):
+    """New tokens k, v [T, Hkv, d] (tokens may be strided) into the slots of the paged cache behind lens [B], keys
+    normed by k_weight [d] and rotated by cos_sin [positions, rot_dim] (None: not at all) on the way; returns the queries
+    q [T, Hq, d] (or None) normed by q_weight and rotated.  token_offsets [B + 1] packs several tokens a request (None: one
+    each); depth [T] is gdn_tree_build_desc's for a draft's nodes."""
+    T, hkv, d = k.shape
+    dt, dev = k.dtype, _device(k, "k")
+    cache = _cache(k_cache, v_cache, page_table, lens, dev_status, dev, dt)
+    B = cache[0]
+    if cache[4] != hkv or cache[5] != d:
+        raise ValueError(f"k has heads {[hkv, d]}, the cache {[cache[4], cache[5]]}")
+    ks, vs = _rows(k, "k", dt, (T, hkv, d), dev), _rows(v, "v", dt, (T, hkv, d), dev)
+    if token_offsets is None:
+        if T != B:
+            raise ValueError(f"{T} tokens for {B} requests need token_offsets")
+        off = 0
+    else:
+        off = _flat(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
+    dp = 0 if depth is None else _flat(depth, "depth", torch.int32, (T,), dev)
+    rot = positions = cp = 0
+    if cos_sin is not None:
+        positions, rot = cos_sin.shape
+        cp = _flat(cos_sin, "cos_sin", torch.float32, (positions, rot), dev)
+    first = q_weight if q_weight is not None else k_weight
+    wt = torch.float32 if first is None else first.dtype
+    qw = 0 if q_weight is None else _flat(q_weight, "q_weight", wt, (d,), dev)
+    kw = 0 if k_weight is None else _flat(k_weight, "k_weight", wt, (d,), dev)
+    hq = qs = qp = op = 0
+    if q is not None:
+        hq = q.shape[1]
+        qs = _rows(q, "q", dt, (T, hq, d), dev)
+        qp = q.data_ptr()
+        if q_out is None:
+            q_out = _empty((T, hq, d), dt, q.device, stream)
+            op = q_out.data_ptr()
+        else:
+            op = _flat(q_out, "q_out", dt, (T, hq, d), dev)
+    _check(lib().gdn_kv_append(
+        _kv_append_args(*cache, T, hq, rot, bool(interleaved), positions, _dtype_code(wt), eps, qs, ks, vs, qp, k.data_ptr(),
+                        v.data_ptr(), off, dp, cp, qw, kw, op), _handle(stream, dev)))
+    return q_out if q is not None else None
+
+
+def _attend(decode: bool, q, k_cache, v_cache, page_table, lens, token_offsets, max_tokens, anc_mask, scale, out, out_dtype,
+            workspace, dev_status, stream):
+    T, hq, d = q.shape
+    dt, dev = q.dtype, _device(q, "q")
+    od = out_dtype or dt
+    out_code = _dtype_code(od)
+    cache = _cache(k_cache, v_cache, page_table, lens, dev_status, dev, dt)
+    if cache[5] != d:
+        raise ValueError(f"q has heads of {d}, the cache of {cache[5]}")
+    if decode and T != cache[0]:
+        raise ValueError(f"{T} tokens for {cache[0]} requests")
+    qs = _rows(q, "q", dt, (T, hq, d), dev)
+    off = 0 if decode else _flat(token_offsets, "token_offsets", torch.int32, (cache[0] + 1,), dev)
+    mp = words = 0
+    if anc_mask is not None:
+        words = anc_mask.shape[1]
+        mp = _flat(anc_mask, "anc_mask", torch.int32, (T, words), dev)
+    if out is None:
+        out = _empty((T, hq, d), od, q.device, stream)
+        op = out.data_ptr()
+    else:
+        op = _flat(out, "out", od, (T, hq, d), dev)
+    L, handle = lib(), _handle(stream, dev)
+    a = (*cache, T, max_tokens, hq, words, out_code, scale, qs, q.data_ptr(), off, mp, op)
+    if workspace is None:
+        need = L.gdn_kv_attend_workspace(_kv_attend_args(*a, 0, 0), decode)
+        if need > 0:
+            workspace = _scratch(need, torch.uint8, q.device, stream)
+            packed = _kv_attend_args(*a, workspace.data_ptr(), need)
+        else:
+            packed = _kv_attend_args(*a, 0, 0)
+    else:
+        packed = _kv_attend_args(*a, _flat(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.numel())
+    _check((L.gdn_kv_decode if decode else L.gdn_kv_attend)(packed, handle))
+    return out
+
+
+def gdn_kv_attend(q, k_cache, v_cache, page_table, lens, token_offsets, max_tokens: int, anc_mask=None, scale: float = 1.0,
+                  out=None, out_dtype=None, workspace=None, dev_status=None, stream=None) -> torch.Tensor:
+    """Attention of each request's new tokens q [T, Hq, d], packed by token_offsets [B + 1] (at most max_tokens each), to
+    its cache: every slot before lens[b], and of the new tokens (appended already) those in its row of anc_mask
+    [T, words] (gdn_tree_build_desc's), or those up to itself where that is None.  o [T, Hq, d]."""
+    return _attend(False, q, k_cache, v_cache, page_table, lens, token_offsets, max_tokens, anc_mask, scale, out, out_dtype,
+                   workspace, dev_status, stream)
+
+
+def gdn_kv_decode(q, k_cache, v_cache, page_table, lens, scale: float = 1.0, out=None, out_dtype=None, workspace=None,
+                  dev_status=None, stream=None) -> torch.Tensor:
+    """Attention of one new token a request, q [B, Hq, d], to the lens[b] + 1 first slots of its cache (its own
+    key and value appended already).  A row whose lens is -1 is not in use: its outputs are zero."""
+    return _attend(True, q, k_cache, v_cache, page_table, lens, None, 1, None, scale, out, out_dtype, workspace, dev_status, stream)
+
+
+def gdn_kv_attend_workspace(q, k_cache, v_cache, page_table, max_tokens: int = 0, anc_mask=None, decode: bool = False, out_dtype=None) -> int:
+    """Bytes of ``workspace`` with which gdn_kv_attend (or gdn_kv_decode) takes tensors of these sizes and strides (they
+    allocate their own otherwise)."""
+    T, hq, d = q.shape
+    dev = _device(q, "q")
+    cache = _cache(k_cache, v_cache, page_table, page_table.new_empty(page_table.shape[0]), None, dev, q.dtype)
+    need = lib().gdn_kv_attend_workspace(
+        _kv_attend_args(*cache, T, max_tokens, hq, anc_mask.shape[1] if anc_mask is not None else 0, _dtype_code(out_dtype or q.dtype), 1.0,
+                        _rows(q, "q", q.dtype, (T, hq, d), dev), q.data_ptr(), 0, 0 if anc_mask is None else anc_mask.data_ptr(), 0, 0, 0),
+        decode)
+    if need < 0:
+        _check(GDN_ERR_INVALID_ARG)
+    return need
+
+
+def gdn_kv_commit(k_cache, v_cache, page_table, lens, node_offsets, path_offsets, path_idx, new_lens=None, dev_status=None, stream=None):
+    """The accepted path's tokens (request-local node ids, ascending) to the slots of committed ones, in place;
+    returns new_lens [B] = lens + the paths' lengths (not lens itself)."""
+    dev = _device(k_cache, "k_cache")
+    cache = _cache(k_cache, v_cache, page_table, lens, dev_status, dev, k_cache.dtype)
+    B = cache[0]
+    n = path_idx.shape[0]
+    if new_lens is None:
+        new_lens = _empty((B,), torch.int32, k_cache.device, stream)
+        lp = new_lens.data_ptr()
+    else:
+        lp = _flat(new_lens, "new_lens", torch.int32, (B,), dev)
+    _check(lib().gdn_kv_commit(
+        _kv_commit_args(*cache, _flat(node_offsets, "node_offsets", torch.int32, (B + 1,), dev),
+                        _flat(path_offsets, "path_offsets", torch.int32, (B + 1,), dev),
+                        _flat(path_idx, "path_idx", torch.int32, (n,), dev) if n else 0, n, lp), _handle(stream, dev)))
+    return new_lens
 
 
 # ----------------------------------------------------------------------------

@@ -1,0 +1,210 @@
+// attend_simt.cu -- attention over a paged cache, general: fp32, and bf16 that the tensor-core kernels do not take.
+//
+// A block has 16 rows and takes 32 slots at a time: keys and values to shared memory as fp32, the scores one slot a
+// lane, four rows a warp, the running maximum and sum of a row in its warp, then the outputs with a column (or two) a thread.
+// fp32 arithmetic throughout.  What bounds it is shared-memory reads beside the multiplications (five 16-byte
+// reads for 16 of them in the scores).
+#include "attn.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace attn;
+
+constexpr int kR = 16, kKT = 32, kThreads = 128;
+
+template <int D>
+struct Shared {
+    float q[kR][D + 4], k[kKT][D + 4], v[kKT][D], p[kR][kKT], m[kR], f[kR], l[kR];
+    int64_t at[kKT];
+    Scratch find;
+};
+
+// `row`, D entries from element `at` of x, as fp32; zeros where at < 0
+template <typename T, int D, bool VEC>
+__device__ __forceinline__ void load_rows(const void *x, const int64_t *at, int rows, float *to, int ld) {
+    const T *src = static_cast<const T *>(x);
+    if constexpr (VEC) {
+        for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), c = i % (D / 4) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (at[row] >= 0) {
+                if constexpr (sizeof(T) == 4) {
+                    y = *reinterpret_cast<const float4 *>(src + at[row] + c);
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src + at[row] + c);
+                    y = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                                    __uint_as_float(w.y & 0xFFFF0000u));
+                }
+            }
+            *reinterpret_cast<float4 *>(to + row * ld + c) = y;
+        }
+    } else {
+        for (int i = threadIdx.x; i < rows * D; i += kThreads) {
+            const int row = i / D, c = i % D;
+            to[row * ld + c] = at[row] >= 0 ? load_f(src, at[row] + c) : 0.f;
+        }
+    }
+}
+
+template <typename T, int D, bool VEC>
+__global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int runs) {
+    after_previous();
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared<D> &s = *reinterpret_cast<Shared<D> *>(raw);
+    constexpr int kCols = D > kThreads ? D / kThreads : 1, kGroups = D < kThreads ? kThreads / D : 1, kMine = kR / kGroups;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
+    int64_t per, t, end;
+    Place at;
+    find<kR, kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
+    if (t >= end) return;
+    Request r = request(p, at.b, nullptr);
+    while (t < end) {
+        const int tiles = item_tiles<kR, kKT>(p, r, at.qt), seen = seen_slots<kR>(p, r, at.qt);
+        const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
+        const int64_t row0 = (int64_t)at.qt * kR, rows = (int64_t)r.n * p.group;
+        if (tid < kR) {
+            const int64_t q = row0 + tid;
+            s.at[tid] = q < rows ? (r.first + q / p.group) * p.q_stride + (at.h * p.group + q % p.group) * D : -1;
+        }
+        if (tid < kR) s.m[tid] = -INFINITY, s.l[tid] = 0.f;
+        __syncthreads();
+        load_rows<T, D, VEC>(p.q, s.at, kR, &s.q[0][0], D + 4);
+        float acc[kMine][kCols] = {};
+        for (int tile = first; tile < last; ++tile) {
+            const int slot0 = tile * kKT;
+            __syncthreads();
+            if (tid < kKT) s.at[tid] = slot0 + tid < seen ? slot_offset(p, at.b, at.h, slot0 + tid) : -1;
+            __syncthreads();
+            load_rows<T, D, VEC>(p.k, s.at, kKT, &s.k[0][0], D + 4);
+            load_rows<T, D, VEC>(p.v, s.at, kKT, &s.v[0][0], D);
+            __syncthreads();
+            float x[kR / 4] = {};
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(&s.k[lane][c]);
+#pragma unroll
+                for (int i = 0; i < kR / 4; ++i) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&s.q[warp + 4 * i][c]);
+                    x[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[i]))));
+                }
+            }
+            const int slot = slot0 + lane;
+#pragma unroll
+            for (int i = 0; i < kR / 4; ++i) {
+                const int row = warp + 4 * i;
+                const int64_t q = row0 + row;
+                float y = slot < seen && q < rows && sees(p, r, (int)(q / p.group), slot) ? x[i] * p.scale_log2 : -INFINITY;
+                float m = y;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    const float z = __shfl_xor_sync(0xffffffffu, m, o);
+                    m = fmaxf(m, z);
+                }
+                const float old = s.m[row];
+                m = fmaxf(m, old);
+                const float base = m == -INFINITY ? 0.f : m;
+                // a NaN score has no place in the maximum, and makes the sum NaN
+                const float e = exp2f(y - base), f = exp2f(old - base);
+                const float sum = warp_sum(e);
+                __syncwarp();
+                s.p[row][lane] = e;
+                if (lane == 0) s.m[row] = m, s.f[row] = f, s.l[row] = fmaf(s.l[row], f, sum);
+            }
+            __syncthreads();
+            const int g = tid / D % kGroups;
+            const bool masked = slot0 + kKT > r.len;  // what is not seen there may be anything
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) acc[i][c] *= s.f[g * kMine + i];
+            for (int j = 0; j < kKT; ++j) {
+                float v[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) v[c] = s.v[j][(tid + c * kThreads) % D];
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const float e = s.p[g * kMine + i][j];
+                    if (!masked || e != 0.f) {
+#pragma unroll
+                        for (int c = 0; c < kCols; ++c) acc[i][c] = fmaf(e, v[c], acc[i][c]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = first == 0 && last == tiles;
+        const int which = first == 0, g = tid / D % kGroups;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int row = g * kMine + i;
+            const int64_t q = row0 + row;
+            if (q >= rows) continue;
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+                const int col = (tid + c * kThreads) % D;
+                if (whole) {
+                    const float y = s.l[row] == 0.f ? 0.f : acc[i][c] / s.l[row];
+                    const int64_t to = ((int64_t)(r.first + q / p.group) * p.hkv * p.group + at.h * p.group + q % p.group) * D + col;
+                    if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to, y);
+                    else store_f(static_cast<float *>(p.o), to, y);
+                } else {
+                    part_out(p, kR, D, run, which)[row * D + col] = acc[i][c];
+                }
+            }
+        }
+        if (!whole && tid < kR) {
+            float *st = part_stat(p, kR, D, runs, run, which) + tid * 2;
+            st[0] = s.m[tid], st[1] = s.l[tid];
+        }
+        t += last - first;
+        if (t < end) next_item<kR>(p, at, r);
+        __syncthreads();
+    }
+}
+
+template <typename T, int D, bool VEC>
+cudaError_t run(Params p, int runs, cudaStream_t stream) {
+    static int have[16];
+    const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
+    if (e != cudaSuccess) return e;
+    const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);
+    return f != cudaSuccess ? f : launch_join<D, kR, kKT>(p, runs, stream);
+}
+
+template <typename T, bool VEC>
+cudaError_t (*pick(int d))(Params, int, cudaStream_t) {
+    switch (d) {
+        case 16: return run<T, 16, VEC>;
+        case 32: return run<T, 32, VEC>;
+        case 64: return run<T, 64, VEC>;
+        case 128: return run<T, 128, VEC>;
+        default: return run<T, 256, VEC>;
+    }
+}
+
+}  // namespace
+
+attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
+    const gdn_kv_cache &c = a.cache;
+    const int e = c.dtype == GDN_BF16 ? 2 : 4;
+    const int64_t qs = a.q_stride ? a.q_stride : (int64_t)a.n_q_heads * c.d;
+    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 15) == 0 &&
+                     qs * e % 16 == 0 && c.page_stride * e % 16 == 0 && c.slot_stride * e % 16 == 0 && c.head_stride * e % 16 == 0;
+    Choice x;
+    // two blocks an SM and no more than there can be tiles
+    const int64_t group = a.n_q_heads / c.n_kv_heads;
+    const int64_t row_tiles = ((decode ? 1 : (int64_t)a.max_tokens) * group + kR - 1) / kR;
+    const int64_t slot_tiles = ((int64_t)c.max_pages * c.page_size + kKT - 1) / kKT;
+    const int64_t room = 2 * (int64_t)sm_count();
+    int64_t most = (int64_t)c.batch * c.n_kv_heads;
+    most = most >= room ? room : most * (row_tiles < room ? row_tiles : room);
+    most = most >= room ? room : most * (slot_tiles < room ? (slot_tiles > 0 ? slot_tiles : 1) : room);
+    x.runs = (int)(most >= room ? room : most < 1 ? 1 : most);
+    x.workspace = 4 * workspace_floats(kR, c.d, x.runs);
+    if (c.dtype == GDN_BF16) x.launch = vec ? pick<__nv_bfloat16, true>(c.d) : pick<__nv_bfloat16, false>(c.d);
+    else x.launch = vec ? pick<float, true>(c.d) : pick<float, false>(c.d);
+    return x;
+}
+
+}  // namespace gdn

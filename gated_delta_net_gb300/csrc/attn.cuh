@@ -1,0 +1,286 @@
+// attn.cuh -- what the attention kernels share (gdn_attention.h): slots of the paged cache, and how the work is cut.
+//
+// An item is a request's key-value head with one tile of R rows (row r: token r / group, query head r % group of
+// those that share the head); its work is the tiles of KT slots that any of its rows sees.  All items' tiles, one
+// item after another, are cut into equal runs, one for each block.  A run that has all of an item writes its
+// outputs; the others write the sum, the maximum and the unscaled output of what they had to the workspace, at most
+// two of them a block (the item it ends, the item it begins), and join_kernel adds an item's parts in order.
+// So every block has the same work whatever the lengths are, nothing depends on the host knowing them, and the result
+// does not depend on timing.
+#pragma once
+
+#include "internal.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Params {
+    int batch, hkv, group, page_size, n_pages, max_pages, total, max_tokens, mask_words, min_tiles;
+    int64_t page_stride, slot_stride, head_stride, q_stride;
+    float scale_log2;
+    const void *k, *v, *q;
+    const int32_t *table, *lens, *offsets;  // offsets NULL: token b is request b's only one
+    const uint32_t *mask;                   // NULL: causal
+    void *o;
+    float *ws;                              // [blocks][2][R][d] outputs, then [blocks][2][R][2] maxima (base 2) and sums
+    int32_t *status;
+    int page_bits;                          // log2 of page_size, or -1
+    bool out_bf16;
+};
+
+// The tokens of request b: the first one's row, how many (0: the request is left out), the committed ones
+// (-1: not in use).
+struct Request {
+    int first, n, len;
+};
+__device__ __forceinline__ Request request(const Params &p, int b, int32_t *status) {
+    Request r = {b, 1, p.lens[b]};
+    int bad = 0;
+    if (p.offsets) {
+        const int lo = p.offsets[b], hi = p.offsets[b + 1];
+        r.first = lo;
+        r.n = hi - lo;
+        if (lo < 0 || hi < lo || hi > p.total) bad = GDN_DEV_BAD_DESC;
+        else if (r.n > p.max_tokens || (p.mask && r.n > 32 * p.mask_words)) bad = GDN_DEV_TOO_MANY;
+    }
+    if (!bad && r.n > 0 && (r.len < -1 || (r.len >= 0 && (int64_t)r.len + r.n > (int64_t)p.max_pages * p.page_size))) bad = GDN_DEV_BAD_PAGE;
+    if (bad) {
+        r.n = 0;
+        if (status) flag(status, bad);
+    }
+    return r;
+}
+
+// Slots that some row of tile qt sees (0: none), and the tiles they make (one at least, which writes the zeros).
+template <int R>
+__device__ __forceinline__ int seen_slots(const Params &p, const Request &r, int qt) {
+    if (r.len < 0) return 0;
+    return r.len + (p.mask ? r.n : min(r.n, ((qt + 1) * R + p.group - 1) / p.group));
+}
+template <int R, int KT>
+__device__ __forceinline__ int item_tiles(const Params &p, const Request &r, int qt) {
+    return max(1, (seen_slots<R>(p, r, qt) + KT - 1) / KT);
+}
+template <int R>
+__device__ __forceinline__ int row_tiles(const Params &p, const Request &r) {
+    return (int)(((int64_t)r.n * p.group + R - 1) / R);
+}
+template <int R, int KT>
+__device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r) {
+    const int nq = row_tiles<R>(p, r);
+    if (nq == 0) return 0;
+    if (p.mask || r.len < 0 || r.n == 1) return (int64_t)nq * item_tiles<R, KT>(p, r, 0);
+    int64_t sum = 0;
+    for (int qt = 0; qt < nq; ++qt) sum += item_tiles<R, KT>(p, r, qt);
+    return sum;
+}
+
+// A place in the work: tile `tile` of an item.
+struct Place {
+    int b, h, qt, tile;
+};
+
+// What find() shares between the threads of a block.
+struct Scratch {
+    int64_t warp_sum[32];
+    Place at;
+};
+
+__device__ __forceinline__ int64_t div_up(int64_t a, int64_t b) {
+    return a >> 31 ? (a + b - 1) / b : (int64_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b);
+}
+
+// How many tiles a run has, and where run number `run` of `runs` begins and ends (begin == end: nothing to do); `at`
+// is the place where it begins.  Every thread of the block calls this.
+template <int R, int KT>
+__device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
+                                     int64_t &end, Place &at) {
+    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int each = (p.batch + nt - 1) / nt, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<R, KT>(p, request(p, b, status));
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) s.warp_sum[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, total = 0;
+    for (int w = 0; w < nt / 32; ++w) {
+        const int64_t x = s.warp_sum[w];
+        if (w < warp) before += x;
+        total += x;
+    }
+    per = max(div_up(total, runs), (int64_t)p.min_tiles);
+    begin = min(total, per * run);
+    end = min(total, begin + per);
+    if (begin < end && before <= begin && begin < before + mine) {
+        int64_t rest = begin - before;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request(p, b, nullptr);
+            const int64_t ht = head_tiles<R, KT>(p, r);
+            if (rest >= ht * p.hkv) {
+                rest -= ht * p.hkv;
+                continue;
+            }
+            const int h = (int)(rest / ht);
+            rest -= h * ht;
+            int qt = 0;
+            if (p.mask || r.len < 0 || r.n == 1) {
+                const int t = item_tiles<R, KT>(p, r, 0);
+                qt = (int)(rest / t);
+                rest -= (int64_t)qt * t;
+            } else {
+                for (int t; rest >= (t = item_tiles<R, KT>(p, r, qt)); ++qt) rest -= t;
+            }
+            s.at = Place{b, h, qt, (int)rest};
+            break;
+        }
+    }
+    __syncthreads();
+    at = s.at;
+}
+
+// the item after `at`'s
+template <int R>
+__device__ __forceinline__ void next_item(const Params &p, Place &at, Request &r) {
+    at.tile = 0;
+    if (++at.qt < row_tiles<R>(p, r)) return;
+    at.qt = 0;
+    if (++at.h < p.hkv) return;
+    at.h = 0;
+    do {
+        if (++at.b >= p.batch) return;
+        r = request(p, at.b, nullptr);
+    } while (r.n == 0);
+}
+
+// The offset of slot s of request b, head h, in the pools; -1 where its page is outside the pool.
+__device__ __forceinline__ int64_t slot_offset(const Params &p, int b, int h, int s) {
+    const int page = p.page_bits >= 0 ? s >> p.page_bits : s / p.page_size;
+    const int row = s - page * p.page_size;
+    const int id = p.table[(int64_t)b * p.max_pages + page];
+    if (id < 0 || id >= p.n_pages) {
+        flag(p.status, GDN_DEV_BAD_PAGE);
+        return -1;
+    }
+    return id * p.page_stride + row * p.slot_stride + h * p.head_stride;
+}
+
+// Whether token i of a request sees slot s.
+__device__ __forceinline__ bool sees(const Params &p, const Request &r, int i, int s) {
+    if (s < r.len) return true;
+    const int j = s - r.len;
+    if (j >= r.n) return false;
+    return p.mask ? (p.mask[(int64_t)(r.first + i) * p.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= i;
+}
+
+__device__ __forceinline__ float *part_out(const Params &p, int R, int d, int run, int which) {
+    return p.ws + ((int64_t)run * 2 + which) * R * d;
+}
+__device__ __forceinline__ float *part_stat(const Params &p, int R, int d, int runs, int run, int which) {
+    return p.ws + (int64_t)runs * 2 * R * d + ((int64_t)run * 2 + which) * R * 2;
+}
+__host__ __device__ inline int64_t workspace_floats(int R, int d, int runs) { return (int64_t)runs * 2 * R * (d + 2); }
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four consecutive entries of row `row` of o (in elements).
+__device__ __forceinline__ void store4(const Params &p, int64_t at, float4 x) {
+    if (p.out_bf16) {
+        __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+        uint2 w = make_uint2(*reinterpret_cast<uint32_t *>(&a), *reinterpret_cast<uint32_t *>(&b));
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + at) = w;
+    } else {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + at) = x;
+    }
+}
+
+// Joins the parts of the item that is cut first at the start of run blockIdx.x + 1: with the parts' maxima m_c, sums l_c
+// and unscaled outputs o_c, o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.  A block takes kJoinRows of the item's rows.
+constexpr int kJoinThreads = 128;
+template <int D>
+constexpr int kJoinRows = kJoinThreads * 4 / D;  // a thread has four entries of one row
+
+template <int D, int R, int KT>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) {
+    after_previous();
+    __shared__ Scratch s;
+    int64_t per, begin, end;
+    Place at;
+    const int run = blockIdx.x + 1;
+    find<R, KT>(p, runs, run, nullptr, s, per, begin, end, at);
+    if (begin >= end || at.tile == 0) return;
+    const int64_t item = begin - at.tile;
+    if (item < begin - per) return;  // cut earlier too: that cut's block joins it
+    const Request r = request(p, at.b, nullptr);
+    const int64_t item_end = item + item_tiles<R, KT>(p, r, at.qt);
+    const int row = blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
+    const int64_t q = (int64_t)at.qt * R + row;
+    if (row >= R || q >= (int64_t)r.n * p.group) return;
+    const int last = (int)((item_end - 1) / per);
+    float m = -INFINITY, l = 0.f;
+    for (int c = run - 1; c <= last; ++c) m = fmaxf(m, part_stat(p, R, D, runs, c, c == run - 1)[row * 2]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = run - 1; c <= last; ++c) {
+        const int which = c == run - 1;
+        const float2 st = *reinterpret_cast<const float2 *>(part_stat(p, R, D, runs, c, which) + row * 2);
+        const float4 x = *reinterpret_cast<const float4 *>(part_out(p, R, D, c, which) + row * D + col);
+        const float f = exp2_fast(st.x - base);
+        l = fmaf(f, st.y, l);
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
+    }
+    // nothing seen: zeros; a NaN sum stays one
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int token = r.first + (int)(q / p.group), head = at.h * p.group + (int)(q % p.group);
+    store4(p, ((int64_t)token * p.hkv * p.group + head) * D + col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+}
+
+// A launch that may take its place while the kernel before it ends; the kernel calls after_previous() first.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int D, int R, int KT>
+cudaError_t launch_join(const Params &p, int runs, cudaStream_t stream) {
+    if (runs < 2) return cudaSuccess;
+    return launch_dependent(join_kernel<D, R, KT>, dim3(runs - 1, (R + kJoinRows<D> - 1) / kJoinRows<D>), kJoinThreads, 0, stream, p, runs);
+}
+
+// A kernel of this family for some sizes: how many blocks, their workspace, and the launch.
+struct Choice {
+    int runs;
+    int64_t workspace;
+    cudaError_t (*launch)(Params p, int runs, cudaStream_t stream);
+};
+
+}  // namespace attn
+
+// kernels for the sizes of a call (the general one always; d is one of the supported widths)
+attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode);
+
+}  // namespace gdn

@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 #include <stdint.h>
 
+#include "gdn_attention.h"
 #include "gdn_layer.h"
 #include "gdn_tree.h"
 
@@ -78,6 +79,10 @@ cudaError_t launch_decode(const gdn_decode_args &a, cudaStream_t stream);
 cudaError_t launch_qk_gates(const gdn_qk_gates_args &a, cudaStream_t stream);
 cudaError_t launch_norm_gate(const gdn_norm_gate_args &a, cudaStream_t stream);
 cudaError_t launch_residual_norm(const gdn_residual_norm_args &a, cudaStream_t stream);
+
+// the attention layers' cache (gdn_attention.h); their attention kernels are declared in attn.cuh
+cudaError_t launch_kv_append(const gdn_kv_append_args &a, cudaStream_t stream);
+cudaError_t launch_kv_commit(const gdn_kv_commit_args &a, cudaStream_t stream);
 
 // driver entry point for TMA descriptors (nullptr when the driver lacks it)
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();

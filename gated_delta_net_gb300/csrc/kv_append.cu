@@ -1,0 +1,212 @@
+// kv_append.cu -- new tokens into the paged cache, norm and position rotation on the way.
+//
+// Per token: each query and key head's row x of d entries, x / sqrt(mean x^2 + eps) * w where there is a norm, the first
+// rot_dim entries turned by the position's angles; values copied.  Every byte is read once and written once: bound
+// by memory, or for a few tokens by the launch and one chain of loads (offsets, length, page, row).
+// A block takes a token; d / 8 lanes take a row with 8 entries each, one row after another, so that a token's cosines and
+// sines are read once into registers.  The partner of an entry in a pair is 8 lanes or fewer away, or its neighbour.
+// Where rows do not start on 16 bytes, or half the rotated width is no multiple of 8, entries and partners are read one by one.
+#include "attn.cuh"
+
+namespace gdn {
+namespace {
+
+using attn::launch_dependent;
+
+constexpr int kThreads = 128;
+
+struct AppendParams {
+    int batch, hq, hkv, page_size, n_pages, max_pages, total, rot, n_positions;
+    float eps;
+    int64_t page_stride, slot_stride, head_stride, qs, ks, vs;
+    const void *q, *k, *v, *q_weight, *k_weight;
+    const int32_t *table, *lens, *offsets, *depth;
+    const float *cos_sin;
+    void *q_out, *k_cache, *v_cache;
+    int32_t *status;
+    bool weight_bf16;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
+    if constexpr (VEC && sizeof(T) == 2) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    } else if constexpr (VEC) {
+        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = load_f(p, i);
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
+    if constexpr (VEC && sizeof(T) == 2) {
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else if constexpr (VEC) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) store_f(p, i, x[i]);
+    }
+}
+
+__device__ __forceinline__ float weight_at(const void *w, bool bf16, int i) {
+    return bf16 ? load_f(static_cast<const __nv_bfloat16 *>(w), i) : load_f(static_cast<const float *>(w), i);
+}
+
+// VEC: 16-byte pieces, and the partner of lane l's entries (halves) is another lane's; INTER: pairs of neighbours
+template <typename T, int D, bool VEC, bool INTER>
+__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
+    after_previous();
+    constexpr int L = D / 8, G = kThreads / L;  // lanes a row, rows a block has in flight
+    const int t = blockIdx.x, tid = threadIdx.x, sub = tid % L, e0 = sub * 8, half = p.rot / 2;
+    int b = t, i = 0;
+    if (p.offsets) {
+        int upto = 0;
+        for (int j = 0; j < p.batch; j += kThreads)
+            upto += __syncthreads_count(j + tid < p.batch && p.offsets[j + tid + 1] <= t);
+        if (t == 0) {  // looked at once
+            bool bad = tid == 0 && p.offsets[0] != 0;
+            for (int j = tid; j < p.batch; j += kThreads) bad = bad || p.offsets[j + 1] < p.offsets[j] || p.offsets[j + 1] > p.total;
+            if (bad) flag(p.status, GDN_DEV_BAD_DESC);
+        }
+        if (upto >= p.batch) return;
+        b = upto;
+        i = t - p.offsets[b];
+        if (i < 0 || p.offsets[b] < 0 || p.offsets[b + 1] > p.total) return;
+    }
+    const int len = p.lens[b];
+    if (len == -1) return;
+    const int64_t slot = (int64_t)len + i, page = slot / p.page_size;
+    const int64_t position = p.depth ? (int64_t)len + p.depth[t] - 1 : slot;
+    int bad = 0, id = 0;
+    if (len < 0 || page >= p.max_pages) bad = GDN_DEV_BAD_PAGE;
+    else if (id = p.table[(int64_t)b * p.max_pages + page]; id < 0 || id >= p.n_pages) bad = GDN_DEV_BAD_PAGE;
+    else if (p.rot && (position < 0 || position >= p.n_positions)) bad = GDN_DEV_BAD_POSITION;
+    if (bad) {
+        if (tid == 0) flag(p.status, bad);
+        return;
+    }
+    const int64_t at = id * p.page_stride + (slot - page * p.page_size) * p.slot_stride;
+
+    // this lane's angles: entry e0 + n turns with pair (e0 + n) % half, or (e0 + n) / 2 in neighbours
+    float cs[8], sn[8];
+    const float *angles = p.cos_sin + position * p.rot;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) {
+        const int e = e0 + n;
+        const int pair = INTER ? e / 2 : e < half ? e : e - half;
+        const bool turned = e < p.rot;
+        cs[n] = turned ? angles[pair] : 1.f;
+        // the first of a pair subtracts
+        sn[n] = turned ? angles[half + pair] * ((INTER ? (e & 1) == 0 : e < half) ? -1.f : 1.f) : 0.f;
+    }
+    const unsigned mates = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << ((tid & 31) / L * L);  // the lanes of a row
+    const int rows = p.hq + 2 * p.hkv;
+    for (int row = tid / L; row < (rows + G - 1) / G * G; row += G) {  // whole warps, for the shuffles
+        const bool live = row < rows, is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
+        const int h = is_q ? row : is_v ? row - p.hq - p.hkv : row - p.hq;
+        const T *src = static_cast<const T *>(is_q ? p.q : is_v ? p.v : p.k) + t * (is_q ? p.qs : is_v ? p.vs : p.ks) + (int64_t)h * D;
+        T *dst = is_q ? static_cast<T *>(p.q_out) + ((int64_t)t * p.hq + h) * D
+                      : static_cast<T *>(is_v ? p.v_cache : p.k_cache) + at + h * p.head_stride;
+        float x[8] = {}, y[8];
+        if (live) load8<T, VEC>(src + e0, x);
+        // the partners
+        if constexpr (INTER) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) y[n] = x[n ^ 1];
+        } else if constexpr (VEC) {
+            const int away = half / 8, from = e0 < half ? sub + away : sub - away;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) y[n] = __shfl_sync(0xffffffffu, x[n], from & (L - 1), L);
+        } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int e = e0 + n;
+                y[n] = live && e < p.rot ? load_f(src, e < half ? e + half : e - half) : 0.f;
+            }
+        }
+        if (is_v) {
+            if (live) store8<T, VEC>(dst + e0, x);
+            continue;
+        }
+        const void *w = is_q ? p.q_weight : p.k_weight;
+        if (w) {
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) sum = fmaf(x[n], x[n], sum);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mates, sum, o, L);
+            const float r = rsqrtf(sum * (1.f / D) + p.eps);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const int e = e0 + n;
+                const int pe = e >= p.rot ? e : INTER ? e ^ 1 : e < half ? e + half : e - half;
+                x[n] *= r * weight_at(w, p.weight_bf16, e);
+                y[n] *= r * weight_at(w, p.weight_bf16, pe);
+            }
+        }
+        float z[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) z[n] = e0 + n < p.rot ? fmaf(x[n], cs[n], y[n] * sn[n]) : x[n];
+        __syncwarp(mates);  // q_out may be q: partners have been read
+        if (live) store8<T, VEC>(dst + e0, z);
+    }
+}
+
+template <typename T, int D>
+cudaError_t run(const AppendParams &p, bool vec, bool inter, cudaStream_t stream) {
+    auto kernel = vec ? (inter ? append_kernel<T, D, true, true> : append_kernel<T, D, true, false>)
+                      : (inter ? append_kernel<T, D, false, true> : append_kernel<T, D, false, false>);
+    return launch_dependent(kernel, dim3(p.total), kThreads, 0, stream, p);
+}
+
+template <typename T>
+cudaError_t pick(const AppendParams &p, int d, bool vec, bool inter, cudaStream_t stream) {
+    switch (d) {
+        case 16: return run<T, 16>(p, vec, inter, stream);
+        case 32: return run<T, 32>(p, vec, inter, stream);
+        case 64: return run<T, 64>(p, vec, inter, stream);
+        case 128: return run<T, 128>(p, vec, inter, stream);
+        default: return run<T, 256>(p, vec, inter, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const gdn_kv_append_args &a, cudaStream_t stream) {
+    const gdn_kv_cache &c = a.cache;
+    const int e = c.dtype == GDN_BF16 ? 2 : 4;
+    AppendParams p = {};
+    p.batch = c.batch; p.hq = a.q ? a.n_q_heads : 0; p.hkv = c.n_kv_heads;
+    p.page_size = c.page_size; p.n_pages = c.n_pages; p.max_pages = c.max_pages; p.total = a.total_tokens;
+    p.rot = a.rot_dim; p.n_positions = a.n_positions; p.eps = a.eps;
+    p.page_stride = c.page_stride; p.slot_stride = c.slot_stride; p.head_stride = c.head_stride;
+    p.qs = a.q_stride ? a.q_stride : (int64_t)a.n_q_heads * c.d;
+    p.ks = a.k_stride ? a.k_stride : (int64_t)c.n_kv_heads * c.d;
+    p.vs = a.v_stride ? a.v_stride : (int64_t)c.n_kv_heads * c.d;
+    p.q = a.q; p.k = a.k; p.v = a.v; p.q_weight = a.q_weight; p.k_weight = a.k_weight;
+    p.table = c.page_table; p.lens = c.lens; p.offsets = a.token_offsets; p.depth = a.depth; p.cos_sin = a.cos_sin;
+    p.q_out = a.q_out; p.k_cache = c.k; p.v_cache = c.v; p.status = c.dev_status;
+    p.weight_bf16 = a.weight_dtype == GDN_BF16;
+    const uintptr_t pointers = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                               reinterpret_cast<uintptr_t>(a.q_out) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
+    const int64_t strides = (p.hq ? p.qs : 0) | p.ks | p.vs | p.page_stride | p.slot_stride | p.head_stride;
+    const bool vec = (pointers & 15) == 0 && strides * e % 16 == 0 && (a.interleaved || a.rot_dim % 16 == 0);
+    return c.dtype == GDN_BF16 ? pick<__nv_bfloat16>(p, c.d, vec, a.interleaved != 0, stream)
+                               : pick<float>(p, c.d, vec, a.interleaved != 0, stream);
+}
+
+}  // namespace gdn
