@@ -187,20 +187,9 @@ cudaError_t (*pick(int d))(Params, int, cudaStream_t) {
 
 attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     const gdn_kv_cache &c = a.cache;
-    const int e = c.dtype == GDN_BF16 ? 2 : 4;
-    const int64_t qs = a.q_stride ? a.q_stride : (int64_t)a.n_q_heads * c.d;
-    const bool vec = ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 15) == 0 &&
-                     qs * e % 16 == 0 && c.page_stride * e % 16 == 0 && c.slot_stride * e % 16 == 0 && c.head_stride * e % 16 == 0;
+    const bool vec = aligned16(a);
     Choice x;
-    // two blocks an SM and no more than there can be tiles
-    const int64_t group = a.n_q_heads / c.n_kv_heads;
-    const int64_t row_tiles = ((decode ? 1 : (int64_t)a.max_tokens) * group + kR - 1) / kR;
-    const int64_t slot_tiles = ((int64_t)c.max_pages * c.page_size + kKT - 1) / kKT;
-    const int64_t room = 2 * (int64_t)sm_count();
-    int64_t most = (int64_t)c.batch * c.n_kv_heads;
-    most = most >= room ? room : most * (row_tiles < room ? row_tiles : room);
-    most = most >= room ? room : most * (slot_tiles < room ? (slot_tiles > 0 ? slot_tiles : 1) : room);
-    x.runs = (int)(most >= room ? room : most < 1 ? 1 : most);
+    x.runs = most_runs(a, decode, kR, kKT, 2);
     x.workspace = 4 * workspace_floats(kR, c.d, x.runs);
     if (c.dtype == GDN_BF16) x.launch = vec ? pick<__nv_bfloat16, true>(c.d) : pick<__nv_bfloat16, false>(c.d);
     else x.launch = vec ? pick<float, true>(c.d) : pick<float, false>(c.d);

@@ -278,9 +278,34 @@ struct Choice {
     cudaError_t (*launch)(Params p, int runs, cudaStream_t stream);
 };
 
+// blocks_an_sm runs for each SM, and no more than there can be tiles
+inline int most_runs(const gdn_kv_attend_args &a, bool decode, int R, int KT, int blocks_an_sm) {
+    const int64_t room = (int64_t)blocks_an_sm * sm_count();
+    const int64_t group = a.n_q_heads / a.cache.n_kv_heads, slots = (int64_t)a.cache.max_pages * a.cache.page_size;
+    const int64_t factors[4] = {a.cache.batch, a.cache.n_kv_heads, ((decode ? 1 : (int64_t)a.max_tokens) * group + R - 1) / R, (slots + KT - 1) / KT};
+    int64_t n = 1;
+    for (int64_t f : factors) {
+        n *= f < 1 ? 1 : f < room ? f : room;
+        if (n > room) n = room;
+    }
+    return (int)n;
+}
+
+// whether every row of the queries and of the cache starts on 16 bytes
+inline bool aligned16(const gdn_kv_attend_args &a) {
+    const gdn_kv_cache &c = a.cache;
+    const int e = c.dtype == GDN_BF16 ? 2 : 4;
+    const int64_t qs = a.q_stride ? a.q_stride : (int64_t)a.n_q_heads * c.d;
+    return ((reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v)) & 15) == 0 &&
+           (qs | c.page_stride | c.slot_stride | c.head_stride) * e % 16 == 0;
+}
+
 }  // namespace attn
 
 // kernels for the sizes of a call (the general one always; d is one of the supported widths)
 attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode);
+// few rows a key-value head: bf16, rows on 16 bytes
+bool attend_mma_supported(const gdn_kv_attend_args &a);
+attn::Choice attend_mma_choice(const gdn_kv_attend_args &a, bool decode);
 
 }  // namespace gdn

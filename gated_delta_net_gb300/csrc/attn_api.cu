@@ -73,7 +73,9 @@ bool nothing(const gdn_kv_attend_args &a, bool decode) {
 }
 
 // the kernel for a call
-gdn::attn::Choice choose(const gdn_kv_attend_args &a, bool decode) { return gdn::attend_simt_choice(a, decode); }
+gdn::attn::Choice choose(const gdn_kv_attend_args &a, bool decode) {
+    return gdn::attend_mma_supported(a) ? gdn::attend_mma_choice(a, decode) : gdn::attend_simt_choice(a, decode);
+}
 
 int attend(const gdn_kv_attend_args *a, bool decode, void *stream) {
     if (int st = check_attend(a, decode)) return st;
