@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     const int g = lane >> 2, t4 = lane & 3;
     int64_t per, t, end;
     Place at;
-    find<kR, kKT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, t, end, at);
+    find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, t, end, at);
     if (t >= end) return;
     uint8_t *ring = sm + warp * S::kWarp;
     float *mine = reinterpret_cast<float *>(sm + kWarps * S::kWarp + (warp & 1) * S::kJoin);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     // ---- the ring: tiles from `load` on are on their way, the next one's page is known
     Place load = at;
     Request lr = request(p, load.b, nullptr);
-    int l_tiles = item_tiles<kR, kKT>(p, lr, load.qt), l_seen = seen_slots<kR>(p, lr, load.qt);
+    int l_tiles = item_tiles<kKT>(p, lr, load.qt), l_seen = seen_slots(p, lr, load.qt);
     int64_t l_left = end - t, l_off = -1;
     const bool aligned_pages = p.page_size % kKeys == 0;  // a warp's 16 slots lie in one page
     auto look_up = [&]() {
@@ -103,9 +103,9 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
             }
             --l_left;
             if (++load.tile == l_tiles && l_left > 0) {
-                next_item<kR>(p, load, lr);
-                l_tiles = item_tiles<kR, kKT>(p, lr, load.qt);
-                l_seen = seen_slots<kR>(p, lr, load.qt);
+                next_item(p, load, lr);
+                l_tiles = item_tiles<kKT>(p, lr, load.qt);
+                l_seen = seen_slots(p, lr, load.qt);
             }
             if (l_left > 0) look_up();
         }
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     Request r = request(p, at.b, nullptr);
     int stage = 0, free_stage = S::kStages - 1;
     while (t < end) {
-        const int tiles = item_tiles<kR, kKT>(p, r, at.qt), seen = seen_slots<kR>(p, r, at.qt);
+        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt);
         const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
         const int row0 = at.qt * kR, rows = r.n * p.group;
         // ---- this lane's rows: g and g + 8
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
         }
         __syncthreads();
         t += last - first;
-        if (t < end) next_item<kR>(p, at, r);
+        if (t < end) next_item(p, at, r);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
 template <int D>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
     static int have[16];
+    p.rows = kR;
     const cudaError_t e = ensure_smem(attend_mma_kernel<D>, Ring<D>::kBytes, have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_mma_kernel<D>, dim3(runs), kThreads, Ring<D>::kBytes, stream, p, runs);

@@ -56,11 +56,11 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
     int64_t per, t, end;
     Place at;
-    find<kR, kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
+    find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
     while (t < end) {
-        const int tiles = item_tiles<kR, kKT>(p, r, at.qt), seen = seen_slots<kR>(p, r, at.qt);
+        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt);
         const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
         const int64_t row0 = (int64_t)at.qt * kR, rows = (int64_t)r.n * p.group;
         if (tid < kR) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
             st[0] = s.m[tid], st[1] = s.l[tid];
         }
         t += last - first;
-        if (t < end) next_item<kR>(p, at, r);
+        if (t < end) next_item(p, at, r);
         __syncthreads();
     }
 }
@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
 template <typename T, int D, bool VEC>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
     static int have[16];
+    p.rows = kR;
     const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);

@@ -1,0 +1,608 @@
+// attend_tc.cu -- attention over a paged cache on the tensor cores: bf16, d = 64, 128 or 256 (sm_103a).
+//
+// For draft trees and prompts the two products bound it: 4 d operations a row and slot.  A block (one an SM) has an item of two
+// tiles of up to 128 rows (whole tokens: 128 / group of them, their query heads side by side; one tile for
+// d = 256), whose queries stay in shared memory, and takes its part of the cache in tiles of 128 slots (64 for d = 256):
+//     S = Q K^T      tcgen05, both from shared memory, to tensor memory
+//     P = 2^(S scale - m)   a thread a row: 128 scores from tensor memory, probabilities as bf16 back over them
+//     O += P V       tcgen05, P from tensor memory, V as it lies in shared memory (MN-major)
+// While one tile's rows are in registers, the other tile's products run.  (d = 256: the outputs take half of the tensor
+// memory; one tile, whose scores are a tile of slots ahead in a second buffer.)
+//
+// The maximum that outputs are scaled by is moved, and they are multiplied, only where a row's maximum grew by more than 2^8: then
+// probabilities are up to 2^8, which neither bf16 nor the fp32 sums lose anything by.
+// P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.
+//
+// 12 warps:
+//     0-3, 4-7  rows of the first and of the second tile: probabilities, and the outputs at an item's end
+//               (d = 256: 4-7 have nothing to do)
+//     8         issues the products
+//     9         loads keys and values: a TMA box for each page's rows, 128-byte swizzled; pages behind the last seen
+//               slot, or outside the pool, are read past the pool's end, as zeros
+//     10        loads queries (TMA: 64 entries of the group's heads of 128 / group tokens)
+//     11        looks at values before they are multiplied: rows behind the last seen slot become zeros (their
+//               probability is zero, but they may be anything), and so do new tokens' that are not finite, whose
+//               readers' sums become NaN instead
+// Every wait is bounded; one that runs out sets GDN_DEV_TIMEOUT.
+#include "attn.cuh"
+#include "sm100.cuh"
+#include "tc_tiles.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace attn;
+using namespace sm100;
+using tiles::pack_bf16;
+
+constexpr int kThreads = 384, kTileRows = 128;
+constexpr float kGrow = 8.f;  // log2 of what a probability may grow to before the maximum moves
+
+template <int D>
+struct Shape {
+    static constexpr int U = D == 256 ? 1 : 2;        // tiles of rows
+    static constexpr int NB = D == 256 ? 2 : 1;       // buffers of scores for each
+    static constexpr int KT = D == 256 ? 64 : 128;    // slots of a tile
+    static constexpr int H = D / 64;                  // halves (64 entries, 128 bytes) of a row
+    static constexpr int kQTile = kTileRows * 128;    // bytes of one half of a tile of queries
+    static constexpr int kHalf = KT * 128;            // of one half of a tile of keys or values
+    static constexpr int kStage = H * kHalf;
+    static constexpr int kQ = U * H * kQTile;
+    static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? 5 : 3;  // tiles of keys, of values held at a time
+    static constexpr int CAP = U * kTileRows;
+    static constexpr uint32_t kScores = 0, kOut = U * NB * KT;  // tensor-memory columns
+    static constexpr int kSpoilt = KT / 32;           // words of a tile's rows that were not finite
+    // barriers
+    static constexpr int KFULL = 0, KEMPTY = KFULL + KS, VFULL = KEMPTY + KS, VEMPTY = VFULL + VS, READY = VEMPTY + VS, SCORES = READY + VS,
+                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, DRAIN = QEMPTY + 1, COUNT = DRAIN + 1;
+    static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_SPOILT = OFF_V + VS * kStage, OFF_BAR = (OFF_SPOILT + VS * kSpoilt * 4 + 7) / 8 * 8;
+    static constexpr int kBytes = OFF_BAR + COUNT * 8 + 16 + 1024;  // and what aligning the base takes
+    static_assert(kOut + U * D <= 512, "tensor memory");
+    static_assert(kBytes + (int)sizeof(Scratch) <= 232448, "shared memory");
+};
+
+struct TcParams {
+    Params p;
+    int tile_tokens;  // tokens of a tile of rows
+    int box;          // slots of a TMA box
+};
+
+// after a wait that ran out the others look once
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, bool &ok) {
+    if (!mbar_wait(bar, parity, ok ? 1u << 20 : 1u)) ok = false;
+    return ok;
+}
+// the same by a whole warp, which goes on or gives up together
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, bool &ok) {
+    wait(bar, parity, ok);
+    return ok = __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Products are issued by a whole converged warp, of which the elected lane (lead) issues.  Low word of a descriptor: start
+// address and, for MN-major operands, the distance between halves; the rest is the same for all 128-byte-swizzled tiles.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t at, int lbo_bytes) { return ((at >> 4) & 0x3FFFu) | ((uint32_t)(lbo_bytes >> 4) << 16); }
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+                 "mov.b64 db, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(lead), "r"(kDescHi) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t *bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];"
+                 ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(uint32_t a, uint32_t b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 parts(f2 x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Bits 0..31: whether token i sees slots from .. from + 31.
+__device__ __forceinline__ uint32_t seen_word(const Params &p, const Request &r, int i, int from) {
+    const int j = from - r.len;  // the first one's number among the new tokens
+    if (j <= -32) return 0xffffffffu;
+    const uint32_t before = j < 0 ? (1u << -j) - 1 : 0u;  // committed slots
+    uint32_t word;
+    if (p.mask) {
+        const uint32_t *row = p.mask + (int64_t)(r.first + i) * p.mask_words;
+        const int w = j >> 5;
+        const uint32_t lo = w >= 0 && w < p.mask_words ? row[w] : 0u, hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
+        word = __funnelshift_r(lo, hi, j & 31);
+        const int left = r.n - j;  // bits of tokens there are
+        word &= left <= 0 ? 0u : left < 32 ? (1u << left) - 1 : 0xffffffffu;
+    } else {
+        const int left = i - j + 1;
+        word = left <= 0 ? 0u : left < 32 ? (1u << left) - 1 : 0xffffffffu;
+    }
+    return word | before;
+}
+
+// The walk over a run's items, alike in every role.
+struct Walk {
+    Place at;
+    Request r;
+    int64_t left;
+    int first, last, tiles, seen;
+    template <int KT>
+    __device__ __forceinline__ void item(const Params &p) {
+        tiles = item_tiles<KT>(p, r, at.qt);
+        seen = seen_slots(p, r, at.qt);
+        first = at.tile;
+        last = (int)min((int64_t)tiles, first + left);
+    }
+    template <int KT>
+    __device__ __forceinline__ bool next(const Params &p) {
+        left -= last - first;
+        if (left <= 0) return false;
+        next_item(p, at, r);
+        item<KT>(p);
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                     const __grid_constant__ TcParams tp, int runs) {
+    after_previous();
+    using S = Shape<D>;
+    constexpr int KT = S::KT, U = S::U, NB = S::NB;
+    extern __shared__ uint8_t raw[];
+    __shared__ Scratch scratch;
+    const Params &p = tp.p;
+    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
+    uint32_t *slot = reinterpret_cast<uint32_t *>(sm + S::OFF_BAR + S::COUNT * 8);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
+    int64_t per, begin, end;
+    Walk w;
+    find<KT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, begin, end, w.at);
+    if (begin >= end) return;
+    if (warp == 8) {
+        tmem_alloc(slot, 512);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        for (int i = 0; i < S::COUNT; ++i) {
+            const bool rows = (i >= S::PROBS && i < S::DONE) || (i >= S::FREE && i < S::QFULL);
+            mbar_init(bar + i, rows ? kTileRows : 1);
+        }
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = uniform(*slot);
+    const uint32_t base = smem_u32(sm);
+    w.r = request(p, w.at.b, nullptr);
+    w.left = end - begin;
+    w.item<KT>(p);
+    bool ok = true;
+
+    if (warp < 4 * U) {
+        // ------------------------------------------------------------------ a row
+        const int u = warp >> 2, x = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+        const uint32_t o_at = tm + S::kOut + u * D + lanes;
+        const float sc = p.scale_log2, grow = kGrow / sc;
+        int c = 0, item = 0;
+        do {
+            const int token = (w.at.qt * U + u) * tp.tile_tokens + x / p.group;
+            const bool live = x < tp.tile_tokens * p.group && token < w.r.n;
+            float m = -INFINITY;
+            f2 l2 = pair(0u, 0u);
+#pragma unroll 1
+            for (int tile = w.first; tile < w.last; ++tile, ++c) {
+                const int buf = u * NB + c % NB;
+                const uint32_t s_at = tm + S::kScores + buf * KT + lanes;
+                if (!warp_wait(&bar[S::SCORES + buf], (c / NB) & 1, ok)) break;
+                tc_fence_after();
+                // scores in chunks of 32, twice: for the maximum, and backwards, from the chunk at hand, for the probabilities
+                constexpr int N = KT / 32;
+                const int slot0 = tile * KT;
+                const bool masked = slot0 + KT > w.r.len;
+                uint32_t s[2][32], see[N];
+                tmem_ld32_nowait(s_at, s[0]);
+                bool spoilt = false;
+                if (masked) {
+                    const int stage = c % S::VS;
+                    if (!warp_wait(&bar[S::READY + stage], (c / S::VS) & 1, ok)) break;
+                    const uint32_t *sp = reinterpret_cast<const uint32_t *>(sm + S::OFF_SPOILT) + stage * S::kSpoilt;
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        see[i] = live ? seen_word(p, w.r, token, slot0 + i * 32) : 0u;
+                        spoilt = spoilt || (see[i] & sp[i]);
+                    }
+                }
+                auto hide = [&](uint32_t (&y)[32], uint32_t word) {
+#pragma unroll
+                    for (int n = 0; n < 32; ++n)
+                        if (!(word >> n & 1)) y[n] = 0xff800000u;  // -infinity
+                };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    uint32_t(&y)[32] = s[i & 1];
+                    tmem_wait_ld_into(y);
+                    if (i + 1 < N) tmem_ld32_nowait(s_at + (i + 1) * 32, s[(i + 1) & 1]);
+                    if (masked) hide(y, see[i]);
+#pragma unroll
+                    for (int n = 0; n < 32; n += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(y[n + 2 * k])), __uint_as_float(y[n + 2 * k + 1]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool move = top > m + grow || m == -INFINITY;
+                // the products before are done: with one buffer these scores came after them
+                if (NB == 2 && c > 0 && !warp_wait(&bar[S::DONE + u], (c - 1) & 1, ok)) break;
+                if (tile == w.first) {
+                    m = top;
+                } else if (__any_sync(0xffffffffu, move)) {
+                    tc_fence_after();
+                    const float now = move ? fmaxf(top, m) : m;
+                    const float f = m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
+                    m = now;
+                    const f2 ff = pair(__float_as_uint(f), __float_as_uint(f)), zero = pair(0x80000000u, 0x80000000u);
+                    l2 = fma2(l2, ff, zero);
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 16) {
+                        uint32_t o[16];
+                        tmem_ld16_nowait(o_at + i, o);
+                        tmem_wait_ld_into(o);
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * f);
+                        tmem_st16(o_at + i, o);
+                    }
+                }
+                const float off = m == -INFINITY ? 0.f : -m * sc;
+                const f2 sc2 = pair(__float_as_uint(sc), __float_as_uint(sc)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
+#pragma unroll
+                for (int i = N - 1; i >= 0; --i) {
+                    uint32_t(&y)[32] = s[i & 1];
+                    if (i < N - 1) {
+                        tmem_wait_ld_into(y);
+                        if (masked) hide(y, see[i]);
+                    }
+                    if (i > 0) tmem_ld32_nowait(s_at + (i - 1) * 32, s[(i - 1) & 1]);
+                    // to the upper half of the scores' columns: of those, what has been read
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int n = 0; n < 16; ++n) {
+                        float2 z = parts(fma2(pair(y[2 * n], y[2 * n + 1]), sc2, off2));
+                        z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
+                        l2 = add2(l2, pair(__float_as_uint(z.x), __float_as_uint(z.y)));
+                        packed[n] = pack_bf16(z.x, z.y);
+                    }
+                    tmem_st16(s_at + KT / 2 + i * 16, packed);
+                }
+                if (spoilt) l2 = pair(0x7fc00000u, 0x7fc00000u);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bar[S::PROBS + buf]);
+            }
+            if (!ok) break;
+            // ---- outputs
+            if (!warp_wait(&bar[S::DONE + u], (c - 1) & 1, ok)) break;
+            tc_fence_after();
+            const float2 ll = parts(l2);
+            const float l = ll.x + ll.y;
+            const bool whole = w.first == 0 && w.last == w.tiles;
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const int64_t to = ((int64_t)(w.r.first + token) * p.hkv * p.group + w.at.h * p.group + x % p.group) * D;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(o_at + i, o);
+                    tmem_wait_ld_into(o);
+                    if (live) {
+                        if (p.out_bf16) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + i);
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                uint32_t y[4];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    y[k] = pack_bf16(__uint_as_float(o[n * 8 + 2 * k]) * inv, __uint_as_float(o[n * 8 + 2 * k + 1]) * inv);
+                                dst[n] = make_uint4(y[0], y[1], y[2], y[3]);
+                            }
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + to + i);
+#pragma unroll
+                            for (int n = 0; n < 8; ++n)
+                                dst[n] = make_float4(__uint_as_float(o[4 * n]) * inv, __uint_as_float(o[4 * n + 1]) * inv,
+                                                     __uint_as_float(o[4 * n + 2]) * inv, __uint_as_float(o[4 * n + 3]) * inv);
+                        }
+                    }
+                }
+            } else {
+                const int which = w.first == 0, row = u * tp.tile_tokens * p.group + x;
+                float *dst = part_out(p, S::CAP, D, run, which) + (int64_t)row * D;
+#pragma unroll 1
+                for (int i = 0; i < D; i += 32) {
+                    uint32_t o[32];
+                    tmem_ld32_nowait(o_at + i, o);
+                    tmem_wait_ld_into(o);
+                    if (live) {
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) reinterpret_cast<uint4 *>(dst + i)[n] = make_uint4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]);
+                    }
+                }
+                if (live) *reinterpret_cast<float2 *>(part_stat(p, S::CAP, D, runs, run, which) + row * 2) = make_float2(m * sc, l);
+            }
+            tc_fence_before();
+            mbar_arrive(&bar[S::FREE + u]);
+            ++item;
+        } while (w.next<KT>(p));
+    } else if (warp < 8) {
+        // (d = 256: one tile of rows)
+    } else if (warp == 8) {
+        // ------------------------------------------------------------------ products
+        const uint32_t lead = elect();
+        const uint32_t id_s = idesc_bf16_f32(128, KT), id_o = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
+        const uint32_t d_q = uniform(desc_lo(base, 0));
+        auto scores = [&](int u, int c) {  // S of tile number c
+            const uint32_t d_k = uniform(desc_lo(base + S::OFF_K + c % S::KS * S::kStage, 0));
+            const int buf = u * NB + c % NB;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_ss(lead, tm + S::kScores + buf * KT, d_q + (((u * S::H + (ks >> 2)) * S::kQTile + (ks & 3) * 32) >> 4),
+                       d_k + (((ks >> 2) * S::kHalf + (ks & 3) * 32) >> 4), id_s, ks > 0);
+            commit(lead, &bar[S::SCORES + buf]);
+        };
+        auto keys = [&](int c) {
+            warp_wait(&bar[S::KFULL + c % S::KS], (c / S::KS) & 1, ok);
+            tc_fence_after();
+            return ok;
+        };
+        int c0 = 0, item = 0;
+        do {
+            const int n = w.last - w.first;
+            if (!warp_wait(&bar[S::QFULL], item & 1, ok) || !keys(c0)) break;
+            for (int u = 0; u < U; ++u) scores(u, c0);
+            commit(lead, &bar[S::KEMPTY + c0 % S::KS]);
+            if (n == 1) commit(lead, &bar[S::QEMPTY]);
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                const int c = c0 + j;
+                const bool more = j + 1 < n;
+                if (NB == 2 && more) {
+                    if (!keys(c + 1)) break;
+                    scores(0, c + 1);
+                    commit(lead, &bar[S::KEMPTY + (c + 1) % S::KS]);
+                    if (j + 2 == n) commit(lead, &bar[S::QEMPTY]);
+                }
+                if (!warp_wait(&bar[S::READY + c % S::VS], (c / S::VS) & 1, ok)) break;
+                const uint32_t d_v = uniform(desc_lo(base + S::OFF_V + c % S::VS * S::kStage, S::kHalf));
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int buf = u * NB + c % NB;
+                    if (!warp_wait(&bar[S::PROBS + buf], (c / NB) & 1, ok)) break;
+                    if (j == 0 && item > 0 && !warp_wait(&bar[S::FREE + u], (item - 1) & 1, ok)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < KT / 16; ++ks)
+                        mma_ts(lead, tm + S::kOut + u * D, tm + S::kScores + buf * KT + KT / 2 + ks * 8, d_v + ((ks * 2048) >> 4), id_o, j + ks > 0);
+                    commit(lead, &bar[S::DONE + u]);
+                    if (NB == 1 && more) {
+                        if (u == 0 && !keys(c + 1)) break;
+                        scores(u, c + 1);
+                    }
+                }
+                if (!ok) break;
+                commit(lead, &bar[S::VEMPTY + c % S::VS]);
+                if (NB == 1 && more) {
+                    commit(lead, &bar[S::KEMPTY + (c + 1) % S::KS]);
+                    if (j + 2 == n) commit(lead, &bar[S::QEMPTY]);
+                }
+            }
+            if (!ok) break;
+            c0 += n;
+            ++item;
+        } while (w.next<KT>(p));
+        // no product is under way when the block ends
+        commit(lead, &bar[S::DRAIN]);
+        bool done = true;
+        if (!wait(&bar[S::DRAIN], 0, done)) ok = false;
+    } else if (warp == 9) {
+        // ------------------------------------------------------------------ keys and values
+        const int boxes = KT / tp.box;  // of one half; lane: half lane / boxes, box lane % boxes
+        const bool mine = lane < boxes * S::H;
+        const int half = lane / boxes, at_slot = lane % boxes * tp.box;
+        auto page_of = [&](const Walk &v, int tile) {
+            const int s = tile * KT + at_slot;
+            if (!mine || s >= v.seen) return p.n_pages;
+            const int id = p.table[(int64_t)v.at.b * p.max_pages + s / p.page_size];
+            if (id >= 0 && id < p.n_pages) return id;
+            flag(p.status, GDN_DEV_BAD_PAGE);
+            return p.n_pages;
+        };
+        int c = 0, id = page_of(w, w.first), k_sent = 0, v_sent = 0;
+        auto load = [&](int kv, int at, uint64_t *full, int page, int row, int h) {
+            if (lane == 0) mbar_arrive_expect_tx(full, S::kStage);
+            __syncwarp();
+            if (mine)
+                tma_load_4d(base + at + half * S::kHalf + at_slot * 128, kv ? &v_map : &k_map, full, half * 64, page == p.n_pages ? 0 : row, h, page);
+        };
+        do {
+            if (c > 0) id = page_of(w, w.first);
+            for (int t = w.first; t < w.last; ++t, ++c) {
+                const int page = id, row = (t * KT + at_slot) % p.page_size;
+                if (t + 1 < w.last) id = page_of(w, t + 1);  // a tile ahead
+                if (c >= S::KS && !warp_wait(&bar[S::KEMPTY + c % S::KS], (c / S::KS - 1) & 1, ok)) break;
+                load(0, S::OFF_K + c % S::KS * S::kStage, &bar[S::KFULL + c % S::KS], page, row, w.at.h);
+                k_sent = c + 1;
+                if (c >= S::VS && !warp_wait(&bar[S::VEMPTY + c % S::VS], (c / S::VS - 1) & 1, ok)) break;
+                load(1, S::OFF_V + c % S::VS * S::kStage, &bar[S::VFULL + c % S::VS], page, row, w.at.h);
+                v_sent = c + 1;
+            }
+        } while (ok && w.next<KT>(p));
+        // no copy is under way when the block ends
+        bool done = true;
+        for (int n = max(0, k_sent - S::KS); n < k_sent; ++n) wait(&bar[S::KFULL + n % S::KS], (n / S::KS) & 1, done);
+        for (int n = max(0, v_sent - S::VS); n < v_sent; ++n) wait(&bar[S::VFULL + n % S::VS], (n / S::VS) & 1, done);
+        ok = ok && done;
+    } else if (warp == 10) {
+        // ------------------------------------------------------------------ queries
+        int item = 0;
+        bool sent = false;
+        do {
+            if (item > 0 && !warp_wait(&bar[S::QEMPTY], (item - 1) & 1, ok)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar[S::QFULL], U * S::H * 128 * tp.tile_tokens * p.group);
+                for (int u = 0; u < U; ++u)
+                    for (int h = 0; h < S::H; ++h)
+                        tma_load_3d(sm + (u * S::H + h) * S::kQTile, &q_map, &bar[S::QFULL], h * 64, w.at.h * p.group,
+                                    w.r.first + (w.at.qt * U + u) * tp.tile_tokens);
+            }
+            sent = true;
+            ++item;
+        } while (w.next<KT>(p));
+        bool done = true;
+        if (sent) wait(&bar[S::QFULL], (item - 1) & 1, done);
+        ok = ok && done;
+    } else if (warp == 11) {
+        // ------------------------------------------------------------------ values
+        int c = 0;
+        do {
+            for (int tile = w.first; tile < w.last; ++tile, ++c) {
+                const int st = c % S::VS, slot0 = tile * KT;
+                if (!warp_wait(&bar[S::VFULL + st], (c / S::VS) & 1, ok)) break;
+                if (slot0 + KT > w.r.len) {
+                    uint32_t *spoilt = reinterpret_cast<uint32_t *>(sm + S::OFF_SPOILT) + st * S::kSpoilt;
+                    uint8_t *v = sm + S::OFF_V + st * S::kStage;
+                    for (int i = 0; i < KT / 32; ++i) {
+                        const int row = i * 32 + lane, s = slot0 + row;
+                        bool bad = false;
+                        if (w.r.n > 1 && s >= w.r.len && s < w.seen) {
+                            uint32_t over = 0;  // bf16 entries with all exponent bits set carry into their sign bit
+                            for (int k = 0; k < S::H * 8; ++k) {
+                                const uint4 y = *reinterpret_cast<const uint4 *>(v + (k >> 3) * S::kHalf + row * 128 + ((k & 7) ^ (row & 7)) * 16);
+                                over |= (y.x & 0x7F807F80u) + 0x00800080u, over |= (y.y & 0x7F807F80u) + 0x00800080u;
+                                over |= (y.z & 0x7F807F80u) + 0x00800080u, over |= (y.w & 0x7F807F80u) + 0x00800080u;
+                            }
+                            bad = over & 0x80008000u;
+                        }
+                        if (bad || s >= w.seen)
+                            for (int k = 0; k < S::H * 8; ++k)
+                                *reinterpret_cast<uint4 *>(v + (k >> 3) * S::kHalf + row * 128 + ((k & 7) ^ (row & 7)) * 16) = make_uint4(0, 0, 0, 0);
+                        const uint32_t word = __ballot_sync(0xffffffffu, bad);
+                        if (lane == 0) spoilt[i] = word;
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar[S::READY + st]);
+            }
+        } while (ok && w.next<KT>(p));
+    }
+    if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tm, 512);
+}
+
+// [n_pages][page_size][hkv][d] with the cache's strides as (d, row, head, page); boxes of 64 x box x 1 x 1
+bool encode_pool(CUtensorMap *map, const void *pool, const Params &p, int d, int box) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)p.page_size, (cuuint64_t)p.hkv, (cuuint64_t)p.n_pages};
+    // (a stride that is never taken may be anything)
+    cuuint64_t strides[3] = {p.page_size > 1 ? (cuuint64_t)p.slot_stride * 2 : 16, p.hkv > 1 ? (cuuint64_t)p.head_stride * 2 : 16,
+                             p.n_pages > 1 ? (cuuint64_t)p.page_stride * 2 : 16};
+    cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_queries(CUtensorMap *map, const Params &p, int d, int tile_tokens) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.hkv * p.group, (cuuint64_t)p.total};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)p.q_stride * 2};
+    cuuint32_t boxes[3] = {64, (cuuint32_t)p.group, (cuuint32_t)tile_tokens}, estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t run(Params p, int runs, cudaStream_t stream) {
+    using S = Shape<D>;
+    static int have[16];
+    const cudaError_t e = ensure_smem(attend_tc_kernel<D>, S::kBytes, have);
+    if (e != cudaSuccess) return e;
+    TcParams tp;
+    tp.tile_tokens = kTileRows / p.group;
+    tp.box = p.page_size & -p.page_size;
+    if (tp.box > S::KT) tp.box = S::KT;
+    p.rows = S::U * tp.tile_tokens * p.group;
+    tp.p = p;
+    CUtensorMap q, k, v;
+    if (!encode_queries(&q, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
+        return cudaErrorInvalidValue;
+    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), kThreads, S::kBytes, stream, q, k, v, tp, runs);
+    return f != cudaSuccess ? f : launch_join<D, S::CAP, S::KT>(p, runs, stream);
+}
+
+template <int D>
+Choice choice(const gdn_kv_attend_args &a) {
+    using S = Shape<D>;
+    const int group = a.n_q_heads / a.cache.n_kv_heads;
+    Choice x;
+    x.runs = most_runs(a, false, S::U * (kTileRows / group) * group, S::KT, 1);
+    x.workspace = 4 * workspace_floats(S::CAP, D, x.runs);
+    x.launch = run<D>;
+    return x;
+}
+
+}  // namespace
+
+bool attend_tc_supported(const gdn_kv_attend_args &a) {
+    const gdn_kv_cache &c = a.cache;
+    // (strides of a tensor map: above 0 where they are taken, below 2^40 bytes)
+    auto fits = [](int64_t stride, int64_t n) { return n <= 1 || (stride > 0 && stride < (int64_t)1 << 39); };
+    return c.dtype == GDN_BF16 && (c.d == 64 || c.d == 128 || c.d == 256) && c.page_size % 8 == 0 && c.n_pages > 0 && a.scale > 0.f &&
+           a.n_q_heads / c.n_kv_heads <= kTileRows && attn::aligned16(a) && fits(c.slot_stride, c.page_size) && fits(c.head_stride, c.n_kv_heads) &&
+           fits(c.page_stride, c.n_pages) && a.q_stride < (int64_t)1 << 39;
+}
+
+attn::Choice attend_tc_choice(const gdn_kv_attend_args &a) {
+    return a.cache.d == 64 ? choice<64>(a) : a.cache.d == 128 ? choice<128>(a) : choice<256>(a);
+}
+
+}  // namespace gdn

@@ -1,6 +1,6 @@
 // attn.cuh -- what the attention kernels share (gdn_attention.h): slots of the paged cache, and how the work is cut.
 //
-// An item is a request's key-value head with one tile of R rows (row r: token r / group, query head r % group of
+// An item is a request's key-value head with one tile of R = Params::rows rows (row r: token r / group, query head r % group of
 // those that share the head); its work is the tiles of KT slots that any of its rows sees.  All items' tiles, one
 // item after another, are cut into equal runs, one for each block.  A run that has all of an item writes its
 // outputs; the others write the sum, the maximum and the unscaled output of what they had to the workspace, at most
@@ -18,13 +18,14 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
     int batch, hkv, group, page_size, n_pages, max_pages, total, max_tokens, mask_words, min_tiles;
+    int rows;                               // R: rows of an item
     int64_t page_stride, slot_stride, head_stride, q_stride;
     float scale_log2;
     const void *k, *v, *q;
     const int32_t *table, *lens, *offsets;  // offsets NULL: token b is request b's only one
     const uint32_t *mask;                   // NULL: causal
     void *o;
-    float *ws;                              // [blocks][2][R][d] outputs, then [blocks][2][R][2] maxima (base 2) and sums
+    float *ws;                              // for R <= CAP rows: [blocks][2][CAP][d] outputs, then [blocks][2][CAP][2] maxima (base 2) and sums
     int32_t *status;
     int page_bits;                          // log2 of page_size, or -1
     bool out_bf16;
@@ -54,26 +55,24 @@ __device__ __forceinline__ Request request(const Params &p, int b, int32_t *stat
 }
 
 // Slots that some row of tile qt sees (0: none), and the tiles they make (one at least, which writes the zeros).
-template <int R>
 __device__ __forceinline__ int seen_slots(const Params &p, const Request &r, int qt) {
     if (r.len < 0) return 0;
-    return r.len + (p.mask ? r.n : min(r.n, ((qt + 1) * R + p.group - 1) / p.group));
+    return r.len + (p.mask ? r.n : min(r.n, ((qt + 1) * p.rows + p.group - 1) / p.group));
 }
-template <int R, int KT>
+template <int KT>
 __device__ __forceinline__ int item_tiles(const Params &p, const Request &r, int qt) {
-    return max(1, (seen_slots<R>(p, r, qt) + KT - 1) / KT);
+    return max(1, (seen_slots(p, r, qt) + KT - 1) / KT);
 }
-template <int R>
 __device__ __forceinline__ int row_tiles(const Params &p, const Request &r) {
-    return (int)(((int64_t)r.n * p.group + R - 1) / R);
+    return (int)(((int64_t)r.n * p.group + p.rows - 1) / p.rows);
 }
-template <int R, int KT>
+template <int KT>
 __device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r) {
-    const int nq = row_tiles<R>(p, r);
+    const int nq = row_tiles(p, r);
     if (nq == 0) return 0;
-    if (p.mask || r.len < 0 || r.n == 1) return (int64_t)nq * item_tiles<R, KT>(p, r, 0);
+    if (p.mask || r.len < 0 || r.n == 1) return (int64_t)nq * item_tiles<KT>(p, r, 0);
     int64_t sum = 0;
-    for (int qt = 0; qt < nq; ++qt) sum += item_tiles<R, KT>(p, r, qt);
+    for (int qt = 0; qt < nq; ++qt) sum += item_tiles<KT>(p, r, qt);
     return sum;
 }
 
@@ -94,13 +93,13 @@ __device__ __forceinline__ int64_t div_up(int64_t a, int64_t b) {
 
 // How many tiles a run has, and where run number `run` of `runs` begins and ends (begin == end: nothing to do); `at`
 // is the place where it begins.  Every thread of the block calls this.
-template <int R, int KT>
+template <int KT>
 __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
                                      int64_t &end, Place &at) {
     const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int each = (p.batch + nt - 1) / nt, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<R, KT>(p, request(p, b, status));
+    for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<KT>(p, request(p, b, status));
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -122,7 +121,7 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
         int64_t rest = begin - before;
         for (int b = b0; b < b1; ++b) {
             const Request r = request(p, b, nullptr);
-            const int64_t ht = head_tiles<R, KT>(p, r);
+            const int64_t ht = head_tiles<KT>(p, r);
             if (rest >= ht * p.hkv) {
                 rest -= ht * p.hkv;
                 continue;
@@ -131,11 +130,11 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
             rest -= h * ht;
             int qt = 0;
             if (p.mask || r.len < 0 || r.n == 1) {
-                const int t = item_tiles<R, KT>(p, r, 0);
+                const int t = item_tiles<KT>(p, r, 0);
                 qt = (int)(rest / t);
                 rest -= (int64_t)qt * t;
             } else {
-                for (int t; rest >= (t = item_tiles<R, KT>(p, r, qt)); ++qt) rest -= t;
+                for (int t; rest >= (t = item_tiles<KT>(p, r, qt)); ++qt) rest -= t;
             }
             s.at = Place{b, h, qt, (int)rest};
             break;
@@ -146,10 +145,9 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
 }
 
 // the item after `at`'s
-template <int R>
 __device__ __forceinline__ void next_item(const Params &p, Place &at, Request &r) {
     at.tile = 0;
-    if (++at.qt < row_tiles<R>(p, r)) return;
+    if (++at.qt < row_tiles(p, r)) return;
     at.qt = 0;
     if (++at.h < p.hkv) return;
     at.h = 0;
@@ -179,13 +177,13 @@ __device__ __forceinline__ bool sees(const Params &p, const Request &r, int i, i
     return p.mask ? (p.mask[(int64_t)(r.first + i) * p.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= i;
 }
 
-__device__ __forceinline__ float *part_out(const Params &p, int R, int d, int run, int which) {
-    return p.ws + ((int64_t)run * 2 + which) * R * d;
+__device__ __forceinline__ float *part_out(const Params &p, int cap, int d, int run, int which) {
+    return p.ws + ((int64_t)run * 2 + which) * cap * d;
 }
-__device__ __forceinline__ float *part_stat(const Params &p, int R, int d, int runs, int run, int which) {
-    return p.ws + (int64_t)runs * 2 * R * d + ((int64_t)run * 2 + which) * R * 2;
+__device__ __forceinline__ float *part_stat(const Params &p, int cap, int d, int runs, int run, int which) {
+    return p.ws + (int64_t)runs * 2 * cap * d + ((int64_t)run * 2 + which) * cap * 2;
 }
-__host__ __device__ inline int64_t workspace_floats(int R, int d, int runs) { return (int64_t)runs * 2 * R * (d + 2); }
+__host__ __device__ inline int64_t workspace_floats(int cap, int d, int runs) { return (int64_t)runs * 2 * cap * (d + 2); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -210,32 +208,32 @@ constexpr int kJoinThreads = 128;
 template <int D>
 constexpr int kJoinRows = kJoinThreads * 4 / D;  // a thread has four entries of one row
 
-template <int D, int R, int KT>
+template <int D, int CAP, int KT>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) {
     after_previous();
     __shared__ Scratch s;
     int64_t per, begin, end;
     Place at;
     const int run = blockIdx.x + 1;
-    find<R, KT>(p, runs, run, nullptr, s, per, begin, end, at);
+    find<KT>(p, runs, run, nullptr, s, per, begin, end, at);
     if (begin >= end || at.tile == 0) return;
     const int64_t item = begin - at.tile;
     if (item < begin - per) return;  // cut earlier too: that cut's block joins it
     const Request r = request(p, at.b, nullptr);
-    const int64_t item_end = item + item_tiles<R, KT>(p, r, at.qt);
+    const int64_t item_end = item + item_tiles<KT>(p, r, at.qt);
     const int row = blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-    const int64_t q = (int64_t)at.qt * R + row;
-    if (row >= R || q >= (int64_t)r.n * p.group) return;
+    const int64_t q = (int64_t)at.qt * p.rows + row;
+    if (row >= p.rows || q >= (int64_t)r.n * p.group) return;
     const int last = (int)((item_end - 1) / per);
     float m = -INFINITY, l = 0.f;
-    for (int c = run - 1; c <= last; ++c) m = fmaxf(m, part_stat(p, R, D, runs, c, c == run - 1)[row * 2]);
+    for (int c = run - 1; c <= last; ++c) m = fmaxf(m, part_stat(p, CAP, D, runs, c, c == run - 1)[row * 2]);
     const float base = m == -INFINITY ? 0.f : m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int c = run - 1; c <= last; ++c) {
         const int which = c == run - 1;
-        const float2 st = *reinterpret_cast<const float2 *>(part_stat(p, R, D, runs, c, which) + row * 2);
-        const float4 x = *reinterpret_cast<const float4 *>(part_out(p, R, D, c, which) + row * D + col);
+        const float2 st = *reinterpret_cast<const float2 *>(part_stat(p, CAP, D, runs, c, which) + row * 2);
+        const float4 x = *reinterpret_cast<const float4 *>(part_out(p, CAP, D, c, which) + row * D + col);
         const float f = exp2_fast(st.x - base);
         l = fmaf(f, st.y, l);
         o.x = fmaf(f, x.x, o.x);
@@ -265,10 +263,10 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int R, int KT>
+template <int D, int CAP, int KT>
 cudaError_t launch_join(const Params &p, int runs, cudaStream_t stream) {
     if (runs < 2) return cudaSuccess;
-    return launch_dependent(join_kernel<D, R, KT>, dim3(runs - 1, (R + kJoinRows<D> - 1) / kJoinRows<D>), kJoinThreads, 0, stream, p, runs);
+    return launch_dependent(join_kernel<D, CAP, KT>, dim3(runs - 1, (p.rows + kJoinRows<D> - 1) / kJoinRows<D>), kJoinThreads, 0, stream, p, runs);
 }
 
 // A kernel of this family for some sizes: how many blocks, their workspace, and the launch.
@@ -307,5 +305,8 @@ attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode);
 // few rows a key-value head: bf16, rows on 16 bytes
 bool attend_mma_supported(const gdn_kv_attend_args &a);
 attn::Choice attend_mma_choice(const gdn_kv_attend_args &a, bool decode);
+// many rows: bf16, d from 64 on, pages of whole groups of 8 slots, a positive scale
+bool attend_tc_supported(const gdn_kv_attend_args &a);
+attn::Choice attend_tc_choice(const gdn_kv_attend_args &a);
 
 }  // namespace gdn

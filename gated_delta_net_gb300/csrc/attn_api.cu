@@ -74,6 +74,7 @@ bool nothing(const gdn_kv_attend_args &a, bool decode) {
 
 // the kernel for a call
 gdn::attn::Choice choose(const gdn_kv_attend_args &a, bool decode) {
+    if (!decode && a.max_tokens * (int64_t)(a.n_q_heads / a.cache.n_kv_heads) > 16 && gdn::attend_tc_supported(a)) return gdn::attend_tc_choice(a);
     return gdn::attend_mma_supported(a) ? gdn::attend_mma_choice(a, decode) : gdn::attend_simt_choice(a, decode);
 }
 

@@ -105,7 +105,7 @@ def test_workspace_size_refuses_what_attend_refuses(L):
     assert L.gdn_kv_attend_workspace(None, 0) == -1
 
 
-KERNELS = ["kv_append.cu", "kv_commit.cu", "attend_simt.cu", "attn.cuh"]
+KERNELS = ["kv_append.cu", "kv_commit.cu", "attend_simt.cu", "attend_mma.cu", "attend_tc.cu", "attn.cuh"]
 
 
 @pytest.mark.parametrize("name", KERNELS)
