@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     Request r = request(p, at.b, nullptr);
     int stage = 0, free_stage = S::kStages - 1;
     while (t < end) {
-        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt);
+        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
         const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
         const int row0 = at.qt * kR, rows = r.n * p.group;
         // ---- this lane's rows: g and g + 8
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
             }
             const int slot0 = tile * kKT + warp * kKeys;
             bool poisoned[2] = {false, false};
-            if (slot0 + kKeys > r.len) {  // new tokens, or the end
-                uint32_t spoilt = 0;      // new tokens' values that are not finite
+            if (slot0 + kKeys > common) {
+                uint32_t spoilt = 0;  // new tokens' values that are not finite
                 if (r.n > 1 && slot0 < seen) {
                     const int row = lane & 15;
                     bool finite = true;

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
     while (t < end) {
-        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt);
+        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
         const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
         const int64_t row0 = (int64_t)at.qt * kR, rows = (int64_t)r.n * p.group;
         if (tid < kR) {
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
             }
             __syncthreads();
             const int g = tid / D % kGroups;
-            const bool masked = slot0 + kKT > r.len;  // what is not seen there may be anything
+            const bool masked = slot0 + kKT > common;  // what is not seen there may be anything
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
 #pragma unroll

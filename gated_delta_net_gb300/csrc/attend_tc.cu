@@ -4,25 +4,25 @@
 // tiles of up to 128 rows (whole tokens: 128 / group of them, their query heads side by side; one tile for
 // d = 256), whose queries stay in shared memory, and takes its part of the cache in tiles of 128 slots (64 for d = 256):
 //     S = Q K^T      tcgen05, both from shared memory, to tensor memory
-//     P = 2^(S scale - m)   a thread a row: 128 scores from tensor memory, probabilities as bf16 back over them
+//     P = 2^(S scale - m)   scores from tensor memory, probabilities as bf16 back over them
 //     O += P V       tcgen05, P from tensor memory, V as it lies in shared memory (MN-major)
-// While one tile's rows are in registers, the other tile's products run.  (d = 256: the outputs take half of the tensor
+// While one tile's scores are in registers, the other tile's products run.  (d = 256: the outputs take half of the tensor
 // memory; one tile, whose scores are a tile of slots ahead in a second buffer.)
 //
 // The maximum that outputs are scaled by is moved, and they are multiplied, only where a row's maximum grew by more than 2^8: then
 // probabilities are up to 2^8, which neither bf16 nor the fp32 sums lose anything by.
 // P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.
 //
-// 12 warps:
-//     0-3, 4-7  rows of the first and of the second tile: probabilities, and the outputs at an item's end
-//               (d = 256: 4-7 have nothing to do)
-//     8         issues the products
-//     9         loads keys and values: a TMA box for each page's rows, 128-byte swizzled; pages behind the last seen
-//               slot, or outside the pool, are read past the pool's end, as zeros
-//     10        loads queries (TMA: 64 entries of the group's heads of 128 / group tokens)
-//     11        looks at values before they are multiplied: rows behind the last seen slot become zeros (their
-//               probability is zero, but they may be anything), and so do new tokens' that are not finite, whose
-//               readers' sums become NaN instead
+// 11 warps (7 for d = 256):
+//     4 for each tile of rows, a thread a row.  The first half of a tile's probabilities is multiplied while the second is made.
+//       (Two threads a row, which swap their maxima, are slower: 744 us against 684 for 8192 tokens, 32 heads of 128.)
+//     1 issues the products
+//     1 loads: keys and values with a TMA box for each page's rows, 128-byte swizzled (pages behind the last seen
+//       slot, or outside the pool, are read past the pool's end, as zeros), queries (64 entries of the group's
+//       heads of 128 / group tokens); and walks the items, which the other roles learn from it
+//     1 looks at values before they are multiplied: rows behind the last seen slot become zeros (their
+//       probability is zero, but they may be anything), and so do new tokens' that are not finite, whose
+//       readers' sums become NaN instead
 // Every wait is bounded; one that runs out sets GDN_DEV_TIMEOUT.
 #include "attn.cuh"
 #include "sm100.cuh"
@@ -35,12 +35,25 @@ using namespace attn;
 using namespace sm100;
 using tiles::pack_bf16;
 
-constexpr int kThreads = 384, kTileRows = 128;
+constexpr int kTileRows = 128;
 constexpr float kGrow = 8.f;  // log2 of what a probability may grow to before the maximum moves
+
+// An item, or the part of it that is this block's, as the other roles see it.
+struct __align__(16) Job {
+    int n;           // tiles; 0: no more
+    int tile, tiles; // the first one, and how many the item has
+    int len, seen, common;
+    int first, tokens;  // the request's
+    int token;       // the item's first one
+    int head;        // key-value head
+    int pad[2];
+};
+constexpr int kJobs = 2;
 
 template <int D>
 struct Shape {
     static constexpr int U = D == 256 ? 1 : 2;        // tiles of rows
+    static constexpr int kRowWarps = U * 4, kThreads = kRowWarps * 32 + 96;
     static constexpr int NB = D == 256 ? 2 : 1;       // buffers of scores for each
     static constexpr int KT = D == 256 ? 64 : 128;    // slots of a tile
     static constexpr int H = D / 64;                  // halves (64 entries, 128 bytes) of a row
@@ -54,11 +67,12 @@ struct Shape {
     static constexpr int kSpoilt = KT / 32;           // words of a tile's rows that were not finite
     // barriers
     static constexpr int KFULL = 0, KEMPTY = KFULL + KS, VFULL = KEMPTY + KS, VEMPTY = VFULL + VS, READY = VEMPTY + VS, SCORES = READY + VS,
-                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, DRAIN = QEMPTY + 1, COUNT = DRAIN + 1;
-    static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_SPOILT = OFF_V + VS * kStage, OFF_BAR = (OFF_SPOILT + VS * kSpoilt * 4 + 7) / 8 * 8;
-    static constexpr int kBytes = OFF_BAR + COUNT * 8 + 16 + 1024;  // and what aligning the base takes
+                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB * 2, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, JFULL = QEMPTY + 1, JEMPTY = JFULL + kJobs, DRAIN = JEMPTY + kJobs, COUNT = DRAIN + 1;
+    static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_SPOILT = OFF_V + VS * kStage, OFF_JOB = (OFF_SPOILT + VS * kSpoilt * 4 + 15) / 16 * 16,
+                         OFF_SCRATCH = OFF_JOB + kJobs * (int)sizeof(Job), OFF_BAR = OFF_SCRATCH + (int)sizeof(Scratch);
+    static constexpr int kBytes = OFF_BAR + COUNT * 8 + 8;
     static_assert(kOut + U * D <= 512, "tensor memory");
-    static_assert(kBytes + (int)sizeof(Scratch) <= 232448, "shared memory");
+    static_assert(kBytes <= 232448, "shared memory");
 };
 
 struct TcParams {
@@ -157,11 +171,12 @@ struct Walk {
     Place at;
     Request r;
     int64_t left;
-    int first, last, tiles, seen;
+    int first, last, tiles, seen, common;
     template <int KT>
     __device__ __forceinline__ void item(const Params &p) {
         tiles = item_tiles<KT>(p, r, at.qt);
         seen = seen_slots(p, r, at.qt);
+        common = common_slots(p, r, at.qt);
         first = at.tile;
         last = (int)min((int64_t)tiles, first + left);
     }
@@ -175,32 +190,41 @@ struct Walk {
     }
 };
 
+// 32 bytes, which a lane's row has in a piece: whole sectors
+__device__ __forceinline__ void store32(void *to, const uint32_t *r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __grid_constant__ TcParams tp, int runs) {
     after_previous();
     using S = Shape<D>;
     constexpr int KT = S::KT, U = S::U, NB = S::NB;
-    extern __shared__ uint8_t raw[];
-    __shared__ Scratch scratch;
+    extern __shared__ __align__(1024) uint8_t sm[];
     const Params &p = tp.p;
-    uint8_t *sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
     uint32_t *slot = reinterpret_cast<uint32_t *>(sm + S::OFF_BAR + S::COUNT * 8);
+    Scratch &scratch = *reinterpret_cast<Scratch *>(sm + S::OFF_SCRATCH);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
     int64_t per, begin, end;
-    Walk w;
-    find<KT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, begin, end, w.at);
+    Place start;
+    find<KT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, begin, end, start);
     if (begin >= end) return;
-    if (warp == 8) {
+    if (smem_u32(sm) & 1023) {  // what the swizzled tiles need
+        flag(p.status, GDN_DEV_INTERNAL);
+        return;
+    }
+    if (warp == S::kRowWarps) {
         tmem_alloc(slot, 512);
         tmem_relinquish();
     }
     if (tid == 0) {
         for (int i = 0; i < S::COUNT; ++i) {
             const bool rows = (i >= S::PROBS && i < S::DONE) || (i >= S::FREE && i < S::QFULL);
-            mbar_init(bar + i, rows ? kTileRows : 1);
+            mbar_init(bar + i, rows ? kTileRows : i >= S::JEMPTY && i < S::DRAIN ? S::kRowWarps + 2 : 1);
         }
         fence_mbar_init();
     }
@@ -209,76 +233,81 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tm = uniform(*slot);
     const uint32_t base = smem_u32(sm);
-    w.r = request(p, w.at.b, nullptr);
-    w.left = end - begin;
-    w.item<KT>(p);
     bool ok = true;
+    int item = 0;
+    Job w;
+    // the next item, or false after the last one
+    auto take = [&]() {
+        const int i = item % kJobs;
+        if (!warp_wait(&bar[S::JFULL + i], (item / kJobs) & 1, ok)) return false;
+        w = *reinterpret_cast<const Job *>(sm + S::OFF_JOB + i * sizeof(Job));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[S::JEMPTY + i]);
+        ++item;
+        return w.n > 0;
+    };
 
-    if (warp < 4 * U) {
+    if (warp < S::kRowWarps) {
         // ------------------------------------------------------------------ a row
         const int u = warp >> 2, x = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t o_at = tm + S::kOut + u * D + lanes;
+        const int own_token = u * tp.tile_tokens + x / p.group, own_head = x % p.group;
+        const bool own = x < tp.tile_tokens * p.group;
         const float sc = p.scale_log2, grow = kGrow / sc;
-        int c = 0, item = 0;
-        do {
-            const int token = (w.at.qt * U + u) * tp.tile_tokens + x / p.group;
-            const bool live = x < tp.tile_tokens * p.group && token < w.r.n;
+        int c = 0;
+        while (take()) {
+            const int token = w.token + own_token;
+            const bool live = own && token < w.tokens;
+            const Request r = {w.first, w.tokens, w.len};
             float m = -INFINITY;
             f2 l2 = pair(0u, 0u);
 #pragma unroll 1
-            for (int tile = w.first; tile < w.last; ++tile, ++c) {
+            for (int j = 0; j < w.n; ++j, ++c) {
                 const int buf = u * NB + c % NB;
                 const uint32_t s_at = tm + S::kScores + buf * KT + lanes;
+                constexpr int N = KT / 32;
+                const int slot0 = (w.tile + j) * KT;
+                uint32_t s[N][32];
                 if (!warp_wait(&bar[S::SCORES + buf], (c / NB) & 1, ok)) break;
                 tc_fence_after();
-                // scores in chunks of 32, twice: for the maximum, and backwards, from the chunk at hand, for the probabilities
-                constexpr int N = KT / 32;
-                const int slot0 = tile * KT;
-                const bool masked = slot0 + KT > w.r.len;
-                uint32_t s[2][32], see[N];
-                tmem_ld32_nowait(s_at, s[0]);
-                bool spoilt = false;
-                if (masked) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) tmem_ld32_nowait(s_at + i * 32, s[i]);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < N; ++i) tmem_wait_ld_into(s[i]);
+                if (slot0 + KT > w.common) {
                     const int stage = c % S::VS;
                     if (!warp_wait(&bar[S::READY + stage], (c / S::VS) & 1, ok)) break;
                     const uint32_t *sp = reinterpret_cast<const uint32_t *>(sm + S::OFF_SPOILT) + stage * S::kSpoilt;
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        see[i] = live ? seen_word(p, w.r, token, slot0 + i * 32) : 0u;
-                        spoilt = spoilt || (see[i] & sp[i]);
+                        const uint32_t see = live ? seen_word(p, r, token, slot0 + i * 32) : 0u;
+                        if (see & sp[i]) l2 = pair(0x7fc00000u, 0x7fc00000u);  // and stays NaN
+#pragma unroll
+                        for (int n = 0; n < 32; ++n)
+                            if (!(see >> n & 1)) s[i][n] = 0xff800000u;  // -infinity
                     }
                 }
-                auto hide = [&](uint32_t (&y)[32], uint32_t word) {
-#pragma unroll
-                    for (int n = 0; n < 32; ++n)
-                        if (!(word >> n & 1)) y[n] = 0xff800000u;  // -infinity
-                };
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    uint32_t(&y)[32] = s[i & 1];
-                    tmem_wait_ld_into(y);
-                    if (i + 1 < N) tmem_ld32_nowait(s_at + (i + 1) * 32, s[(i + 1) & 1]);
-                    if (masked) hide(y, see[i]);
+                for (int i = 0; i < N; ++i)
 #pragma unroll
                     for (int n = 0; n < 32; n += 8)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(y[n + 2 * k])), __uint_as_float(y[n + 2 * k + 1]));
-                }
+                        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[i][n + 2 * k])), __uint_as_float(s[i][n + 2 * k + 1]));
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool move = top > m + grow || m == -INFINITY;
                 // the products before are done: with one buffer these scores came after them
                 if (NB == 2 && c > 0 && !warp_wait(&bar[S::DONE + u], (c - 1) & 1, ok)) break;
-                if (tile == w.first) {
+                if (j == 0) {
                     m = top;
                 } else if (__any_sync(0xffffffffu, move)) {
                     tc_fence_after();
                     const float now = move ? fmaxf(top, m) : m;
                     const float f = m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
                     m = now;
-                    const f2 ff = pair(__float_as_uint(f), __float_as_uint(f)), zero = pair(0x80000000u, 0x80000000u);
-                    l2 = fma2(l2, ff, zero);
+                    l2 = fma2(l2, pair(__float_as_uint(f), __float_as_uint(f)), pair(0x80000000u, 0x80000000u));
 #pragma unroll 1
                     for (int i = 0; i < D; i += 16) {
                         uint32_t o[16];
@@ -291,29 +320,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const float off = m == -INFINITY ? 0.f : -m * sc;
                 const f2 sc2 = pair(__float_as_uint(sc), __float_as_uint(sc)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
+                // the first half of the probabilities is multiplied while the second is made
 #pragma unroll
-                for (int i = N - 1; i >= 0; --i) {
-                    uint32_t(&y)[32] = s[i & 1];
-                    if (i < N - 1) {
-                        tmem_wait_ld_into(y);
-                        if (masked) hide(y, see[i]);
-                    }
-                    if (i > 0) tmem_ld32_nowait(s_at + (i - 1) * 32, s[(i - 1) & 1]);
-                    // to the upper half of the scores' columns: of those, what has been read
+                for (int i = 0; i < N; ++i) {
                     uint32_t packed[16];
 #pragma unroll
                     for (int n = 0; n < 16; ++n) {
-                        float2 z = parts(fma2(pair(y[2 * n], y[2 * n + 1]), sc2, off2));
+                        float2 z = parts(fma2(pair(s[i][2 * n], s[i][2 * n + 1]), sc2, off2));
                         z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
                         l2 = add2(l2, pair(__float_as_uint(z.x), __float_as_uint(z.y)));
                         packed[n] = pack_bf16(z.x, z.y);
                     }
-                    tmem_st16(s_at + KT / 2 + i * 16, packed);
+                    tmem_st16(s_at + i * 16, packed);
+                    if (i == N / 2 - 1 || i == N - 1) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&bar[S::PROBS + buf * 2 + (i == N - 1)]);
+                    }
                 }
-                if (spoilt) l2 = pair(0x7fc00000u, 0x7fc00000u);
-                tmem_wait_st();
-                tc_fence_before();
-                mbar_arrive(&bar[S::PROBS + buf]);
             }
             if (!ok) break;
             // ---- outputs
@@ -321,37 +345,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const float2 ll = parts(l2);
             const float l = ll.x + ll.y;
-            const bool whole = w.first == 0 && w.last == w.tiles;
+            const bool whole = w.n == w.tiles;
             if (whole) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t to = ((int64_t)(w.r.first + token) * p.hkv * p.group + w.at.h * p.group + x % p.group) * D;
+                const int64_t to = ((int64_t)(w.first + token) * p.hkv * p.group + w.head * p.group + own_head) * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                     uint32_t o[32];
                     tmem_ld32_nowait(o_at + i, o);
                     tmem_wait_ld_into(o);
+#pragma unroll
+                    for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * inv);
                     if (live) {
                         if (p.out_bf16) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + i);
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) {
-                                uint32_t y[4];
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    y[k] = pack_bf16(__uint_as_float(o[n * 8 + 2 * k]) * inv, __uint_as_float(o[n * 8 + 2 * k + 1]) * inv);
-                                dst[n] = make_uint4(y[0], y[1], y[2], y[3]);
-                            }
+                            for (int n = 0; n < 16; ++n) o[n] = pack_bf16(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1]));
+                            store32(static_cast<__nv_bfloat16 *>(p.o) + to + i, o);
+                            store32(static_cast<__nv_bfloat16 *>(p.o) + to + i + 16, o + 8);
                         } else {
-                            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.o) + to + i);
 #pragma unroll
-                            for (int n = 0; n < 8; ++n)
-                                dst[n] = make_float4(__uint_as_float(o[4 * n]) * inv, __uint_as_float(o[4 * n + 1]) * inv,
-                                                     __uint_as_float(o[4 * n + 2]) * inv, __uint_as_float(o[4 * n + 3]) * inv);
+                            for (int n = 0; n < 4; ++n) store32(static_cast<float *>(p.o) + to + i + n * 8, o + n * 8);
                         }
                     }
                 }
             } else {
-                const int which = w.first == 0, row = u * tp.tile_tokens * p.group + x;
+                const int which = w.tile == 0, row = own_token * p.group + own_head;
                 float *dst = part_out(p, S::CAP, D, run, which) + (int64_t)row * D;
 #pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
@@ -360,18 +378,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_ld_into(o);
                     if (live) {
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) reinterpret_cast<uint4 *>(dst + i)[n] = make_uint4(o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]);
+                        for (int n = 0; n < 4; ++n) store32(dst + i + n * 8, o + n * 8);
                     }
                 }
                 if (live) *reinterpret_cast<float2 *>(part_stat(p, S::CAP, D, runs, run, which) + row * 2) = make_float2(m * sc, l);
             }
             tc_fence_before();
             mbar_arrive(&bar[S::FREE + u]);
-            ++item;
-        } while (w.next<KT>(p));
-    } else if (warp < 8) {
-        // (d = 256: one tile of rows)
-    } else if (warp == 8) {
+        }
+    } else if (warp == S::kRowWarps) {
         // ------------------------------------------------------------------ products
         const uint32_t lead = elect();
         const uint32_t id_s = idesc_bf16_f32(128, KT), id_o = idesc_bf16_f32(128, D) | (1u << 16);  // V is MN-major
@@ -390,10 +405,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             return ok;
         };
-        int c0 = 0, item = 0;
-        do {
-            const int n = w.last - w.first;
-            if (!warp_wait(&bar[S::QFULL], item & 1, ok) || !keys(c0)) break;
+        int c0 = 0;
+        while (take()) {
+            const int n = w.n;
+            if (!warp_wait(&bar[S::QFULL], (item - 1) & 1, ok) || !keys(c0)) break;
             for (int u = 0; u < U; ++u) scores(u, c0);
             commit(lead, &bar[S::KEMPTY + c0 % S::KS]);
             if (n == 1) commit(lead, &bar[S::QEMPTY]);
@@ -412,12 +427,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int buf = u * NB + c % NB;
-                    if (!warp_wait(&bar[S::PROBS + buf], (c / NB) & 1, ok)) break;
-                    if (j == 0 && item > 0 && !warp_wait(&bar[S::FREE + u], (item - 1) & 1, ok)) break;
+                    if (!warp_wait(&bar[S::PROBS + buf * 2], (c / NB) & 1, ok)) break;
+                    if (j == 0 && item > 1 && !warp_wait(&bar[S::FREE + u], item & 1, ok)) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < KT / 16; ++ks)
-                        mma_ts(lead, tm + S::kOut + u * D, tm + S::kScores + buf * KT + KT / 2 + ks * 8, d_v + ((ks * 2048) >> 4), id_o, j + ks > 0);
+                    for (int ks = 0; ks < KT / 16; ++ks) {
+                        if (ks == KT / 32) {
+                            if (!warp_wait(&bar[S::PROBS + buf * 2 + 1], (c / NB) & 1, ok)) break;
+                            tc_fence_after();
+                        }
+                        mma_ts(lead, tm + S::kOut + u * D, tm + S::kScores + buf * KT + ks * 8, d_v + ((ks * 2048) >> 4), id_o, j + ks > 0);
+                    }
+                    if (!ok) break;
                     commit(lead, &bar[S::DONE + u]);
                     if (NB == 1 && more) {
                         if (u == 0 && !keys(c + 1)) break;
@@ -433,14 +454,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!ok) break;
             c0 += n;
-            ++item;
-        } while (w.next<KT>(p));
+        }
         // no product is under way when the block ends
         commit(lead, &bar[S::DRAIN]);
         bool done = true;
         if (!wait(&bar[S::DRAIN], 0, done)) ok = false;
-    } else if (warp == 9) {
-        // ------------------------------------------------------------------ keys and values
+    } else if (warp == S::kRowWarps + 1) {
+        // ------------------------------------------------------------------ keys, values, queries
         const int boxes = KT / tp.box;  // of one half; lane: half lane / boxes, box lane % boxes
         const bool mine = lane < boxes * S::H;
         const int half = lane / boxes, at_slot = lane % boxes * tp.box;
@@ -452,64 +472,87 @@ __global__ void __launch_bounds__(kThreads, 1)
             flag(p.status, GDN_DEV_BAD_PAGE);
             return p.n_pages;
         };
-        int c = 0, id = page_of(w, w.first), k_sent = 0, v_sent = 0;
+        Walk v;
+        v.at = start;
+        v.r = request(p, start.b, nullptr);
+        v.left = end - begin;
+        v.item<KT>(p);
+        int c = 0, id = page_of(v, v.first), k_sent = 0, v_sent = 0, q_sent = 0;
         auto load = [&](int kv, int at, uint64_t *full, int page, int row, int h) {
             if (lane == 0) mbar_arrive_expect_tx(full, S::kStage);
             __syncwarp();
             if (mine)
                 tma_load_4d(base + at + half * S::kHalf + at_slot * 128, kv ? &v_map : &k_map, full, half * 64, page == p.n_pages ? 0 : row, h, page);
         };
-        do {
-            if (c > 0) id = page_of(w, w.first);
-            for (int t = w.first; t < w.last; ++t, ++c) {
+        auto load_queries = [&](int first, int h) {
+            if (q_sent > 0 && !warp_wait(&bar[S::QEMPTY], (q_sent - 1) & 1, ok)) return;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bar[S::QFULL], U * S::H * 128 * tp.tile_tokens * p.group);
+#pragma unroll 1
+                for (int i = 0; i < U * S::H; ++i)
+                    tma_load_3d(sm + i * S::kQTile, &q_map, &bar[S::QFULL], i % S::H * 64, h * p.group, first + i / S::H * tp.tile_tokens);
+            }
+            ++q_sent;
+        };
+        auto tell = [&](bool more) {
+            const int i = item % kJobs;
+            if (item >= kJobs && !warp_wait(&bar[S::JEMPTY + i], (item / kJobs - 1) & 1, ok)) return;
+            if (lane == 0) {
+                Job j = {};
+                if (more)
+                    j = Job{v.last - v.first, v.first, v.tiles, v.r.len, v.seen, v.common, v.r.first, v.r.n, v.at.qt * U * tp.tile_tokens, v.at.h};
+                *reinterpret_cast<Job *>(sm + S::OFF_JOB + i * sizeof(Job)) = j;
+                mbar_arrive(&bar[S::JFULL + i]);
+            }
+            ++item;
+        };
+        tell(true);
+        bool more = true;
+        while (more && ok) {
+            // this item's loads, the next one's place worked out behind the first of them
+            const int first = v.first, last = v.last, h = v.at.h, q_first = v.r.first + v.at.qt * U * tp.tile_tokens;
+            Walk now = v;
+            for (int t = first; t < last; ++t, ++c) {
                 const int page = id, row = (t * KT + at_slot) % p.page_size;
-                if (t + 1 < w.last) id = page_of(w, t + 1);  // a tile ahead
+                if (t + 1 < last) id = page_of(now, t + 1);  // a tile ahead
+                if (c == 0) load_queries(q_first, h);
                 if (c >= S::KS && !warp_wait(&bar[S::KEMPTY + c % S::KS], (c / S::KS - 1) & 1, ok)) break;
-                load(0, S::OFF_K + c % S::KS * S::kStage, &bar[S::KFULL + c % S::KS], page, row, w.at.h);
+                load(0, S::OFF_K + c % S::KS * S::kStage, &bar[S::KFULL + c % S::KS], page, row, h);
                 k_sent = c + 1;
                 if (c >= S::VS && !warp_wait(&bar[S::VEMPTY + c % S::VS], (c / S::VS - 1) & 1, ok)) break;
-                load(1, S::OFF_V + c % S::VS * S::kStage, &bar[S::VFULL + c % S::VS], page, row, w.at.h);
+                load(1, S::OFF_V + c % S::VS * S::kStage, &bar[S::VFULL + c % S::VS], page, row, h);
                 v_sent = c + 1;
+                if (t == first) {
+                    // queries once the item's before are done with: behind the first keys and values
+                    if (c > 0) load_queries(q_first, h);
+                    if (!ok) break;
+                    more = v.next<KT>(p);
+                    tell(more);
+                    if (!ok) break;
+                }
             }
-        } while (ok && w.next<KT>(p));
+            if (more) id = page_of(v, v.first);
+        }
         // no copy is under way when the block ends
         bool done = true;
         for (int n = max(0, k_sent - S::KS); n < k_sent; ++n) wait(&bar[S::KFULL + n % S::KS], (n / S::KS) & 1, done);
         for (int n = max(0, v_sent - S::VS); n < v_sent; ++n) wait(&bar[S::VFULL + n % S::VS], (n / S::VS) & 1, done);
+        if (q_sent > 0) wait(&bar[S::QFULL], (q_sent - 1) & 1, done);
         ok = ok && done;
-    } else if (warp == 10) {
-        // ------------------------------------------------------------------ queries
-        int item = 0;
-        bool sent = false;
-        do {
-            if (item > 0 && !warp_wait(&bar[S::QEMPTY], (item - 1) & 1, ok)) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bar[S::QFULL], U * S::H * 128 * tp.tile_tokens * p.group);
-                for (int u = 0; u < U; ++u)
-                    for (int h = 0; h < S::H; ++h)
-                        tma_load_3d(sm + (u * S::H + h) * S::kQTile, &q_map, &bar[S::QFULL], h * 64, w.at.h * p.group,
-                                    w.r.first + (w.at.qt * U + u) * tp.tile_tokens);
-            }
-            sent = true;
-            ++item;
-        } while (w.next<KT>(p));
-        bool done = true;
-        if (sent) wait(&bar[S::QFULL], (item - 1) & 1, done);
-        ok = ok && done;
-    } else if (warp == 11) {
+    } else {
         // ------------------------------------------------------------------ values
         int c = 0;
-        do {
-            for (int tile = w.first; tile < w.last; ++tile, ++c) {
-                const int st = c % S::VS, slot0 = tile * KT;
+        while (ok && take()) {
+            for (int j = 0; j < w.n; ++j, ++c) {
+                const int st = c % S::VS, slot0 = (w.tile + j) * KT;
                 if (!warp_wait(&bar[S::VFULL + st], (c / S::VS) & 1, ok)) break;
-                if (slot0 + KT > w.r.len) {
+                if (slot0 + KT > w.common) {
                     uint32_t *spoilt = reinterpret_cast<uint32_t *>(sm + S::OFF_SPOILT) + st * S::kSpoilt;
                     uint8_t *v = sm + S::OFF_V + st * S::kStage;
                     for (int i = 0; i < KT / 32; ++i) {
                         const int row = i * 32 + lane, s = slot0 + row;
                         bool bad = false;
-                        if (w.r.n > 1 && s >= w.r.len && s < w.seen) {
+                        if (w.tokens > 1 && s >= w.len && s < w.seen) {
                             uint32_t over = 0;  // bf16 entries with all exponent bits set carry into their sign bit
                             for (int k = 0; k < S::H * 8; ++k) {
                                 const uint4 y = *reinterpret_cast<const uint4 *>(v + (k >> 3) * S::kHalf + row * 128 + ((k & 7) ^ (row & 7)) * 16);
@@ -529,12 +572,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[S::READY + st]);
             }
-        } while (ok && w.next<KT>(p));
+        }
     }
     if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) tmem_dealloc(tm, 512);
+    if (warp == S::kRowWarps) tmem_dealloc(tm, 512);
 }
 
 // [n_pages][page_size][hkv][d] with the cache's strides as (d, row, head, page); boxes of 64 x box x 1 x 1
@@ -575,7 +618,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     CUtensorMap q, k, v;
     if (!encode_queries(&q, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
         return cudaErrorInvalidValue;
-    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), kThreads, S::kBytes, stream, q, k, v, tp, runs);
+    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), S::kThreads, S::kBytes, stream, q, k, v, tp, runs);
     return f != cudaSuccess ? f : launch_join<D, S::CAP, S::KT>(p, runs, stream);
 }
 

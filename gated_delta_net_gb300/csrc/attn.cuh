@@ -59,6 +59,10 @@ __device__ __forceinline__ int seen_slots(const Params &p, const Request &r, int
     if (r.len < 0) return 0;
     return r.len + (p.mask ? r.n : min(r.n, ((qt + 1) * p.rows + p.group - 1) / p.group));
 }
+// Slots from the first on that all of its rows see.
+__device__ __forceinline__ int common_slots(const Params &p, const Request &r, int qt) {
+    return r.len < 0 ? 0 : r.len + (p.mask ? 0 : qt * p.rows / p.group + 1);
+}
 template <int KT>
 __device__ __forceinline__ int item_tiles(const Params &p, const Request &r, int qt) {
     return max(1, (seen_slots(p, r, qt) + KT - 1) / KT);
