@@ -13,13 +13,14 @@
 // probabilities are up to 2^8, which neither bf16 nor the fp32 sums lose anything by.
 // P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.
 //
-// 11 warps (7 for d = 256):
+// 12 warps (8 for d = 256):
 //     4 for each tile of rows, a thread a row.  The first half of a tile's probabilities is multiplied while the second is made.
 //       (Two threads a row, which swap their maxima, are slower: 744 us against 684 for 8192 tokens, 32 heads of 128.)
 //     1 issues the products
 //     1 loads: keys and values with a TMA box for each page's rows, 128-byte swizzled (pages behind the last seen
 //       slot, or outside the pool, are read past the pool's end, as zeros), queries (64 entries of the group's
 //       heads of 128 / group tokens); and walks the items, which the other roles learn from it
+//     1 sends outputs
 //     1 looks at values before they are multiplied: rows behind the last seen slot become zeros (their
 //       probability is zero, but they may be anything), and so do new tokens' that are not finite, whose
 //       readers' sums become NaN instead
@@ -38,22 +39,30 @@ using tiles::pack_bf16;
 constexpr int kTileRows = 128;
 constexpr float kGrow = 8.f;  // log2 of what a probability may grow to before the maximum moves
 
-// An item, or the part of it that is this block's, as the other roles see it.
+// An item, or the part of it that is this block's, as the other roles see it: with all that they need at its end, for reading
+// the kernel's parameters there, out of a cache that nobody else keeps them in, takes over a thousand cycles.
 struct __align__(16) Job {
-    int n;           // tiles; 0: no more
-    int tile, tiles; // the first one, and how many the item has
-    int len, seen, common;
-    int first, tokens;  // the request's
-    int token;       // the item's first one
-    int head;        // key-value head
-    int pad[2];
+    int n;              // tiles; 0: no more
+    int tile;           // the first one
+    int seen, common;
+    int len, tokens;    // the request's
+    int token;          // the item's first one
+    int mask_words;
+    const uint32_t *mask;  // the request's rows, or NULL: causal
+    uint8_t *to;        // where the item's first row goes
+    float2 *stat;       // a part's maxima and sums; NULL: the item is whole
+    int64_t token_pitch;  // bytes between outputs
+    int head_pitch;
+    int first, head;    // the request's first row; key-value head
+    int bf16;           // outputs are
+    int boxes;          // tiles of rows that go out as TMA boxes
 };
-constexpr int kJobs = 2;
+constexpr int kJobs = 3;  // an item is told while the one before it begins and the one before that may be read
 
 template <int D>
 struct Shape {
     static constexpr int U = D == 256 ? 1 : 2;        // tiles of rows
-    static constexpr int kRowWarps = U * 4, kThreads = kRowWarps * 32 + 96;
+    static constexpr int kRowWarps = U * 4, kThreads = kRowWarps * 32 + 128;
     static constexpr int NB = D == 256 ? 2 : 1;       // buffers of scores for each
     static constexpr int KT = D == 256 ? 64 : 128;    // slots of a tile
     static constexpr int H = D / 64;                  // halves (64 entries, 128 bytes) of a row
@@ -61,14 +70,16 @@ struct Shape {
     static constexpr int kHalf = KT * 128;            // of one half of a tile of keys or values
     static constexpr int kStage = H * kHalf;
     static constexpr int kQ = U * H * kQTile;
-    static constexpr int KS = D == 64 ? 5 : 2, VS = D == 64 ? 5 : 3;  // tiles of keys, of values held at a time
+    static constexpr int KS = D == 64 ? 5 : 2, VS = KS;  // tiles of keys, of values held at a time
     static constexpr int CAP = U * kTileRows;
     static constexpr uint32_t kScores = 0, kOut = U * NB * KT;  // tensor-memory columns
-    static constexpr int kSpoilt = KT / 32;           // words of a tile's rows that were not finite
+    // words of a tile's rows that were not finite.  They are read after the tile's probabilities have been handed over, so there is
+    // room for twice the tiles: those of tile c + 2 VS are written when tile c + VS has been multiplied
+    static constexpr int kSpoilt = KT / 32;
     // barriers
     static constexpr int KFULL = 0, KEMPTY = KFULL + KS, VFULL = KEMPTY + KS, VEMPTY = VFULL + VS, READY = VEMPTY + VS, SCORES = READY + VS,
-                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB * 2, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, JFULL = QEMPTY + 1, JEMPTY = JFULL + kJobs, DRAIN = JEMPTY + kJobs, COUNT = DRAIN + 1;
-    static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_SPOILT = OFF_V + VS * kStage, OFF_JOB = (OFF_SPOILT + VS * kSpoilt * 4 + 15) / 16 * 16,
+                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB * 2, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, JFULL = QEMPTY + 1, JEMPTY = JFULL + kJobs, OUT = JEMPTY + kJobs, TAKEN = OUT + U, DRAIN = TAKEN + U, COUNT = DRAIN + 1;
+    static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_OUT = OFF_V + VS * kStage, OFF_SPOILT = OFF_OUT + kRowWarps * 4096, OFF_JOB = (OFF_SPOILT + 2 * VS * kSpoilt * 4 + 15) / 16 * 16,
                          OFF_SCRATCH = OFF_JOB + kJobs * (int)sizeof(Job), OFF_BAR = OFF_SCRATCH + (int)sizeof(Scratch);
     static constexpr int kBytes = OFF_BAR + COUNT * 8 + 8;
     static_assert(kOut + U * D <= 512, "tensor memory");
@@ -146,24 +157,15 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     return r;
 }
 
-// Bits 0..31: whether token i sees slots from .. from + 31.
-__device__ __forceinline__ uint32_t seen_word(const Params &p, const Request &r, int i, int from) {
-    const int j = from - r.len;  // the first one's number among the new tokens
-    if (j <= -32) return 0xffffffffu;
-    const uint32_t before = j < 0 ? (1u << -j) - 1 : 0u;  // committed slots
-    uint32_t word;
-    if (p.mask) {
-        const uint32_t *row = p.mask + (int64_t)(r.first + i) * p.mask_words;
-        const int w = j >> 5;
-        const uint32_t lo = w >= 0 && w < p.mask_words ? row[w] : 0u, hi = w + 1 < p.mask_words ? row[w + 1] : 0u;
-        word = __funnelshift_r(lo, hi, j & 31);
-        const int left = r.n - j;  // bits of tokens there are
-        word &= left <= 0 ? 0u : left < 32 ? (1u << left) - 1 : 0xffffffffu;
-    } else {
-        const int left = i - j + 1;
-        word = left <= 0 ? 0u : left < 32 ? (1u << left) - 1 : 0xffffffffu;
-    }
-    return word | before;
+// Bits 0..31: whether token i of the request sees slots from .. from + 31.
+__device__ __forceinline__ uint32_t seen_word(const Job &w, int i, int from) {
+    const int j = from - w.len;  // the first one's number among the new tokens
+    auto below = [](int n) { return n <= 0 ? 0u : n < 32 ? (1u << n) - 1 : 0xffffffffu; };
+    if (!w.mask) return below(i - j + 1);
+    const uint32_t *row = w.mask + (int64_t)i * w.mask_words;
+    const int at = j >> 5;
+    const uint32_t lo = at >= 0 && at < w.mask_words ? row[at] : 0u, hi = at >= -1 && at + 1 < w.mask_words ? row[at + 1] : 0u;
+    return (__funnelshift_r(lo, hi, j & 31) & below(w.tokens - j)) | below(-j);  // committed slots
 }
 
 // The walk over a run's items, alike in every role.
@@ -190,15 +192,9 @@ struct Walk {
     }
 };
 
-// 32 bytes, which a lane's row has in a piece: whole sectors
-__device__ __forceinline__ void store32(void *to, const uint32_t *r) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
-    attend_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+    attend_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __grid_constant__ TcParams tp, int runs) {
     after_previous();
     using S = Shape<D>;
@@ -223,8 +219,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     }
     if (tid == 0) {
         for (int i = 0; i < S::COUNT; ++i) {
-            const bool rows = (i >= S::PROBS && i < S::DONE) || (i >= S::FREE && i < S::QFULL);
-            mbar_init(bar + i, rows ? kTileRows : i >= S::JEMPTY && i < S::DRAIN ? S::kRowWarps + 2 : 1);
+            const bool rows = (i >= S::PROBS && i < S::DONE) || (i >= S::FREE && i < S::QFULL) || (i >= S::OUT && i < S::TAKEN);
+            mbar_init(bar + i, rows ? kTileRows : i >= S::JEMPTY && i < S::OUT ? S::kRowWarps + 3 : 1);
         }
         fence_mbar_init();
     }
@@ -235,16 +231,17 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     const uint32_t base = smem_u32(sm);
     bool ok = true;
     int item = 0;
-    Job w;
-    // the next item, or false after the last one
-    auto take = [&]() {
+    // the next item, or NULL after the last one; and the end of reading it
+    auto take = [&]() -> const Job * {
         const int i = item % kJobs;
-        if (!warp_wait(&bar[S::JFULL + i], (item / kJobs) & 1, ok)) return false;
-        w = *reinterpret_cast<const Job *>(sm + S::OFF_JOB + i * sizeof(Job));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[S::JEMPTY + i]);
+        if (!warp_wait(&bar[S::JFULL + i], (item / kJobs) & 1, ok)) return nullptr;
         ++item;
-        return w.n > 0;
+        const Job *w = reinterpret_cast<const Job *>(sm + S::OFF_JOB) + i;
+        return w->n > 0 ? w : nullptr;
+    };
+    auto drop = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[S::JEMPTY + (item - 1) % kJobs]);
     };
 
     if (warp < S::kRowWarps) {
@@ -253,13 +250,14 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
         const uint32_t o_at = tm + S::kOut + u * D + lanes;
         const int own_token = u * tp.tile_tokens + x / p.group, own_head = x % p.group;
+        const int own_row = own_token * p.group + own_head;
         const bool own = x < tp.tile_tokens * p.group;
         const float sc = p.scale_log2, grow = kGrow / sc;
-        int c = 0;
-        while (take()) {
+        int c = 0, rounds = 0;
+        while (const Job *wp = take()) {
+            const Job &w = *wp;
             const int token = w.token + own_token;
             const bool live = own && token < w.tokens;
-            const Request r = {w.first, w.tokens, w.len};
             float m = -INFINITY;
             f2 l2 = pair(0u, 0u);
 #pragma unroll 1
@@ -273,20 +271,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 tc_fence_after();
 #pragma unroll
                 for (int i = 0; i < N; ++i) tmem_ld32_nowait(s_at + i * 32, s[i]);
-                tmem_wait_ld();
+                const bool masked = slot0 + KT > w.common;
 #pragma unroll
                 for (int i = 0; i < N; ++i) tmem_wait_ld_into(s[i]);
-                if (slot0 + KT > w.common) {
-                    const int stage = c % S::VS;
-                    if (!warp_wait(&bar[S::READY + stage], (c / S::VS) & 1, ok)) break;
-                    const uint32_t *sp = reinterpret_cast<const uint32_t *>(sm + S::OFF_SPOILT) + stage * S::kSpoilt;
+                if (masked) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) {
-                        const uint32_t see = live ? seen_word(p, r, token, slot0 + i * 32) : 0u;
-                        if (see & sp[i]) l2 = pair(0x7fc00000u, 0x7fc00000u);  // and stays NaN
+                        const uint32_t see = live ? seen_word(w, token, slot0 + i * 32) : 0u;
 #pragma unroll
-                        for (int n = 0; n < 32; ++n)
-                            if (!(see >> n & 1)) s[i][n] = 0xff800000u;  // -infinity
+                        for (int n = 0; n < 32; ++n) s[i][n] = see & 1u << n ? s[i][n] : 0xff800000u;  // -infinity
                     }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -323,20 +316,32 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 // the first half of the probabilities is multiplied while the second is made
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    uint32_t packed[16];
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        float2 z = parts(fma2(pair(s[i][2 * n], s[i][2 * n + 1]), sc2, off2));
-                        z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
-                        l2 = add2(l2, pair(__float_as_uint(z.x), __float_as_uint(z.y)));
-                        packed[n] = pack_bf16(z.x, z.y);
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t packed[8];
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            float2 z = parts(fma2(pair(s[i][h * 16 + 2 * n], s[i][h * 16 + 2 * n + 1]), sc2, off2));
+                            z.x = exp2_fast(z.x), z.y = exp2_fast(z.y);
+                            l2 = add2(l2, pair(__float_as_uint(z.x), __float_as_uint(z.y)));
+                            packed[n] = pack_bf16(z.x, z.y);
+                        }
+                        tmem_st8(s_at + i * 16 + h * 8, packed);
                     }
-                    tmem_st16(s_at + i * 16, packed);
                     if (i == N / 2 - 1 || i == N - 1) {
                         tmem_wait_st();
                         tc_fence_before();
                         mbar_arrive(&bar[S::PROBS + buf * 2 + (i == N - 1)]);
                     }
+                }
+                if (masked) {
+                    if (!warp_wait(&bar[S::READY + c % S::VS], (c / S::VS) & 1, ok)) break;
+                    const uint32_t *sp = reinterpret_cast<const uint32_t *>(sm + S::OFF_SPOILT) + c % (2 * S::VS) * S::kSpoilt;
+                    uint32_t hit = 0;
+#pragma unroll 1
+                    for (int i = 0; i < N; ++i)
+                        if (sp[i] && live) hit |= sp[i] & seen_word(w, token, slot0 + i * 32);
+                    if (hit) l2 = pair(0x7fc00000u, 0x7fc00000u);  // and stays NaN
                 }
             }
             if (!ok) break;
@@ -345,46 +350,65 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             tc_fence_after();
             const float2 ll = parts(l2);
             const float l = ll.x + ll.y;
-            const bool whole = w.n == w.tiles;
-            if (whole) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                const int64_t to = ((int64_t)(w.first + token) * p.hkv * p.group + w.head * p.group + own_head) * D;
+            const float inv = w.stat ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            if (w.stat && live) w.stat[own_row] = make_float2(m * sc, l);
+            // 64 columns at a time to shared memory, from where another warp sends them as TMA boxes.  (Stores by these warps
+            // keep the memory pipe, and what stands behind it in the block, for 4000 cycles an item, whole rows or 16 bytes a
+            // lane.)  Parts, and a request's last tokens where they do not fill a tile, go out from here, four rows at a time.
+            const bool boxed = u < w.boxes;
+            uint8_t *out = sm + S::OFF_OUT + warp * 4096;
+            const int64_t mine = live ? own_token * w.token_pitch + own_head * w.head_pitch : -1;
+            auto rows_out = [&](int at) {  // the 128 bytes from `at` on
+                __syncwarp();
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int k = n * 4 + (lane >> 3);
+                    const int64_t row = __shfl_sync(0xffffffffu, mine, k);
+                    if (row >= 0)
+                        *reinterpret_cast<uint4 *>(w.to + row + at + (lane & 7) * 16) = *reinterpret_cast<const uint4 *>(out + k * 128 + ((lane & 7) ^ (k & 7)) * 16);
+                }
+                __syncwarp();
+            };
 #pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(o_at + i, o);
-                    tmem_wait_ld_into(o);
+            for (int i = 0; i < D; i += 64) {
+                uint32_t o[64];
+                tmem_ld32_nowait(o_at + i, reinterpret_cast<uint32_t(&)[32]>(o[0]));
+                tmem_ld32_nowait(o_at + i + 32, reinterpret_cast<uint32_t(&)[32]>(o[32]));
+                tmem_wait_ld_into(reinterpret_cast<uint32_t(&)[32]>(o[0]));
+                tmem_wait_ld_into(reinterpret_cast<uint32_t(&)[32]>(o[32]));
+                if (i + 64 == D) {
+                    tc_fence_before();
+                    mbar_arrive(&bar[S::FREE + u]);
+                }
 #pragma unroll
-                    for (int n = 0; n < 32; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * inv);
-                    if (live) {
-                        if (p.out_bf16) {
+                for (int n = 0; n < 64; ++n) o[n] = __float_as_uint(__uint_as_float(o[n]) * inv);
+                auto put = [&](int n, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+                    *reinterpret_cast<uint4 *>(out + lane * 128 + (n ^ (lane & 7)) * 16) = make_uint4(a, b, c, d);
+                };
+                if (rounds > 0 && !warp_wait(&bar[S::TAKEN + u], (rounds - 1) & 1, ok)) break;  // the place is free
+                if (w.bf16) {
 #pragma unroll
-                            for (int n = 0; n < 16; ++n) o[n] = pack_bf16(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1]));
-                            store32(static_cast<__nv_bfloat16 *>(p.o) + to + i, o);
-                            store32(static_cast<__nv_bfloat16 *>(p.o) + to + i + 16, o + 8);
-                        } else {
+                    for (int n = 0; n < 32; ++n) o[n] = pack_bf16(__uint_as_float(o[2 * n]), __uint_as_float(o[2 * n + 1]));
 #pragma unroll
-                            for (int n = 0; n < 4; ++n) store32(static_cast<float *>(p.o) + to + i + n * 8, o + n * 8);
-                        }
+                    for (int n = 0; n < 8; ++n) put(n, o[4 * n], o[4 * n + 1], o[4 * n + 2], o[4 * n + 3]);
+                    if (boxed) {
+                        fence_proxy_async_smem();
+                        mbar_arrive(&bar[S::OUT + u]);
+                        ++rounds;
+                    } else {
+                        rows_out(i * 2);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) put(n, o[h * 32 + 4 * n], o[h * 32 + 4 * n + 1], o[h * 32 + 4 * n + 2], o[h * 32 + 4 * n + 3]);
+                        rows_out(i * 4 + h * 128);
                     }
                 }
-            } else {
-                const int which = w.tile == 0, row = own_token * p.group + own_head;
-                float *dst = part_out(p, S::CAP, D, run, which) + (int64_t)row * D;
-#pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                    uint32_t o[32];
-                    tmem_ld32_nowait(o_at + i, o);
-                    tmem_wait_ld_into(o);
-                    if (live) {
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) store32(dst + i + n * 8, o + n * 8);
-                    }
-                }
-                if (live) *reinterpret_cast<float2 *>(part_stat(p, S::CAP, D, runs, run, which) + row * 2) = make_float2(m * sc, l);
             }
-            tc_fence_before();
-            mbar_arrive(&bar[S::FREE + u]);
+            if (!ok) break;
+            drop();
         }
     } else if (warp == S::kRowWarps) {
         // ------------------------------------------------------------------ products
@@ -406,9 +430,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             return ok;
         };
         int c0 = 0;
-        while (take()) {
+        while (const Job *wp = take()) {
+            const Job &w = *wp;
             const int n = w.n;
             if (!warp_wait(&bar[S::QFULL], (item - 1) & 1, ok) || !keys(c0)) break;
+#pragma unroll 1
             for (int u = 0; u < U; ++u) scores(u, c0);
             commit(lead, &bar[S::KEMPTY + c0 % S::KS]);
             if (n == 1) commit(lead, &bar[S::QEMPTY]);
@@ -454,6 +480,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             }
             if (!ok) break;
             c0 += n;
+            drop();
         }
         // no product is under way when the block ends
         commit(lead, &bar[S::DRAIN]);
@@ -499,8 +526,24 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
             if (item >= kJobs && !warp_wait(&bar[S::JEMPTY + i], (item / kJobs - 1) & 1, ok)) return;
             if (lane == 0) {
                 Job j = {};
-                if (more)
-                    j = Job{v.last - v.first, v.first, v.tiles, v.r.len, v.seen, v.common, v.r.first, v.r.n, v.at.qt * U * tp.tile_tokens, v.at.h};
+                if (more) {
+                    const bool whole = v.last - v.first == v.tiles;
+                    const int token = v.at.qt * U * tp.tile_tokens, e = whole && p.out_bf16 ? 2 : 4;
+                    j.n = v.last - v.first, j.tile = v.first, j.seen = v.seen, j.common = v.common;
+                    j.len = v.r.len, j.tokens = v.r.n, j.token = token, j.first = v.r.first, j.head = v.at.h;
+                    j.mask_words = p.mask_words;
+                    j.mask = p.mask ? p.mask + (int64_t)v.r.first * p.mask_words : nullptr;
+                    j.bf16 = e == 2;
+                    j.boxes = e == 2 ? min(U, (v.r.n - token) / tp.tile_tokens) : 0;
+                    j.head_pitch = D * e;
+                    j.token_pitch = (int64_t)D * e * (whole ? p.hkv * p.group : p.group);
+                    if (whole) {
+                        j.to = static_cast<uint8_t *>(p.o) + ((int64_t)(v.r.first + token) * p.hkv * p.group + v.at.h * p.group) * (D * e);
+                    } else {
+                        j.to = reinterpret_cast<uint8_t *>(part_out(p, S::CAP, D, run, v.first == 0));
+                        j.stat = reinterpret_cast<float2 *>(part_stat(p, S::CAP, D, runs, run, v.first == 0));
+                    }
+                }
                 *reinterpret_cast<Job *>(sm + S::OFF_JOB + i * sizeof(Job)) = j;
                 mbar_arrive(&bar[S::JFULL + i]);
             }
@@ -539,21 +582,46 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
         for (int n = max(0, v_sent - S::VS); n < v_sent; ++n) wait(&bar[S::VFULL + n % S::VS], (n / S::VS) & 1, done);
         if (q_sent > 0) wait(&bar[S::QFULL], (q_sent - 1) & 1, done);
         ok = ok && done;
+    } else if (warp == S::kRowWarps + 3) {
+        // ------------------------------------------------------------------ outputs
+        int rounds[U] = {};
+        while (const Job *wp = ok ? take() : nullptr) {
+            const Job &w = *wp;
+            for (int n = 0; n < w.boxes * S::H && ok; ++n) {
+                // the tiles take turns, as their outputs come
+                const int u = n % w.boxes, x = n / w.boxes * 64;
+                const int k = u ? rounds[U - 1] : rounds[0];
+                if (!warp_wait(&bar[S::OUT + u], k & 1, ok)) break;
+                if (lane == 0) {
+                    tma_store_3d(&o_map, sm + S::OFF_OUT + u * kTileRows * 128, x, w.head * p.group, w.first + w.token + u * tp.tile_tokens);
+                    bulk_commit();
+                    bulk_wait_read();
+                    mbar_arrive(&bar[S::TAKEN + u]);
+                }
+                __syncwarp();
+                if (u) ++rounds[U - 1];
+                else ++rounds[0];
+            }
+            if (ok) drop();
+        }
     } else {
         // ------------------------------------------------------------------ values
         int c = 0;
-        while (ok && take()) {
+        while (const Job *wp = ok ? take() : nullptr) {
+            const Job &w = *wp;
             for (int j = 0; j < w.n; ++j, ++c) {
                 const int st = c % S::VS, slot0 = (w.tile + j) * KT;
                 if (!warp_wait(&bar[S::VFULL + st], (c / S::VS) & 1, ok)) break;
                 if (slot0 + KT > w.common) {
-                    uint32_t *spoilt = reinterpret_cast<uint32_t *>(sm + S::OFF_SPOILT) + st * S::kSpoilt;
+                    uint32_t *spoilt = reinterpret_cast<uint32_t *>(sm + S::OFF_SPOILT) + c % (2 * S::VS) * S::kSpoilt;
                     uint8_t *v = sm + S::OFF_V + st * S::kStage;
+#pragma unroll 1
                     for (int i = 0; i < KT / 32; ++i) {
                         const int row = i * 32 + lane, s = slot0 + row;
                         bool bad = false;
                         if (w.tokens > 1 && s >= w.len && s < w.seen) {
                             uint32_t over = 0;  // bf16 entries with all exponent bits set carry into their sign bit
+#pragma unroll 8
                             for (int k = 0; k < S::H * 8; ++k) {
                                 const uint4 y = *reinterpret_cast<const uint4 *>(v + (k >> 3) * S::kHalf + row * 128 + ((k & 7) ^ (row & 7)) * 16);
                                 over |= (y.x & 0x7F807F80u) + 0x00800080u, over |= (y.y & 0x7F807F80u) + 0x00800080u;
@@ -562,6 +630,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                             bad = over & 0x80008000u;
                         }
                         if (bad || s >= w.seen)
+#pragma unroll 8
                             for (int k = 0; k < S::H * 8; ++k)
                                 *reinterpret_cast<uint4 *>(v + (k >> 3) * S::kHalf + row * 128 + ((k & 7) ^ (row & 7)) * 16) = make_uint4(0, 0, 0, 0);
                         const uint32_t word = __ballot_sync(0xffffffffu, bad);
@@ -572,6 +641,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar[S::READY + st]);
             }
+            drop();
         }
     }
     if (!ok) flag(p.status, GDN_DEV_TIMEOUT);
@@ -593,13 +663,14 @@ bool encode_pool(CUtensorMap *map, const void *pool, const Params &p, int d, int
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_queries(CUtensorMap *map, const Params &p, int d, int tile_tokens) {
+// [T][heads][d] as (d, head, token); boxes of a tile of rows
+bool encode_tokens(CUtensorMap *map, const void *rows, int64_t stride, const Params &p, int d, int tile_tokens) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)p.hkv * p.group, (cuuint64_t)p.total};
-    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)p.q_stride * 2};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
     cuuint32_t boxes[3] = {64, (cuuint32_t)p.group, (cuuint32_t)tile_tokens}, estr[3] = {1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p.q), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(rows), dims, strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -615,10 +686,10 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     if (tp.box > S::KT) tp.box = S::KT;
     p.rows = S::U * tp.tile_tokens * p.group;
     tp.p = p;
-    CUtensorMap q, k, v;
-    if (!encode_queries(&q, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
+    CUtensorMap q, o, k, v;
+    if (!encode_tokens(&q, p.q, p.q_stride, p, D, tp.tile_tokens) || !encode_tokens(&o, p.o, (int64_t)p.hkv * p.group * D, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
         return cudaErrorInvalidValue;
-    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), S::kThreads, S::kBytes, stream, q, k, v, tp, runs);
+    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), S::kThreads, S::kBytes, stream, q, o, k, v, tp, runs);
     return f != cudaSuccess ? f : launch_join<D, S::CAP, S::KT>(p, runs, stream);
 }
 

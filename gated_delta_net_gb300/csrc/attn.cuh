@@ -68,7 +68,7 @@ __device__ __forceinline__ int item_tiles(const Params &p, const Request &r, int
     return max(1, (seen_slots(p, r, qt) + KT - 1) / KT);
 }
 __device__ __forceinline__ int row_tiles(const Params &p, const Request &r) {
-    return (int)(((int64_t)r.n * p.group + p.rows - 1) / p.rows);
+    return (int)((uint32_t)(r.n * p.group + p.rows - 1) / (uint32_t)p.rows);  // (n group is at most 2^30)
 }
 template <int KT>
 __device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r) {
@@ -76,6 +76,7 @@ __device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r)
     if (nq == 0) return 0;
     if (p.mask || r.len < 0 || r.n == 1) return (int64_t)nq * item_tiles<KT>(p, r, 0);
     int64_t sum = 0;
+#pragma unroll 1
     for (int qt = 0; qt < nq; ++qt) sum += item_tiles<KT>(p, r, qt);
     return sum;
 }
@@ -98,11 +99,12 @@ __device__ __forceinline__ int64_t div_up(int64_t a, int64_t b) {
 // How many tiles a run has, and where run number `run` of `runs` begins and ends (begin == end: nothing to do); `at`
 // is the place where it begins.  Every thread of the block calls this.
 template <int KT>
-__device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
+static __device__ __noinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
                                      int64_t &end, Place &at) {
     const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int each = (p.batch + nt - 1) / nt, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
     int64_t mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<KT>(p, request(p, b, status));
     int64_t upto = mine;
 #pragma unroll
@@ -113,6 +115,7 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
     if (lane == 31) s.warp_sum[warp] = upto;
     __syncthreads();
     int64_t before = upto - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < nt / 32; ++w) {
         const int64_t x = s.warp_sum[w];
         if (w < warp) before += x;
@@ -123,6 +126,7 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
     end = min(total, begin + per);
     if (begin < end && before <= begin && begin < before + mine) {
         int64_t rest = begin - before;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const Request r = request(p, b, nullptr);
             const int64_t ht = head_tiles<KT>(p, r);
@@ -130,14 +134,15 @@ __device__ __forceinline__ void find(const Params &p, int runs, int run, int32_t
                 rest -= ht * p.hkv;
                 continue;
             }
-            const int h = (int)(rest / ht);
+            const int h = (int)(div_up(rest + 1, ht) - 1);
             rest -= h * ht;
             int qt = 0;
             if (p.mask || r.len < 0 || r.n == 1) {
                 const int t = item_tiles<KT>(p, r, 0);
-                qt = (int)(rest / t);
+                qt = (int)(div_up(rest + 1, t) - 1);
                 rest -= (int64_t)qt * t;
             } else {
+#pragma unroll 1
                 for (int t; rest >= (t = item_tiles<KT>(p, r, qt)); ++qt) rest -= t;
             }
             s.at = Place{b, h, qt, (int)rest};
@@ -226,10 +231,11 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) 
     const Request r = request(p, at.b, nullptr);
     const int64_t item_end = item + item_tiles<KT>(p, r, at.qt);
     const int row = blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-    const int64_t q = (int64_t)at.qt * p.rows + row;
-    if (row >= p.rows || q >= (int64_t)r.n * p.group) return;
-    const int last = (int)((item_end - 1) / per);
+    const int q = at.qt * p.rows + row;
+    if (row >= p.rows || q >= r.n * p.group) return;
+    const int last = (int)(div_up(item_end, per) - 1);
     float m = -INFINITY, l = 0.f;
+#pragma unroll 4
     for (int c = run - 1; c <= last; ++c) m = fmaxf(m, part_stat(p, CAP, D, runs, c, c == run - 1)[row * 2]);
     const float base = m == -INFINITY ? 0.f : m;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) 
     }
     // nothing seen: zeros; a NaN sum stays one
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int token = r.first + (int)(q / p.group), head = at.h * p.group + (int)(q % p.group);
+    const int token = r.first + q / p.group, head = at.h * p.group + q % p.group;
     store4(p, ((int64_t)token * p.hkv * p.group + head) * D + col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
