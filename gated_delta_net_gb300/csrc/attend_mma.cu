@@ -70,6 +70,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     int64_t per, t, end;
     Place at;
     find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, t, end, at);
+    if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
     if (t >= end) return;
     uint8_t *ring = sm + warp * S::kWarp;
     float *mine = reinterpret_cast<float *>(sm + kWarps * S::kWarp + (warp & 1) * S::kJoin);
@@ -322,7 +323,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     const cudaError_t e = ensure_smem(attend_mma_kernel<D>, Ring<D>::kBytes, have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_mma_kernel<D>, dim3(runs), kThreads, Ring<D>::kBytes, stream, p, runs);
-    return f != cudaSuccess ? f : launch_join<D, kR, kKT>(p, runs, stream);
+    return f != cudaSuccess ? f : launch_join<D, kR>(p, runs, stream);
 }
 
 template <int D>

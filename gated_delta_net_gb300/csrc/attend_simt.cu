@@ -57,6 +57,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     int64_t per, t, end;
     Place at;
     find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
+    if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
     while (t < end) {
@@ -170,7 +171,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);
-    return f != cudaSuccess ? f : launch_join<D, kR, kKT>(p, runs, stream);
+    return f != cudaSuccess ? f : launch_join<D, kR>(p, runs, stream);
 }
 
 template <typename T, bool VEC>

@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1)
     int64_t per, begin, end;
     Place start;
     find<KT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, begin, end, start);
+    if (tid == 0) tell_cut<KT>(p, S::CAP, D, runs, run, per, begin, end, start);
     if (begin >= end) return;
     if (smem_u32(sm) & 1023) {  // what the swizzled tiles need
         flag(p.status, GDN_DEV_INTERNAL);
@@ -690,7 +691,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     if (!encode_tokens(&q, p.q, p.q_stride, p, D, tp.tile_tokens) || !encode_tokens(&o, p.o, (int64_t)p.hkv * p.group * D, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
         return cudaErrorInvalidValue;
     const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), S::kThreads, S::kBytes, stream, q, o, k, v, tp, runs);
-    return f != cudaSuccess ? f : launch_join<D, S::CAP, S::KT>(p, runs, stream);
+    return f != cudaSuccess ? f : launch_join<D, S::CAP>(p, runs, stream);
 }
 
 template <int D>

@@ -25,7 +25,7 @@ struct Params {
     const int32_t *table, *lens, *offsets;  // offsets NULL: token b is request b's only one
     const uint32_t *mask;                   // NULL: causal
     void *o;
-    float *ws;                              // for R <= CAP rows: [blocks][2][CAP][d] outputs, then [blocks][2][CAP][2] maxima (base 2) and sums
+    float *ws;                              // for R <= CAP rows: [blocks][2][CAP][d] outputs, [blocks][2][CAP][2] maxima (base 2) and sums, [blocks] Cut
     int32_t *status;
     int page_bits;                          // log2 of page_size, or -1
     bool out_bf16;
@@ -70,15 +70,29 @@ __device__ __forceinline__ int item_tiles(const Params &p, const Request &r, int
 __device__ __forceinline__ int row_tiles(const Params &p, const Request &r) {
     return (int)((uint32_t)(r.n * p.group + p.rows - 1) / (uint32_t)p.rows);  // (n group is at most 2^30)
 }
+// sum of floor((a i + b) / m) for i = 0 .. n - 1 (a, b >= 0), by turning the lattice points under the line over as in Euclid's algorithm
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+#pragma unroll 1
+    while (n > 0) {
+        if (a >= m) sum += n * (n - 1) / 2 * (a / m), a %= m;
+        if (b >= m) sum += n * (b / m), b %= m;
+        const int64_t top = a * n + b;
+        if (top < m) break;
+        n = top / m, b = top % m;
+        const int64_t old = m;
+        m = a, a = old;
+    }
+    return sum;
+}
+// all tiles of one head of a request: tile qt ends at floor((R (qt + 1) + group - 1) / group) of the new tokens
 template <int KT>
 __device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r) {
     const int nq = row_tiles(p, r);
     if (nq == 0) return 0;
-    if (p.mask || r.len < 0 || r.n == 1) return (int64_t)nq * item_tiles<KT>(p, r, 0);
-    int64_t sum = 0;
-#pragma unroll 1
-    for (int qt = 0; qt < nq; ++qt) sum += item_tiles<KT>(p, r, qt);
-    return sum;
+    const int last = item_tiles<KT>(p, r, nq - 1);
+    if (p.mask || r.len < 0 || nq == 1) return (int64_t)nq * last;
+    return last + floor_sum(nq - 1, (int64_t)p.group * KT, p.rows, p.rows + p.group - 1 + p.group * ((int64_t)r.len + KT - 1));
 }
 
 // A place in the work: tile `tile` of an item.
@@ -89,23 +103,17 @@ struct Place {
 // What find() shares between the threads of a block.
 struct Scratch {
     int64_t warp_sum[32];
+    int64_t rest;
     Place at;
 };
 
 __device__ __forceinline__ int64_t div_up(int64_t a, int64_t b) {
-    return a >> 31 ? (a + b - 1) / b : (int64_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b);
+    return (a | b) >> 31 ? (a + b - 1) / b : (int64_t)(((uint32_t)a + (uint32_t)b - 1) / (uint32_t)b);
 }
 
-// How many tiles a run has, and where run number `run` of `runs` begins and ends (begin == end: nothing to do); `at`
-// is the place where it begins.  Every thread of the block calls this.
-template <int KT>
-static __device__ __noinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
-                                     int64_t &end, Place &at) {
-    const int nt = blockDim.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int each = (p.batch + nt - 1) / nt, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
-    int64_t mine = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<KT>(p, request(p, b, status));
+// Sum of `mine` over the block's threads before this one, and over all.  Every thread of the block calls this.
+__device__ __forceinline__ int64_t scan(int64_t mine, Scratch &s, int64_t &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -114,17 +122,33 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
     }
     if (lane == 31) s.warp_sum[warp] = upto;
     __syncthreads();
-    int64_t before = upto - mine, total = 0;
+    int64_t before = upto - mine;
+    total = 0;
 #pragma unroll 1
-    for (int w = 0; w < nt / 32; ++w) {
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         const int64_t x = s.warp_sum[w];
         if (w < warp) before += x;
         total += x;
     }
+    return before;
+}
+
+// How many tiles a run has, and where run number `run` of `runs` begins and ends (begin == end: nothing to do); `at`
+// is the place where it begins.  Every thread of the block calls this.
+template <int KT>
+static __device__ __noinline__ void find(const Params &p, int runs, int run, int32_t *status, Scratch &s, int64_t &per, int64_t &begin,
+                                     int64_t &end, Place &at) {
+    const int nt = blockDim.x, tid = threadIdx.x;
+    const int each = (p.batch + nt - 1) / nt, b0 = min(p.batch, tid * each), b1 = min(p.batch, b0 + each);
+    int64_t mine = 0, total;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<KT>(p, request(p, b, status));
+    const int64_t before = scan(mine, s, total);
     per = max(div_up(total, runs), (int64_t)p.min_tiles);
     begin = min(total, per * run);
     end = min(total, begin + per);
-    if (begin < end && before <= begin && begin < before + mine) {
+    if (begin >= end) return;
+    if (before <= begin && begin < before + mine) {
         int64_t rest = begin - before;
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
@@ -141,13 +165,31 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
                 const int t = item_tiles<KT>(p, r, 0);
                 qt = (int)(div_up(rest + 1, t) - 1);
                 rest -= (int64_t)qt * t;
-            } else {
-#pragma unroll 1
-                for (int t; rest >= (t = item_tiles<KT>(p, r, qt)); ++qt) rest -= t;
             }
-            s.at = Place{b, h, qt, (int)rest};
+            s.at = Place{b, h, qt, 0};
+            s.rest = rest;
             break;
         }
+    }
+    __syncthreads();
+    at = s.at;
+    const Request r = request(p, at.b, nullptr);
+    if (p.mask || r.len < 0 || r.n == 1) {
+        at.tile = (int)s.rest;
+        return;
+    }
+    // a prompt's tiles differ: the threads share its rows
+    const int nq = row_tiles(p, r), share = (nq + nt - 1) / nt, q0 = min(nq, tid * share), q1 = min(nq, q0 + share);
+    mine = 0;
+#pragma unroll 1
+    for (int q = q0; q < q1; ++q) mine += item_tiles<KT>(p, r, q);
+    int64_t rest = s.rest - scan(mine, s, total);
+    if (rest >= 0 && rest < mine) {
+        int q = q0;
+#pragma unroll 1
+        for (int t; rest >= (t = item_tiles<KT>(p, r, q)); ++q) rest -= t;
+        s.at.qt = q;
+        s.at.tile = (int)rest;
     }
     __syncthreads();
     at = s.at;
@@ -192,7 +234,29 @@ __device__ __forceinline__ float *part_out(const Params &p, int cap, int d, int 
 __device__ __forceinline__ float *part_stat(const Params &p, int cap, int d, int runs, int run, int which) {
     return p.ws + (int64_t)runs * 2 * cap * d + ((int64_t)run * 2 + which) * cap * 2;
 }
-__host__ __device__ inline int64_t workspace_floats(int cap, int d, int runs) { return (int64_t)runs * 2 * cap * (d + 2); }
+
+// What joins an item that is cut at the start of a run, told by that run's block: rows 0 where there is nothing to join, because
+// the run begins with an item, or the item was cut earlier already.
+struct Cut {
+    int rows, last;    // the item's rows, and the last run that has a part of it
+    int row, first, head;  // its first row in the request, the request's first token, the key-value head
+    int pad[3];
+};
+__device__ __forceinline__ Cut *cut_of(const Params &p, int cap, int d, int runs, int run) {
+    return reinterpret_cast<Cut *>(p.ws + (int64_t)runs * 2 * cap * (d + 2)) + run;
+}
+template <int KT>
+__device__ __forceinline__ void tell_cut(const Params &p, int cap, int d, int runs, int run, int64_t per, int64_t begin, int64_t end, const Place &at) {
+    Cut c = {};
+    if (begin < end && at.tile > 0 && at.tile <= per) {
+        const Request r = request(p, at.b, nullptr);
+        c.rows = min(p.rows, r.n * p.group - at.qt * p.rows);
+        c.last = (int)(div_up(begin - at.tile + item_tiles<KT>(p, r, at.qt), per) - 1);
+        c.row = at.qt * p.rows, c.first = r.first, c.head = at.h;
+    }
+    *cut_of(p, cap, d, runs, run) = c;
+}
+inline int64_t workspace_floats(int cap, int d, int runs) { return (int64_t)runs * (2 * cap * (d + 2) + (int)sizeof(Cut) / 4); }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -212,49 +276,90 @@ __device__ __forceinline__ void store4(const Params &p, int64_t at, float4 x) {
 }
 
 // Joins the parts of the item that is cut first at the start of run blockIdx.x + 1: with the parts' maxima m_c, sums l_c
-// and unscaled outputs o_c, o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.  A block takes kJoinRows of the item's rows.
-constexpr int kJoinThreads = 128;
-template <int D>
-constexpr int kJoinRows = kJoinThreads * 4 / D;  // a thread has four entries of one row
+// and unscaled outputs o_c, o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.  A warp has a row; where there are many parts (one
+// long cache has them by the dozen) a block's warps have one together, and every fourth part each.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
-template <int D, int CAP, int KT>
+template <int D, int CAP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) {
     after_previous();
-    __shared__ Scratch s;
-    int64_t per, begin, end;
-    Place at;
-    const int run = blockIdx.x + 1;
-    find<KT>(p, runs, run, nullptr, s, per, begin, end, at);
-    if (begin >= end || at.tile == 0) return;
-    const int64_t item = begin - at.tile;
-    if (item < begin - per) return;  // cut earlier too: that cut's block joins it
-    const Request r = request(p, at.b, nullptr);
-    const int64_t item_end = item + item_tiles<KT>(p, r, at.qt);
-    const int row = blockIdx.y * kJoinRows<D> + threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
-    const int q = at.qt * p.rows + row;
-    if (row >= p.rows || q >= r.n * p.group) return;
-    const int last = (int)(div_up(item_end, per) - 1);
-    float m = -INFINITY, l = 0.f;
+    constexpr int V = D >= 128 ? 4 : D / 32 ? D / 32 : 1, N = D > 128 ? D / 128 : 1;  // consecutive entries of a lane, and how often
+    __shared__ float sums[kJoinWarps][D];
+    const int run = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Cut cut = *cut_of(p, CAP, D, runs, run);
+    const int parts = cut.last - run + 2;
+    const bool together = parts > kJoinWarps;
+    const float *stat = part_stat(p, CAP, D, runs, run, 0) - 2 * CAP * 2, *out = part_out(p, CAP, D, run, 0) - 2 * CAP * D;
+    // part 0 is the second of the run before, the others the first of theirs
+    auto which = [&](int c) { return c * 2 + (c == 0); };
+#pragma unroll 1
+    for (int row = together ? blockIdx.y : blockIdx.y * kJoinWarps + warp; row < cut.rows; row += gridDim.y * (together ? 1 : kJoinWarps)) {
+        float m = -INFINITY, l = 0.f;
+        for (int c = lane; c < parts; c += 32) m = fmaxf(m, stat[(int64_t)which(c) * CAP * 2 + row * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        for (int c = lane; c < parts; c += 32) {
+            const float2 st = *reinterpret_cast<const float2 *>(stat + (int64_t)which(c) * CAP * 2 + row * 2);
+            l = fmaf(exp2_fast(st.x - base), st.y, l);
+        }
+        l = warp_sum(l);
+        float o[N][V] = {};
+        if (lane * V < D) {
 #pragma unroll 4
-    for (int c = run - 1; c <= last; ++c) m = fmaxf(m, part_stat(p, CAP, D, runs, c, c == run - 1)[row * 2]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int c = run - 1; c <= last; ++c) {
-        const int which = c == run - 1;
-        const float2 st = *reinterpret_cast<const float2 *>(part_stat(p, CAP, D, runs, c, which) + row * 2);
-        const float4 x = *reinterpret_cast<const float4 *>(part_out(p, CAP, D, c, which) + row * D + col);
-        const float f = exp2_fast(st.x - base);
-        l = fmaf(f, st.y, l);
-        o.x = fmaf(f, x.x, o.x);
-        o.y = fmaf(f, x.y, o.y);
-        o.z = fmaf(f, x.z, o.z);
-        o.w = fmaf(f, x.w, o.w);
+            for (int c = together ? warp : 0; c < parts; c += together ? kJoinWarps : 1) {
+                const float f = exp2_fast(stat[(int64_t)which(c) * CAP * 2 + row * 2] - base);
+                const float *x = out + ((int64_t)which(c) * CAP + row) * D + lane * V;
+#pragma unroll
+                for (int n = 0; n < N; ++n) {
+                    if constexpr (V == 4) {
+                        const float4 y = *reinterpret_cast<const float4 *>(x + n * 128);
+                        o[n][0] = fmaf(f, y.x, o[n][0]), o[n][1] = fmaf(f, y.y, o[n][1]), o[n][2] = fmaf(f, y.z, o[n][2]), o[n][3] = fmaf(f, y.w, o[n][3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < V; ++k) o[n][k] = fmaf(f, x[k], o[n][k]);
+                    }
+                }
+            }
+        }
+        if (together) {
+            if (lane * V < D) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) sums[warp][n * 128 + lane * V + k] = o[n][k];
+            }
+            __syncthreads();
+            if (warp == 0 && lane * V < D) {
+#pragma unroll
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        const int col = n * 128 + lane * V + k;
+                        o[n][k] = (sums[0][col] + sums[1][col]) + (sums[2][col] + sums[3][col]);
+                    }
+            }
+            __syncthreads();
+        }
+        if (lane * V < D && (warp == 0 || !together)) {
+            // nothing seen: zeros; a NaN sum stays one
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int q = cut.row + row, token = cut.first + q / p.group, head = cut.head * p.group + q % p.group;
+            const int64_t to = ((int64_t)token * p.hkv * p.group + head) * D + lane * V;
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                if constexpr (V == 4) {
+                    store4(p, to + n * 128, make_float4(o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to + k, o[n][k] * inv);
+                        else store_f(static_cast<float *>(p.o), to + k, o[n][k] * inv);
+                    }
+                }
+            }
+        }
     }
-    // nothing seen: zeros; a NaN sum stays one
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int token = r.first + q / p.group, head = at.h * p.group + q % p.group;
-    store4(p, ((int64_t)token * p.hkv * p.group + head) * D + col, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
 }
 
 // A launch that may take its place while the kernel before it ends; the kernel calls after_previous() first.
@@ -273,10 +378,10 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int CAP, int KT>
+template <int D, int CAP>
 cudaError_t launch_join(const Params &p, int runs, cudaStream_t stream) {
     if (runs < 2) return cudaSuccess;
-    return launch_dependent(join_kernel<D, CAP, KT>, dim3(runs - 1, (p.rows + kJoinRows<D> - 1) / kJoinRows<D>), kJoinThreads, 0, stream, p, runs);
+    return launch_dependent(join_kernel<D, CAP>, dim3(runs - 1, p.rows < 16 ? p.rows : 16), kJoinThreads, 0, stream, p, runs);
 }
 
 // A kernel of this family for some sizes: how many blocks, their workspace, and the launch.
