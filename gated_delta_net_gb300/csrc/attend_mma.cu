@@ -19,7 +19,7 @@ namespace {
 using namespace attn;
 using sm100::smem_u32;
 
-constexpr int kR = 16, kWarps = 4, kThreads = kWarps * 32, kKeys = 16, kKT = kWarps * kKeys;
+constexpr int kR = 16, kWarps = 4, kThreads = kWarps * 32, kKeys = 16, kKT = kWarps * kKeys, kMostWhole = 16;
 
 template <int D>
 struct Ring {
@@ -69,8 +69,12 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     const int g = lane >> 2, t4 = lane & 3;
     int64_t per, t, end;
     Place at;
-    find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, t, end, at);
-    if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
+    if (p.whole) {
+        item_of<kKT>(p, run, (p.max_tokens * p.group + kR - 1) / kR, t, end, at);
+    } else {
+        find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, scratch, per, t, end, at);
+        if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
+    }
     if (t >= end) return;
     uint8_t *ring = sm + warp * S::kWarp;
     float *mine = reinterpret_cast<float *>(sm + kWarps * S::kWarp + (warp & 1) * S::kJoin);
@@ -323,12 +327,15 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     const cudaError_t e = ensure_smem(attend_mma_kernel<D>, Ring<D>::kBytes, have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_mma_kernel<D>, dim3(runs), kThreads, Ring<D>::kBytes, stream, p, runs);
-    return f != cudaSuccess ? f : launch_join<D, kR>(p, runs, stream);
+    return f != cudaSuccess || p.whole ? f : launch_join<D, kR>(p, runs, stream);
 }
 
 template <int D>
 Choice choice(const gdn_kv_attend_args &a, bool decode) {
-    return Choice{most_runs(a, decode, kR, kKT, Ring<D>::kBlocks), 0, run<D>};
+    Choice x = {0, 0, run<D>, false};
+    x.whole = whole_items(a, decode, kR, kKT, kMostWhole, x.runs);
+    if (!x.whole) x.runs = most_runs(a, decode, kR, kKT, Ring<D>::kBlocks);
+    return x;
 }
 
 }  // namespace
@@ -344,7 +351,7 @@ attn::Choice attend_mma_choice(const gdn_kv_attend_args &a, bool decode) {
         case 128: x = choice<128>(a, decode); break;
         default: x = choice<256>(a, decode);
     }
-    x.workspace = 4 * workspace_floats(kR, a.cache.d, x.runs);
+    x.workspace = x.whole ? 0 : 4 * workspace_floats(kR, a.cache.d, x.runs);
     return x;
 }
 

@@ -11,7 +11,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kR = 16, kKT = 32, kThreads = 128;
+constexpr int kR = 16, kKT = 32, kThreads = 128, kMostWhole = 4;
 
 template <int D>
 struct Shared {
@@ -56,8 +56,12 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
     int64_t per, t, end;
     Place at;
-    find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
-    if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
+    if (p.whole) {
+        item_of<kKT>(p, run, (p.max_tokens * p.group + kR - 1) / kR, t, end, at);
+    } else {
+        find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
+        if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
+    }
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
     while (t < end) {
@@ -171,7 +175,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);
-    return f != cudaSuccess ? f : launch_join<D, kR>(p, runs, stream);
+    return f != cudaSuccess || p.whole ? f : launch_join<D, kR>(p, runs, stream);
 }
 
 template <typename T, bool VEC>
@@ -191,8 +195,9 @@ attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     const gdn_kv_cache &c = a.cache;
     const bool vec = aligned16(a);
     Choice x;
-    x.runs = most_runs(a, decode, kR, kKT, 2);
-    x.workspace = 4 * workspace_floats(kR, c.d, x.runs);
+    x.whole = whole_items(a, decode, kR, kKT, kMostWhole, x.runs);
+    if (!x.whole) x.runs = most_runs(a, decode, kR, kKT, 2);
+    x.workspace = x.whole ? 0 : 4 * workspace_floats(kR, c.d, x.runs);
     if (c.dtype == GDN_BF16) x.launch = vec ? pick<__nv_bfloat16, true>(c.d) : pick<__nv_bfloat16, false>(c.d);
     else x.launch = vec ? pick<float, true>(c.d) : pick<float, false>(c.d);
     return x;

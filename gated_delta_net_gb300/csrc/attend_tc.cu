@@ -6,14 +6,14 @@
 //     S = Q K^T      tcgen05, both from shared memory, to tensor memory
 //     P = 2^(S scale - m)   scores from tensor memory, probabilities as bf16 back over them
 //     O += P V       tcgen05, P from tensor memory, V as it lies in shared memory (MN-major)
-// While one tile's scores are in registers, the other tile's products run.  (d = 256: the outputs take half of the tensor
-// memory; one tile, whose scores are a tile of slots ahead in a second buffer.)
+// While one tile's scores are in registers, the other tile's products run.  Where there is one tile of rows (they fit into it,
+// or d = 256, whose outputs take half of the tensor memory), its scores are a tile of slots ahead in a second buffer.
 //
 // The maximum that outputs are scaled by is moved, and they are multiplied, only where a row's maximum grew by more than 2^8: then
 // probabilities are up to 2^8, which neither bf16 nor the fp32 sums lose anything by.
 // P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.
 //
-// 12 warps (8 for d = 256):
+// 12 warps (8 for one tile of rows):
 //     4 for each tile of rows, a thread a row.  The first half of a tile's probabilities is multiplied while the second is made.
 //       (Two threads a row, which swap their maxima, are slower: 744 us against 684 for 8192 tokens, 32 heads of 128.)
 //     1 issues the products
@@ -59,18 +59,18 @@ struct __align__(16) Job {
 };
 constexpr int kJobs = 3;  // an item is told while the one before it begins and the one before that may be read
 
-template <int D>
+// U: tiles of rows
+template <int D, int U>
 struct Shape {
-    static constexpr int U = D == 256 ? 1 : 2;        // tiles of rows
     static constexpr int kRowWarps = U * 4, kThreads = kRowWarps * 32 + 128;
-    static constexpr int NB = D == 256 ? 2 : 1;       // buffers of scores for each
+    static constexpr int NB = U == 1 ? 2 : 1;       // buffers of scores for each
     static constexpr int KT = D == 256 ? 64 : 128;    // slots of a tile
     static constexpr int H = D / 64;                  // halves (64 entries, 128 bytes) of a row
     static constexpr int kQTile = kTileRows * 128;    // bytes of one half of a tile of queries
     static constexpr int kHalf = KT * 128;            // of one half of a tile of keys or values
     static constexpr int kStage = H * kHalf;
     static constexpr int kQ = U * H * kQTile;
-    static constexpr int KS = D == 64 ? 5 : 2, VS = KS;  // tiles of keys, of values held at a time
+    static constexpr int KS = D == 64 ? 5 : D == 128 && U == 1 ? 3 : 2, VS = D == 64 ? 5 : 2;  // tiles of keys, of values held at a time
     static constexpr int CAP = U * kTileRows;
     static constexpr uint32_t kScores = 0, kOut = U * NB * KT;  // tensor-memory columns
     // words of a tile's rows that were not finite.  They are read after the tile's probabilities have been handed over, so there is
@@ -192,13 +192,13 @@ struct Walk {
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+template <int D, int U>
+__global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap o_map, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                      const __grid_constant__ TcParams tp, int runs) {
     after_previous();
-    using S = Shape<D>;
-    constexpr int KT = S::KT, U = S::U, NB = S::NB;
+    using S = Shape<D, U>;
+    constexpr int KT = S::KT, NB = S::NB;
     extern __shared__ __align__(1024) uint8_t sm[];
     const Params &p = tp.p;
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
@@ -675,33 +675,33 @@ bool encode_tokens(CUtensorMap *map, const void *rows, int64_t stride, const Par
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
+template <int D, int U>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
-    using S = Shape<D>;
+    using S = Shape<D, U>;
     static int have[16];
-    const cudaError_t e = ensure_smem(attend_tc_kernel<D>, S::kBytes, have);
+    const cudaError_t e = ensure_smem(attend_tc_kernel<D, U>, S::kBytes, have);
     if (e != cudaSuccess) return e;
     TcParams tp;
     tp.tile_tokens = kTileRows / p.group;
     tp.box = p.page_size & -p.page_size;
     if (tp.box > S::KT) tp.box = S::KT;
-    p.rows = S::U * tp.tile_tokens * p.group;
+    p.rows = U * tp.tile_tokens * p.group;
     tp.p = p;
     CUtensorMap q, o, k, v;
     if (!encode_tokens(&q, p.q, p.q_stride, p, D, tp.tile_tokens) || !encode_tokens(&o, p.o, (int64_t)p.hkv * p.group * D, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))
         return cudaErrorInvalidValue;
-    const cudaError_t f = launch_dependent(attend_tc_kernel<D>, dim3(runs), S::kThreads, S::kBytes, stream, q, o, k, v, tp, runs);
+    const cudaError_t f = launch_dependent(attend_tc_kernel<D, U>, dim3(runs), S::kThreads, S::kBytes, stream, q, o, k, v, tp, runs);
     return f != cudaSuccess ? f : launch_join<D, S::CAP>(p, runs, stream);
 }
 
-template <int D>
+template <int D, int U>
 Choice choice(const gdn_kv_attend_args &a) {
-    using S = Shape<D>;
+    using S = Shape<D, U>;
     const int group = a.n_q_heads / a.cache.n_kv_heads;
-    Choice x;
-    x.runs = most_runs(a, false, S::U * (kTileRows / group) * group, S::KT, 1);
+    Choice x = {};
+    x.runs = most_runs(a, false, U * (kTileRows / group) * group, S::KT, 1);
     x.workspace = 4 * workspace_floats(S::CAP, D, x.runs);
-    x.launch = run<D>;
+    x.launch = run<D, U>;
     return x;
 }
 
@@ -717,7 +717,12 @@ bool attend_tc_supported(const gdn_kv_attend_args &a) {
 }
 
 attn::Choice attend_tc_choice(const gdn_kv_attend_args &a) {
-    return a.cache.d == 64 ? choice<64>(a) : a.cache.d == 128 ? choice<128>(a) : choice<256>(a);
+    // one tile of rows where all of a request's fit
+    const int group = a.n_q_heads / a.cache.n_kv_heads;
+    const bool one = a.max_tokens <= kTileRows / group;
+    if (a.cache.d == 64) return one ? choice<64, 1>(a) : choice<64, 2>(a);
+    if (a.cache.d == 128) return one ? choice<128, 1>(a) : choice<128, 2>(a);
+    return choice<256, 1>(a);
 }
 
 }  // namespace gdn

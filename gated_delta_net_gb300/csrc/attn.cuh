@@ -29,6 +29,7 @@ struct Params {
     int32_t *status;
     int page_bits;                          // log2 of page_size, or -1
     bool out_bf16;
+    bool whole;                             // a run for each item, none cut
 };
 
 // The tokens of request b: the first one's row, how many (0: the request is left out), the committed ones
@@ -235,6 +236,16 @@ __device__ __forceinline__ float *part_stat(const Params &p, int cap, int d, int
     return p.ws + (int64_t)runs * 2 * cap * d + ((int64_t)run * 2 + which) * cap * 2;
 }
 
+// The same where every item has a run of its own (the first rows of a head, the others, the next head, ..): begin is 0.
+template <int KT>
+__device__ __forceinline__ void item_of(const Params &p, int run, int tiles_of_rows, int64_t &begin, int64_t &end, Place &at) {
+    const int item = run / tiles_of_rows;
+    at = Place{item / p.hkv, item % p.hkv, run % tiles_of_rows, 0};
+    const Request r = request(p, at.b, at.h == 0 && at.qt == 0 && threadIdx.x == 0 ? p.status : nullptr);
+    begin = 0;
+    end = at.qt < row_tiles(p, r) ? item_tiles<KT>(p, r, at.qt) : 0;
+}
+
 // What joins an item that is cut at the start of a run, told by that run's block: rows 0 where there is nothing to join, because
 // the run begins with an item, or the item was cut earlier already.
 struct Cut {
@@ -389,6 +400,7 @@ struct Choice {
     int runs;
     int64_t workspace;
     cudaError_t (*launch)(Params p, int runs, cudaStream_t stream);
+    bool whole;
 };
 
 // blocks_an_sm runs for each SM, and no more than there can be tiles
@@ -402,6 +414,15 @@ inline int most_runs(const gdn_kv_attend_args &a, bool decode, int R, int KT, in
         if (n > room) n = room;
     }
     return (int)n;
+}
+
+// Whether each item gets a block of its own, and how many there are: where no request can have more than `most` tiles of slots, and
+// a call's items fit into a few waves.  (Sizes are looked at, not lengths, which the host does not know.)
+inline bool whole_items(const gdn_kv_attend_args &a, bool decode, int R, int KT, int most, int &items) {
+    const int64_t group = a.n_q_heads / a.cache.n_kv_heads, slots = (int64_t)a.cache.max_pages * a.cache.page_size;
+    const int64_t n = (int64_t)a.cache.batch * a.cache.n_kv_heads * (((decode ? 1 : (int64_t)a.max_tokens) * group + R - 1) / R);
+    items = (int)(n < 1 << 30 ? n : 1 << 30);
+    return slots <= (int64_t)most * KT && n <= 1 << 20;
 }
 
 // whether every row of the queries and of the cache starts on 16 bytes

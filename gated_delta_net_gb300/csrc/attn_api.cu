@@ -86,15 +86,15 @@ int attend(const gdn_kv_attend_args *a, bool decode, void *stream) {
     if (!a->q || !a->o || (!decode && !a->token_offsets)) return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
     if (reinterpret_cast<uintptr_t>(a->o) & 15) return fail(GDN_ERR_INVALID_ARG, "o must be 16-byte aligned");
     const gdn::attn::Choice x = choose(*a, decode);
-    if (!a->workspace || a->workspace_bytes < x.workspace)
+    if (x.workspace > 0 && (!a->workspace || a->workspace_bytes < x.workspace))
         return fail(GDN_ERR_INVALID_ARG, "workspace of %lld bytes: %lld are needed", (long long)(a->workspace ? a->workspace_bytes : 0),
                     (long long)x.workspace);
-    if (reinterpret_cast<uintptr_t>(a->workspace) & 255) return fail(GDN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    if (x.workspace > 0 && reinterpret_cast<uintptr_t>(a->workspace) & 255) return fail(GDN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     gdn::attn::Params p = {};
     p.batch = c.batch; p.hkv = c.n_kv_heads; p.group = a->n_q_heads / c.n_kv_heads;
     p.page_size = c.page_size; p.n_pages = c.n_pages; p.max_pages = c.max_pages;
     p.page_bits = (c.page_size & (c.page_size - 1)) ? -1 : __builtin_ctz((unsigned)c.page_size);
-    p.total = a->total_tokens; p.max_tokens = a->max_tokens; p.min_tiles = 1;
+    p.total = a->total_tokens; p.max_tokens = decode ? 1 : a->max_tokens; p.min_tiles = 1;
     p.page_stride = c.page_stride; p.slot_stride = c.slot_stride; p.head_stride = c.head_stride;
     p.q_stride = a->q_stride ? a->q_stride : (int64_t)a->n_q_heads * c.d;
     p.scale_log2 = a->scale * gdn::attn::kLog2e;
@@ -102,6 +102,7 @@ int attend(const gdn_kv_attend_args *a, bool decode, void *stream) {
     p.offsets = decode ? nullptr : a->token_offsets;
     p.mask = decode ? nullptr : a->anc_mask;
     p.mask_words = a->mask_words;
+    p.whole = x.whole;
     p.o = a->o; p.out_bf16 = a->out_dtype == GDN_BF16; p.ws = static_cast<float *>(a->workspace); p.status = c.dev_status;
     return done(x.launch(p, x.runs, (cudaStream_t)stream), decode ? "kv_decode launch" : "kv_attend launch");
 }

@@ -27,21 +27,26 @@ struct AppendParams {
     bool weight_bf16;
 };
 
+// eight entries as they lie in memory
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T *p, float (&x)[8]) {
-    if constexpr (VEC && sizeof(T) == 2) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[2 * i] = __uint_as_float(u[i] << 16), x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    } else if constexpr (VEC) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+        } else {
+            T *x = reinterpret_cast<T *>(w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = load_f(p, i);
+            for (int i = 0; i < 8; ++i) x[i] = p[i];
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+        const T *y = reinterpret_cast<const T *>(w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = load_f(y, i);
+    }
+};
 
 template <typename T, bool VEC>
 __device__ __forceinline__ void store8(T *p, const float (&x)[8]) {
@@ -66,12 +71,22 @@ __device__ __forceinline__ float weight_at(const void *w, bool bf16, int i) {
     return bf16 ? load_f(static_cast<const __nv_bfloat16 *>(w), i) : load_f(static_cast<const float *>(w), i);
 }
 
-// VEC: 16-byte pieces, and the partner of lane l's entries (halves) is another lane's; INTER: pairs of neighbours
+// VEC: 16-byte pieces (weights and angles too), and the partner of lane l's entries (halves) is another lane's; INTER: pairs of neighbours
 template <typename T, int D, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 8) append_kernel(AppendParams p) {
     after_previous();
     constexpr int L = D / 8, G = kThreads / L;  // lanes a row, rows a block has in flight
     const int t = blockIdx.x, tid = threadIdx.x, sub = tid % L, e0 = sub * 8, half = p.rot / 2;
+    const int rows = p.hq + 2 * p.hkv, turns = (rows + G - 1) / G;
+    // (row, what it is) of this lane's turn: queries, keys, values
+    auto source = [&](int row) {
+        const T *from = static_cast<const T *>(row < p.hq ? p.q : row < p.hq + p.hkv ? p.k : p.v);
+        const int h = row < p.hq ? row : row < p.hq + p.hkv ? row - p.hq : row - p.hq - p.hkv;
+        return from + t * (row < p.hq ? p.qs : row < p.hq + p.hkv ? p.ks : p.vs) + h * D + e0;
+    };
+    // the first row is on its way while the token's place is found, each other one while the row before it is worked on
+    Raw<T, VEC> next = {};
+    if (tid / L < rows) next.load(source(tid / L));
     int b = t, i = 0;
     if (p.offsets) {
         int upto = 0;
@@ -89,8 +104,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
     }
     const int len = p.lens[b];
     if (len == -1) return;
-    const int64_t slot = (int64_t)len + i, page = slot / p.page_size;
+    const int64_t slot = (int64_t)len + i;
     const int64_t position = p.depth ? (int64_t)len + p.depth[t] - 1 : slot;
+    // (a table has at most 2^30 slots)
+    const int page = slot < (1 << 30) ? (int)slot / p.page_size : p.max_pages;
     int bad = 0, id = 0;
     if (len < 0 || page >= p.max_pages) bad = GDN_DEV_BAD_PAGE;
     else if (id = p.table[(int64_t)b * p.max_pages + page]; id < 0 || id >= p.n_pages) bad = GDN_DEV_BAD_PAGE;
@@ -99,70 +116,97 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendParams p) {
         if (tid == 0) flag(p.status, bad);
         return;
     }
-    const int64_t at = id * p.page_stride + (slot - page * p.page_size) * p.slot_stride;
+    const int64_t at = id * p.page_stride + ((int)slot - page * p.page_size) * p.slot_stride;
 
-    // this lane's angles: entry e0 + n turns with pair (e0 + n) % half, or (e0 + n) / 2 in neighbours
+    // this lane's angles: entry e0 + n turns with pair (e0 + n) % half, or (e0 + n) / 2 in neighbours; the first of a pair subtracts
     float cs[8], sn[8];
     const float *angles = p.cos_sin + position * p.rot;
+    if (VEC && !INTER) {
+        // (half is a multiple of 8: all eight are turned or none, and their angles lie side by side)
+        const bool turned = e0 < p.rot;
+        const float sign = e0 < half ? -1.f : 1.f;
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-        const int e = e0 + n;
-        const int pair = INTER ? e / 2 : e < half ? e : e - half;
-        const bool turned = e < p.rot;
-        cs[n] = turned ? angles[pair] : 1.f;
-        // the first of a pair subtracts
-        sn[n] = turned ? angles[half + pair] * ((INTER ? (e & 1) == 0 : e < half) ? -1.f : 1.f) : 0.f;
+        for (int n = 0; n < 8; ++n) cs[n] = 1.f, sn[n] = 0.f;
+        if (turned) {
+            const float *c = angles + (e0 < half ? e0 : e0 - half);
+            Raw<float, true> raw;
+            raw.load(c);
+            raw.values(cs);
+            raw.load(c + half);
+            raw.values(sn);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) sn[n] *= sign;
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const int e = e0 + n;
+            const int pair = INTER ? e / 2 : e < half ? e : e - half;
+            const bool turned = e < p.rot;
+            cs[n] = turned ? angles[pair] : 1.f;
+            sn[n] = turned ? angles[half + pair] * ((INTER ? (e & 1) == 0 : e < half) ? -1.f : 1.f) : 0.f;
+        }
     }
     const unsigned mates = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << ((tid & 31) / L * L);  // the lanes of a row
-    const int rows = p.hq + 2 * p.hkv;
-    for (int row = tid / L; row < (rows + G - 1) / G * G; row += G) {  // whole warps, for the shuffles
+    for (int turn = 0; turn < turns; ++turn) {  // alike in a whole warp, for the shuffles
+        const int row = turn * G + tid / L;
         const bool live = row < rows, is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
         const int h = is_q ? row : is_v ? row - p.hq - p.hkv : row - p.hq;
-        const T *src = static_cast<const T *>(is_q ? p.q : is_v ? p.v : p.k) + t * (is_q ? p.qs : is_v ? p.vs : p.ks) + (int64_t)h * D;
+        const Raw<T, VEC> now = next;
+        if (row + G < rows) next.load(source(row + G));
         T *dst = is_q ? static_cast<T *>(p.q_out) + ((int64_t)t * p.hq + h) * D
                       : static_cast<T *>(is_v ? p.v_cache : p.k_cache) + at + h * p.head_stride;
-        float x[8] = {}, y[8];
-        if (live) load8<T, VEC>(src + e0, x);
-        // the partners
-        if constexpr (INTER) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) y[n] = x[n ^ 1];
-        } else if constexpr (VEC) {
-            const int away = half / 8, from = e0 < half ? sub + away : sub - away;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) y[n] = __shfl_sync(0xffffffffu, x[n], from & (L - 1), L);
-        } else {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) {
-                const int e = e0 + n;
-                y[n] = live && e < p.rot ? load_f(src, e < half ? e + half : e - half) : 0.f;
-            }
-        }
+        float x[8], y[8];
+        now.values(x);
         if (is_v) {
             if (live) store8<T, VEC>(dst + e0, x);
-            continue;
         }
+        // weights before the exchange, so that a partner comes with its own; the norm's factor after it
         const void *w = is_q ? p.q_weight : p.k_weight;
+        float r = 1.f;
         if (w) {
             float sum = 0.f;
 #pragma unroll
             for (int n = 0; n < 8; ++n) sum = fmaf(x[n], x[n], sum);
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mates, sum, o, L);
-            const float r = rsqrtf(sum * (1.f / D) + p.eps);
+            r = rsqrtf(sum * (1.f / D) + p.eps);
+            float g[8];
+            if (VEC && p.weight_bf16) {
+                Raw<__nv_bfloat16, true> raw;
+                raw.load(static_cast<const __nv_bfloat16 *>(w) + e0);
+                raw.values(g);
+            } else if (VEC) {
+                Raw<float, true> raw;
+                raw.load(static_cast<const float *>(w) + e0);
+                raw.values(g);
+            } else {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) g[n] = weight_at(w, p.weight_bf16, e0 + n);
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) x[n] *= g[n];
+        }
+        if constexpr (INTER) {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) y[n] = x[n ^ 1];
+        } else if constexpr (VEC) {
+            const int away = half / 8, from = e0 < half ? sub + away : sub - away;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) y[n] = __shfl_sync(mates, x[n], from & (L - 1), L);
+        } else {
+            const T *src = live ? source(row) - e0 : nullptr;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                const int e = e0 + n;
-                const int pe = e >= p.rot ? e : INTER ? e ^ 1 : e < half ? e + half : e - half;
-                x[n] *= r * weight_at(w, p.weight_bf16, e);
-                y[n] *= r * weight_at(w, p.weight_bf16, pe);
+                const int e = e0 + n, pe = e < half ? e + half : e - half;
+                y[n] = live && e < p.rot ? load_f(src, pe) * (w ? weight_at(w, p.weight_bf16, pe) : 1.f) : 0.f;
             }
         }
         float z[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) z[n] = e0 + n < p.rot ? fmaf(x[n], cs[n], y[n] * sn[n]) : x[n];
+        for (int n = 0; n < 8; ++n) z[n] = r * (e0 + n < p.rot ? fmaf(x[n], cs[n], y[n] * sn[n]) : x[n]);
         __syncwarp(mates);  // q_out may be q: partners have been read
-        if (live) store8<T, VEC>(dst + e0, z);
+        if (live && !is_v) store8<T, VEC>(dst + e0, z);
     }
 }
 
@@ -202,7 +246,8 @@ cudaError_t launch_kv_append(const gdn_kv_append_args &a, cudaStream_t stream) {
     p.q_out = a.q_out; p.k_cache = c.k; p.v_cache = c.v; p.status = c.dev_status;
     p.weight_bf16 = a.weight_dtype == GDN_BF16;
     const uintptr_t pointers = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
-                               reinterpret_cast<uintptr_t>(a.q_out) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
+                               reinterpret_cast<uintptr_t>(a.q_out) | reinterpret_cast<uintptr_t>(a.q_weight) | reinterpret_cast<uintptr_t>(a.k_weight) |
+                               reinterpret_cast<uintptr_t>(a.cos_sin) | reinterpret_cast<uintptr_t>(c.k) | reinterpret_cast<uintptr_t>(c.v);
     const int64_t strides = (p.hq ? p.qs : 0) | p.ks | p.vs | p.page_stride | p.slot_stride | p.head_stride;
     const bool vec = (pointers & 15) == 0 && strides * e % 16 == 0 && (a.interleaved || a.rot_dim % 16 == 0);
     return c.dtype == GDN_BF16 ? pick<__nv_bfloat16>(p, c.d, vec, a.interleaved != 0, stream)

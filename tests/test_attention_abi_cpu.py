@@ -51,7 +51,7 @@ def _fill(struct, sizes, **kw):
 
 CACHE = dict(batch=2, n_pages=4, page_size=16, max_pages=3, n_kv_heads=2, d=64, page_stride=2048, slot_stride=128, head_stride=64)
 APPEND = dict(CACHE, total_tokens=5, n_q_heads=4, rot_dim=32, n_positions=9, eps=1e-6)
-ATTEND = dict(CACHE, total_tokens=5, max_tokens=3, n_q_heads=4, mask_words=1, scale=1.0, workspace_bytes=1 << 40)
+ATTEND = dict(CACHE, max_pages=300, total_tokens=5, max_tokens=3, n_q_heads=4, mask_words=1, scale=1.0, workspace_bytes=1 << 40)
 DECODE = dict(ATTEND, total_tokens=2)
 COMMIT = dict(CACHE, total_path=3)
 
@@ -102,6 +102,7 @@ def test_workspace_size_refuses_what_attend_refuses(L):
     assert need(d=48) == -1 and need(1, n_q_heads=3) == -1 and need(1, total_tokens=3) == -1
     assert need() > 0 and need(1) > 0 and need(total_tokens=0) == 0
     assert need() % 4 == 0
+    assert need(1, max_pages=3) == 0  # no request long enough to be cut
     assert L.gdn_kv_attend_workspace(None, 0) == -1
 
 
