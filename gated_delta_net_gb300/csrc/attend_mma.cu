@@ -19,7 +19,7 @@ namespace {
 using namespace attn;
 using sm100::smem_u32;
 
-constexpr int kR = 16, kWarps = 4, kThreads = kWarps * 32, kKeys = 16, kKT = kWarps * kKeys, kMostWhole = 16;
+constexpr int kR = 16, kWarps = 4, kThreads = kWarps * 32, kKeys = 16, kKT = kWarps * kKeys, kMostWhole = 16, kCost = 2;
 
 template <int D>
 struct Ring {
@@ -81,41 +81,69 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     const uint32_t ring_at = smem_u32(ring);
     const __nv_bfloat16 *K = static_cast<const __nv_bfloat16 *>(p.k), *V = static_cast<const __nv_bfloat16 *>(p.v);
 
-    // ---- the ring: tiles from `load` on are on their way, the next one's page is known
+    // ---- the ring: tiles from `l_tile` on are on their way, and where the next one lies is known
     Place load = at;
     Request lr = request(p, load.b, nullptr);
-    int l_tiles = item_tiles<kKT>(p, lr, load.qt), l_seen = seen_slots(p, lr, load.qt);
     int64_t l_left = end - t, l_off = -1;
-    const bool aligned_pages = p.page_size % kKeys == 0;  // a warp's 16 slots lie in one page
+    Span ls = span_of<kKT>(p, lr, load, l_left);
+    int l_seen = seen_slots(p, lr, load.qt), l_tile = ls.first, l_ids = 0, l_ids_at = ls.first - 32;
+    bool l_more = ls.first < ls.last;
+    const bool aligned_pages = p.page_size % kKeys == 0;  // a warp's 16 slots lie in one page: lanes look up 32 tiles' at once
     auto look_up = [&]() {
-        const int slot = load.tile * kKT + warp * kKeys + (aligned_pages ? 0 : lane & 15);
-        l_off = slot < l_seen ? slot_offset(p, load.b, load.h, slot) : -1;
+        if (aligned_pages) {
+            if (l_tile - l_ids_at >= 32) {
+                l_ids_at = l_tile;
+                const int slot = (l_tile + lane) * kKT + warp * kKeys;
+                l_ids = l_tile + lane < ls.last && slot < l_seen ? p.table[(int64_t)load.b * p.max_pages + (p.page_bits >= 0 ? slot >> p.page_bits : slot / p.page_size)] : 0;
+            }
+        } else {
+            const int slot = l_tile * kKT + warp * kKeys + (lane & 15);
+            l_off = slot < l_seen ? slot_offset(p, load.b, load.h, slot) : -1;
+        }
     };
     auto issue = [&](int stage) {
-        if (l_left > 0) {
-            const int there = l_seen - load.tile * kKT - warp * kKeys;  // slots of these 16 that are seen
+        if (l_more) {
+            const int slot0 = l_tile * kKT + warp * kKeys;
+            int there = l_seen - slot0;  // slots of these 16 that are seen
             const uint32_t to = ring_at + stage * 2 * S::kTile;
+            int64_t base = 0;
+            if (aligned_pages) {
+                const int id = __shfl_sync(0xffffffffu, l_ids, l_tile - l_ids_at);
+                base = id * p.page_stride + (p.page_bits >= 0 ? slot0 & (p.page_size - 1) : slot0 % p.page_size) * p.slot_stride + load.h * p.head_stride;
+                if (there > 0 && (id < 0 || id >= p.n_pages)) {
+                    there = 0;
+                    if (lane == 0) flag(p.status, GDN_DEV_BAD_PAGE);
+                }
+            }
 #pragma unroll
             for (int i = 0; i < (kKeys * C + 31) / 32; ++i) {
                 const int n = i * 32 + lane, row = n / C, c = n % C;
-                if (kKeys * C >= 32 || n < kKeys * C) {
-                    const int64_t off = aligned_pages ? l_off : __shfl_sync(0xffffffffu, l_off, row & 15);
-                    const bool ok = row < there && off >= 0;
-                    const int64_t from = ok ? off + (aligned_pages ? row * p.slot_stride : 0) + c * 8 : 0;
-                    copy16(to + piece<D>(row, c), K + from, ok);
-                    copy16(to + S::kTile + piece<D>(row, c), V + from, ok);
+                int64_t from = base + row * p.slot_stride;
+                bool ok = row < there;
+                if (!aligned_pages) {
+                    from = __shfl_sync(0xffffffffu, l_off, row & 15);
+                    ok = ok && from >= 0;
+                }
+                from = ok ? from + c * 8 : 0;
+                copy16(to + piece<D>(row, c), K + from, ok);
+                copy16(to + S::kTile + piece<D>(row, c), V + from, ok);
+            }
+            if (++l_tile == ls.last) {
+                l_left -= ls.units;
+                l_more = l_left > 0;
+                if (l_more) {
+                    next_item(p, load, lr);
+                    ls = span_of<kKT>(p, lr, load, l_left);
+                    l_seen = seen_slots(p, lr, load.qt);
+                    l_tile = ls.first, l_ids_at = ls.first - 32;
+                    l_more = ls.first < ls.last;
                 }
             }
-            --l_left;
-            if (++load.tile == l_tiles && l_left > 0) {
-                next_item(p, load, lr);
-                l_tiles = item_tiles<kKT>(p, lr, load.qt);
-                l_seen = seen_slots(p, lr, load.qt);
-            }
-            if (l_left > 0) look_up();
+            if (l_more) look_up();
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    if (!l_more) return;
     look_up();
 #pragma unroll 1
     for (int s = 0; s < S::kStages - 1; ++s) issue(s);
@@ -123,8 +151,9 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
     Request r = request(p, at.b, nullptr);
     int stage = 0, free_stage = S::kStages - 1;
     while (t < end) {
-        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
-        const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
+        const Span span = span_of<kKT>(p, r, at, end - t);
+        const int tiles = span.tiles, first = span.first, last = span.last, seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
+        if (last <= first) break;
         const int row0 = at.qt * kR, rows = r.n * p.group;
         // ---- this lane's rows: g and g + 8
         const __nv_bfloat16 *q[2];
@@ -314,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
             }
         }
         __syncthreads();
-        t += last - first;
+        t += span.units;
         if (t < end) next_item(p, at, r);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -323,7 +352,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
 template <int D>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
     static int have[16];
-    p.rows = kR;
+    p.rows = kR, p.cost = kCost;
     const cudaError_t e = ensure_smem(attend_mma_kernel<D>, Ring<D>::kBytes, have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_mma_kernel<D>, dim3(runs), kThreads, Ring<D>::kBytes, stream, p, runs);

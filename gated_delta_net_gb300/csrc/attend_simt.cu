@@ -11,7 +11,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kR = 16, kKT = 32, kThreads = 128, kMostWhole = 4;
+constexpr int kR = 16, kKT = 32, kThreads = 128, kMostWhole = 4, kCost = 1;
 
 template <int D>
 struct Shared {
@@ -65,8 +65,9 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
     while (t < end) {
-        const int tiles = item_tiles<kKT>(p, r, at.qt), seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
-        const int first = at.tile, last = (int)min((int64_t)tiles, first + (end - t));
+        const Span span = span_of<kKT>(p, r, at, end - t);
+        const int tiles = span.tiles, first = span.first, last = span.last, seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
+        if (last <= first) break;
         const int64_t row0 = (int64_t)at.qt * kR, rows = (int64_t)r.n * p.group;
         if (tid < kR) {
             const int64_t q = row0 + tid;
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
             float *st = part_stat(p, kR, D, runs, run, which) + tid * 2;
             st[0] = s.m[tid], st[1] = s.l[tid];
         }
-        t += last - first;
+        t += span.units;
         if (t < end) next_item(p, at, r);
         __syncthreads();
     }
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
 template <typename T, int D, bool VEC>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
     static int have[16];
-    p.rows = kR;
+    p.rows = kR, p.cost = kCost;
     const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
     if (e != cudaSuccess) return e;
     const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);

@@ -173,22 +173,21 @@ struct Walk {
     Place at;
     Request r;
     int64_t left;
-    int first, last, tiles, seen, common;
+    int first, last, tiles, units, seen, common;
     template <int KT>
     __device__ __forceinline__ void item(const Params &p) {
-        tiles = item_tiles<KT>(p, r, at.qt);
+        const Span s = span_of<KT>(p, r, at, left);
+        tiles = s.tiles, first = s.first, last = s.last, units = s.units;
         seen = seen_slots(p, r, at.qt);
         common = common_slots(p, r, at.qt);
-        first = at.tile;
-        last = (int)min((int64_t)tiles, first + left);
     }
     template <int KT>
     __device__ __forceinline__ bool next(const Params &p) {
-        left -= last - first;
+        left -= units;
         if (left <= 0) return false;
         next_item(p, at, r);
         item<KT>(p);
-        return true;
+        return first < last;
     }
 };
 
@@ -550,8 +549,8 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
             }
             ++item;
         };
-        tell(true);
-        bool more = true;
+        bool more = v.first < v.last;
+        tell(more);
         while (more && ok) {
             // this item's loads, the next one's place worked out behind the first of them
             const int first = v.first, last = v.last, h = v.at.h, q_first = v.r.first + v.at.qt * U * tp.tile_tokens;
@@ -685,7 +684,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     tp.tile_tokens = kTileRows / p.group;
     tp.box = p.page_size & -p.page_size;
     if (tp.box > S::KT) tp.box = S::KT;
-    p.rows = U * tp.tile_tokens * p.group;
+    p.rows = U * tp.tile_tokens * p.group, p.cost = U == 2 ? 3 : 2;
     tp.p = p;
     CUtensorMap q, o, k, v;
     if (!encode_tokens(&q, p.q, p.q_stride, p, D, tp.tile_tokens) || !encode_tokens(&o, p.o, (int64_t)p.hkv * p.group * D, p, D, tp.tile_tokens) || !encode_pool(&k, p.k, p, D, tp.box) || !encode_pool(&v, p.v, p, D, tp.box))

@@ -1,7 +1,8 @@
 // attn.cuh -- what the attention kernels share (gdn_attention.h): slots of the paged cache, and how the work is cut.
 //
 // An item is a request's key-value head with one tile of R = Params::rows rows (row r: token r / group, query head r % group of
-// those that share the head); its work is the tiles of KT slots that any of its rows sees.  All items' tiles, one
+// those that share the head); its work is the tiles of KT slots that any of its rows sees, and what beginning and ending it
+// costs (Params::cost, in tiles).  All items' work, one
 // item after another, are cut into equal runs, one for each block.  A run that has all of an item writes its
 // outputs; the others write the sum, the maximum and the unscaled output of what they had to the workspace, at most
 // two of them a block (the item it ends, the item it begins), and join_kernel adds an item's parts in order.
@@ -18,7 +19,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
     int batch, hkv, group, page_size, n_pages, max_pages, total, max_tokens, mask_words, min_tiles;
-    int rows;                               // R: rows of an item
+    int rows, cost;                         // R: rows of an item; what an item costs besides its tiles, in tiles
     int64_t page_stride, slot_stride, head_stride, q_stride;
     float scale_log2;
     const void *k, *v, *q;
@@ -91,14 +92,14 @@ template <int KT>
 __device__ __forceinline__ int64_t head_tiles(const Params &p, const Request &r) {
     const int nq = row_tiles(p, r);
     if (nq == 0) return 0;
-    const int last = item_tiles<KT>(p, r, nq - 1);
+    const int last = item_tiles<KT>(p, r, nq - 1) + p.cost;
     if (p.mask || r.len < 0 || nq == 1) return (int64_t)nq * last;
-    return last + floor_sum(nq - 1, (int64_t)p.group * KT, p.rows, p.rows + p.group - 1 + p.group * ((int64_t)r.len + KT - 1));
+    return last + (int64_t)(nq - 1) * p.cost + floor_sum(nq - 1, (int64_t)p.group * KT, p.rows, p.rows + p.group - 1 + p.group * ((int64_t)r.len + KT - 1));
 }
 
-// A place in the work: tile `tile` of an item.
+// A place in the work: unit `off` of an item, whose tiles come after `cost` units.
 struct Place {
-    int b, h, qt, tile;
+    int b, h, qt, off;
 };
 
 // What find() shares between the threads of a block.
@@ -163,7 +164,7 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
             rest -= h * ht;
             int qt = 0;
             if (p.mask || r.len < 0 || r.n == 1) {
-                const int t = item_tiles<KT>(p, r, 0);
+                const int t = item_tiles<KT>(p, r, 0) + p.cost;
                 qt = (int)(div_up(rest + 1, t) - 1);
                 rest -= (int64_t)qt * t;
             }
@@ -176,21 +177,21 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
     at = s.at;
     const Request r = request(p, at.b, nullptr);
     if (p.mask || r.len < 0 || r.n == 1) {
-        at.tile = (int)s.rest;
+        at.off = (int)s.rest;
         return;
     }
     // a prompt's tiles differ: the threads share its rows
     const int nq = row_tiles(p, r), share = (nq + nt - 1) / nt, q0 = min(nq, tid * share), q1 = min(nq, q0 + share);
     mine = 0;
 #pragma unroll 1
-    for (int q = q0; q < q1; ++q) mine += item_tiles<KT>(p, r, q);
+    for (int q = q0; q < q1; ++q) mine += item_tiles<KT>(p, r, q) + p.cost;
     int64_t rest = s.rest - scan(mine, s, total);
     if (rest >= 0 && rest < mine) {
         int q = q0;
 #pragma unroll 1
-        for (int t; rest >= (t = item_tiles<KT>(p, r, q)); ++q) rest -= t;
+        for (int t; rest >= (t = item_tiles<KT>(p, r, q) + p.cost); ++q) rest -= t;
         s.at.qt = q;
-        s.at.tile = (int)rest;
+        s.at.off = (int)rest;
     }
     __syncthreads();
     at = s.at;
@@ -198,7 +199,7 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
 
 // the item after `at`'s
 __device__ __forceinline__ void next_item(const Params &p, Place &at, Request &r) {
-    at.tile = 0;
+    at.off = 0;
     if (++at.qt < row_tiles(p, r)) return;
     at.qt = 0;
     if (++at.h < p.hkv) return;
@@ -207,6 +208,21 @@ __device__ __forceinline__ void next_item(const Params &p, Place &at, Request &r
         if (++at.b >= p.batch) return;
         r = request(p, at.b, nullptr);
     } while (r.n == 0);
+}
+
+// What a run with `left` units of work has of the item it is at: tiles first .. last - 1 (none where it ends before them), and
+// how many units that takes.
+struct Span {
+    int tiles, first, last, units;
+};
+template <int KT>
+__device__ __forceinline__ Span span_of(const Params &p, const Request &r, const Place &at, int64_t left) {
+    Span s;
+    s.tiles = item_tiles<KT>(p, r, at.qt);
+    s.first = max(0, at.off - p.cost);
+    s.last = (int)min((int64_t)s.tiles, at.off + left - p.cost);
+    s.units = p.cost + s.tiles - at.off;
+    return s;
 }
 
 // The offset of slot s of request b, head h, in the pools; -1 where its page is outside the pool.
@@ -243,7 +259,7 @@ __device__ __forceinline__ void item_of(const Params &p, int run, int tiles_of_r
     at = Place{item / p.hkv, item % p.hkv, run % tiles_of_rows, 0};
     const Request r = request(p, at.b, at.h == 0 && at.qt == 0 && threadIdx.x == 0 ? p.status : nullptr);
     begin = 0;
-    end = at.qt < row_tiles(p, r) ? item_tiles<KT>(p, r, at.qt) : 0;
+    end = at.qt < row_tiles(p, r) ? p.cost + item_tiles<KT>(p, r, at.qt) : 0;
 }
 
 // What joins an item that is cut at the start of a run, told by that run's block: rows 0 where there is nothing to join, because
@@ -259,10 +275,10 @@ __device__ __forceinline__ Cut *cut_of(const Params &p, int cap, int d, int runs
 template <int KT>
 __device__ __forceinline__ void tell_cut(const Params &p, int cap, int d, int runs, int run, int64_t per, int64_t begin, int64_t end, const Place &at) {
     Cut c = {};
-    if (begin < end && at.tile > 0 && at.tile <= per) {
+    if (begin < end && at.off > p.cost && at.off - p.cost <= per) {
         const Request r = request(p, at.b, nullptr);
         c.rows = min(p.rows, r.n * p.group - at.qt * p.rows);
-        c.last = (int)(div_up(begin - at.tile + item_tiles<KT>(p, r, at.qt), per) - 1);
+        c.last = (int)(div_up(begin - at.off + p.cost + item_tiles<KT>(p, r, at.qt), per) - 1);
         c.row = at.qt * p.rows, c.first = r.first, c.head = at.h;
     }
     *cut_of(p, cap, d, runs, run) = c;
