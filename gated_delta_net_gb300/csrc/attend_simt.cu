@@ -1,6 +1,7 @@
 // attend_simt.cu -- attention over a paged cache, general: fp32, and bf16 that the tensor-core kernels do not take.
 //
-// A block has 16 rows and takes 32 slots at a time: keys and values to shared memory as fp32, the scores one slot a
+// A block has 16 rows (or 4) and takes 32 slots at a time: keys and values to shared memory as fp32 (the next tile's are on their way in
+// registers meanwhile, where rows start on 16 bytes), the scores one slot a
 // lane, four rows a warp, the running maximum and sum of a row in its warp, then the outputs with a column (or two) a thread.
 // fp32 arithmetic throughout.  What bounds it is shared-memory reads beside the multiplications (five 16-byte
 // reads for 16 of them in the scores).
@@ -11,11 +12,12 @@ namespace {
 
 using namespace attn;
 
-constexpr int kR = 16, kKT = 32, kThreads = 128, kMostWhole = 4, kCost = 1;
+constexpr int kKT = 32, kThreads = 128, kMostWhole = 4, kCost = 1;
 
-template <int D>
+// R: rows of a block
+template <int D, int R>
 struct Shared {
-    float q[kR][D + 4], k[kKT][D + 4], v[kKT][D], p[kR][kKT], m[kR], f[kR], l[kR];
+    float q[R][D + 4], k[kKT][D + 4], v[kKT][D], p[R][kKT], m[R], f[R], l[R];
     int64_t at[kKT];
     Scratch find;
 };
@@ -47,20 +49,71 @@ __device__ __forceinline__ void load_rows(const void *x, const int64_t *at, int 
     }
 }
 
-template <typename T, int D, bool VEC>
+// four entries as they lie in memory
+template <typename T>
+struct Four {
+    uint32_t w[sizeof(T)];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (sizeof(T) == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(p);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+        } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(p);
+            w[0] = x.x, w[1] = x.y;
+        }
+    }
+    __device__ __forceinline__ float4 values() const {
+        if constexpr (sizeof(T) == 4)
+            return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
+        else
+            return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
+                               __uint_as_float(w[1] & 0xFFFF0000u));
+    }
+};
+
+// A thread's share of a tile's keys and values, on its way while the tile before it is worked on.
+template <typename T, int D>
+struct Ahead {
+    static constexpr int N = kKT * (D / 4) / kThreads;
+    Four<T> k[N], v[N];
+    __device__ __forceinline__ void load(const Params &p, const Place &at, int slot0, int seen) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int n = i * kThreads + threadIdx.x, slot = slot0 + n / (D / 4);
+            const int64_t off = slot < seen ? slot_offset(p, at.b, at.h, slot) : -1;
+            k[i] = v[i] = Four<T>{};
+            if (off >= 0) {
+                k[i].load(static_cast<const T *>(p.k) + off + n % (D / 4) * 4);
+                v[i].load(static_cast<const T *>(p.v) + off + n % (D / 4) * 4);
+            }
+        }
+    }
+    __device__ __forceinline__ void store(float *k_to, int k_ld, float *v_to, int v_ld) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int n = i * kThreads + threadIdx.x, row = n / (D / 4), c = n % (D / 4) * 4;
+            *reinterpret_cast<float4 *>(k_to + row * k_ld + c) = k[i].values();
+            *reinterpret_cast<float4 *>(v_to + row * v_ld + c) = v[i].values();
+        }
+    }
+};
+
+template <typename T, int D, bool VEC, int R>
 __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int runs) {
     after_previous();
     extern __shared__ __align__(16) uint8_t raw[];
-    Shared<D> &s = *reinterpret_cast<Shared<D> *>(raw);
-    constexpr int kCols = D > kThreads ? D / kThreads : 1, kGroups = D < kThreads ? kThreads / D : 1, kMine = kR / kGroups;
+    using S = Shared<D, R>;
+    S &s = *reinterpret_cast<S *>(raw);
+    // for the outputs: columns of a thread, groups of threads that share the rows (threads past them have none), rows of each
+    constexpr int kCols = D > kThreads ? D / kThreads : 1, kGroups = D >= kThreads ? 1 : kThreads / D < R ? kThreads / D : R, kMine = R / kGroups;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, run = blockIdx.x;
     int64_t per, t, end;
     Place at;
     if (p.whole) {
-        item_of<kKT>(p, run, (p.max_tokens * p.group + kR - 1) / kR, t, end, at);
+        item_of<kKT>(p, run, (p.max_tokens * p.group + R - 1) / R, t, end, at);
     } else {
         find<kKT>(p, runs, run, run == 0 ? p.status : nullptr, s.find, per, t, end, at);
-        if (tid == 0) tell_cut<kKT>(p, kR, D, runs, run, per, t, end, at);
+        if (tid == 0) tell_cut<kKT>(p, R, D, runs, run, per, t, end, at);
     }
     if (t >= end) return;
     Request r = request(p, at.b, nullptr);
@@ -68,36 +121,44 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
         const Span span = span_of<kKT>(p, r, at, end - t);
         const int tiles = span.tiles, first = span.first, last = span.last, seen = seen_slots(p, r, at.qt), common = common_slots(p, r, at.qt);
         if (last <= first) break;
-        const int64_t row0 = (int64_t)at.qt * kR, rows = (int64_t)r.n * p.group;
-        if (tid < kR) {
+        const int64_t row0 = (int64_t)at.qt * R, rows = (int64_t)r.n * p.group;
+        if (tid < R) {
             const int64_t q = row0 + tid;
             s.at[tid] = q < rows ? (r.first + q / p.group) * p.q_stride + (at.h * p.group + q % p.group) * D : -1;
         }
-        if (tid < kR) s.m[tid] = -INFINITY, s.l[tid] = 0.f;
+        if (tid < R) s.m[tid] = -INFINITY, s.l[tid] = 0.f;
         __syncthreads();
-        load_rows<T, D, VEC>(p.q, s.at, kR, &s.q[0][0], D + 4);
+        load_rows<T, D, VEC>(p.q, s.at, R, &s.q[0][0], D + 4);
         float acc[kMine][kCols] = {};
+        Ahead<T, D> ahead;
+        if constexpr (VEC) ahead.load(p, at, first * kKT, seen);
         for (int tile = first; tile < last; ++tile) {
             const int slot0 = tile * kKT;
             __syncthreads();
-            if (tid < kKT) s.at[tid] = slot0 + tid < seen ? slot_offset(p, at.b, at.h, slot0 + tid) : -1;
-            __syncthreads();
-            load_rows<T, D, VEC>(p.k, s.at, kKT, &s.k[0][0], D + 4);
-            load_rows<T, D, VEC>(p.v, s.at, kKT, &s.v[0][0], D);
-            __syncthreads();
-            float x[kR / 4] = {};
-#pragma unroll 4
+            if constexpr (VEC) {
+                ahead.store(&s.k[0][0], D + 4, &s.v[0][0], D);
+                __syncthreads();
+                if (tile + 1 < last) ahead.load(p, at, slot0 + kKT, seen);
+            } else {
+                if (tid < kKT) s.at[tid] = slot0 + tid < seen ? slot_offset(p, at.b, at.h, slot0 + tid) : -1;
+                __syncthreads();
+                load_rows<T, D, VEC>(p.k, s.at, kKT, &s.k[0][0], D + 4);
+                load_rows<T, D, VEC>(p.v, s.at, kKT, &s.v[0][0], D);
+                __syncthreads();
+            }
+            float x[R / 4] = {};
+#pragma unroll 8
             for (int c = 0; c < D; c += 4) {
                 const float4 k = *reinterpret_cast<const float4 *>(&s.k[lane][c]);
 #pragma unroll
-                for (int i = 0; i < kR / 4; ++i) {
+                for (int i = 0; i < R / 4; ++i) {
                     const float4 q = *reinterpret_cast<const float4 *>(&s.q[warp + 4 * i][c]);
                     x[i] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, x[i]))));
                 }
             }
             const int slot = slot0 + lane;
 #pragma unroll
-            for (int i = 0; i < kR / 4; ++i) {
+            for (int i = 0; i < R / 4; ++i) {
                 const int row = warp + 4 * i;
                 const int64_t q = row0 + row;
                 float y = slot < seen && q < rows && sees(p, r, (int)(q / p.group), slot) ? x[i] * p.scale_log2 : -INFINITY;
@@ -118,12 +179,13 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
                 if (lane == 0) s.m[row] = m, s.f[row] = f, s.l[row] = fmaf(s.l[row], f, sum);
             }
             __syncthreads();
-            const int g = tid / D % kGroups;
+            const int g = min(tid / D, kGroups - 1);
             const bool masked = slot0 + kKT > common;  // what is not seen there may be anything
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) acc[i][c] *= s.f[g * kMine + i];
+#pragma unroll 8
             for (int j = 0; j < kKT; ++j) {
                 float v[kCols];
 #pragma unroll
@@ -140,12 +202,12 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
         }
         __syncthreads();
         const bool whole = first == 0 && last == tiles;
-        const int which = first == 0, g = tid / D % kGroups;
+        const int which = first == 0, g = tid / D;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int row = g * kMine + i;
             const int64_t q = row0 + row;
-            if (q >= rows) continue;
+            if (g >= kGroups || q >= rows) continue;
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
                 const int col = (tid + c * kThreads) % D;
@@ -155,12 +217,12 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
                     if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to, y);
                     else store_f(static_cast<float *>(p.o), to, y);
                 } else {
-                    part_out(p, kR, D, run, which)[row * D + col] = acc[i][c];
+                    part_out(p, R, D, run, which)[row * D + col] = acc[i][c];
                 }
             }
         }
-        if (!whole && tid < kR) {
-            float *st = part_stat(p, kR, D, runs, run, which) + tid * 2;
+        if (!whole && tid < R) {
+            float *st = part_stat(p, R, D, runs, run, which) + tid * 2;
             st[0] = s.m[tid], st[1] = s.l[tid];
         }
         t += span.units;
@@ -169,24 +231,24 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
     }
 }
 
-template <typename T, int D, bool VEC>
+template <typename T, int D, bool VEC, int R>
 cudaError_t run(Params p, int runs, cudaStream_t stream) {
     static int have[16];
-    p.rows = kR, p.cost = kCost;
-    const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC>, (int)sizeof(Shared<D>), have);
+    p.rows = R, p.cost = kCost;
+    const cudaError_t e = ensure_smem(attend_simt_kernel<T, D, VEC, R>, (int)sizeof(Shared<D, R>), have);
     if (e != cudaSuccess) return e;
-    const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC>, dim3(runs), kThreads, sizeof(Shared<D>), stream, p, runs);
-    return f != cudaSuccess || p.whole ? f : launch_join<D, kR>(p, runs, stream);
+    const cudaError_t f = launch_dependent(attend_simt_kernel<T, D, VEC, R>, dim3(runs), kThreads, sizeof(Shared<D, R>), stream, p, runs);
+    return f != cudaSuccess || p.whole ? f : launch_join<D, R>(p, runs, stream);
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int R>
 cudaError_t (*pick(int d))(Params, int, cudaStream_t) {
     switch (d) {
-        case 16: return run<T, 16, VEC>;
-        case 32: return run<T, 32, VEC>;
-        case 64: return run<T, 64, VEC>;
-        case 128: return run<T, 128, VEC>;
-        default: return run<T, 256, VEC>;
+        case 16: return run<T, 16, VEC, R>;
+        case 32: return run<T, 32, VEC, R>;
+        case 64: return run<T, 64, VEC, R>;
+        case 128: return run<T, 128, VEC, R>;
+        default: return run<T, 256, VEC, R>;
     }
 }
 
@@ -194,13 +256,19 @@ cudaError_t (*pick(int d))(Params, int, cudaStream_t) {
 
 attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     const gdn_kv_cache &c = a.cache;
-    const bool vec = aligned16(a);
+    // fp32 rows on 16 bytes: four rows a block where a request has no more (16 would compute four times what one head needs: 6 single
+    // tokens over 100..23617 slots, 8 heads of 128, 373 us)
+    const bool vec = c.dtype == GDN_F32 && aligned16(a), few = vec && (decode ? 1 : (int64_t)a.max_tokens) * (a.n_q_heads / c.n_kv_heads) <= 4;
+    const int R = few ? 4 : 16;
     Choice x;
-    x.whole = whole_items(a, decode, kR, kKT, kMostWhole, x.runs);
-    if (!x.whole) x.runs = most_runs(a, decode, kR, kKT, 2);
-    x.workspace = x.whole ? 0 : 4 * workspace_floats(kR, c.d, x.runs);
-    if (c.dtype == GDN_BF16) x.launch = vec ? pick<__nv_bfloat16, true>(c.d) : pick<__nv_bfloat16, false>(c.d);
-    else x.launch = vec ? pick<float, true>(c.d) : pick<float, false>(c.d);
+    x.whole = whole_items(a, decode, R, kKT, kMostWhole, x.runs);
+    if (!x.whole) x.runs = most_runs(a, decode, R, kKT, 2);
+    x.workspace = x.whole ? 0 : 4 * workspace_floats(R, c.d, x.runs);
+    // (bf16 rows on 16 bytes are the tensor cores')
+    x.launch = c.dtype == GDN_BF16 ? pick<__nv_bfloat16, false, 16>(c.d)
+               : few               ? pick<float, true, 4>(c.d)
+               : vec               ? pick<float, true, 16>(c.d)
+                                   : pick<float, false, 16>(c.d);
     return x;
 }
 
