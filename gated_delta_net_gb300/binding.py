@@ -886,14 +886,15 @@ def gdn_kv_decode(q, k_cache, v_cache, page_table, lens, scale: float = 1.0, out
     return _attend(True, q, k_cache, v_cache, page_table, lens, None, 1, None, scale, out, out_dtype, workspace, dev_status, stream)
 
 
-def gdn_kv_attend_workspace(q, k_cache, v_cache, page_table, max_tokens: int = 0, anc_mask=None, decode: bool = False, out_dtype=None) -> int:
+def gdn_kv_attend_workspace(q, k_cache, v_cache, page_table, max_tokens: int = 0, anc_mask=None, decode: bool = False,
+                            scale: float = 1.0, out_dtype=None) -> int:
     """Bytes of ``workspace`` with which gdn_kv_attend (or gdn_kv_decode) takes tensors of these sizes and strides (they
     allocate their own otherwise)."""
     T, hq, d = q.shape
     dev = _device(q, "q")
     cache = _cache(k_cache, v_cache, page_table, page_table.new_empty(page_table.shape[0]), None, dev, q.dtype)
     need = lib().gdn_kv_attend_workspace(
-        _kv_attend_args(*cache, T, max_tokens, hq, anc_mask.shape[1] if anc_mask is not None else 0, _dtype_code(out_dtype or q.dtype), 1.0,
+        _kv_attend_args(*cache, T, max_tokens, hq, anc_mask.shape[1] if anc_mask is not None else 0, _dtype_code(out_dtype or q.dtype), scale,
                         _rows(q, "q", q.dtype, (T, hq, d), dev), q.data_ptr(), 0, 0 if anc_mask is None else anc_mask.data_ptr(), 0, 0, 0),
         decode)
     if need < 0:

@@ -262,7 +262,7 @@ attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     const int R = few ? 4 : 16;
     Choice x;
     x.whole = whole_items(a, decode, R, kKT, kMostWhole, x.runs);
-    if (!x.whole) x.runs = most_runs(a, decode, R, kKT, 2);
+    if (!x.whole) x.runs = most_runs(a, decode, R, kKT, c.d == 256 ? 2 : 3);  // (what their registers leave room for)
     x.workspace = x.whole ? 0 : 4 * workspace_floats(R, c.d, x.runs);
     // (bf16 rows on 16 bytes are the tensor cores')
     x.launch = c.dtype == GDN_BF16 ? pick<__nv_bfloat16, false, 16>(c.d)

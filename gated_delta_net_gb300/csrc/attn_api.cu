@@ -64,7 +64,7 @@ int check_attend(const gdn_kv_attend_args *a, bool decode) {
     if (!decode && a->anc_mask && a->mask_words < 1) return fail(GDN_ERR_INVALID_ARG, "mask_words %d < 1", a->mask_words);
     if (!decode && a->anc_mask && a->mask_words > 1 << 20) return fail(GDN_ERR_UNSUPPORTED, "mask_words %d > 2^20", a->mask_words);
     if ((int64_t)a->total_tokens * a->n_q_heads > kMost) return fail(GDN_ERR_UNSUPPORTED, "more than 2^30 rows of query heads in a call");
-    if (!std::isfinite(a->scale)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(a->scale * gdn::attn::kLog2e)) return fail(GDN_ERR_INVALID_ARG, "scale %g is not finite, or too large", a->scale);
     return check_stride("q", a->q_stride, (int64_t)a->n_q_heads * c.d);
 }
 
@@ -72,7 +72,9 @@ bool nothing(const gdn_kv_attend_args &a, bool decode) {
     return a.cache.batch == 0 || a.total_tokens == 0 || (!decode && a.max_tokens == 0);
 }
 
-// the kernel for a call
+// The kernel for a call: the tensor cores where a key-value head has more rows than the 16 of a warp product (eight drafts of 6 to 16
+// nodes, 4 query heads each: 73 us by 16 rows at a time, 55 in tiles), by warp products below that, and the general kernel
+// for fp32 and rows that do not start on 16 bytes.
 gdn::attn::Choice choose(const gdn_kv_attend_args &a, bool decode) {
     if (!decode && a.max_tokens * (int64_t)(a.n_q_heads / a.cache.n_kv_heads) > 16 && gdn::attend_tc_supported(a)) return gdn::attend_tc_choice(a);
     return gdn::attend_mma_supported(a) ? gdn::attend_mma_choice(a, decode) : gdn::attend_simt_choice(a, decode);

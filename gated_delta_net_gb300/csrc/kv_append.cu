@@ -3,7 +3,7 @@
 // Per token: each query and key head's row x of d entries, x / sqrt(mean x^2 + eps) * w where there is a norm, the first
 // rot_dim entries turned by the position's angles; values copied.  Every byte is read once and written once: bound
 // by memory, or for a few tokens by the launch and one chain of loads (offsets, length, page, row).
-// A block takes a token; d / 8 lanes take a row with 8 entries each, one row after another, so that a token's cosines and
+// A block takes a token, with one warp or four; d / 8 lanes take a row with 8 entries each, one row after another, so that a token's cosines and
 // sines are read once into registers.  The partner of an entry in a pair is 8 lanes or fewer away, or its neighbour.
 // Where rows do not start on 16 bytes, or half the rotated width is no multiple of 8, entries and partners are read one by one.
 #include "attn.cuh"
@@ -13,7 +13,6 @@ namespace {
 
 using attn::launch_dependent;
 
-constexpr int kThreads = 128;
 
 struct AppendParams {
     int batch, hq, hkv, page_size, n_pages, max_pages, total, rot, n_positions;
@@ -72,8 +71,8 @@ __device__ __forceinline__ float weight_at(const void *w, bool bf16, int i) {
 }
 
 // VEC: 16-byte pieces (weights and angles too), and the partner of lane l's entries (halves) is another lane's; INTER: pairs of neighbours
-template <typename T, int D, bool VEC, bool INTER>
-__global__ void __launch_bounds__(kThreads, 8) append_kernel(AppendParams p) {
+template <typename T, int D, bool VEC, bool INTER, int kThreads>
+__global__ void __launch_bounds__(kThreads, VEC ? 1024 / kThreads : 1) append_kernel(AppendParams p) {
     after_previous();
     constexpr int L = D / 8, G = kThreads / L;  // lanes a row, rows a block has in flight
     const int t = blockIdx.x, tid = threadIdx.x, sub = tid % L, e0 = sub * 8, half = p.rot / 2;
@@ -210,11 +209,18 @@ __global__ void __launch_bounds__(kThreads, 8) append_kernel(AppendParams p) {
     }
 }
 
+template <typename T, int D, int kThreads>
+cudaError_t run_threads(const AppendParams &p, bool vec, bool inter, cudaStream_t stream) {
+    auto kernel = vec ? (inter ? append_kernel<T, D, true, true, kThreads> : append_kernel<T, D, true, false, kThreads>)
+                      : (inter ? append_kernel<T, D, false, true, kThreads> : append_kernel<T, D, false, false, kThreads>);
+    return launch_dependent(kernel, dim3(p.total), kThreads, 0, stream, p);
+}
+
+// One warp a token where there are many: finding a token's place takes as many instructions as five rows, and is done by each warp
+// (16384 tokens of 20 rows of 256: 86 us with four warps).  Few tokens are spread over more threads.
 template <typename T, int D>
 cudaError_t run(const AppendParams &p, bool vec, bool inter, cudaStream_t stream) {
-    auto kernel = vec ? (inter ? append_kernel<T, D, true, true> : append_kernel<T, D, true, false>)
-                      : (inter ? append_kernel<T, D, false, true> : append_kernel<T, D, false, false>);
-    return launch_dependent(kernel, dim3(p.total), kThreads, 0, stream, p);
+    return p.total >= 16 * sm_count() ? run_threads<T, D, 32>(p, vec, inter, stream) : run_threads<T, D, 128>(p, vec, inter, stream);
 }
 
 template <typename T>

@@ -11,7 +11,7 @@ namespace {
 
 using attn::launch_dependent;
 
-constexpr int kThreads = 128, kPieces = 4;
+constexpr int kThreads = 128, kPieces = 4, kLongest = 1 << 20;  // entries of a path, so that its pieces can be counted in 32 bits
 
 struct CommitParams {
     int hkv, page_size, n_pages, max_pages, row_pieces, total_path;
@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitParams p) {
     const int lo = p.path_offsets[b], hi = p.path_offsets[b + 1], n_lo = p.node_offsets[b], n_hi = p.node_offsets[b + 1];
     int bad = 0;
     if (lo < 0 || hi < lo || hi > p.total_path || n_lo < 0 || n_hi < n_lo) bad = GDN_DEV_BAD_DESC;
+    if (!bad && hi - lo > kLongest) bad = GDN_DEV_BAD_PATH;
     const int n = bad || len == -1 ? 0 : hi - lo;
     if (!bad && len < -1) bad = GDN_DEV_BAD_PAGE;
     const int32_t *table = p.table + (int64_t)b * p.max_pages;

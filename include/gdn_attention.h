@@ -99,8 +99,8 @@ typedef struct {
     const void *q;              /* [T][n_q_heads][d] */
     const int32_t *token_offsets;  /* [B+1] ascending from 0 (gdn_kv_decode: not read) */
     const uint32_t *anc_mask;   /* [T][mask_words], or NULL: causal (gdn_kv_decode: not read) */
-    void *o;                    /* [T][n_q_heads][d] */
-    void *workspace;            /* gdn_kv_attend_workspace() bytes, 256-byte aligned */
+    void *o;                    /* [T][n_q_heads][d], 16-byte aligned */
+    void *workspace;            /* gdn_kv_attend_workspace() bytes, 256-byte aligned; NULL if that is 0 */
     int64_t workspace_bytes;
 } gdn_kv_attend_args;
 
@@ -117,8 +117,13 @@ typedef struct {
  * A NaN or infinity in a key or value reaches the tokens that see it, and no others (the whole
  * rows of those, as NaN, where it stands in the value of a new token).
  * The work is cut along the slots into equal parts, one for each running block, whatever the lengths
- * are; parts of one token's softmax are joined by a second kernel in a fixed order: the same call gives
- * the same bits.
+ * are (caches of up to 1024 slots, with few rows, are not cut); parts of one token's softmax are joined by a second
+ * kernel in a fixed order: the same call gives the same bits.
+ * bf16 rows that start on 16 bytes run on the tensor cores: probabilities are rounded to bf16 before they are multiplied
+ * by values (2^-8 of each; their sum is kept of the unrounded ones), so that outputs are up to 1.4 times their own rounding to
+ * bf16 from exact (norm-wise 2.3e-3, 1.7e-3).  More than 16 rows (new tokens x query heads of a key-value head) in a request
+ * take tcgen05, with d from 64 on, pages of a multiple of 8 slots, at most 128 query heads to a key-value head and a positive scale;
+ * others warp products.  fp32, and rows that do not start on 16 bytes, run the general kernel in fp32 arithmetic.
  */
 GDN_API int gdn_kv_attend(const gdn_kv_attend_args *args, void *stream);
 
@@ -128,8 +133,8 @@ GDN_API int gdn_kv_attend(const gdn_kv_attend_args *args, void *stream);
  */
 GDN_API int gdn_kv_decode(const gdn_kv_attend_args *args, void *stream);
 
-/* Bytes of workspace that gdn_kv_attend, or gdn_kv_decode (decode nonzero), needs for these sizes (only the
- * sizes, types, strides and the alignment of pointers are read); -1 for sizes that it would refuse.  A call uses its workspace alone:
+/* Bytes of workspace that gdn_kv_attend, or gdn_kv_decode (decode nonzero), needs for these sizes (only the sizes, types,
+ * strides, the sign of scale and the alignment of q and the pools are read); -1 for sizes that it would refuse.  A call uses its workspace alone:
  * two calls that may run at the same time need two. */
 GDN_API int64_t gdn_kv_attend_workspace(const gdn_kv_attend_args *args, int32_t decode);
 
@@ -145,7 +150,7 @@ typedef struct {
 /*
  * gdn_kv_commit -- the accepted path's tokens move to where committed ones stand: slot
  * lens[b] + path[i] to slot lens[b] + i, in place, and new_lens[b] = lens[b] + the path's length.
- * A path that does not ascend within its request's nodes sets GDN_DEV_BAD_PATH, offsets that descend
+ * A path that does not ascend within its request's nodes, or has more than 2^20, sets GDN_DEV_BAD_PATH, offsets that descend
  * (or pass total_path) GDN_DEV_BAD_DESC, a slot past the page table or a page outside the
  * pool GDN_DEV_BAD_PAGE: that request's cache stays as it was, and new_lens[b] = lens[b].
  */

@@ -359,6 +359,69 @@ def test_graph_replays_with_other_lengths(dtype):
         close(got[1], *tree.oracle(mask), dtype)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (4, 1, 64), (8, 1, 256), (32, 1, 16)])
+def test_attend_of_many_requests(hq, hkv, d):
+    # more requests than a block has threads, some empty, some not in use
+    counts = [(i * 7) % 6 for i in range(900)]
+    lens = [(i * 53) % 70 - 1 for i in range(900)]
+    c = Case(41, lens, counts, hq, hkv, d, 16, BF)
+    for mask in (None, tree_masks(9, counts)):
+        o = gb.gdn_kv_attend(c.q, *c.cache, c.off, 5, anc_mask=mask, scale=c.scale)
+        close(o, *c.oracle(mask), BF)
+
+
+@pytest.mark.parametrize("dtype,d,lens,counts", [(BF, 128, [5000, 4000, 100], [3, 3, 2]), (BF, 64, [3000, 2000], [2, 40]), (F32, 64, [3000, 900], [2, 3]),
+                                                 (BF, 128, [900, 30], [300, 20]), (BF, 256, [2500, 60], [40, 9])])
+def test_attend_parts_of_trees_are_joined(dtype, d, lens, counts):
+    # few items, long caches: most of them are cut, inside their committed slots and inside the new ones
+    c = Case(42, lens, counts, 8, 2, d, 16, dtype)
+    mask = tree_masks(10, counts)
+    for m in (mask, None):
+        o = gb.gdn_kv_attend(c.q, *c.cache, c.off, max(counts), anc_mask=m, scale=c.scale)
+        close(o, *c.oracle(m), dtype)
+
+
+def test_negative_and_zero_scales_of_several_tokens():
+    c = Case(43, [300, 20], [40, 30], 8, 2, 128, 16, BF)
+    for scale in (-0.1, 0.0):
+        c.scale = scale
+        close(gb.gdn_kv_attend(c.q, *c.cache, c.off, 40, scale=scale), *c.oracle(), BF)
+
+
+def test_memory_of_a_dropped_result_on_another_stream():
+    # what a call on the side stream returned goes back to the allocator while the call may still write it
+    c = Case(44, [9000, 300], [1, 1], 8, 1, 128, 16, BF)
+    ref = gb.gdn_kv_decode(c.q, *c.cache, scale=c.scale)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for _ in range(3):
+            gb.gdn_kv_decode(c.q, *c.cache, scale=c.scale, stream=side)
+        ones = torch.ones(2, 8, 128, dtype=BF, device="cuda")
+        got = gb.gdn_kv_decode(c.q, *c.cache, scale=c.scale, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, ref) and np.all(ones.float().cpu().numpy() == 1.0)
+
+
+def test_append_then_attend_back_to_back():
+    # the kernels may take their places while the one before ends: what it wrote is seen
+    c = Case(45, [700, 90], [20, 9], 8, 2, 128, 16, BF)
+    k, v = torch.randn(29, 2, 128, device="cuda").to(BF), torch.randn(29, 2, 128, device="cuda").to(BF)
+    angles = table_of_angles(800, 64)
+    mask = tree_masks(11, [20, 9])
+    want = None
+    for i in range(30):
+        q = gb.gdn_kv_append(c.q, k, v, *c.cache, token_offsets=c.off, cos_sin=angles)
+        o = gb.gdn_kv_attend(q, *c.cache, c.off, 20, anc_mask=mask, scale=c.scale)
+        d = gb.gdn_kv_decode(q[:2].contiguous(), *c.cache, scale=c.scale)
+        # another token's keys in between, so that a stale read shows
+        gb.gdn_kv_append(None, v, k, *c.cache, token_offsets=c.off, cos_sin=angles)
+        if want is None:
+            torch.cuda.synchronize()
+            want = o.clone(), d.clone()
+        assert torch.equal(o, want[0]) and torch.equal(d, want[1])
+
+
 def test_two_streams_at_once():
     cs = [Case(20 + i, [9000, 500], [1, 1], 8, 1, 128, 16, BF) for i in range(2)]
     refs = []
@@ -541,7 +604,39 @@ def test_commit_device_checks():
     assert run(path=((), ())) == (0, [10, 30], [0, 0])
 
 
+def test_append_of_many_tokens():
+    # past 16 tokens an SM a token has one warp
+    counts = [1200, 0, 1400, 37]
+    lens = [5, 9, 0, -1]
+    for dtype, d, hq, hkv, rot, pad in ((BF, 64, 2, 1, 32, 0), (F32, 16, 3, 3, 16, 0), (BF, 256, 1, 1, 64, 3)):
+        c = Case(34, lens, counts, hq, hkv, d, 16, dtype)
+        T = sum(counts)
+        gen = torch.Generator().manual_seed(6)
+        rows = torch.randn(T, (hq + 2 * hkv) * d + pad, generator=gen).to(dtype).cuda()
+        q, k, v = (rows[:, a * d:b * d].view(T, b - a, d) for a, b in ((0, hq), (hq, hq + hkv), (hq + hkv, hq + 2 * hkv)))
+        angles, w = table_of_angles(1500, rot), (1 + 0.2 * torch.randn(d, generator=gen)).to(dtype).cuda()
+        before = f64(c.k), f64(c.v)
+        st, out = gb.new_status(), torch.full((T, hq, d), float("nan"), dtype=dtype, device="cuda")
+        gb.gdn_kv_append(q, k, v, *c.cache, token_offsets=c.off, cos_sin=angles, q_weight=w, k_weight=w, q_out=out, dev_status=st)
+        gb.check_status(st)
+        rq, rk, rv = OA.append(f64(q), f64(k), f64(v), *before, c.table.cpu().numpy(), lens, c.off.cpu().numpy(), None, f64(angles), False, f64(w), f64(w))
+        near(out, rq, np.max(np.abs(np.nan_to_num(rq)), axis=-1, keepdims=True) * 2, dtype)
+        near(c.k, rk, np.nanmax(np.abs(rk)) * 2, dtype)
+        assert np.array_equal(f64(c.v), rv, equal_nan=True)
+
+
 # ---------------------------------------------------------------------------------------------- together
+
+
+def test_the_hybrid_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "hybrid_serving.py")
+    spec = importlib.util.spec_from_file_location("hybrid_serving", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    # bf16 activations through two layers, four roundings of 2^-8 of the largest value each way
+    assert module.run() <= 2.0 ** -5
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
