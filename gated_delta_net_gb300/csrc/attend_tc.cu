@@ -78,7 +78,7 @@ struct Shape {
     static constexpr int kSpoilt = KT / 32;
     // barriers
     static constexpr int KFULL = 0, KEMPTY = KFULL + KS, VFULL = KEMPTY + KS, VEMPTY = VFULL + VS, READY = VEMPTY + VS, SCORES = READY + VS,
-                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB * 2, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, JFULL = QEMPTY + 1, JEMPTY = JFULL + kJobs, OUT = JEMPTY + kJobs, TAKEN = OUT + U, DRAIN = TAKEN + U, COUNT = DRAIN + 1;
+                         PROBS = SCORES + U * NB, DONE = PROBS + U * NB * 2, FREE = DONE + U, QFULL = FREE + U, QEMPTY = QFULL + 1, JFULL = QEMPTY + 1, JEMPTY = JFULL + kJobs, OUT = JEMPTY + kJobs, TAKEN = OUT + U, DRAIN = TAKEN + U, PROBE = DRAIN + 1, COUNT = PROBE + 1;
     static constexpr int OFF_K = kQ, OFF_V = OFF_K + KS * kStage, OFF_OUT = OFF_V + VS * kStage, OFF_SPOILT = OFF_OUT + kRowWarps * 4096, OFF_JOB = (OFF_SPOILT + 2 * VS * kSpoilt * 4 + 15) / 16 * 16,
                          OFF_SCRATCH = OFF_JOB + kJobs * (int)sizeof(Job), OFF_BAR = OFF_SCRATCH + (int)sizeof(Scratch);
     static constexpr int kBytes = OFF_BAR + COUNT * 8 + 8;
@@ -90,6 +90,7 @@ struct TcParams {
     Params p;
     int tile_tokens;  // tokens of a tile of rows
     int box;          // slots of a TMA box
+    int probe;        // polls of a wait that runs out, for tests (0: none)
 };
 
 // after a wait that ran out the others look once
@@ -585,6 +586,7 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
     } else if (warp == S::kRowWarps + 3) {
         // ------------------------------------------------------------------ outputs
         int rounds[U] = {};
+        if (tp.probe > 0 && !mbar_wait(&bar[S::PROBE], 0, (uint32_t)tp.probe) && lane == 0) flag(p.status, GDN_DEV_TIMEOUT);
         while (const Job *wp = ok ? take() : nullptr) {
             const Job &w = *wp;
             for (int n = 0; n < w.boxes * S::H && ok; ++n) {
@@ -682,6 +684,7 @@ cudaError_t run(Params p, int runs, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     TcParams tp;
     tp.tile_tokens = kTileRows / p.group;
+    tp.probe = wait_probe_polls();
     tp.box = p.page_size & -p.page_size;
     if (tp.box > S::KT) tp.box = S::KT;
     p.rows = U * tp.tile_tokens * p.group, p.cost = U == 2 ? 3 : 2;

@@ -40,6 +40,16 @@ struct Raw {
             for (int i = 0; i < 8; ++i) x[i] = p[i];
         }
     }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
+        } else {
+            const T *x = reinterpret_cast<const T *>(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[i] = x[i];
+        }
+    }
     __device__ __forceinline__ void values(float (&x)[8]) const {
         const T *y = reinterpret_cast<const T *>(w);
 #pragma unroll
@@ -72,20 +82,19 @@ __device__ __forceinline__ float weight_at(const void *w, bool bf16, int i) {
 
 // VEC: 16-byte pieces (weights and angles too), and the partner of lane l's entries (halves) is another lane's; INTER: pairs of neighbours
 template <typename T, int D, bool VEC, bool INTER, int kThreads>
-__global__ void __launch_bounds__(kThreads, VEC ? 1024 / kThreads : 1) append_kernel(AppendParams p) {
+__global__ void __launch_bounds__(kThreads, VEC ? 640 / kThreads : 1) append_kernel(AppendParams p) {
     after_previous();
     constexpr int L = D / 8, G = kThreads / L;  // lanes a row, rows a block has in flight
-    const int t = blockIdx.x, tid = threadIdx.x, sub = tid % L, e0 = sub * 8, half = p.rot / 2;
-    const int rows = p.hq + 2 * p.hkv, turns = (rows + G - 1) / G;
-    // (row, what it is) of this lane's turn: queries, keys, values
-    auto source = [&](int row) {
-        const T *from = static_cast<const T *>(row < p.hq ? p.q : row < p.hq + p.hkv ? p.k : p.v);
-        const int h = row < p.hq ? row : row < p.hq + p.hkv ? row - p.hq : row - p.hq - p.hkv;
-        return from + t * (row < p.hq ? p.qs : row < p.hq + p.hkv ? p.ks : p.vs) + h * D + e0;
-    };
-    // the first row is on its way while the token's place is found, each other one while the row before it is worked on
-    Raw<T, VEC> next = {};
-    if (tid / L < rows) next.load(source(tid / L));
+    const int t = blockIdx.x, tid = threadIdx.x, sub = tid % L, e0 = sub * 8, half = p.rot / 2, h0 = tid / L;
+    // the first rows are on their way while the token's place is found, the later ones while those before them are worked on
+    const T *q_from = static_cast<const T *>(p.q) + t * p.qs + e0, *k_from = static_cast<const T *>(p.k) + t * p.ks + e0,
+            *v_from = static_cast<const T *>(p.v) + t * p.vs + e0;
+    constexpr int kAhead = 3;  // rows of a lane on their way
+    Raw<T, VEC> q_next[kAhead] = {}, k_next[1] = {}, v_next = {};
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (h0 + i * G < p.hq) q_next[i].load(q_from + (h0 + i * G) * D);
+    if (h0 < p.hkv) k_next[0].load(k_from + h0 * D), v_next.load(v_from + h0 * D);
     int b = t, i = 0;
     if (p.offsets) {
         int upto = 0;
@@ -147,65 +156,82 @@ __global__ void __launch_bounds__(kThreads, VEC ? 1024 / kThreads : 1) append_ke
         }
     }
     const unsigned mates = (L == 32 ? 0xffffffffu : (1u << (L & 31)) - 1) << ((tid & 31) / L * L);  // the lanes of a row
-    for (int turn = 0; turn < turns; ++turn) {  // alike in a whole warp, for the shuffles
-        const int row = turn * G + tid / L;
-        const bool live = row < rows, is_q = row < p.hq, is_v = row >= p.hq + p.hkv;
-        const int h = is_q ? row : is_v ? row - p.hq - p.hkv : row - p.hq;
-        const Raw<T, VEC> now = next;
-        if (row + G < rows) next.load(source(row + G));
-        T *dst = is_q ? static_cast<T *>(p.q_out) + ((int64_t)t * p.hq + h) * D
-                      : static_cast<T *>(is_v ? p.v_cache : p.k_cache) + at + h * p.head_stride;
-        float x[8], y[8];
-        now.values(x);
-        if (is_v) {
-            if (live) store8<T, VEC>(dst + e0, x);
-        }
-        // weights before the exchange, so that a partner comes with its own; the norm's factor after it
-        const void *w = is_q ? p.q_weight : p.k_weight;
-        float r = 1.f;
-        if (w) {
-            float sum = 0.f;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) sum = fmaf(x[n], x[n], sum);
-#pragma unroll
-            for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mates, sum, o, L);
-            r = rsqrtf(sum * (1.f / D) + p.eps);
-            float g[8];
-            if (VEC && p.weight_bf16) {
+    // entry n of a row is r (x_n a_n + y_n b_n), y its partner and r the norm's factor: weights and angles make a and b once
+    auto turn = [&](const T *from, int n_heads, auto &next, const void *w, T *to, int64_t pitch) {
+        const bool turned = VEC && !INTER && e0 < p.rot;  // (otherwise each entry by itself)
+        const int away = half / 8, mate = (e0 < half ? sub + away : sub - away) & (L - 1);
+        float a[8], b[8];
+        if (VEC && !INTER && w) {
+            if (p.weight_bf16) {
                 Raw<__nv_bfloat16, true> raw;
                 raw.load(static_cast<const __nv_bfloat16 *>(w) + e0);
-                raw.values(g);
-            } else if (VEC) {
+                raw.values(a);
+            } else {
                 Raw<float, true> raw;
                 raw.load(static_cast<const float *>(w) + e0);
-                raw.values(g);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 8; ++n) g[n] = weight_at(w, p.weight_bf16, e0 + n);
+                raw.values(a);
             }
 #pragma unroll
-            for (int n = 0; n < 8; ++n) x[n] *= g[n];
-        }
-        if constexpr (INTER) {
-#pragma unroll
-            for (int n = 0; n < 8; ++n) y[n] = x[n ^ 1];
-        } else if constexpr (VEC) {
-            const int away = half / 8, from = e0 < half ? sub + away : sub - away;
-#pragma unroll
-            for (int n = 0; n < 8; ++n) y[n] = __shfl_sync(mates, x[n], from & (L - 1), L);
+            for (int n = 0; n < 8; ++n) b[n] = __shfl_sync(mates, a[n], mate, L);
         } else {
-            const T *src = live ? source(row) - e0 : nullptr;
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                const int e = e0 + n, pe = e < half ? e + half : e - half;
-                y[n] = live && e < p.rot ? load_f(src, pe) * (w ? weight_at(w, p.weight_bf16, pe) : 1.f) : 0.f;
+                const int e = e0 + n, pe = INTER ? e ^ 1 : e < half ? e + half : e - half;
+                a[n] = w ? weight_at(w, p.weight_bf16, e) : 1.f;
+                b[n] = w && e < p.rot ? weight_at(w, p.weight_bf16, pe) : 1.f;
             }
         }
-        float z[8];
 #pragma unroll
-        for (int n = 0; n < 8; ++n) z[n] = r * (e0 + n < p.rot ? fmaf(x[n], cs[n], y[n] * sn[n]) : x[n]);
-        __syncwarp(mates);  // q_out may be q: partners have been read
-        if (live && !is_v) store8<T, VEC>(dst + e0, z);
+        for (int n = 0; n < 8; ++n) a[n] *= cs[n], b[n] *= sn[n];
+        constexpr int N = sizeof(next) / sizeof(next[0]);
+        auto one = [&](int h, Raw<T, VEC> &place) {
+            const Raw<T, VEC> now = place;
+            if (h + N * G < n_heads) place.load(from + (h + N * G) * D);
+            float x[8], y[8], z[8], r = 1.f;
+            now.values(x);
+            if (w) {
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) sum = fmaf(x[n], x[n], sum);
+#pragma unroll
+                for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mates, sum, o, L);
+                r = rsqrtf(sum * (1.f / D) + p.eps);
+            }
+            if constexpr (INTER) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) y[n] = x[n ^ 1];
+            } else if constexpr (VEC) {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) y[n] = __shfl_sync(mates, x[n], mate, L);
+            } else {
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const int e = e0 + n;
+                    y[n] = e < p.rot ? load_f(from - e0 + h * D, e < half ? e + half : e - half) : 0.f;
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                z[n] = x[n] * a[n];
+                if (VEC && !INTER ? turned : e0 + n < p.rot) z[n] = fmaf(y[n], b[n], z[n]);
+                if (w) z[n] *= r;
+            }
+            __syncwarp(mates);  // q_out may be q: partners have been read
+            store8<T, VEC>(to + h * pitch, z);
+        };
+        for (int h = h0; h < n_heads; h += N * G) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (h + i * G < n_heads) one(h + i * G, next[i]);
+        }
+    };
+    if (p.hq) turn(q_from, p.hq, q_next, p.q_weight, static_cast<T *>(p.q_out) + (int64_t)t * p.hq * D + e0, D);
+    turn(k_from, p.hkv, k_next, p.k_weight, static_cast<T *>(p.k_cache) + at + e0, p.head_stride);
+    T *v_to = static_cast<T *>(p.v_cache) + at + e0;
+    for (int h = h0; h < p.hkv; h += G) {
+        const Raw<T, VEC> now = v_next;
+        if (h + G < p.hkv) v_next.load(v_from + (h + G) * D);
+        now.store(v_to + h * p.head_stride);
     }
 }
 
@@ -216,7 +242,7 @@ cudaError_t run_threads(const AppendParams &p, bool vec, bool inter, cudaStream_
     return launch_dependent(kernel, dim3(p.total), kThreads, 0, stream, p);
 }
 
-// One warp a token where there are many: finding a token's place takes as many instructions as five rows, and is done by each warp
+// One warp a token where there are many: a token's place is found, and its factors made, by each warp that has a part of it
 // (16384 tokens of 20 rows of 256: 86 us with four warps).  Few tokens are spread over more threads.
 template <typename T, int D>
 cudaError_t run(const AppendParams &p, bool vec, bool inter, cudaStream_t stream) {

@@ -14,7 +14,7 @@ using attn::launch_dependent;
 constexpr int kThreads = 128, kPieces = 4, kLongest = 1 << 20;  // entries of a path, so that its pieces can be counted in 32 bits
 
 struct CommitParams {
-    int hkv, page_size, n_pages, max_pages, row_pieces, total_path;
+    int hkv, page_size, n_pages, max_pages, row_bits, total_path;
     int64_t page_stride, slot_stride, head_stride;  // in pieces
     void *k, *v;
     const int32_t *table, *lens, *node_offsets, *path_offsets, *path;
@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitParams p) {
                 wrong |= GDN_DEV_BAD_PATH;
                 continue;
             }
-            const int64_t from = ((int64_t)len + at) / p.page_size, to = ((int64_t)len + i) / p.page_size;
+            // (a table has at most 2^30 slots)
+            const int64_t slot = (int64_t)len + at;
+            const int from = slot < 1 << 30 ? (int)slot / p.page_size : p.max_pages, to = from < p.max_pages ? (len + i) / p.page_size : 0;
             if (from >= p.max_pages || table[from] < 0 || table[from] >= p.n_pages || table[to] < 0 || table[to] >= p.n_pages)
                 wrong |= GDN_DEV_BAD_PAGE;
         }
@@ -54,15 +56,15 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitParams p) {
     }
     if (bad) return;
     P *pool = static_cast<P *>(blockIdx.y ? p.v : p.k) + h * p.head_stride;
-    const int pieces = n * p.row_pieces;
+    const int pieces = n << p.row_bits;
     for (int first = 0; first < pieces; first += kPieces * kThreads) {
         P x[kPieces];
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             const int at = first + j * kThreads + tid;
             if (at < pieces) {
-                const int64_t slot = (int64_t)len + p.path[lo + at / p.row_pieces], page = slot / p.page_size;
-                x[j] = pool[table[page] * p.page_stride + (slot - page * p.page_size) * p.slot_stride + at % p.row_pieces];
+                const int slot = len + p.path[lo + (at >> p.row_bits)], page = slot / p.page_size;
+                x[j] = pool[table[page] * p.page_stride + (slot - page * p.page_size) * p.slot_stride + (at & ((1 << p.row_bits) - 1))];
             }
         }
         __syncthreads();
@@ -70,8 +72,8 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitParams p) {
         for (int j = 0; j < kPieces; ++j) {
             const int at = first + j * kThreads + tid;
             if (at < pieces) {
-                const int64_t slot = (int64_t)len + at / p.row_pieces, page = slot / p.page_size;
-                pool[table[page] * p.page_stride + (slot - page * p.page_size) * p.slot_stride + at % p.row_pieces] = x[j];
+                const int slot = len + (at >> p.row_bits), page = slot / p.page_size;
+                pool[table[page] * p.page_stride + (slot - page * p.page_size) * p.slot_stride + (at & ((1 << p.row_bits) - 1))] = x[j];
             }
         }
         __syncthreads();
@@ -88,7 +90,7 @@ cudaError_t launch_kv_commit(const gdn_kv_commit_args &a, cudaStream_t stream) {
                      (c.page_stride | c.slot_stride | c.head_stride) * e % 16 == 0;
     const int piece = vec ? 16 / e : 1;  // entries
     p.hkv = c.n_kv_heads; p.page_size = c.page_size; p.n_pages = c.n_pages; p.max_pages = c.max_pages;
-    p.row_pieces = c.d / piece; p.total_path = a.total_path;
+    p.row_bits = __builtin_ctz((unsigned)(c.d / piece)); p.total_path = a.total_path;
     p.page_stride = c.page_stride / piece; p.slot_stride = c.slot_stride / piece; p.head_stride = c.head_stride / piece;
     p.k = c.k; p.v = c.v; p.table = c.page_table; p.lens = c.lens;
     p.node_offsets = a.node_offsets; p.path_offsets = a.path_offsets; p.path = a.path_idx;

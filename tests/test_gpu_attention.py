@@ -422,6 +422,21 @@ def test_append_then_attend_back_to_back():
         assert torch.equal(o, want[0]) and torch.equal(d, want[1])
 
 
+def test_a_wait_that_runs_out_is_reported_and_changes_nothing():
+    c = Case(46, [700, 90], [20, 40], 8, 2, 128, 16, BF)
+    run = lambda st: gb.gdn_kv_attend(c.q, *c.cache, c.off, 40, scale=c.scale, dev_status=st)  # noqa: E731
+    want = run(None)
+    st = gb.new_status()
+    gb.gdn_test_set_wait_probe(64)
+    try:
+        got = run(st)
+    finally:
+        gb.gdn_test_set_wait_probe(0)
+    assert int(st.item()) == 16 and torch.equal(got, want)
+    st = gb.new_status()
+    assert torch.equal(run(st), want) and int(st.item()) == 0
+
+
 def test_two_streams_at_once():
     cs = [Case(20 + i, [9000, 500], [1, 1], 8, 1, 128, 16, BF) for i in range(2)]
     refs = []
