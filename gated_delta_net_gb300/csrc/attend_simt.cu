@@ -17,7 +17,7 @@ constexpr int kKT = 32, kThreads = 128, kMostWhole = 4, kCost = 1;
 // R: rows of a block
 template <int D, int R>
 struct Shared {
-    float q[R][D + 4], k[kKT][D + 4], v[kKT][D], p[R][kKT], m[R], f[R], l[R];
+    float q[R][D + 4], k[kKT][D + 4], v[kKT][D], p[kKT][R + 4], m[R], f[R], l[R];
     int64_t at[kKT];
     Scratch find;
 };
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
                 const float e = exp2f(y - base), f = exp2f(old - base);
                 const float sum = warp_sum(e);
                 __syncwarp();
-                s.p[row][lane] = e;
+                s.p[lane][row] = e;
                 if (lane == 0) s.m[row] = m, s.f[row] = f, s.l[row] = fmaf(s.l[row], f, sum);
             }
             __syncthreads();
@@ -190,12 +190,22 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
                 float v[kCols];
 #pragma unroll
                 for (int c = 0; c < kCols; ++c) v[c] = s.v[j][(tid + c * kThreads) % D];
+                float e[kMine];
+                if constexpr (kMine % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < kMine; i += 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(&s.p[j][g * kMine + i]);
+                        e[i] = x.x, e[i + 1] = x.y, e[i + 2] = x.z, e[i + 3] = x.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i) e[i] = s.p[j][g * kMine + i];
+                }
 #pragma unroll
                 for (int i = 0; i < kMine; ++i) {
-                    const float e = s.p[g * kMine + i][j];
-                    if (!masked || e != 0.f) {
+                    if (!masked || e[i] != 0.f) {
 #pragma unroll
-                        for (int c = 0; c < kCols; ++c) acc[i][c] = fmaf(e, v[c], acc[i][c]);
+                        for (int c = 0; c < kCols; ++c) acc[i][c] = fmaf(e[i], v[c], acc[i][c]);
                     }
                 }
             }
@@ -256,10 +266,11 @@ cudaError_t (*pick(int d))(Params, int, cudaStream_t) {
 
 attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     const gdn_kv_cache &c = a.cache;
-    // fp32 rows on 16 bytes: four rows a block where a request has no more (16 would compute four times what one head needs: 6 single
+    // fp32 rows on 16 bytes: four (or eight) rows a block where a request has no more (16 would compute four times what one head needs: 6 single
     // tokens over 100..23617 slots, 8 heads of 128, 373 us)
     const bool vec = c.dtype == GDN_F32 && aligned16(a), few = vec && (decode ? 1 : (int64_t)a.max_tokens) * (a.n_q_heads / c.n_kv_heads) <= 4;
-    const int R = few ? 4 : 16;
+    const bool some = vec && !few && (decode ? 1 : (int64_t)a.max_tokens) * (a.n_q_heads / c.n_kv_heads) <= 8;
+    const int R = few ? 4 : some ? 8 : 16;
     Choice x;
     x.whole = whole_items(a, decode, R, kKT, kMostWhole, x.runs);
     if (!x.whole) x.runs = most_runs(a, decode, R, kKT, c.d == 256 ? 2 : 3);  // (what their registers leave room for)
@@ -267,6 +278,7 @@ attn::Choice attend_simt_choice(const gdn_kv_attend_args &a, bool decode) {
     // (bf16 rows on 16 bytes are the tensor cores')
     x.launch = c.dtype == GDN_BF16 ? pick<__nv_bfloat16, false, 16>(c.d)
                : few               ? pick<float, true, 4>(c.d)
+               : some              ? pick<float, true, 8>(c.d)
                : vec               ? pick<float, true, 16>(c.d)
                                    : pick<float, false, 16>(c.d);
     return x;
