@@ -7,6 +7,8 @@
 // empty, and what they cost here is a tenth of the time the bytes take.  The ring runs ahead over the ends of items,
 // with the page of the tile after the next looked up one tile earlier.  At an item's end the warps' parts are joined in
 // shared memory.
+// 128 single tokens over 10 to 6000 slots, 32 heads of 128 to 8: 234 us for 1.47 GB, 6.3 TB/s; one over 131072, 4 heads: 54 us for
+// 268 MB, of which 40 are the bytes, the rest the start (finding the work, the first loads) and the join.
 // Probabilities are rounded to bf16 for their product with the values (2^-8 of each; their sum is kept of the unrounded ones).
 // A new token's value that is not finite is replaced by zeros and makes the sums of the rows that see it NaN: a
 // probability of zero times it would reach the others.
@@ -19,6 +21,8 @@ namespace {
 using namespace attn;
 using sm100::smem_u32;
 
+// kMostWhole: a request's tiles up to which its items are not cut (700 slots, 8 heads: 16 us so, 26 cut and joined, of which the second
+// launch is the most).  kCost: what an item costs besides its tiles (128 tokens over 10 to 6000 slots with 1, 2, 3, 4: 241, 229, 230, 231 us).
 constexpr int kR = 16, kWarps = 4, kThreads = kWarps * 32, kKeys = 16, kKT = kWarps * kKeys, kMostWhole = 16, kCost = 2;
 
 template <int D>
