@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 640 / kThreads : 1) append_ker
         if (upto >= p.batch) return;
         b = upto;
         i = t - p.offsets[b];
-        if (i < 0 || p.offsets[b] < 0 || p.offsets[b + 1] > p.total) return;
+        if (i < 0 || p.offsets[b] < 0 || p.offsets[b + 1] > p.total || t >= p.offsets[b + 1]) return;
     }
     const int len = p.lens[b];
     if (len == -1) return;

@@ -44,8 +44,9 @@ __global__ void __launch_bounds__(kThreads) commit_kernel(CommitParams p) {
             }
             // (a table has at most 2^30 slots)
             const int64_t slot = (int64_t)len + at;
-            const int from = slot < 1 << 30 ? (int)slot / p.page_size : p.max_pages, to = from < p.max_pages ? (len + i) / p.page_size : 0;
-            if (from >= p.max_pages || table[from] < 0 || table[from] >= p.n_pages || table[to] < 0 || table[to] >= p.n_pages)
+            const int from = slot < 1 << 30 ? (int)slot / p.page_size : p.max_pages;
+            const int to = from < p.max_pages ? (len + i) / p.page_size : 0;  // past the table where the path does not ascend
+            if (from >= p.max_pages || to >= p.max_pages || table[from] < 0 || table[from] >= p.n_pages || table[to] < 0 || table[to] >= p.n_pages)
                 wrong |= GDN_DEV_BAD_PAGE;
         }
         if (__syncthreads_or(wrong & GDN_DEV_BAD_PATH)) bad |= GDN_DEV_BAD_PATH;

@@ -610,6 +610,8 @@ def test_commit_device_checks():
     assert run(path=((2, 2), (1, 4))) == (2, [10, 32], [0, 2])
     assert run(path=((3, 1), (1, 4))) == (2, [10, 32], [0, 2])
     assert run(path=((-1, 1), (1, 4))) == (2, [10, 32], [0, 2])
+    # (a path that does not ascend, at the end of the table: its targets lie past it)
+    assert run(path=((5, 0, 1, 2, 3, 4), (1, 4)), lens=(59, 30), no=(0, 6, 12))[:2] == (258, [59, 32])
     assert run(table={(1, 2): 99}) == (256, [13, 30], [2, 0])
     assert run(lens=(10, 500)) == (256, [13, 500], [2, 0])
     assert run(lens=(10, -3)) == (256, [13, -3], [2, 0])
