@@ -303,89 +303,126 @@ __device__ __forceinline__ void store4(const Params &p, int64_t at, float4 x) {
 }
 
 // Joins the parts of the item that is cut first at the start of run blockIdx.x + 1: with the parts' maxima m_c, sums l_c
-// and unscaled outputs o_c, o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.  A warp has a row; where there are many parts (one
-// long cache has them by the dozen) a block's warps have one together, and every fourth part each.
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+// and unscaled outputs o_c, o = sum_c 2^(m_c - m) o_c / sum_c 2^(m_c - m) l_c.  What it takes is the latency of its loads: a warp has
+// two rows at once; where there are many parts (one long cache has them by the dozen) a block's warps have one row together, and
+// every eighth part each.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinRows = 2, kJoinFew = 8;
+
+// V consecutive entries of a lane, N times 128 apart
+template <int V, int N>
+__device__ __forceinline__ void add_part(const float *x, float f, float (&o)[N][V]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if constexpr (V == 4) {
+            const float4 y = *reinterpret_cast<const float4 *>(x + n * 128);
+            o[n][0] = fmaf(f, y.x, o[n][0]), o[n][1] = fmaf(f, y.y, o[n][1]), o[n][2] = fmaf(f, y.z, o[n][2]), o[n][3] = fmaf(f, y.w, o[n][3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) o[n][k] = fmaf(f, x[k], o[n][k]);
+        }
+    }
+}
+template <int D, int V, int N>
+__device__ __forceinline__ void put_row(const Params &p, const Cut &cut, int row, int lane, float l, const float (&o)[N][V]) {
+    // nothing seen: zeros; a NaN sum stays one
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int q = cut.row + row, token = cut.first + q / p.group, head = cut.head * p.group + q % p.group;
+    const int64_t to = ((int64_t)token * p.hkv * p.group + head) * D + lane * V;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if constexpr (V == 4) {
+            store4(p, to + n * 128, make_float4(o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv));
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to + k, o[n][k] * inv);
+                else store_f(static_cast<float *>(p.o), to + k, o[n][k] * inv);
+            }
+        }
+    }
+}
 
 template <int D, int CAP>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Params p, int runs) {
     after_previous();
-    constexpr int V = D >= 128 ? 4 : D / 32 ? D / 32 : 1, N = D > 128 ? D / 128 : 1;  // consecutive entries of a lane, and how often
+    constexpr int V = D >= 128 ? 4 : D / 32 ? D / 32 : 1, N = D > 128 ? D / 128 : 1;
     __shared__ float sums[kJoinWarps][D];
     const int run = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cut cut = *cut_of(p, CAP, D, runs, run);
     const int parts = cut.last - run + 2;
-    const bool together = parts > kJoinWarps;
-    const float *stat = part_stat(p, CAP, D, runs, run, 0) - 2 * CAP * 2, *out = part_out(p, CAP, D, run, 0) - 2 * CAP * D;
+    const float *stat = part_stat(p, CAP, D, runs, run, 0) - 2 * CAP * 2, *out = part_out(p, CAP, D, run, 0) - 2 * CAP * D + lane * V;
     // part 0 is the second of the run before, the others the first of theirs
-    auto which = [&](int c) { return c * 2 + (c == 0); };
+    auto which = [&](int c) { return (int64_t)(c * 2 + (c == 0)) * CAP; };
+    const bool mine = lane * V < D;
+    if (parts <= kJoinFew) {
 #pragma unroll 1
-    for (int row = together ? blockIdx.y : blockIdx.y * kJoinWarps + warp; row < cut.rows; row += gridDim.y * (together ? 1 : kJoinWarps)) {
-        float m = -INFINITY, l = 0.f;
-        for (int c = lane; c < parts; c += 32) m = fmaxf(m, stat[(int64_t)which(c) * CAP * 2 + row * 2]);
+        for (int row = (blockIdx.y * kJoinWarps + warp) * kJoinRows; row < cut.rows; row += gridDim.y * kJoinWarps * kJoinRows) {
+            float m[kJoinRows], l[kJoinRows] = {}, o[kJoinRows][N][V] = {};
+            float2 st[kJoinFew][kJoinRows];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float base = m == -INFINITY ? 0.f : m;
+            for (int c = 0; c < kJoinFew; ++c)
+#pragma unroll
+                for (int i = 0; i < kJoinRows; ++i)
+                    st[c][i] = c < parts && row + i < cut.rows ? *reinterpret_cast<const float2 *>(stat + (which(c) + row + i) * 2) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < kJoinRows; ++i) {
+                m[i] = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kJoinFew; ++c) m[i] = fmaxf(m[i], st[c][i].x);
+                if (m[i] == -INFINITY) m[i] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < kJoinFew; ++c) {
+                if (c < parts) {
+#pragma unroll
+                    for (int i = 0; i < kJoinRows; ++i) {
+                        const float f = exp2_fast(st[c][i].x - m[i]);
+                        l[i] = fmaf(f, st[c][i].y, l[i]);
+                        if (mine && row + i < cut.rows) add_part<V, N>(out + (which(c) + row + i) * D, f, o[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinRows; ++i)
+                if (mine && row + i < cut.rows) put_row<D, V, N>(p, cut, row + i, lane, l[i], o[i]);
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int row = blockIdx.y; row < cut.rows; row += gridDim.y) {
+        float m = -INFINITY, l = 0.f, o[N][V] = {};
+        for (int c = lane; c < parts; c += 32) m = fmaxf(m, stat[(which(c) + row) * 2]);
+#pragma unroll
+        for (int w = 16; w > 0; w >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+        if (m == -INFINITY) m = 0.f;
         for (int c = lane; c < parts; c += 32) {
-            const float2 st = *reinterpret_cast<const float2 *>(stat + (int64_t)which(c) * CAP * 2 + row * 2);
-            l = fmaf(exp2_fast(st.x - base), st.y, l);
+            const float2 st = *reinterpret_cast<const float2 *>(stat + (which(c) + row) * 2);
+            l = fmaf(exp2_fast(st.x - m), st.y, l);
         }
         l = warp_sum(l);
-        float o[N][V] = {};
-        if (lane * V < D) {
-#pragma unroll 4
-            for (int c = together ? warp : 0; c < parts; c += together ? kJoinWarps : 1) {
-                const float f = exp2_fast(stat[(int64_t)which(c) * CAP * 2 + row * 2] - base);
-                const float *x = out + ((int64_t)which(c) * CAP + row) * D + lane * V;
+        if (mine) {
+#pragma unroll 8
+            for (int c = warp; c < parts; c += kJoinWarps) add_part<V, N>(out + (which(c) + row) * D, exp2_fast(stat[(which(c) + row) * 2] - m), o);
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    if constexpr (V == 4) {
-                        const float4 y = *reinterpret_cast<const float4 *>(x + n * 128);
-                        o[n][0] = fmaf(f, y.x, o[n][0]), o[n][1] = fmaf(f, y.y, o[n][1]), o[n][2] = fmaf(f, y.z, o[n][2]), o[n][3] = fmaf(f, y.w, o[n][3]);
-                    } else {
+            for (int n = 0; n < N; ++n)
 #pragma unroll
-                        for (int k = 0; k < V; ++k) o[n][k] = fmaf(f, x[k], o[n][k]);
-                    }
+                for (int k = 0; k < V; ++k) sums[warp][n * 128 + lane * V + k] = o[n][k];
+        }
+        __syncthreads();
+        if (warp == 0 && mine) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const int col = n * 128 + lane * V + k;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kJoinWarps; ++w) sum += sums[w][col];
+                    o[n][k] = sum;
                 }
-            }
+            put_row<D, V, N>(p, cut, row, lane, l, o);
         }
-        if (together) {
-            if (lane * V < D) {
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) sums[warp][n * 128 + lane * V + k] = o[n][k];
-            }
-            __syncthreads();
-            if (warp == 0 && lane * V < D) {
-#pragma unroll
-                for (int n = 0; n < N; ++n)
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        const int col = n * 128 + lane * V + k;
-                        o[n][k] = (sums[0][col] + sums[1][col]) + (sums[2][col] + sums[3][col]);
-                    }
-            }
-            __syncthreads();
-        }
-        if (lane * V < D && (warp == 0 || !together)) {
-            // nothing seen: zeros; a NaN sum stays one
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int q = cut.row + row, token = cut.first + q / p.group, head = cut.head * p.group + q % p.group;
-            const int64_t to = ((int64_t)token * p.hkv * p.group + head) * D + lane * V;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                if constexpr (V == 4) {
-                    store4(p, to + n * 128, make_float4(o[n][0] * inv, o[n][1] * inv, o[n][2] * inv, o[n][3] * inv));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to + k, o[n][k] * inv);
-                        else store_f(static_cast<float *>(p.o), to + k, o[n][k] * inv);
-                    }
-                }
-            }
-        }
+        __syncthreads();
     }
 }
 
