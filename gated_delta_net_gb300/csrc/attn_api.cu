@@ -100,7 +100,8 @@ int attend(const gdn_kv_attend_args *a, bool decode, void *stream) {
     p.page_stride = c.page_stride; p.slot_stride = c.slot_stride; p.head_stride = c.head_stride;
     p.q_stride = a->q_stride ? a->q_stride : (int64_t)a->n_q_heads * c.d;
     p.scale_log2 = a->scale * gdn::attn::kLog2e;
-    p.k = c.k; p.v = c.v; p.q = a->q; p.table = c.page_table; p.lens = c.lens;
+    // (a pool without pages is not read, but an address of its own spares the kernels a case)
+    p.k = c.n_pages > 0 ? c.k : a->q; p.v = c.n_pages > 0 ? c.v : a->q; p.q = a->q; p.table = c.page_table; p.lens = c.lens;
     p.offsets = decode ? nullptr : a->token_offsets;
     p.mask = decode ? nullptr : a->anc_mask;
     p.mask_words = a->mask_words;
