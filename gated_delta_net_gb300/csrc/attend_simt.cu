@@ -24,23 +24,14 @@ struct Shared {
     Scratch find;
 };
 
-// `row`, D entries from element `at` of x, as fp32; zeros where at < 0
+// Rows of D entries from elements `at` of x, as fp32 (VEC: that is what they are); zeros where at < 0.
 template <typename T, int D, bool VEC>
 __device__ __forceinline__ void load_rows(const void *x, const int64_t *at, int rows, float *to, int ld) {
     const T *src = static_cast<const T *>(x);
     if constexpr (VEC) {
         for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
             const int row = i / (D / 4), c = i % (D / 4) * 4;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (at[row] >= 0) {
-                if constexpr (sizeof(T) == 4) {
-                    y = *reinterpret_cast<const float4 *>(src + at[row] + c);
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + at[row] + c);
-                    y = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                                    __uint_as_float(w.y & 0xFFFF0000u));
-                }
-            }
+            const float4 y = at[row] >= 0 ? *reinterpret_cast<const float4 *>(src + at[row] + c) : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4 *>(to + row * ld + c) = y;
         }
     } else {
@@ -51,42 +42,20 @@ __device__ __forceinline__ void load_rows(const void *x, const int64_t *at, int 
     }
 }
 
-// four entries as they lie in memory
-template <typename T>
-struct Four {
-    uint32_t w[sizeof(T)];
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (sizeof(T) == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(p);
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-        } else {
-            const uint2 x = *reinterpret_cast<const uint2 *>(p);
-            w[0] = x.x, w[1] = x.y;
-        }
-    }
-    __device__ __forceinline__ float4 values() const {
-        if constexpr (sizeof(T) == 4)
-            return make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]));
-        else
-            return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
-                               __uint_as_float(w[1] & 0xFFFF0000u));
-    }
-};
-
-// A thread's share of a tile's keys and values, on its way while the tile before it is worked on.
-template <typename T, int D>
+// A thread's share of a tile's keys and values in fp32, on its way while the tile before it is worked on.
+template <int D>
 struct Ahead {
     static constexpr int N = kKT * (D / 4) / kThreads;
-    Four<T> k[N], v[N];
+    float4 k[N], v[N];
     __device__ __forceinline__ void load(const Params &p, const Place &at, int slot0, int seen) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int n = i * kThreads + threadIdx.x, slot = slot0 + n / (D / 4);
             const int64_t off = slot < seen ? slot_offset(p, at.b, at.h, slot) : -1;
-            k[i] = v[i] = Four<T>{};
+            k[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (off >= 0) {
-                k[i].load(static_cast<const T *>(p.k) + off + n % (D / 4) * 4);
-                v[i].load(static_cast<const T *>(p.v) + off + n % (D / 4) * 4);
+                k[i] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + off + n % (D / 4) * 4);
+                v[i] = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.v) + off + n % (D / 4) * 4);
             }
         }
     }
@@ -94,8 +63,8 @@ struct Ahead {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int n = i * kThreads + threadIdx.x, row = n / (D / 4), c = n % (D / 4) * 4;
-            *reinterpret_cast<float4 *>(k_to + row * k_ld + c) = k[i].values();
-            *reinterpret_cast<float4 *>(v_to + row * v_ld + c) = v[i].values();
+            *reinterpret_cast<float4 *>(k_to + row * k_ld + c) = k[i];
+            *reinterpret_cast<float4 *>(v_to + row * v_ld + c) = v[i];
         }
     }
 };
@@ -132,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
         __syncthreads();
         load_rows<T, D, VEC>(p.q, s.at, R, &s.q[0][0], D + 4);
         float acc[kMine][kCols] = {};
-        Ahead<T, D> ahead;
+        Ahead<D> ahead;
         if constexpr (VEC) ahead.load(p, at, first * kKT, seen);
         for (int tile = first; tile < last; ++tile) {
             const int slot0 = tile * kKT;

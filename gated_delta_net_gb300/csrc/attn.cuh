@@ -18,7 +18,7 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
-    int batch, hkv, group, page_size, n_pages, max_pages, total, max_tokens, mask_words, min_tiles;
+    int batch, hkv, group, page_size, n_pages, max_pages, total, max_tokens, mask_words;
     int rows, cost;                         // R: rows of an item; what an item costs besides its tiles, in tiles
     int64_t page_stride, slot_stride, head_stride, q_stride;
     float scale_log2;
@@ -146,7 +146,7 @@ static __device__ __noinline__ void find(const Params &p, int runs, int run, int
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) mine += p.hkv * head_tiles<KT>(p, request(p, b, status));
     const int64_t before = scan(mine, s, total);
-    per = max(div_up(total, runs), (int64_t)p.min_tiles);
+    per = div_up(total, runs);
     begin = min(total, per * run);
     end = min(total, begin + per);
     if (begin >= end) return;

@@ -96,7 +96,7 @@ int attend(const gdn_kv_attend_args *a, bool decode, void *stream) {
     p.batch = c.batch; p.hkv = c.n_kv_heads; p.group = a->n_q_heads / c.n_kv_heads;
     p.page_size = c.page_size; p.n_pages = c.n_pages; p.max_pages = c.max_pages;
     p.page_bits = (c.page_size & (c.page_size - 1)) ? -1 : __builtin_ctz((unsigned)c.page_size);
-    p.total = a->total_tokens; p.max_tokens = decode ? 1 : a->max_tokens; p.min_tiles = 1;
+    p.total = a->total_tokens; p.max_tokens = decode ? 1 : a->max_tokens;
     p.page_stride = c.page_stride; p.slot_stride = c.slot_stride; p.head_stride = c.head_stride;
     p.q_stride = a->q_stride ? a->q_stride : (int64_t)a->n_q_heads * c.d;
     p.scale_log2 = a->scale * gdn::attn::kLog2e;
