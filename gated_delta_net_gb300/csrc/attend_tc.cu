@@ -335,13 +335,15 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
                         tmem_st8(s_at + i * 16 + h * 8, packed);
                     }
                     if (i == N / 2 - 1 || i == N - 1) {
+                        // before the last hand-over, behind which nothing keeps the barrier from a phase more
+                        if (masked && i == N - 1) warp_wait(&bar[S::READY + c % S::VS], (c / S::VS) & 1, ok);
                         tmem_wait_st();
                         tc_fence_before();
                         mbar_arrive(&bar[S::PROBS + buf * 2 + (i == N - 1)]);
                     }
                 }
                 if (masked) {
-                    if (!warp_wait(&bar[S::READY + c % S::VS], (c / S::VS) & 1, ok)) break;
+                    if (!ok) break;
                     const uint32_t *sp = reinterpret_cast<const uint32_t *>(sm + S::OFF_SPOILT) + c % (2 * S::VS) * S::kSpoilt;
                     uint32_t hit = 0;
 #pragma unroll 1
