@@ -13,8 +13,8 @@ int done(cudaError_t e, const char *what) {
 
 bool valid_dtype(int t) { return t == GDN_F32 || t == GDN_BF16; }
 
-// Limits that keep slots, rows and grids within 32 bits: 2^30 slots a request, 2^30 rows of query heads a call, 2^30
-// (request, head)s.
+// Limits that keep slots, rows, grids and places within a token's row within 32 bits: 2^30 slots a request, 2^30 rows of
+// query heads a call, 2^30 (request, head)s, 2^31 - 1 entries of a token's heads.
 constexpr int64_t kMost = 1 << 30;
 
 int check_cache(const gdn_kv_cache &c) {
@@ -51,11 +51,17 @@ int check_heads(int hq, int hkv) {
     return GDN_OK;
 }
 
+int check_row(const char *name, int heads, int d) {
+    if ((int64_t)heads * d > INT32_MAX) return fail(GDN_ERR_UNSUPPORTED, "%s %d of %d entries: a token's row has 2^31 or more", name, heads, d);
+    return GDN_OK;
+}
+
 int check_attend(const gdn_kv_attend_args *a, bool decode) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "args is NULL");
     const gdn_kv_cache &c = a->cache;
     if (int st = check_cache(c)) return st;
     if (int st = check_heads(a->n_q_heads, c.n_kv_heads)) return st;
+    if (int st = check_row("n_q_heads", a->n_q_heads, c.d)) return st;
     if (!valid_dtype(a->out_dtype)) return fail(GDN_ERR_UNSUPPORTED, "unknown dtype (out %d)", a->out_dtype);
     if (a->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "total_tokens %d < 0", a->total_tokens);
     if (decode && a->total_tokens != c.batch)
@@ -122,9 +128,11 @@ int gdn_kv_append(const gdn_kv_append_args *a, void *stream) {
     if (a->total_tokens < 0) return fail(GDN_ERR_INVALID_ARG, "total_tokens %d < 0", a->total_tokens);
     if (a->q) {
         if (int st = check_heads(a->n_q_heads, c.n_kv_heads)) return st;
+        if (int st = check_row("n_q_heads", a->n_q_heads, c.d)) return st;
         if ((int64_t)a->total_tokens * a->n_q_heads > kMost) return fail(GDN_ERR_UNSUPPORTED, "more than 2^30 rows of query heads in a call");
         if (int st = check_stride("q", a->q_stride, (int64_t)a->n_q_heads * c.d)) return st;
     }
+    if (int st = check_row("n_kv_heads", c.n_kv_heads, c.d)) return st;
     if (a->rot_dim < 0 || a->rot_dim > c.d || a->rot_dim % 2)
         return fail(GDN_ERR_INVALID_ARG, "rot_dim %d: must be even, at most d=%d", a->rot_dim, c.d);
     if (a->n_positions < 0) return fail(GDN_ERR_INVALID_ARG, "n_positions %d < 0", a->n_positions);

@@ -25,7 +25,8 @@
  *   - Query head h reads key-value head h / (n_q_heads / n_kv_heads).
  *   - A page outside the pool, or a slot past the table, sets GDN_DEV_BAD_PAGE.
  *   - Supported: d in {16, 32, 64, 128, 256}, n_q_heads a multiple of n_kv_heads, page sizes
- *     from 1 on, tokens and cache in fp32 or bf16 (alike).  Sums and softmax statistics are fp32.
+ *     from 1 on, tokens and cache in fp32 or bf16 (alike), heads of a token up to 2^31 - 1 entries
+ *     together.  Sums and softmax statistics are fp32.
  */
 #ifndef GDN_ATTENTION_H_
 #define GDN_ATTENTION_H_
