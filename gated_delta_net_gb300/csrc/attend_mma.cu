@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
             bool poisoned[2] = {false, false};
             if (slot0 + kKeys > common) {
                 uint32_t spoilt = 0;  // new tokens' values that are not finite
-                if (r.n > 1 && slot0 < seen) {
+                if ((r.n > 1 || p.mask) && slot0 < seen) {  // (a single token sees itself, unless a mask leaves it out)
                     const int row = lane & 15;
                     bool finite = true;
                     for (int c = lane >> 4; c < C; c += 2) {

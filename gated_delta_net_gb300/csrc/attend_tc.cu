@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
                     for (int i = 0; i < KT / 32; ++i) {
                         const int row = i * 32 + lane, s = slot0 + row;
                         bool bad = false;
-                        if (w.tokens > 1 && s >= w.len && s < w.seen) {
+                        if ((w.tokens > 1 || w.mask) && s >= w.len && s < w.seen) {  // (a single token sees itself, unless a mask leaves it out)
                             uint32_t over = 0;  // bf16 entries with all exponent bits set carry into their sign bit
 #pragma unroll 8
                             for (int k = 0; k < S::H * 8; ++k) {
