@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) attend_mma_kernel(Params p, int runs
                 y.x = fmaf(e, x.x, y.x), y.y = fmaf(e, x.y, y.y), y.z = fmaf(e, x.z, y.z), y.w = fmaf(e, x.w, y.w);
             }
             if (whole) {
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+                const float inv = inverse(p, r, n / p.group, ll);
                 const int64_t to = ((int64_t)(r.first + n / p.group) * p.hkv * p.group + at.h * p.group + n % p.group) * D + col;
                 store4(p, to, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
             } else {

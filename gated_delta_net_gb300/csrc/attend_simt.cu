@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) attend_simt_kernel(Params p, int run
             for (int c = 0; c < kCols; ++c) {
                 const int col = (tid + c * kThreads) % D;
                 if (whole) {
-                    const float y = s.l[row] == 0.f ? 0.f : acc[i][c] / s.l[row];
+                    const float y = s.l[row] == 0.f ? inverse(p, r, (int)(q / p.group), 0.f) : acc[i][c] / s.l[row];
                     const int64_t to = ((int64_t)(r.first + q / p.group) * p.hkv * p.group + at.h * p.group + q % p.group) * D + col;
                     if (p.out_bf16) store_f(static_cast<__nv_bfloat16 *>(p.o), to, y);
                     else store_f(static_cast<float *>(p.o), to, y);

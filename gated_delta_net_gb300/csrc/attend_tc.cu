@@ -360,7 +360,9 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
             tc_fence_after();
             const float2 ll = parts(l2);
             const float l = ll.x + ll.y;
-            const float inv = w.stat ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            float inv = w.stat ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            // (scores that are all -infinity)
+            if (l == 0.f && !w.stat && live && sees_any(w.len, w.tokens, w.mask ? w.mask + (int64_t)token * w.mask_words : nullptr)) inv = __int_as_float(0x7fc00000);
             if (w.stat && live) w.stat[own_row] = make_float2(m * sc, l);
             // 64 columns at a time to shared memory, from where another warp sends them as TMA boxes.  (Stores by these warps
             // keep the memory pipe, and what stands behind it in the block, for 4000 cycles an item, whole rows or 16 bytes a

@@ -245,6 +245,21 @@ __device__ __forceinline__ bool sees(const Params &p, const Request &r, int i, i
     return p.mask ? (p.mask[(int64_t)(r.first + i) * p.mask_words + (j >> 5)] >> (j & 31)) & 1 : j <= i;
 }
 
+// Whether a new token sees any slot (row: its words of the mask, NULL: causal).  Only then is a row whose sum is zero one whose
+// scores are all -infinity: their softmax is NaN, where nothing is seen outputs are zeros.
+__device__ __forceinline__ bool sees_any(int len, int n, const uint32_t *row) {
+    if (len != 0 || !row) return len >= 0;
+#pragma unroll 1
+    for (int j = 0; j < n; j += 32)
+        if (row[j >> 5] & (n - j < 32 ? (1u << (n - j)) - 1 : 0xffffffffu)) return true;
+    return false;
+}
+// the factor of token i's outputs, whose sum is l
+__device__ __forceinline__ float inverse(const Params &p, const Request &r, int i, float l) {
+    if (l != 0.f) return 1.f / l;
+    return sees_any(r.len, r.n, p.mask ? p.mask + (int64_t)(r.first + i) * p.mask_words : nullptr) ? __int_as_float(0x7fc00000) : 0.f;
+}
+
 __device__ __forceinline__ float *part_out(const Params &p, int cap, int d, int run, int which) {
     return p.ws + ((int64_t)run * 2 + which) * cap * d;
 }
@@ -267,7 +282,8 @@ __device__ __forceinline__ void item_of(const Params &p, int run, int tiles_of_r
 struct Cut {
     int rows, last;    // the item's rows, and the last run that has a part of it
     int row, first, head;  // its first row in the request, the request's first token, the key-value head
-    int pad[3];
+    int request;
+    int pad[2];
 };
 __device__ __forceinline__ Cut *cut_of(const Params &p, int cap, int d, int runs, int run) {
     return reinterpret_cast<Cut *>(p.ws + (int64_t)runs * 2 * cap * (d + 2)) + run;
@@ -279,7 +295,7 @@ __device__ __forceinline__ void tell_cut(const Params &p, int cap, int d, int ru
         const Request r = request(p, at.b, nullptr);
         c.rows = min(p.rows, r.n * p.group - at.qt * p.rows);
         c.last = (int)(div_up(begin - at.off + p.cost + item_tiles<KT>(p, r, at.qt), per) - 1);
-        c.row = at.qt * p.rows, c.first = r.first, c.head = at.h;
+        c.row = at.qt * p.rows, c.first = r.first, c.head = at.h, c.request = at.b;
     }
     *cut_of(p, cap, d, runs, run) = c;
 }
@@ -324,9 +340,9 @@ __device__ __forceinline__ void add_part(const float *x, float f, float (&o)[N][
 }
 template <int D, int V, int N>
 __device__ __forceinline__ void put_row(const Params &p, const Cut &cut, int row, int lane, float l, const float (&o)[N][V]) {
-    // nothing seen: zeros; a NaN sum stays one
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int q = cut.row + row, token = cut.first + q / p.group, head = cut.head * p.group + q % p.group;
+    const int q = cut.row + row;
+    const float inv = l != 0.f ? 1.f / l : inverse(p, request(p, cut.request, nullptr), q / p.group, l);
+    const int token = cut.first + q / p.group, head = cut.head * p.group + q % p.group;
     const int64_t to = ((int64_t)token * p.hkv * p.group + head) * D + lane * V;
 #pragma unroll
     for (int n = 0; n < N; ++n) {

@@ -2,12 +2,13 @@
 
 Cases and tolerances are those of test_gpu_attention; what has to be zero, NaN or unchanged is so exactly.
 """
+import numpy as np
 import pytest
 import torch
 
 from gated_delta_net_gb300 import binding as gb
 from oracle import attention as OA
-from tests.test_gpu_attention import BF, F32, Case, tree_masks
+from tests.test_gpu_attention import BF, F32, Case, close, f64, tree_masks
 
 pytestmark = pytest.mark.gpu
 NAN, INF = float("nan"), float("inf")
@@ -48,3 +49,58 @@ def test_a_single_token_that_does_not_see_itself(hq, hkv, d, other, length, wher
     assert torch.isfinite(outs[0]).all() and (length > 0 or not torch.any(outs[0][0]))
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+def definition(c, mask=None, decode=False):
+    """The definition with what is infinite (slots that hold nothing are not seen)."""
+    k, v = (np.nan_to_num(f64(x), nan=0.0, posinf=np.inf, neginf=-np.inf) for x in (c.k, c.v))
+    a = (c.table.cpu().numpy(), c.lens_list, None if decode else c.off.cpu().numpy(), None if mask is None else mask.cpu().numpy(), c.scale)
+    with np.errstate(invalid="ignore"):
+        return OA.attend(f64(c.q), k, v, *a), OA.attend(f64(c.q), k, np.abs(v), *a)
+
+
+def same_but_where_nan(got, ref, A, dtype):
+    bad = np.isnan(ref)
+    assert np.array_equal(np.isnan(f64(got)), bad)
+    close(torch.where(torch.from_numpy(bad).cuda(), torch.zeros_like(got), got), np.where(bad, 0.0, ref), np.where(bad, 0.0, A), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("hq,hkv,d,lens,counts", [(8, 2, 128, [0, 9], [1, 2]), (8, 2, 128, [0, 9], [40, 3]), (8, 2, 64, [0, 0], [130, 2]), (4, 1, 256, [0, 30], [70, 1]),
+                                                  (4, 1, 32, [0, 3], [20, 4])])
+def test_an_infinite_entry_of_the_first_key(hq, hkv, d, lens, counts, value, dtype):
+    # its scores are infinite, of either sign: the first token sees nothing else, the softmax is NaN; the later tokens' heads
+    # with a negative one give it no weight
+    c = Case(61, lens, counts, hq, hkv, d, 16, dtype)
+    for b in range(2):
+        c.k[int(c.table[b, 0]), 0, :, 5] = value
+    for mask in (None, tree_masks(2, counts)):
+        ref, A = definition(c, mask)
+        assert np.isnan(ref[0]).all() and (counts[0] < 20 or np.isfinite(ref[19]).any())
+        same_but_where_nan(attend(c, mask), ref, A, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hkv,d,lens,counts", [(8, 2, 128, [20, 0], [3, 4]), (8, 1, 128, [0, 700], [200, 60]), (4, 1, 64, [0, 40], [300, 2]), (4, 1, 256, [0, 3000], [130, 60]),
+                                                  (8, 2, 128, [3000, 0], [2, 2])])
+def test_infinite_scores_in_every_slot(hq, hkv, d, lens, counts, dtype):
+    # NaN for the tokens that see a slot, zeros for those that see none, in items that are cut and joined too
+    c = Case(62, lens, counts, hq, hkv, d, 16, dtype)
+    c.k[..., 5] = -INF
+    empty = [sum(counts[:b]) + i for b in range(2) for i in {0, counts[b] // 2, counts[b] - 1}]
+    mask = tree_masks(3, counts, empty=empty)
+    for m in (None, mask):
+        ref, A = definition(c, m)
+        assert np.isnan(ref).any() and (m is None) == np.isnan(ref).all()
+        same_but_where_nan(attend(c, m), ref, A, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 128), (4, 1, 16), (4, 2, 256)])
+def test_decode_of_infinite_scores(hq, hkv, d, dtype):
+    c = Case(63, [0, 40, -1, 5000], [1] * 4, hq, hkv, d, 16, dtype)
+    c.k[..., 5] = INF
+    ref, A = definition(c, decode=True)
+    same_but_where_nan(gb.gdn_kv_decode(c.q, *c.cache, scale=c.scale), ref, A, dtype)
+    assert np.isnan(ref[[0, 1, 3]]).all() and not ref[2].any()
