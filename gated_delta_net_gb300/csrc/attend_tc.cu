@@ -44,6 +44,10 @@ using tiles::pack_bf16;
 constexpr int kTileRows = 128;
 constexpr float kGrow = 8.f;  // log2 of what a probability may grow to before the maximum moves
 
+// stands for the length of a row that is not in use: slots lie 2^30 tokens behind it, where neither causally (a request has at most
+// 2^30) nor by the mask (2^25) a token sees them
+constexpr int kNotInUse = -(1 << 30);
+
 // An item, or the part of it that is this block's, as the other roles see it: with all that they need at its end, for reading
 // the kernel's parameters there, out of a cache that nobody else keeps them in, takes over a thousand cycles.
 struct __align__(16) Job {
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
                     const bool whole = v.last - v.first == v.tiles;
                     const int token = v.at.qt * U * tp.tile_tokens, e = whole && p.out_bf16 ? 2 : 4;
                     j.n = v.last - v.first, j.tile = v.first, j.seen = v.seen, j.common = v.common;
-                    j.len = v.r.len, j.tokens = v.r.n, j.token = token, j.first = v.r.first, j.head = v.at.h;
+                    j.len = v.r.len < 0 ? kNotInUse : v.r.len, j.tokens = v.r.n, j.token = token, j.first = v.r.first, j.head = v.at.h;
                     j.mask_words = p.mask_words;
                     j.mask = p.mask ? p.mask + (int64_t)v.r.first * p.mask_words : nullptr;
                     j.bf16 = e == 2;

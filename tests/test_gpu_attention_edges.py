@@ -104,3 +104,20 @@ def test_decode_of_infinite_scores(hq, hkv, d, dtype):
     ref, A = definition(c, decode=True)
     same_but_where_nan(gb.gdn_kv_decode(c.q, *c.cache, scale=c.scale), ref, A, dtype)
     assert np.isnan(ref[[0, 1, 3]]).all() and not ref[2].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hkv,d,counts", [(8, 2, 128, [2, 3]), (8, 2, 128, [100, 40]), (8, 2, 64, [300, 40]), (4, 1, 256, [40, 2]), (4, 1, 16, [40, 2])])
+def test_queries_of_a_row_that_is_not_in_use(hq, hkv, d, counts, dtype):
+    # nothing writes them in a padded batch: they may be anything
+    c = Case(64, [-1, 50], counts, hq, hkv, d, 16, dtype)
+    c.q[:counts[0]] = NAN
+    for mask in (None, tree_masks(4, counts)):
+        o = attend(c, mask)
+        assert not torch.any(o[:counts[0]].isnan()) and not torch.any(o[:counts[0]])
+        c.q[:counts[0]] = 1.0
+        assert torch.equal(attend(c, mask), o)
+        c.q[:counts[0]] = NAN
+    one = Case(65, [-1, 50], [1, 1], hq, hkv, d, 16, dtype)
+    one.q[0] = NAN
+    assert not torch.any(gb.gdn_kv_decode(one.q, *one.cache, scale=one.scale)[0])
