@@ -121,3 +121,34 @@ def test_queries_of_a_row_that_is_not_in_use(hq, hkv, d, counts, dtype):
     one = Case(65, [-1, 50], [1, 1], hq, hkv, d, 16, dtype)
     one.q[0] = NAN
     assert not torch.any(gb.gdn_kv_decode(one.q, *one.cache, scale=one.scale)[0])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hkv,d,lens,counts", [(8, 2, 128, [50, 33], [3, 3]), (8, 2, 128, [300, 33], [40, 40]), (8, 2, 64, [500, 3], [130, 9]), (4, 1, 256, [90, 3], [70, 9]),
+                                                  (8, 1, 128, [5000, 20], [2, 1]), (8, 1, 128, [5000, 20], [60, 1]), (4, 1, 256, [5000, 20], [60, 1])])
+def test_tokens_that_see_a_key_of_nan_are_nan(hq, hkv, d, lens, counts, dtype):
+    n = counts[0]
+    c = Case(66, lens, counts, hq, hkv, d, 16, dtype)
+    mask = tree_masks(5, counts)
+    for m in (mask, None):
+        clean = attend(c, m)
+        for j in (0, n // 2, -lens[0], -(lens[0] // 2), -1):  # new tokens, then committed ones
+            page, row = OA.slot(c.table.cpu().numpy(), 0, lens[0] + j, 16)
+            kept = c.k[page, row].clone()
+            c.k[page, row, :, 3] = NAN
+            got = attend(c, m)
+            c.k[page, row] = kept
+            seen = np.ones(n, dtype=bool) if j < 0 else OA.bits(mask.cpu().numpy(), n)[:n, j] if m is not None else np.arange(n) >= j
+            seen = torch.from_numpy(np.concatenate([seen, np.zeros(counts[1], dtype=bool)])).cuda()
+            assert torch.all(got[seen].isnan()) and torch.equal(got[~seen], clean[~seen])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("hq,hkv,d", [(64, 1, 64), (65, 1, 128), (128, 1, 128), (128, 2, 256), (129, 1, 64), (256, 2, 128)])
+def test_many_query_heads_to_one(hq, hkv, d, dtype):
+    counts, lens = [3, 1, 7], [200, 1100, 0]
+    c = Case(67, lens, counts, hq, hkv, d, 16, dtype)
+    for mask in (None, tree_masks(6, counts, empty=(1,))):
+        close(attend(c, mask), *c.oracle(mask), dtype)
+    one = Case(68, [200, 1100, 0, -1], [1] * 4, hq, hkv, d, 16, dtype)
+    close(gb.gdn_kv_decode(one.q, *one.cache, scale=one.scale), *one.oracle(decode=True), dtype)
