@@ -120,11 +120,11 @@ typedef struct {
  * The work is cut along the slots into equal parts, one for each running block, whatever the lengths
  * are (caches of up to 1024 slots, with few rows, are not cut); parts of one token's softmax are joined by a second
  * kernel in a fixed order: the same call gives the same bits.
- * bf16 rows that start on 16 bytes run on the tensor cores: probabilities are rounded to bf16 before they are multiplied
- * by values (2^-8 of each; their sum is kept of the unrounded ones), so that outputs are up to 1.4 times their own rounding to
- * bf16 from exact (norm-wise 2.3e-3, 1.7e-3).  More than 16 rows (new tokens x query heads of a key-value head) in a request
- * take tcgen05, with d from 64 on, pages of a multiple of 8 slots, at most 128 query heads to a key-value head and a positive scale;
- * others warp products.  fp32, and rows that do not start on 16 bytes, run the general kernel in fp32 arithmetic.
+ * bf16 rows that start on 16 bytes run on the tensor cores.  More than 16 rows (max_tokens x query heads of a key-value head)
+ * take tcgen05, with d from 64 on, pages of a multiple of 8 slots, at most 128 query heads to a key-value head and a positive
+ * scale: there probabilities are rounded to bf16 before they are multiplied by values (2^-8 of each; their sum is kept of the
+ * unrounded ones).  Others, and every gdn_kv_decode, take warp products of 16 rows, with probabilities as two bf16 numbers (2^-16).
+ * fp32, and rows that do not start on 16 bytes, run the general kernel in fp32 arithmetic.
  */
 GDN_API int gdn_kv_attend(const gdn_kv_attend_args *args, void *stream);
 
