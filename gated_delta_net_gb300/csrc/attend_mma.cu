@@ -7,8 +7,9 @@
 // empty, and what they cost here is a tenth of the time the bytes take.  The ring runs ahead over the ends of items,
 // with the page of the tile after the next looked up one tile earlier.  At an item's end the warps' parts are joined in
 // shared memory.
-// 128 single tokens over 10 to 6000 slots, 32 heads of 128 to 8: 234 us for 1.47 GB, 6.3 TB/s; one over 131072, 4 heads: 54 us for
-// 268 MB, of which 40 are the bytes, the rest the start (finding the work, the first loads) and the join.
+// 128 single tokens over 10 to 6000 slots, 32 heads of 128 to 8: 237 us for 1.47 GB, 6.2 TB/s; one over 131072, 4 heads: 55 us for
+// 268 MB, of which 40 are the bytes, the rest the start (finding the work, the first loads) and the join.  Heads of 256 have one block
+// an SM and a ring of two tiles: 64 tokens over 100 to 8000 slots, 16 heads to 2, 114 us, 4.7 TB/s.
 // Probabilities are two bf16 numbers for their product with the values, the second what rounding leaves of the first (2^-16 of each
 // together): outputs lose no more than their own rounding.  With one (2^-8), widths to 128 take as long within 2 %, 64 tokens over 100
 // to 8000 slots, 16 heads of 256 to 2, 109 us where this takes 114.

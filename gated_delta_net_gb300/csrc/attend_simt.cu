@@ -1,12 +1,12 @@
 // attend_simt.cu -- attention over a paged cache, general: fp32, and bf16 that the tensor-core kernels do not take.
 //
-// A block has 16 rows (or 4) and takes 32 slots at a time: keys and values to shared memory as fp32 (the next tile's are on their way in
+// A block has 16 rows (or 8, or 4) and takes 32 slots at a time: keys and values to shared memory as fp32 (the next tile's are on their way in
 // registers meanwhile, where rows start on 16 bytes), the scores one slot a
-// lane, four rows a warp, the running maximum and sum of a row in its warp, then the outputs with a column (or two) a thread.
+// lane, a quarter of the rows a warp, the running maximum and sum of a row in its warp, then the outputs with a column (or two) a thread.
 // fp32 arithmetic throughout.  What bounds it is shared-memory reads beside the multiplications (five 16-byte
 // reads for 16 of them in the scores): 6 single tokens over 100 to 23617 slots, 8 heads of 128, 167 us for 582 MB (86); 71
 // over 100 to 7194, 8 query heads to one of 128, 100 us for 236 MB (35); 3 trees of 100 nodes behind 1000 slots, 16 heads
-// of 128 to 4, 212 us.
+// of 128 to 4, 212 us; 8 trees of 128 nodes behind 200 to 2200 slots, the same heads, 817 us, 12.6 TFLOP/s.
 #include "attn.cuh"
 
 namespace gdn {

@@ -11,7 +11,8 @@
 //
 // The maximum that outputs are scaled by is moved, and they are multiplied, only where a row's maximum grew by more than 2^8: then
 // probabilities are up to 2^8, which neither bf16 nor the fp32 sums lose anything by.
-// P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.
+// P is rounded to bf16 (2^-8 of each) as the operand beside V; their sum is kept of the unrounded ones.  As two bf16 numbers
+// (2^-16) it takes a third longer: the prompt below 635 us, the trees 250.
 //
 // 12 warps (8 for one tile of rows):
 //     4 for each tile of rows, a thread a row.  The first half of a tile's probabilities is multiplied while the second is made.
@@ -26,10 +27,11 @@
 //       readers' sums become NaN instead
 // Every wait is bounded; one that runs out sets GDN_DEV_TIMEOUT.
 //
-// One prompt of 8192 tokens behind 777, 32 heads of 128 to 8: 493 us, 1330 TFLOP/s; 64 trees of 128 nodes behind 200 to 2200 slots:
-// 188 us.  A tile of 128 slots takes two tiles of rows 2750 cycles, of which their products need 2048, at which shared memory is
+// One prompt of 8192 tokens behind 777, 32 heads of 128 to 8: 453 us, 1445 TFLOP/s; 64 trees of 128 nodes behind 200 to 2200 slots:
+// 186 us.  A tile of 128 slots takes two tiles of rows about 2450 cycles, of which their products need 2048, at which shared memory is
 // busy as well (operands 192 KB, loads 64 KB, at 128 bytes a cycle); an item's end and beginning take 7000, and an item's
-// masked tiles 1000 more each.  The first product of a block starts 10 us after its launch.
+// masked tiles 1000 more each.  The first product of a block starts 10 us after its launch.  Heads of 256: a tile of 64 slots has 1024
+// cycles of products and 1536 of shared memory, and the prompt with 16 heads to 2 takes 605 us, 1080 TFLOP/s.
 #include "attn.cuh"
 #include "sm100.cuh"
 #include "tc_tiles.cuh"

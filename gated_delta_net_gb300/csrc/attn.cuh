@@ -73,6 +73,7 @@ __device__ __forceinline__ int row_tiles(const Params &p, const Request &r) {
     return (int)((uint32_t)(r.n * p.group + p.rows - 1) / (uint32_t)p.rows);  // (n group is at most 2^30)
 }
 // sum of floor((a i + b) / m) for i = 0 .. n - 1 (a, b >= 0), by turning the lattice points under the line over as in Euclid's algorithm
+// (the reciprocity of such sums: Graham, Knuth, Patashnik, Concrete Mathematics, section 3.5)
 __device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
     int64_t sum = 0;
 #pragma unroll 1

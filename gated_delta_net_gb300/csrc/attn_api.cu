@@ -79,7 +79,7 @@ bool nothing(const gdn_kv_attend_args &a, bool decode) {
 }
 
 // The kernel for a call: the tensor cores where a key-value head has more rows than the 16 of a warp product (eight drafts of 6 to 16
-// nodes, 4 query heads each: 73 us by 16 rows at a time, 55 in tiles), by warp products below that, and the general kernel
+// nodes, 4 query heads each: 72 us by 16 rows at a time, 43 in tiles), by warp products below that, and the general kernel
 // for fp32 and rows that do not start on 16 bytes.
 gdn::attn::Choice choose(const gdn_kv_attend_args &a, bool decode) {
     if (!decode && a.max_tokens * (int64_t)(a.n_q_heads / a.cache.n_kv_heads) > 16 && gdn::attend_tc_supported(a)) return gdn::attend_tc_choice(a);

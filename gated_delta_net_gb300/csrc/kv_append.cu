@@ -6,7 +6,8 @@
 // A block takes a token, with one warp or four; d / 8 lanes take a row with 8 entries each, one row after another, so that a token's cosines and
 // sines are read once into registers.  The partner of an entry in a pair is 8 lanes or fewer away, or its neighbour.
 // 16384 tokens of 16 + 2 heads of 256, a quarter turned, with norms: 72 us for 340 MB, 4.7 TB/s (50 at the copy's rate); what is left is
-// latency, with three rows of a lane on their way (one: 78 us).
+// latency (half the issue slots are free, waits for loads come first), with three rows of a lane on their way (one: 78 us).  In fp32 three
+// do not fit the registers and 56 to 104 bytes spill.
 // Where rows do not start on 16 bytes, or half the rotated width is no multiple of 8, entries and partners are read one by one.
 #include "attn.cuh"
 

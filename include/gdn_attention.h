@@ -116,10 +116,12 @@ typedef struct {
  * descend or pass T GDN_DEV_BAD_DESC, slots past the page table GDN_DEV_BAD_PAGE; that request is left out,
  * its outputs are not written.  After a page outside the pool the request's outputs are unspecified.
  * A NaN or infinity in a key or value reaches the tokens that see it, and no others (the whole
- * rows of those, as NaN, where it stands in the value of a new token).
+ * rows of those, as NaN, where it stands in the value of a new token); a token all of whose scores are
+ * -infinity is NaN.
  * The work is cut along the slots into equal parts, one for each running block, whatever the lengths
- * are (caches of up to 1024 slots, with few rows, are not cut); parts of one token's softmax are joined by a second
- * kernel in a fixed order: the same call gives the same bits.
+ * are; parts of one token's softmax are joined by a second kernel in a fixed order: the same call gives the
+ * same bits.  Page tables with room for few slots (1024 for the warp products, 128 for the general kernel; the room
+ * counts, not the lengths) are not cut.
  * bf16 rows that start on 16 bytes run on the tensor cores.  More than 16 rows (max_tokens x query heads of a key-value head)
  * take tcgen05, with d from 64 on, pages of a multiple of 8 slots, at most 128 query heads to a key-value head and a positive
  * scale: there probabilities are rounded to bf16 before they are multiplied by values (2^-8 of each; their sum is kept of the
@@ -130,7 +132,9 @@ GDN_API int gdn_kv_attend(const gdn_kv_attend_args *args, void *stream);
 
 /*
  * gdn_kv_decode -- one new token for each request, token b for request b: gdn_kv_attend with
- * lens[b] + 1 slots seen.
+ * lens[b] + 1 slots seen.  The cache is read once for every 16 query heads of a key-value head; with more of them gdn_kv_attend
+ * with one token a request, which reads it once, takes less (64 tokens over 100 to 8000 slots, heads of 128, 32 to one: 66 us
+ * where this takes 94, 128 to one: 48 and 163).
  */
 GDN_API int gdn_kv_decode(const gdn_kv_attend_args *args, void *stream);
 
