@@ -27,11 +27,11 @@
 //       readers' sums become NaN instead
 // Every wait is bounded; one that runs out sets GDN_DEV_TIMEOUT.
 //
-// One prompt of 8192 tokens behind 777, 32 heads of 128 to 8: 453 us, 1445 TFLOP/s; 64 trees of 128 nodes behind 200 to 2200 slots:
-// 186 us.  A tile of 128 slots takes two tiles of rows about 2450 cycles, of which their products need 2048, at which shared memory is
+// One prompt of 8192 tokens behind 777, 32 heads of 128 to 8: 450 us, 1454 TFLOP/s; 64 trees of 128 nodes behind 200 to 2200 slots:
+// 185 us.  A tile of 128 slots takes two tiles of rows about 2450 cycles, of which their products need 2048, at which shared memory is
 // busy as well (operands 192 KB, loads 64 KB, at 128 bytes a cycle); an item's end and beginning take 7000, and an item's
 // masked tiles 1000 more each.  The first product of a block starts 10 us after its launch.  Heads of 256: a tile of 64 slots has 1024
-// cycles of products and 1536 of shared memory, and the prompt with 16 heads to 2 takes 605 us, 1080 TFLOP/s.
+// cycles of products and 1536 of shared memory, and the prompt with 16 heads to 2 takes 610 us, 1073 TFLOP/s.
 #include "attn.cuh"
 #include "sm100.cuh"
 #include "tc_tiles.cuh"
@@ -167,6 +167,14 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     f2 r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
+}
+
+// What a row with maximum m multiplies its scores by.  m times sc is rounded, past 2^30 by so much that the largest score's power may
+// not be finite.  There fp32 scores that differ at all have weights 2^64 or more apart, 2^32 or more with the power of two below sc,
+// whose product is exact: the largest has all the weight either way.  (Subtracting the maximum before the product, in a
+// branch that such rows take, cost others 1 to 3 %; this 0 at d = 128, 1 to 2 % at 64 and 256.)
+__device__ __forceinline__ float scale_of(float m, float sc) {
+    return fabsf(m * sc) > 1073741824.f ? __uint_as_float(max(__float_as_uint(sc) & 0x7F800000u, 0x00800000u)) : sc;
 }
 
 // Bits 0..31: whether token i of the request sees slots from .. from + 31.
@@ -310,7 +318,8 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
                 } else if (__any_sync(0xffffffffu, move)) {
                     tc_fence_after();
                     const float now = move ? fmaxf(top, m) : m;
-                    const float f = m == -INFINITY ? 0.f : exp2_fast((m - now) * sc);
+                    // (from the products as they are rounded beside the scores, or the difference, which is exact, where those are exact)
+                    const float f = m == -INFINITY ? 0.f : exp2_fast(scale_of(now, sc) == sc ? __fsub_rn(__fmul_rn(m, sc), __fmul_rn(now, sc)) : (m - now) * sc);
                     m = now;
                     l2 = fma2(l2, pair(__float_as_uint(f), __float_as_uint(f)), pair(0x80000000u, 0x80000000u));
 #pragma unroll 1
@@ -323,8 +332,8 @@ __global__ void __launch_bounds__(Shape<D, U>::kThreads, 1)
                         tmem_st16(o_at + i, o);
                     }
                 }
-                const float off = m == -INFINITY ? 0.f : -m * sc;
-                const f2 sc2 = pair(__float_as_uint(sc), __float_as_uint(sc)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
+                const float by = scale_of(m, sc), off = m == -INFINITY ? 0.f : -m * by;
+                const f2 sc2 = pair(__float_as_uint(by), __float_as_uint(by)), off2 = pair(__float_as_uint(off), __float_as_uint(off));
                 // the first half of the probabilities is multiplied while the second is made
 #pragma unroll
                 for (int i = 0; i < N; ++i) {

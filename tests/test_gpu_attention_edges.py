@@ -152,3 +152,41 @@ def test_many_query_heads_to_one(hq, hkv, d, dtype):
         close(attend(c, mask), *c.oracle(mask), dtype)
     one = Case(68, [200, 1100, 0, -1], [1] * 4, hq, hkv, d, 16, dtype)
     close(gb.gdn_kv_decode(one.q, *one.cache, scale=one.scale), *one.oracle(decode=True), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("size", [3e4, 3e5, 1e7])
+@pytest.mark.parametrize("hq,hkv,d,lens,counts", [(8, 2, 128, [20, 300], [3, 4]), (8, 2, 128, [20, 300], [40, 3]), (4, 1, 64, [1000, 0], [300, 2]), (8, 1, 256, [500, 70], [30, 9]),
+                                                  (8, 1, 128, [5000, 3], [60, 1])])
+def test_scores_far_past_what_their_softmax_can_tell_apart(hq, hkv, d, lens, counts, size, dtype):
+    # scores of 1e9 to 1e15, finite: the largest one has all the weight (their distances, 1e-3 of them and more here, are far more
+    # than fp32 sums of d products are off, 2^-20 of their terms' sizes)
+    c = Case(70, lens, counts, hq, hkv, d, 16, dtype)
+    c.k *= size
+    c.q *= size
+    for mask in (None, tree_masks(7, counts)):
+        ref, A = definition(c, mask)
+        rows = sure_rows(c, mask)
+        assert rows.mean() > 0.8
+        o = attend(c, mask)
+        assert torch.isfinite(o).all()
+        close(torch.where(torch.from_numpy(rows)[..., None].cuda(), o, torch.zeros_like(o)), np.where(rows[..., None], ref, 0.0), np.where(rows[..., None], A, 0.0), dtype)
+
+
+def sure_rows(c, mask):
+    """[T, Hq]: whether a row's two largest scores differ by more than 2^-18 of the sum of their terms' sizes."""
+    q, k = f64(c.q), np.nan_to_num(f64(c.k))
+    table, off, group = c.table.cpu().numpy(), c.off.cpu().numpy(), c.q.shape[1] // c.k.shape[2]
+    sure = np.ones(q.shape[:2], dtype=bool)
+    bits = None if mask is None else OA.bits(mask.cpu().numpy(), max(c.counts))
+    for b, n in enumerate(c.counts):
+        at = [OA.slot(table, b, s, k.shape[1]) for s in range(c.lens_list[b] + n)]
+        keys = np.stack([k[p, r] for p, r in at])
+        for i in range(n):
+            seen = np.concatenate([np.ones(c.lens_list[b], dtype=bool), np.arange(n) <= i if bits is None else bits[off[b] + i, :n]])
+            for h in range(q.shape[1]):
+                mine, row = keys[seen, h // group], q[off[b] + i, h]
+                two = np.sort(mine @ row)[-2:]
+                if len(two) == 2:
+                    sure[off[b] + i, h] = two[1] - two[0] > 2.0 ** -18 * np.max(np.abs(mine) @ np.abs(row))
+    return sure
